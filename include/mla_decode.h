@@ -9,6 +9,11 @@
  *   mla_value_gate     : absorbed W_UV projection fused with the sigmoid gate
  *                        -> o_proj's input
  *
+ * and the operators around it: mla_kv_append, mla_add_rms_norm (the norms in
+ * front of the projections), mla_value_gate_lora (the projection with the
+ * requests' adapters), mla_token_weights and mla_kv_evict (the cache held to
+ * a budget by attention weight).
+ *
  * Sources (vLLM API pages):
  *   - vllm.models.kimi_k3.amd.specialized_decode.runtime.mla: attend,
  *     m1c_inputs, post (the decode split, the cache as one 576-byte row per
@@ -59,6 +64,7 @@ typedef int mla_status;
 #define MLA_DEV_BAD_INDPTR 2u    /* indptr not monotone or beyond num_pages      */
 #define MLA_DEV_TIMEOUT 4u       /* a bounded device wait ran out                */
 #define MLA_DEV_BAD_PLAN 8u      /* a work plan did not fit this launch          */
+#define MLA_DEV_BAD_ADAPTER 16u  /* an adapter index was outside [-1, num_adapters) */
 
 /*
  * mla_decode_attend -- split-KV attention of one decode step.
@@ -355,6 +361,152 @@ mla_status mla_merge_value_gate(const void *o, const float *lse, int num_splits,
 mla_status mla_kv_append(const void *kv_c, int64_t kv_c_row_stride, const void *k_pe, int64_t k_pe_row_stride,
                          const int64_t *slots, int64_t num_tokens, float k_scale, void *kv, int64_t pool_rows,
                          void *stream);
+
+/* Element types of mla_add_rms_norm. */
+#define MLA_TYPE_BF16 0
+#define MLA_TYPE_F16 1
+#define MLA_TYPE_F32 2
+
+/* Output forms of mla_add_rms_norm. */
+#define MLA_QUANT_NONE 0   /* x's type                                          */
+#define MLA_QUANT_ROW 1    /* e4m3 codes, one scale per row                     */
+#define MLA_QUANT_GROUP 2  /* e4m3 codes, one scale per 128 columns             */
+#define MLA_QUANT_STATIC 3 /* e4m3 codes, the given scale                       */
+#define MLA_MAX_NORM_WIDTH 32768
+
+/*
+ * mla_add_rms_norm -- residual addition and root-mean-square norm, with an
+ * output in 16 or 8 bits: the norms in front of a layer's projections, and
+ * of its latents.
+ *
+ * For row t < tokens, in float32 (s is not rounded before the norm):
+ *   s = x[t] + residual[t]                    (x[t] without a residual)
+ *   residual_out[t] = s rounded to the residual's type
+ *   y = s * rsqrt(sum(s^2) / width + eps) * weight
+ * and, by `quant`:
+ *   NONE    out[t] = y rounded to x's type
+ *   ROW     sc = scale_of(max |y|); out_scales[t] = sc
+ *   GROUP   the same for each 128 columns (the last group may be narrower):
+ *           out_scales[t * ceil(width / 128) + g]
+ *   STATIC  sc = scale (nothing is written to out_scales)
+ *   and out[t] = e4m3(y * (1 / sc)), to nearest even, saturating at +-448.
+ * scale_of(m) is m / 448, at least 2^-126; 1 when m is 0.  A NaN in a row
+ * makes the row's y NaN (and its scales); an infinite s is NaN in y, the
+ * rest of its row 0.
+ *
+ *   x            bf16 or f16 (x_type), row t at x + t*x_stride (elements).
+ *   residual     x's type or f32 (residual_type), row stride residual_stride;
+ *                NULL: none (residual_out must then be NULL too).
+ *   weight       x's type [width].
+ *   out          x's type, or e4m3 codes; row stride out_stride (elements).
+ *   residual_out residual's type, row stride residual_out_stride (written).
+ * width: a multiple of 8, 8..32768.  Strides >= width and multiples of 8;
+ * pointers 16-byte aligned, out_scales 4.  eps finite and > 0; a STATIC
+ * scale finite and >= 2^-126.  residual_out may be residual or x, and out
+ * (16-bit) x or residual, as long as pointer, stride and element size are
+ * the same; any other overlap of what is written with what is read or
+ * written is MLA_ERR_INVALID (columns side by side in one buffer of one
+ * stride do not overlap).
+ */
+mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const void *residual,
+                            int64_t residual_stride, int residual_type, const void *weight, float eps,
+                            int64_t tokens, int width, int quant, float scale, void *out, int64_t out_stride,
+                            float *out_scales, void *residual_out, int64_t residual_out_stride, void *stream);
+
+/*
+ * mla_token_weights -- the attention weight that each cached token received
+ * in a decode step, accumulated: what an eviction policy ranks tokens by.
+ *
+ * For request r, its token j (entry i = indptr[r] + j of pages) and
+ * K_j = e4m3fn(kv[pages[i]]) * kv_scale:
+ *   out[i] = decay * weights[i]
+ *            + sum over rows t of r that see j, heads h, with lse[t, h] > -inf, of
+ *              exp(scale * q_scale * <q[t, h, :], K_j> - lse[t, h])
+ * With lse the merged LSE of the same step (mla_merge_splits) the new
+ * weights of a request sum to its rows x heads.  Every entry below
+ * indptr[num_requests] is written, others are left as they were.  The sum
+ * has a fixed order: equal inputs give equal bits.
+ *
+ *   q, q_row_stride, kv, pool_rows, pages, num_pages, indptr, num_requests,
+ *   qlen, heads, scale, kv_scale, q_scale, flags: as
+ *                mla_decode_attend_planned at page size 1 (flags:
+ *                MLA_ATTEND_CAUSAL, MLA_ATTEND_Q_FP8).
+ *   lse          f32 [num_requests * qlen, heads].
+ *   decay        finite; 0 does not read weights.
+ *   weights      f32 [num_pages]; may be NULL when decay is 0.
+ *   out          f32 [num_pages] (written); may be weights itself, otherwise
+ *                must not overlap it.
+ * A page outside the pool reads as row 0 of the pool and sets
+ * MLA_DEV_BAD_PAGE; a bad indptr entry sets MLA_DEV_BAD_INDPTR and leaves
+ * its request's entries as they were.
+ */
+mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
+                             const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
+                             int qlen, int heads, float scale, float kv_scale, float q_scale, const float *lse,
+                             float decay, const float *weights, float *out, unsigned int flags, void *stream);
+
+/*
+ * mla_kv_evict -- cut every request's page list to a budget, by weight.
+ *
+ * Request r of L tokens keeps n = min(L, max(budget, 0)) of them:
+ *   its last min(recent, n) tokens; its first min(sinks, n - those); and of
+ *   the tokens in between those with the largest weights until n are kept
+ *   (NaN counts as -inf, -0 equals +0, equal weights by the lower position).
+ * Kept tokens keep their order.  With N = indptr[R] and K = indptr_out[R]:
+ *   indptr_out[r]         the requests' kept tokens, as indptr counts them
+ *   pages_out[0 .. K)     kept rows, request by request (with indptr_out:
+ *                         what mla_decode_attend takes next)
+ *   pages_out[K .. N)     freed rows, request by request, in order
+ *   weights_out[0 .. K)   the kept tokens' weights; [K .. N) zeros
+ * Entries from N on are left as they were.  The cache itself is not touched
+ * and pages are not looked up: a row is only an index here.
+ *
+ *   pages, weights  int32 / f32 [num_pages]; indptr int32 [num_requests + 1].
+ *   budgets         int32 [num_requests], device; NULL: `budget` for all.
+ *   recent, sinks   >= 0.
+ *   pages_out, weights_out  [num_pages], indptr_out [num_requests + 1]; no
+ *                   output may overlap an input or another output.
+ * A bad indptr entry sets MLA_DEV_BAD_INDPTR and its request is empty.
+ */
+mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
+                        const float *weights, const int32_t *budgets, int budget, int recent, int sinks,
+                        int32_t *pages_out, int32_t *indptr_out, float *weights_out, void *stream);
+
+/*
+ * mla_value_gate_lora -- mla_value_gate with one low-rank adapter per
+ * request beside W_UV.
+ *
+ * For row t, head h, output v < 128, with r = t / qlen and a = adapters[r]:
+ *   val = sum_c latent[t, h, c] * w_uv[h, v, c]
+ *         + lora_scale[a] * sum_k (sum_c latent[t, h, c] * lora_a[a, k, c]) * lora_b[a, h*128 + v, k]
+ *   out[t, h*128 + v] = lengths[r] > 0 ? bf16( val * sigmoid(f32(gate[t, h*128 + v])) ) : 0
+ * in float32, rounded once (mla_value_gate also rounds its value to bf16
+ * before the gate, so rows without an adapter may differ from it by that
+ * rounding); the low-rank products are carried as two bf16 terms (relative
+ * error 2^-17).  adapters[r] = -1: no adapter.  Another index outside
+ * [0, num_adapters) sets MLA_DEV_BAD_ADAPTER and counts as -1.  The zeroing
+ * is a select, so NaN gates, latents or adapters of empty requests never
+ * reach out.
+ *
+ *   latent, w_uv, gate, lengths, out   as mla_value_gate
+ *   lora_a       bf16 [num_adapters, rank, 512]
+ *   lora_b       bf16 [num_adapters, heads*128, rank]
+ *   rank         a multiple of 8, 8..128 (pad narrower adapters with zeros)
+ *   adapters     int32 [num_requests], lora_scale f32 [num_adapters], device
+ *   workspace    device, 16-byte aligned, at least
+ *                mla_value_gate_lora_workspace() bytes; holds nothing
+ *                between calls, but two calls that may overlap on the GPU
+ *                need one each.
+ */
+#define MLA_MAX_LORA_RANK 128
+mla_status mla_value_gate_lora(const void *latent, const void *w_uv, const void *gate, const int32_t *lengths,
+                               const void *lora_a, const void *lora_b, const int32_t *adapters,
+                               const float *lora_scale, int num_adapters, int rank, int num_requests, int qlen,
+                               int heads, void *out, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that mla_value_gate_lora needs; a negative mla_status
+ * on bad sizes. */
+int64_t mla_value_gate_lora_workspace(int num_requests, int qlen, int heads, int rank);
 
 /*
  * mla_choose_splits -- a split plan for mla_decode_attend from host-known

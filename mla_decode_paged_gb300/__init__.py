@@ -7,6 +7,9 @@ The three calls of one decode step of a Multi-head Latent Attention layer:
     latent, lse_merged = merge(o, lse)
     out = value_gate(latent, w_uv, gate, lengths, qlen)
 
+and the operators around them: ``kv_append``, ``add_rms_norm``,
+``token_weights`` / ``kv_evict`` and ``value_gate_lora``.
+
 This module only marshals arguments: it checks dtypes / shapes, allocates
 outputs with torch (device memory), passes raw pointers and the current CUDA
 stream to the native library, and turns error codes into exceptions.  Every
@@ -27,13 +30,14 @@ from . import build as _build
 D_QK, D_LATENT, D_V = 576, 512, 128
 MLA_OK, MLA_ERR_INVALID, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA = 0, -1, -2, -3
 ATTEND_CAUSAL, ATTEND_Q_FP8 = 1, 2
-DEV_BAD_PAGE, DEV_BAD_INDPTR, DEV_TIMEOUT, DEV_BAD_PLAN = 1, 2, 4, 8
+DEV_BAD_PAGE, DEV_BAD_INDPTR, DEV_TIMEOUT, DEV_BAD_PLAN, DEV_BAD_ADAPTER = 1, 2, 4, 8, 16
 STATIC_SCRATCH_BYTES = 32 << 20   # MLA_STATIC_SCRATCH_BYTES: the partials buffer of decode_step_static
 
 __all__ = ["Prepared", "attend", "merge", "value_gate", "merge_value_gate", "decode_step", "decode_step_static",
            "STATIC_SCRATCH_BYTES", "choose_splits", "plan_units", "debug_gather",
            "debug_wait_timeout", "debug_attend_mma",
-           "kv_append", "device_status", "build", "library", "MlaError"]
+           "kv_append", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
+           "value_gate_lora_workspace", "device_status", "build", "library", "MlaError"]
 
 
 class MlaError(RuntimeError):
@@ -88,7 +92,15 @@ def library() -> ctypes.CDLL:
     lib.mla_kv_append.argtypes = [vp, i64, vp, i64, vp, i64, f32, vp, i64, vp]
     lib.mla_decode_step_static.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, i32, i32,
                                            vp, i64, vp, vp, vp, vp, vp, vp, vp]
-    for name in ("mla_decode_attend", "mla_decode_attend_ex", "mla_decode_attend_paged", "mla_decode_attend_planned", "mla_merge_splits", "mla_value_gate", "mla_merge_value_gate", "mla_debug_gather",
+    lib.mla_add_rms_norm.argtypes = [vp, i64, i32, vp, i64, i32, vp, f32, i64, i32, i32, f32, vp, i64, vp, vp, i64, vp]
+    lib.mla_token_weights.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, f32, vp, f32, vp, vp,
+                                      ctypes.c_uint, vp]
+    lib.mla_kv_evict.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    lib.mla_value_gate_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
+    lib.mla_value_gate_lora_workspace.argtypes = [i32, i32, i32, i32]
+    lib.mla_value_gate_lora_workspace.restype = i64
+    for name in ("mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
+                 "mla_decode_attend", "mla_decode_attend_ex", "mla_decode_attend_paged", "mla_decode_attend_planned", "mla_merge_splits", "mla_value_gate", "mla_merge_value_gate", "mla_debug_gather",
                  "mla_device_status", "mla_choose_splits", "mla_kv_append", "mla_debug_wait_timeout",
                  "mla_decode_step_static", "mla_debug_attend_mma"):
         getattr(lib, name).restype = ctypes.c_int
@@ -449,6 +461,242 @@ def kv_append(kv, kv_c, k_pe, slots, k_scale, *, stream=None):
     return kv
 
 
+_NORM_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_NORM_QUANT = {None: 0, "row": 1, "group": 2, "static": 3}
+
+
+def _empty(shape, dtype, device, stream):
+    """An output on ``device``; one that a call launches on a ``stream`` of
+    its own is allocated there, so that its memory is not still in use by
+    work of the current stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _launch(fn, where, device, stream, *args):
+    """``fn(*args, stream)`` with ``device`` current (plain ints are passed
+    as pointers)."""
+    dev = device.index
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream, dev))
+    else:
+        st = fn(*args, _stream(stream, dev))
+    if st != MLA_OK:
+        _check(st, where)
+
+
+def _rows_of(t, name, dtypes, n, width):
+    _need(t.dtype in dtypes and t.dim() == 2 and t.shape[0] == n and t.shape[1] == width
+          and (t.stride(1) == 1 or width == 1), "%s must be %s [%d, %d] with contiguous rows"
+          % (name, " or ".join(str(d) for d in dtypes), n, width))
+    return t.stride(0) if n > 1 else width
+
+
+def add_rms_norm(x, weight, eps, residual=None, *, quant=None, scale=None, out=None, out_scales=None,
+                 residual_out=None, stream=None):
+    """Residual addition and root-mean-square norm (``mla_add_rms_norm``):
+    returns ``(out, out_scales, residual_out)`` (None for what does not
+    apply).
+
+    ``x``: bf16 / fp16 ``[T, D]``, rows may be strided (D a multiple of 8);
+    ``weight``: x's type ``[D]``; ``residual``: x's type or float32 ``[T, D]``:
+    the norm is of the float32 sum, which ``residual_out`` gets rounded to
+    the residual's type (pass ``residual`` itself to update it in place).
+    ``quant=None``: ``out`` in x's type.  Otherwise e4m3 codes
+    (float8_e4m3fn) with scales ``"row"`` ``[T]``, ``"group"``
+    ``[T, ceil(D / 128)]`` (128 columns each) or ``"static"`` (the float
+    ``scale``; no scales returned): a code stands for code * scale.
+    """
+    _need(x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float16), "x must be bf16 or fp16 [T, D]")
+    T, D = x.shape
+    dev = x.device
+    _same_device(dev, weight=weight, residual=residual, out=out, out_scales=out_scales, residual_out=residual_out)
+    xs = _rows_of(x, "x", (x.dtype,), T, D)
+    _need(weight.dtype == x.dtype and weight.shape == (D,) and weight.is_contiguous(),
+          "weight must be contiguous, x's type, [D]")
+    _need(quant in _NORM_QUANT, "quant must be None, 'row', 'group' or 'static'")
+    _need((scale is not None) == (quant == "static"), "scale goes with quant='static'")
+    rs = ros = 0
+    if residual is not None:
+        rs = _rows_of(residual, "residual", (x.dtype, torch.float32), T, D)
+        if residual_out is None:
+            residual_out = _empty((T, D), residual.dtype, dev, stream)
+            ros = D
+        else:
+            ros = _rows_of(residual_out, "residual_out", (residual.dtype,), T, D)
+    else:
+        _need(residual_out is None, "residual_out needs a residual")
+    otype = x.dtype if quant is None else torch.float8_e4m3fn
+    if out is None:
+        out = _empty((T, D), otype, dev, stream)
+        os_ = D
+    else:
+        os_ = _rows_of(out, "out", (otype,) if quant is None else (otype, torch.uint8), T, D)
+    if quant in ("row", "group"):
+        shape = (T,) if quant == "row" else (T, (D + 127) // 128)
+        if out_scales is None:
+            out_scales = _empty(shape, torch.float32, dev, stream)
+        else:
+            _buffer(out_scales, "out_scales", torch.float32, shape)
+    else:
+        _need(out_scales is None, "out_scales goes with quant='row' or 'group'")
+    _launch(library().mla_add_rms_norm, "mla_add_rms_norm", dev, stream, x.data_ptr(), xs, _NORM_TYPES[x.dtype],
+            None if residual is None else residual.data_ptr(), rs,
+            0 if residual is None else _NORM_TYPES[residual.dtype], weight.data_ptr(), eps, T, D, _NORM_QUANT[quant],
+            0.0 if scale is None else scale, out.data_ptr(), os_, None if out_scales is None else out_scales.data_ptr(),
+            None if residual_out is None else residual_out.data_ptr(), ros)
+    return out, out_scales, residual_out
+
+
+def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qlen=1, weights=None, decay=1.0,
+                  causal=False, q_scale=1.0, out=None, stream=None):
+    """The attention weight every cached token received in a decode step,
+    added to ``decay`` times the weights gathered so far
+    (``mla_token_weights``): returns ``out`` float32 ``[len(pages)]``.
+
+    ``q``, ``kv``, ``pages``, ``indptr``, ``scale``, ``kv_scale``, ``heads``,
+    ``qlen``, ``causal``, ``q_scale`` as in :func:`attend` (page size 1);
+    ``lse``: the step's merged LSE float32 ``[S, heads]`` (from
+    :func:`merge` or :func:`decode_step`).  ``weights``: float32, one entry
+    per entry of ``pages`` (None: zeros); ``out=weights`` updates in place.
+    Entries past ``indptr[-1]`` are left as they were.
+    """
+    kv = _as_u8(kv)
+    heads = q.shape[1] if heads is None else heads
+    R = indptr.numel() - 1
+    S = R * qlen
+    q8 = q.dtype in (torch.float8_e4m3fn, torch.uint8)
+    _need((q8 or q.dtype == torch.bfloat16) and q.dim() == 3 and q.shape[2] == D_QK,
+          "q must be bf16 or fp8 e4m3 [S, H, 576]")
+    _need(q.stride(2) == 1 and (q.stride(1) == D_QK or q.shape[1] == 1), "q rows must have contiguous [H, 576] heads")
+    _need(q.shape[0] == S and heads <= q.shape[1], "q shape does not match indptr / qlen / heads")
+    _need(kv.dim() == 2 and kv.shape[1] == D_QK and kv.is_contiguous(), "kv must be contiguous [pool, 576]")
+    _need(pages.dtype == torch.int32 and indptr.dtype == torch.int32 and pages.is_contiguous()
+          and indptr.is_contiguous(), "pages / indptr must be contiguous int32")
+    _need(lse.dtype == torch.float32 and lse.shape == (S, heads) and lse.is_contiguous(),
+          "lse must be contiguous f32 [S, heads]")
+    dev = q.device
+    _same_device(dev, kv=kv, pages=pages, indptr=indptr, lse=lse, weights=weights, out=out)
+    n = pages.numel()
+    if weights is not None:
+        _buffer(weights, "weights", torch.float32, (n,))
+    if out is None:
+        out = _empty((n,), torch.float32, dev, stream)
+    else:
+        _buffer(out, "out", torch.float32, (n,))
+    _launch(library().mla_token_weights, "mla_token_weights", dev, stream, q.data_ptr(),
+            q.stride(0) if S > 1 else heads * D_QK, kv.data_ptr(), kv.shape[0], pages.data_ptr(), n,
+            indptr.data_ptr(), R, qlen, heads, scale, kv_scale, q_scale, lse.data_ptr(),
+            0.0 if weights is None else decay, None if weights is None else weights.data_ptr(), out.data_ptr(),
+            (ATTEND_CAUSAL if causal else 0) | (ATTEND_Q_FP8 if q8 else 0))
+    return out
+
+
+def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=None, indptr_out=None, weights_out=None,
+             stream=None):
+    """Cut every request's page list to ``budget`` tokens (``mla_kv_evict``):
+    its last ``recent``, its first ``sinks`` and, between them, the heaviest
+    by ``weights`` (float32, one per entry of ``pages``; from
+    :func:`token_weights`).  Returns ``(pages_out, indptr_out,
+    weights_out)``: ``pages_out`` holds the kept rows of every request in
+    order (``indptr_out`` counts them; both go to :func:`attend` as they
+    are), then the freed rows; ``weights_out`` the kept tokens' weights,
+    then zeros.  ``budget``: an int, or int32 ``[R]`` on the device.
+    """
+    _need(pages.dtype == torch.int32 and indptr.dtype == torch.int32 and pages.dim() == 1 and indptr.dim() == 1
+          and indptr.numel() >= 1 and pages.is_contiguous() and indptr.is_contiguous(),
+          "pages / indptr must be contiguous int32")
+    n, R = pages.numel(), indptr.numel() - 1
+    _buffer(weights, "weights", torch.float32, (n,))
+    budgets = None
+    if isinstance(budget, torch.Tensor):
+        _buffer(budget, "budget", torch.int32, (R,))
+        budgets, budget = budget, 0
+    dev = pages.device
+    _same_device(dev, indptr=indptr, weights=weights, budget=budgets, pages_out=pages_out, indptr_out=indptr_out,
+                 weights_out=weights_out)
+    if pages_out is None:
+        pages_out = _empty((n,), torch.int32, dev, stream)
+    else:
+        _buffer(pages_out, "pages_out", torch.int32, (n,))
+    if indptr_out is None:
+        indptr_out = _empty((R + 1,), torch.int32, dev, stream)
+    else:
+        _buffer(indptr_out, "indptr_out", torch.int32, (R + 1,))
+    if weights_out is None:
+        weights_out = _empty((n,), torch.float32, dev, stream)
+    else:
+        _buffer(weights_out, "weights_out", torch.float32, (n,))
+    _need(-2**31 <= budget < 2**31 and 0 <= recent < 2**31 and 0 <= sinks < 2**31,
+          "budget, recent, sinks must fit int32, recent and sinks >= 0")
+    _launch(library().mla_kv_evict, "mla_kv_evict", dev, stream, pages.data_ptr(), n, indptr.data_ptr(), R,
+            weights.data_ptr(), None if budgets is None else budgets.data_ptr(), budget, recent, sinks,
+            pages_out.data_ptr(), indptr_out.data_ptr(), weights_out.data_ptr())
+    return pages_out, indptr_out, weights_out
+
+
+def value_gate_lora(latent, w_uv, gate, lengths, lora_a, lora_b, adapters, lora_scale, qlen=1, *, out=None,
+                    workspace=None, stream=None):
+    """:func:`value_gate` with one low-rank adapter per request beside W_UV
+    (``mla_value_gate_lora``): returns ``out [S, heads*128] bf16``.
+
+    ``lora_a``: bf16 ``[n, rank, 512]``, ``lora_b``: bf16 ``[n, heads*128,
+    rank]`` (rank a multiple of 8 up to 128), ``lora_scale``: float32
+    ``[n]``; ``adapters``: int32 ``[R]``, request r's adapter, -1 for none.
+    ``workspace``: uint8, at least :func:`value_gate_lora_workspace` bytes,
+    16-byte aligned (allocated if not given; not shared by calls that may
+    overlap).
+    """
+    _need(latent.dtype == torch.bfloat16 and latent.dim() == 3 and latent.shape[2] == D_LATENT
+          and latent.is_contiguous(), "latent must be contiguous bf16 [S, heads, 512]")
+    S, H = latent.shape[:2]
+    R = lengths.numel()
+    _need(w_uv.dtype == torch.bfloat16 and w_uv.shape == (H, D_V, D_LATENT) and w_uv.is_contiguous(),
+          "w_uv must be contiguous bf16 [heads, 128, 512]")
+    _need(gate.dtype == torch.bfloat16 and gate.shape == (S, H * D_V) and gate.is_contiguous(),
+          "gate must be contiguous bf16 [S, heads*128]")
+    _need(lengths.dtype == torch.int32 and R * qlen == S and lengths.is_contiguous(),
+          "lengths must be contiguous int32 [S / qlen]")
+    _need(lora_a.dtype == torch.bfloat16 and lora_a.dim() == 3 and lora_a.shape[2] == D_LATENT
+          and lora_a.is_contiguous(), "lora_a must be contiguous bf16 [n, rank, 512]")
+    n, rank = lora_a.shape[:2]
+    _need(lora_b.dtype == torch.bfloat16 and lora_b.shape == (n, H * D_V, rank) and lora_b.is_contiguous(),
+          "lora_b must be contiguous bf16 [n, heads*128, rank]")
+    _need(adapters.dtype == torch.int32 and adapters.shape == (R,) and adapters.is_contiguous(),
+          "adapters must be contiguous int32 [R]")
+    _need(lora_scale.dtype == torch.float32 and lora_scale.shape == (n,) and lora_scale.is_contiguous(),
+          "lora_scale must be contiguous f32 [n]")
+    dev = latent.device
+    _same_device(dev, w_uv=w_uv, gate=gate, lengths=lengths, lora_a=lora_a, lora_b=lora_b, adapters=adapters,
+                 lora_scale=lora_scale, out=out, workspace=workspace)
+    if out is None:
+        out = _empty((S, H * D_V), torch.bfloat16, dev, stream)
+    else:
+        _buffer(out, "out", torch.bfloat16, (S, H * D_V))
+    if workspace is None:
+        workspace = _empty((value_gate_lora_workspace(R, qlen, H, rank),), torch.uint8, dev, stream)
+    else:
+        _need(workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous(),
+              "workspace must be contiguous uint8")
+    _launch(library().mla_value_gate_lora, "mla_value_gate_lora", dev, stream, latent.data_ptr(), w_uv.data_ptr(),
+            gate.data_ptr(), lengths.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
+            lora_scale.data_ptr(), n, rank, R, qlen, H, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def value_gate_lora_workspace(requests, qlen, heads, rank):
+    """Bytes of workspace that :func:`value_gate_lora` needs."""
+    n = library().mla_value_gate_lora_workspace(requests, qlen, heads, rank)
+    if n < 0:
+        _check(int(n), "mla_value_gate_lora_workspace")
+    return int(n)
+
+
 def debug_wait_timeout(stream=None):
     """Test hook: enqueue a kernel whose bounded wait runs out (about 2 s);
     it sets DEV_TIMEOUT, which :func:`device_status` then reports."""
@@ -457,7 +705,8 @@ def debug_wait_timeout(stream=None):
 
 def device_status(stream=None) -> int:
     """Synchronise the stream, return and clear the device status bits
-    (DEV_BAD_PAGE, DEV_BAD_INDPTR, DEV_TIMEOUT, DEV_BAD_PLAN)."""
+    (DEV_BAD_PAGE, DEV_BAD_INDPTR, DEV_TIMEOUT, DEV_BAD_PLAN,
+    DEV_BAD_ADAPTER)."""
     flags = ctypes.c_uint(0)
     _check(library().mla_device_status(ctypes.c_void_p(_stream(stream)), ctypes.byref(flags)),
            "mla_device_status")

@@ -46,6 +46,26 @@ cudaError_t kv_append_launch(const void *kv_c, int64_t kv_c_stride, const void *
                              const int64_t *slots, int64_t T, float k_scale, void *kv, int64_t pool_rows, int sms,
                              cudaStream_t st);
 cudaError_t kv_append_status(unsigned int *flags, bool clear);
+cudaError_t add_rms_norm_launch(const void *x, int64_t x_stride, int x_type, const void *residual,
+                                int64_t residual_stride, int residual_type, const void *weight, float eps,
+                                int64_t rows, int width, int quant, float scale, void *out, int64_t out_stride,
+                                float *out_scales, void *residual_out, int64_t residual_out_stride, int sms,
+                                cudaStream_t st);
+cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
+                                 const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
+                                 int heads, float sc, const float *lse, float decay, const float *weights, float *out,
+                                 bool causal, bool q8, int sms, cudaStream_t st);
+cudaError_t token_weights_status(unsigned int *flags, bool clear);
+cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, const float *weights,
+                            const int32_t *budgets, int budget, int recent, int sinks, int32_t *pages_out,
+                            int32_t *indptr_out, float *weights_out, cudaStream_t st);
+cudaError_t evict_status(unsigned int *flags, bool clear);
+int64_t value_lora_workspace(int64_t rows, int heads, int rank);
+cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *gate, const int32_t *lengths,
+                              const void *lora_a, const void *lora_b, const int32_t *adapters, const float *lora_scale,
+                              int num_adapters, int rank, int R, int qlen, int H, void *out, void *workspace, int sms,
+                              cudaStream_t st);
+cudaError_t value_lora_status(unsigned int *flags, bool clear);
 }  // namespace mla
 
 namespace {
@@ -61,6 +81,30 @@ mla_status cuda_fail(cudaError_t e, const char *where) {
     g_last_error = std::string(where) + ": " + cudaGetErrorString(e);
     return MLA_ERR_CUDA;
 }
+
+// Whether two blocks of bytes share one.
+bool overlap(const void *p, int64_t pn, const void *q, int64_t qn) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && pn > 0 && qn > 0 && a < b + (uintptr_t)qn && b < a + (uintptr_t)pn;
+}
+
+// Rows of `width` bytes every `stride` bytes.
+struct Rows {
+    const void *p;
+    int64_t stride, width;
+};
+
+// Whether two such matrices of n rows share a byte.  With one stride it is
+// the columns that decide: parts of one buffer side by side do not overlap.
+bool overlap_rows(const Rows &x, const Rows &y, int64_t n) {
+    if (!overlap(x.p, (n - 1) * x.stride + x.width, y.p, (n - 1) * y.stride + y.width)) return false;
+    if (x.stride != y.stride) return true;
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p));
+    const int64_t at = ((d % x.stride) + x.stride) % x.stride;   // where y's columns start in x's row
+    return at < x.width || at + y.width > x.stride;
+}
+
+bool same_rows(const Rows &x, const Rows &y) { return x.p == y.p && x.stride == y.stride && x.width == y.width; }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -544,6 +588,165 @@ mla_status mla_kv_append(const void *kv_c, int64_t kv_c_row_stride, const void *
     return MLA_OK;
 }
 
+mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const void *residual,
+                            int64_t residual_stride, int residual_type, const void *weight, float eps,
+                            int64_t tokens, int width, int quant, float scale, void *out, int64_t out_stride,
+                            float *out_scales, void *residual_out, int64_t residual_out_stride, void *stream) {
+    if (x_type != MLA_TYPE_BF16 && x_type != MLA_TYPE_F16) return fail(MLA_ERR_INVALID, "x_type must be bf16 or f16");
+    if (residual && residual_type != x_type && residual_type != MLA_TYPE_F32)
+        return fail(MLA_ERR_INVALID, "residual_type must be x's type or f32");
+    if (quant < MLA_QUANT_NONE || quant > MLA_QUANT_STATIC) return fail(MLA_ERR_INVALID, "unknown quant");
+    if (tokens < 0) return fail(MLA_ERR_INVALID, "negative tokens");
+    if (width < 8 || width > MLA_MAX_NORM_WIDTH || width % 8 != 0)
+        return fail(MLA_ERR_INVALID, "width must be a multiple of 8 in 8..32768");
+    if (!(eps > 0.f) || !std::isfinite(eps)) return fail(MLA_ERR_INVALID, "eps must be finite and > 0");
+    if (quant == MLA_QUANT_STATIC && !(std::isfinite(scale) && scale >= 1.17549435e-38f))
+        return fail(MLA_ERR_INVALID, "scale must be finite and >= 2^-126");
+    if ((residual == nullptr) != (residual_out == nullptr))
+        return fail(MLA_ERR_INVALID, "residual and residual_out go together");
+    const auto bad_stride = [&](int64_t s) { return s < width || s % 8 != 0 || s > (INT64_MAX >> 3); };
+    if (bad_stride(x_stride) || bad_stride(out_stride) ||
+        (residual && (bad_stride(residual_stride) || bad_stride(residual_out_stride))))
+        return fail(MLA_ERR_INVALID, "row strides must be >= width and multiples of 8");
+    if (tokens == 0) return MLA_OK;
+    const bool scales = quant == MLA_QUANT_ROW || quant == MLA_QUANT_GROUP;
+    if (!x || !weight || !out || (scales && !out_scales)) return fail(MLA_ERR_INVALID, "null pointer");
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(out, 16) ||
+        !aligned(residual_out, 16) || !aligned(out_scales, 4))
+        return fail(MLA_ERR_INVALID, "misaligned pointer (16 bytes; out_scales 4)");
+    const int rsize = residual_type == MLA_TYPE_F32 ? 4 : 2, osize = quant == MLA_QUANT_NONE ? 2 : 1;
+    if (tokens > INT64_MAX / 64 / std::max(std::max(x_stride, out_stride),
+                                           residual ? std::max(residual_stride, residual_out_stride) : (int64_t)1))
+        return fail(MLA_ERR_INVALID, "tokens x stride too large");
+    const Rows rx = {x, x_stride * 2, width * 2}, ro = {out, out_stride * osize, width * osize};
+    const Rows rr = {residual, residual_stride * rsize, width * rsize};
+    const Rows rw = {residual_out, residual_out_stride * rsize, width * rsize};
+    const int64_t nscales = !scales ? 0 : tokens * (quant == MLA_QUANT_ROW ? 1 : (width + 127) / 128);
+    const Rows rs = {scales ? out_scales : nullptr, nscales * 4, nscales * 4};
+    const auto clash = [&](const Rows &w, const Rows &r) { return r.p && !same_rows(w, r) && overlap_rows(w, r, tokens); };
+    const auto whole = [&](const Rows &m) { return m.p ? (tokens - 1) * m.stride + m.width : 0; };
+    bool bad = clash(ro, rx) || overlap(out, whole(ro), weight, (int64_t)width * 2);
+    if (residual)
+        bad = bad || clash(ro, rr) || clash(rw, rx) || clash(rw, rr) || overlap_rows(rw, ro, tokens) ||
+              overlap(residual_out, whole(rw), weight, (int64_t)width * 2);
+    if (scales)
+        for (const Rows *m : {&rx, &rr, &ro, &rw}) bad = bad || overlap(m->p, whole(*m), rs.p, nscales * 4);
+    bad = bad || overlap(weight, (int64_t)width * 2, rs.p, nscales * 4);
+    if (bad) return fail(MLA_ERR_INVALID, "an output overlaps an input or another output");
+    const int sms = device_sms();
+    if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = mla::add_rms_norm_launch(x, x_stride, x_type, residual, residual_stride, residual_type, weight, eps,
+                                             tokens, width, quant, scale, out, out_stride, out_scales, residual_out,
+                                             residual_out_stride, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "add_rms_norm launch");
+    return MLA_OK;
+}
+
+mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
+                             const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
+                             int qlen, int heads, float scale, float kv_scale, float q_scale, const float *lse,
+                             float decay, const float *weights, float *out, unsigned int flags, void *stream) {
+    if (flags & ~(MLA_ATTEND_CAUSAL | MLA_ATTEND_Q_FP8)) return fail(MLA_ERR_INVALID, "unknown flag bits");
+    const bool q8 = (flags & MLA_ATTEND_Q_FP8) != 0;
+    if (num_requests < 0) return fail(MLA_ERR_INVALID, "num_requests < 0");
+    if (qlen < 1 || qlen > MLA_MAX_QLEN) return fail(MLA_ERR_INVALID, "qlen outside 1..16");
+    if (heads < 1 || heads > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID, "heads outside 1..128");
+    if (q_row_stride < (int64_t)heads * MLA_D_QK || q_row_stride % (q8 ? 16 : 8) != 0)
+        return fail(MLA_ERR_INVALID, q8 ? "q_row_stride must be >= heads*576 and a multiple of 16 (fp8 q)"
+                                        : "q_row_stride must be >= heads*576 and a multiple of 8");
+    if (pool_rows < 0 || num_pages < 0) return fail(MLA_ERR_INVALID, "negative pool_rows / num_pages");
+    if (!std::isfinite(scale) || !std::isfinite(kv_scale) || !std::isfinite(q_scale))
+        return fail(MLA_ERR_INVALID, "non-finite scale");
+    if (!std::isfinite(decay)) return fail(MLA_ERR_INVALID, "non-finite decay");
+    if (num_requests == 0 || num_pages == 0) return MLA_OK;
+    if (!q || !kv || !indptr || !pages || !lse || !out || (decay != 0.f && !weights))
+        return fail(MLA_ERR_INVALID, "null pointer");
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(indptr, 4) || !aligned(pages, 4) || !aligned(lse, 4) ||
+        !aligned(weights, 4) || !aligned(out, 4))
+        return fail(MLA_ERR_INVALID, "misaligned pointer (q, kv need 16 bytes)");
+    if (pool_rows == 0) return fail(MLA_ERR_INVALID, "empty KV pool");
+    if (pool_rows > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "pool_rows above 2^31 - 1");
+    if (num_pages > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 1");
+    if (out != weights && overlap(out, num_pages * 4, weights, num_pages * 4))
+        return fail(MLA_ERR_INVALID, "out overlaps weights");
+    const int sms = device_sms();
+    if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = mla::token_weights_launch(q, q_row_stride, kv, pool_rows, pages, num_pages, indptr, num_requests,
+                                              qlen, heads, scale * q_scale * kv_scale, lse, decay, weights, out,
+                                              (flags & MLA_ATTEND_CAUSAL) != 0, q8, sms,
+                                              static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "token_weights launch");
+    return MLA_OK;
+}
+
+mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
+                        const float *weights, const int32_t *budgets, int budget, int recent, int sinks,
+                        int32_t *pages_out, int32_t *indptr_out, float *weights_out, void *stream) {
+    if (num_requests < 0 || num_pages < 0) return fail(MLA_ERR_INVALID, "negative num_requests / num_pages");
+    if (recent < 0 || sinks < 0) return fail(MLA_ERR_INVALID, "negative recent / sinks");
+    if (!indptr || !indptr_out || (num_pages > 0 && (!pages || !weights || !pages_out || !weights_out)))
+        return fail(MLA_ERR_INVALID, "null pointer");
+    if (!aligned(pages, 4) || !aligned(indptr, 4) || !aligned(weights, 4) || !aligned(budgets, 4) ||
+        !aligned(pages_out, 4) || !aligned(indptr_out, 4) || !aligned(weights_out, 4))
+        return fail(MLA_ERR_INVALID, "misaligned pointer (4 bytes)");
+    if (num_pages > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 1");
+    const int64_t n = num_pages * 4, r = (int64_t)num_requests * 4;
+    const struct { const void *p; int64_t n; } in[4] = {{pages, n}, {weights, n}, {indptr, r + 4}, {budgets, r}},
+                                               to[3] = {{pages_out, n}, {weights_out, n}, {indptr_out, r + 4}};
+    for (int i = 0; i < 3; ++i) {
+        for (const auto &x : in)
+            if (overlap(to[i].p, to[i].n, x.p, x.n)) return fail(MLA_ERR_INVALID, "an output overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return fail(MLA_ERR_INVALID, "two outputs overlap");
+    }
+    cudaError_t e = mla::kv_evict_launch(pages, num_pages, indptr, num_requests, weights, budgets, budget, recent, sinks,
+                                         pages_out, indptr_out, weights_out, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_evict launch");
+    return MLA_OK;
+}
+
+namespace {
+const char *bad_lora_sizes(int num_requests, int qlen, int heads, int rank) {
+    if (num_requests < 0) return "num_requests < 0";
+    if (qlen < 1 || qlen > MLA_MAX_QLEN) return "qlen outside 1..16";
+    if (heads < 1 || heads > MLA_MAX_HEADS) return "heads outside 1..128";
+    if (rank < 8 || rank > MLA_MAX_LORA_RANK || rank % 8 != 0) return "rank must be a multiple of 8 in 8..128";
+    return nullptr;
+}
+}  // namespace
+
+int64_t mla_value_gate_lora_workspace(int num_requests, int qlen, int heads, int rank) {
+    if (const char *why = bad_lora_sizes(num_requests, qlen, heads, rank)) return fail(MLA_ERR_INVALID, why);
+    return mla::value_lora_workspace((int64_t)num_requests * qlen, heads, rank);
+}
+
+mla_status mla_value_gate_lora(const void *latent, const void *w_uv, const void *gate, const int32_t *lengths,
+                               const void *lora_a, const void *lora_b, const int32_t *adapters,
+                               const float *lora_scale, int num_adapters, int rank, int num_requests, int qlen,
+                               int heads, void *out, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (const char *why = bad_lora_sizes(num_requests, qlen, heads, rank)) return fail(MLA_ERR_INVALID, why);
+    if (num_adapters < 1) return fail(MLA_ERR_INVALID, "num_adapters < 1");
+    if (num_requests == 0) return MLA_OK;
+    if (!latent || !w_uv || !gate || !lengths || !lora_a || !lora_b || !adapters || !lora_scale || !out)
+        return fail(MLA_ERR_INVALID, "null pointer");
+    if (!aligned(latent, 16) || !aligned(w_uv, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) ||
+        !aligned(workspace, 16) || !aligned(gate, 4) || !aligned(out, 4) || !aligned(lengths, 4) ||
+        !aligned(adapters, 4) || !aligned(lora_scale, 4))
+        return fail(MLA_ERR_INVALID, "misaligned pointer (latent, w_uv, lora_a, lora_b, workspace need 16 bytes)");
+    const int64_t S = (int64_t)num_requests * qlen;
+    if (S > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "too many rows");
+    if ((int64_t)num_adapters * heads * MLA_D_V > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "too many adapters");
+    const int64_t need = mla::value_lora_workspace(S, heads, rank);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return fail(MLA_ERR_INVALID, "workspace too small");
+    const int sms = device_sms();
+    if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = mla::value_lora_launch(latent, w_uv, gate, lengths, lora_a, lora_b, adapters, lora_scale,
+                                           num_adapters, rank, num_requests, qlen, heads, out, workspace, sms,
+                                           static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "value_gate_lora launch");
+    return MLA_OK;
+}
+
 mla_status mla_debug_wait_timeout(void *stream) {
     if (device_sms() <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
     cudaError_t e = mla::stuck_wait_launch(static_cast<cudaStream_t>(stream));
@@ -575,7 +778,8 @@ mla_status mla_device_status(void *stream, unsigned int *flags) {
     if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
     cudaError_t (*readers[])(unsigned int *, bool) = {mla::attend_mma_status, mla::attend_tc_status, mla::merge_status,
                                                       mla::value_gate_status, mla::gather_status,
-                                                      mla::kv_append_status};
+                                                      mla::kv_append_status, mla::token_weights_status,
+                                                      mla::evict_status, mla::value_lora_status};
     for (auto rd : readers) {
         unsigned int f = 0;
         e = rd(&f, true);
