@@ -436,6 +436,10 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
  *   weights      f32 [num_pages]; may be NULL when decay is 0.
  *   out          f32 [num_pages] (written); may be weights itself, otherwise
  *                must not overlap it.
+ *   workspace    device, 16-byte aligned, at least
+ *                mla_token_weights_workspace() bytes (may be NULL for 0);
+ *                holds nothing between calls, but two calls that may overlap
+ *                on the GPU need one each.
  * A page outside the pool reads as row 0 of the pool and sets
  * MLA_DEV_BAD_PAGE; a bad indptr entry sets MLA_DEV_BAD_INDPTR and leaves
  * its request's entries as they were.
@@ -443,7 +447,12 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
 mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                              const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
                              int qlen, int heads, float scale, float kv_scale, float q_scale, const float *lse,
-                             float decay, const float *weights, float *out, unsigned int flags, void *stream);
+                             float decay, const float *weights, float *out, unsigned int flags, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that mla_token_weights needs (0 up to 64 query rows a
+ * request, 128 of an fp8 query); a negative mla_status on bad sizes. */
+int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsigned int flags);
 
 /*
  * mla_kv_evict -- cut every request's page list to a budget, by weight.

@@ -37,7 +37,7 @@ __all__ = ["Prepared", "attend", "merge", "value_gate", "merge_value_gate", "dec
            "STATIC_SCRATCH_BYTES", "choose_splits", "plan_units", "debug_gather",
            "debug_wait_timeout", "debug_attend_mma",
            "kv_append", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
-           "value_gate_lora_workspace", "device_status", "build", "library", "MlaError"]
+           "value_gate_lora_workspace", "token_weights_workspace", "device_status", "build", "library", "MlaError"]
 
 
 class MlaError(RuntimeError):
@@ -94,7 +94,9 @@ def library() -> ctypes.CDLL:
                                            vp, i64, vp, vp, vp, vp, vp, vp, vp]
     lib.mla_add_rms_norm.argtypes = [vp, i64, i32, vp, i64, i32, vp, f32, i64, i32, i32, f32, vp, i64, vp, vp, i64, vp]
     lib.mla_token_weights.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, f32, vp, f32, vp, vp,
-                                      ctypes.c_uint, vp]
+                                      ctypes.c_uint, vp, i64, vp]
+    lib.mla_token_weights_workspace.argtypes = [i32, i32, i64, ctypes.c_uint]
+    lib.mla_token_weights_workspace.restype = i64
     lib.mla_kv_evict.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
     lib.mla_value_gate_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mla_value_gate_lora_workspace.argtypes = [i32, i32, i32, i32]
@@ -554,7 +556,7 @@ def add_rms_norm(x, weight, eps, residual=None, *, quant=None, scale=None, out=N
 
 
 def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qlen=1, weights=None, decay=1.0,
-                  causal=False, q_scale=1.0, out=None, stream=None):
+                  causal=False, q_scale=1.0, out=None, workspace=None, stream=None):
     """The attention weight every cached token received in a decode step,
     added to ``decay`` times the weights gathered so far
     (``mla_token_weights``): returns ``out`` float32 ``[len(pages)]``.
@@ -564,7 +566,10 @@ def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qle
     ``lse``: the step's merged LSE float32 ``[S, heads]`` (from
     :func:`merge` or :func:`decode_step`).  ``weights``: float32, one entry
     per entry of ``pages`` (None: zeros); ``out=weights`` updates in place.
-    Entries past ``indptr[-1]`` are left as they were.
+    Entries past ``indptr[-1]`` are left as they were.  ``workspace``: uint8,
+    at least :func:`token_weights_workspace` bytes, 16-byte aligned
+    (allocated if not given and needed; not shared by calls that may
+    overlap).
     """
     kv = _as_u8(kv)
     heads = q.shape[1] if heads is None else heads
@@ -581,7 +586,7 @@ def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qle
     _need(lse.dtype == torch.float32 and lse.shape == (S, heads) and lse.is_contiguous(),
           "lse must be contiguous f32 [S, heads]")
     dev = q.device
-    _same_device(dev, kv=kv, pages=pages, indptr=indptr, lse=lse, weights=weights, out=out)
+    _same_device(dev, kv=kv, pages=pages, indptr=indptr, lse=lse, weights=weights, out=out, workspace=workspace)
     n = pages.numel()
     if weights is not None:
         _buffer(weights, "weights", torch.float32, (n,))
@@ -589,12 +594,28 @@ def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qle
         out = _empty((n,), torch.float32, dev, stream)
     else:
         _buffer(out, "out", torch.float32, (n,))
+    if workspace is None:
+        need = token_weights_workspace(qlen, heads, n, q8)
+        if need:
+            workspace = _empty((need,), torch.uint8, dev, stream)
+    else:
+        _need(workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous(),
+              "workspace must be contiguous uint8")
     _launch(library().mla_token_weights, "mla_token_weights", dev, stream, q.data_ptr(),
             q.stride(0) if S > 1 else heads * D_QK, kv.data_ptr(), kv.shape[0], pages.data_ptr(), n,
             indptr.data_ptr(), R, qlen, heads, scale, kv_scale, q_scale, lse.data_ptr(),
             0.0 if weights is None else decay, None if weights is None else weights.data_ptr(), out.data_ptr(),
-            (ATTEND_CAUSAL if causal else 0) | (ATTEND_Q_FP8 if q8 else 0))
+            (ATTEND_CAUSAL if causal else 0) | (ATTEND_Q_FP8 if q8 else 0),
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return out
+
+
+def token_weights_workspace(qlen, heads, num_pages, fp8_query=False):
+    """Bytes of workspace that :func:`token_weights` needs."""
+    n = library().mla_token_weights_workspace(qlen, heads, num_pages, ATTEND_Q_FP8 if fp8_query else 0)
+    if n < 0:
+        _check(int(n), "mla_token_weights_workspace")
+    return int(n)
 
 
 def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=None, indptr_out=None, weights_out=None,

@@ -53,8 +53,9 @@ cudaError_t add_rms_norm_launch(const void *x, int64_t x_stride, int x_type, con
                                 cudaStream_t st);
 cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                                  const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
-                                 int heads, float sc, const float *lse, float decay, const float *weights, float *out,
-                                 bool causal, bool q8, int sms, cudaStream_t st);
+                                 int heads, double sc, const float *lse, float decay, const float *weights, float *out,
+                                 bool causal, bool q8, void *workspace, int sms, cudaStream_t st);
+int64_t token_weights_workspace(int rows, bool q8, int64_t num_pages);
 cudaError_t token_weights_status(unsigned int *flags, bool clear);
 cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, const float *weights,
                             const int32_t *budgets, int budget, int recent, int sinks, int32_t *pages_out,
@@ -645,7 +646,8 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
 mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                              const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
                              int qlen, int heads, float scale, float kv_scale, float q_scale, const float *lse,
-                             float decay, const float *weights, float *out, unsigned int flags, void *stream) {
+                             float decay, const float *weights, float *out, unsigned int flags, void *workspace,
+                             int64_t workspace_bytes, void *stream) {
     if (flags & ~(MLA_ATTEND_CAUSAL | MLA_ATTEND_Q_FP8)) return fail(MLA_ERR_INVALID, "unknown flag bits");
     const bool q8 = (flags & MLA_ATTEND_Q_FP8) != 0;
     if (num_requests < 0) return fail(MLA_ERR_INVALID, "num_requests < 0");
@@ -657,6 +659,8 @@ mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv
     if (pool_rows < 0 || num_pages < 0) return fail(MLA_ERR_INVALID, "negative pool_rows / num_pages");
     if (!std::isfinite(scale) || !std::isfinite(kv_scale) || !std::isfinite(q_scale))
         return fail(MLA_ERR_INVALID, "non-finite scale");
+    const double sc = (double)scale * q_scale * kv_scale;
+    if (!std::isfinite((float)(sc * 1.5))) return fail(MLA_ERR_INVALID, "scale * q_scale * kv_scale too large");
     if (!std::isfinite(decay)) return fail(MLA_ERR_INVALID, "non-finite decay");
     if (num_requests == 0 || num_pages == 0) return MLA_OK;
     if (!q || !kv || !indptr || !pages || !lse || !out || (decay != 0.f && !weights))
@@ -669,14 +673,27 @@ mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv
     if (num_pages > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 1");
     if (out != weights && overlap(out, num_pages * 4, weights, num_pages * 4))
         return fail(MLA_ERR_INVALID, "out overlaps weights");
+    const int64_t need = mla::token_weights_workspace(qlen * heads, q8, num_pages);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return fail(MLA_ERR_INVALID, "workspace too small");
+    if (need > 0 && !aligned(workspace, 16)) return fail(MLA_ERR_INVALID, "misaligned workspace (16 bytes)");
+    if (overlap(workspace, need, out, num_pages * 4) || overlap(workspace, need, weights, num_pages * 4))
+        return fail(MLA_ERR_INVALID, "workspace overlaps weights or out");
     const int sms = device_sms();
     if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
     cudaError_t e = mla::token_weights_launch(q, q_row_stride, kv, pool_rows, pages, num_pages, indptr, num_requests,
-                                              qlen, heads, scale * q_scale * kv_scale, lse, decay, weights, out,
-                                              (flags & MLA_ATTEND_CAUSAL) != 0, q8, sms,
+                                              qlen, heads, sc, lse, decay, weights, out,
+                                              (flags & MLA_ATTEND_CAUSAL) != 0, q8, workspace, sms,
                                               static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "token_weights launch");
     return MLA_OK;
+}
+
+int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsigned int flags) {
+    if (flags & ~(MLA_ATTEND_CAUSAL | MLA_ATTEND_Q_FP8)) return fail(MLA_ERR_INVALID, "unknown flag bits");
+    if (qlen < 1 || qlen > MLA_MAX_QLEN) return fail(MLA_ERR_INVALID, "qlen outside 1..16");
+    if (heads < 1 || heads > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID, "heads outside 1..128");
+    if (num_pages < 0 || num_pages > INT32_MAX) return fail(MLA_ERR_INVALID, "num_pages outside 0..2^31 - 1");
+    return mla::token_weights_workspace(qlen * heads, (flags & MLA_ATTEND_Q_FP8) != 0, num_pages);
 }
 
 mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,

@@ -1,107 +1,615 @@
-// Attention weight received by each cached token in one decode step.
+// Attention weight received by each cached token in one decode step --
+// tcgen05 tensor-memory kernel (sm_103a).
 //
 // What it computes, for token j of request r at entry i = indptr[r] + j of
 // the page list:
 //   out[i] = decay * weights[i] + sum_{t, h} exp(sc * <q[t, h], K_j> - lse[t, h])
 // over r's query rows t that see token j and heads h with lse[t, h] > -inf,
 // K_j the e4m3 cache row of pages[i] and sc = scale * q_scale * kv_scale.
+// The LSE is given, so one pass over the scores does: no running maximum,
+// and a token's sum needs no other token.
 //
-// One warp per token: a lane holds 18 of the row's 576 values, the products
-// are summed by shuffles, row by row.
+// Bound by the cache rows (576 bytes a token) up to about 160 query rows a
+// request, by the tensor cores above.
+//
+// Design: one persistent CTA per SM walks a contiguous range of the batch's
+// 128-token tiles (equal shares; a request's query is prepared once per CTA
+// that meets it).  Tokens are the MMA's M dimension: S[tok, n] = K[tok, :] .
+// Q'[n, :] as 18 kind::f8f6f4 MMAs over the e4m3 rows as they are stored, so
+// a token is a TMEM lane, one thread sums its row of scores, and no sum
+// crosses threads (equal inputs give equal bits).  A bf16 query row is two
+// e4m3 terms, q * 2^e = hi + lo / 16 (exact except below 2^-21 of the row's
+// largest element), two columns of the same MMA; an fp8 query is one.
+//   warps 0..7   two warpgroups take the tiles in turn: scores from TMEM,
+//                exponentials, the sum, the output
+//   warp 8       MMA issuer (D double-buffered in TMEM, so the next tile's
+//                MMAs overlap this tile's exponentials)
+//   warps 9..13  producers: one 128- or 64-byte column block each, a
+//                gather4 (four cache rows) a lane and tile, two 72 KB stages
+//   warps 14..17 convert the next request's query rows once the last MMA on
+//                the previous ones has completed
+// Requests of more rows than one CTA's Q' buffer (64, or 128 of an fp8
+// query) are cut into row groups on neighbouring CTAs, which read the same
+// tiles at about the same time (the later ones from L2); each writes its
+// partial sums to the workspace, joined in group order by a small kernel.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "tc.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPairs = MLA_D_QK / 64;   // 9 column pairs a lane
+constexpr int kEpiWarps = 8, kMmaWarp = 8, kProdWarp0 = 9, kProdWarps = 5, kPrepWarp0 = 14, kPrepWarps = 4;
+constexpr int kThreads = (kPrepWarp0 + kPrepWarps) * 32;
+constexpr int kStages = 2, kTile = 128;
+constexpr int kLatBlock = (kTile / 8) * 1024;              // one 128-byte column block of a stage
+constexpr int kRopeOff = 4 * kLatBlock;
+constexpr int kStageBytes = kRopeOff + (kTile / 8) * 512;  // 73,728
+constexpr int kOffQ = kStages * kStageBytes;
 
 struct TokenArgs {
     const void *q;
     int64_t q_row_stride, pool_rows, num_pages;
-    const uint8_t *kv;
     const int32_t *pages, *indptr;
     const float *lse, *weights;
-    float *out;
-    int R, qlen, heads, causal, q8;
-    float sc, decay;
+    float *out;             // the result, or (groups > 1) the groups' partial sums
+    int64_t group_stride;
+    int R, qlen, heads, causal, groups, virt;
+    float sc_hi, sc_lo;     // sc * log2(e) as two floats
+    float decay;
 };
 
-__device__ __forceinline__ float2 e4m3_pair(uint16_t v) { return unpack_f16x2(e4m3x2_to_f16x2(v)); }
+// A query row's constants: with acc = hi + lo / 16, the exponent (base 2) is
+// (acc * c.x - c.z) + (acc * c.y - c.w), its two halves each a float pair.
+constexpr int kConstBufs = 3;   // a unit's constants outlive two more units' (one-tile units in flight)
 
-__global__ void __launch_bounds__(kThreads) token_weights_kernel(const TokenArgs a) {
-    const int r = blockIdx.x, lane = threadIdx.x & 31;
-    int base;
-    const int len = request_len(a.indptr, r, a.num_pages, &base);
-    for (int j = blockIdx.y * kWarps + (threadIdx.x >> 5); j < len; j += gridDim.y * kWarps) {
-        const int64_t i = (int64_t)base + j;
-        const uint16_t *k = reinterpret_cast<const uint16_t *>(kv_row(a.kv, a.pages, i, a.pool_rows));
-        float2 kf[kPairs];
+// NP MMA columns, TERMS of them per query row.
+template <int NP, int TERMS>
+struct Cfg {
+    static constexpr int NQ = NP / TERMS;
+    static constexpr int QLatBlock = (NP / 8) * 1024;
+    static constexpr int QRope = 4 * QLatBlock;
+    static constexpr int OffMisc = kOffQ + NP * MLA_D_QK;
+    static constexpr uint32_t TmemCols = 2 * NP <= 64 ? 64 : 2 * NP <= 128 ? 128 : 256;
+};
+
+template <int NQ>
+struct Misc {
+    float4 c[kConstBufs][NQ];
+    int vis[kConstBufs][NQ];    // tokens of the request that the row counts (0: a skipped row)
+    int all_vis[kConstBufs];    // smallest of them over the real rows
+    uint64_t kv_full[kStages], kv_empty[kStages], d_full[2], d_free[2], q_ready, q_free, fin;
+    uint32_t tmem;
+    int abort_flag;
+    int start[3];               // this CTA's first request, its first tile there, tiles in all
+};
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t par, int *abort_flag) {
+    if (*(volatile int *)abort_flag) return false;
+    if (!mbar_wait(bar, par)) {
+        *(volatile int *)abort_flag = 1;
+        return false;
+    }
+    return true;
+}
+
+// A CTA's tiles in order; every role walks them on its own (uniform loads).
+struct Walk {
+    int r, t, ntiles, len, base, left, unit;
+    bool first;     // the tile is its unit's first in this CTA
+
+    template <int NQ>
+    __device__ void init(const TokenArgs &a, const Misc<NQ> &ms) {
+        r = ms.start[0];
+        t = ms.start[1];
+        left = ms.start[2];
+        unit = 0;
+        first = true;
+        if (left > 0) open(a);
+    }
+    __device__ void open(const TokenArgs &a) {
+        len = request_len(a.indptr, r, a.num_pages, &base);
+        ntiles = (len + kTile - 1) / kTile;
+    }
+    __device__ bool valid() const { return left > 0; }
+    __device__ bool last() const { return left == 1 || t + 1 == ntiles; }
+    __device__ int ntok() const { return min(kTile, len - t * kTile); }
+    __device__ void next(const TokenArgs &a) {
+        --left;
+        first = false;
+        if (++t < ntiles || left <= 0) return;
+        t = 0;
+        first = true;
+        ++unit;
+        do {        // at least one more tile is to come, so a request with tokens follows
+            ++r;
+            open(a);
+        } while (ntiles == 0 && r + 1 < a.R);
+    }
+};
+
+// This CTA's range of the batch's tiles -> ms.start.
+template <int NQ>
+__device__ void find_start(const TokenArgs &a, Misc<NQ> &ms, int v) {
+    __shared__ int part[kThreads / 32 + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const auto tiles_of = [&](int r) {
+        int base;
+        return (request_len(a.indptr, r, a.num_pages, &base) + kTile - 1) / kTile;
+    };
+    int mine = 0, sum = 0;
+    for (int r = tid; r < a.R; r += kThreads) {
+        const int n = tiles_of(r);
+        if (r == tid) mine = n;
+        sum += n;
+    }
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) total += part[w];
+    const int64_t lo = (int64_t)total * v / a.virt, hi = (int64_t)total * (v + 1) / a.virt;
+    if (tid == 0) ms.start[2] = (int)(hi - lo);
+    int64_t before = 0;   // tiles of the requests before this chunk
+    for (int r0 = 0; r0 < a.R && before <= lo; r0 += kThreads) {
+        const int r = r0 + tid;
+        const int n = r0 == 0 ? mine : r < a.R ? tiles_of(r) : 0;
+        int incl = n;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += x;
+        }
+        __syncthreads();
+        if (lane == 31) part[warp] = incl;
+        __syncthreads();
+        int64_t at = before;
+        int all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) at += part[w];
+            all += part[w];
+        }
+        at += incl - n;
+        if (n > 0 && at <= lo && lo < at + n) {
+            ms.start[0] = r;
+            ms.start[1] = (int)(lo - at);
+        }
+        before += all;
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------ producers
+
+template <int NQ>
+__device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUtensorMap *mrope, uint8_t *sm,
+                         Misc<NQ> &ms) {
+    const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kProdWarp0;
+    Walk w;
+    w.init(a, ms);
+    const uint64_t pol = tc::l2_policy(true);   // the rows stream through L2; the query and the outputs stay
+    const auto fetch = [&](int (&rows)[4]) {
+        const int ntok = w.valid() ? w.ntok() : 0;
 #pragma unroll
-        for (int c = 0; c < kPairs; ++c) kf[c] = e4m3_pair(__ldg(k + lane + 32 * c));
-        float sum = 0.f;
-        for (int t = 0; t < a.qlen; ++t) {
-            if (a.causal && j >= len - a.qlen + t + 1) continue;
-            const int64_t row = (int64_t)r * a.qlen + t;
-            for (int h = 0; h < a.heads; ++h) {
-                const float lse = __ldg(a.lse + row * a.heads + h);
-                if (lse == -INFINITY) continue;
-                float dot = 0.f;
-                if (a.q8) {
-                    const uint16_t *q = reinterpret_cast<const uint16_t *>(
-                        static_cast<const uint8_t *>(a.q) + row * a.q_row_stride + h * MLA_D_QK);
-#pragma unroll
-                    for (int c = 0; c < kPairs; ++c) {
-                        const float2 v = e4m3_pair(__ldg(q + lane + 32 * c));
-                        dot = fmaf(v.x, kf[c].x, fmaf(v.y, kf[c].y, dot));
-                    }
-                } else {
-                    const uint32_t *q = reinterpret_cast<const uint32_t *>(
-                        static_cast<const __nv_bfloat16 *>(a.q) + row * a.q_row_stride + h * MLA_D_QK);
-#pragma unroll
-                    for (int c = 0; c < kPairs; ++c) {
-                        const uint32_t v = __ldg(q + lane + 32 * c);
-                        dot = fmaf(bf16_lo(v), kf[c].x, fmaf(bf16_hi(v), kf[c].y, dot));
-                    }
+        for (int i = 0; i < 4; ++i) {
+            const int tok = 4 * lane + i;
+            rows[i] = -1;                       // past the tile: the copy fills zeros
+            if (tok < ntok) {
+                const int p = __ldg(a.pages + (int64_t)w.base + w.t * kTile + tok);
+                rows[i] = p;
+                if (p < 0 || p >= a.pool_rows) {
+                    flag(MLA_DEV_BAD_PAGE);
+                    rows[i] = 0;
                 }
-#pragma unroll
-                for (int d = 16; d >= 1; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-                sum += expf(fmaf(dot, a.sc, -lse));
             }
         }
-        if (lane == 0) a.out[i] = a.decay == 0.f ? sum : fmaf(a.decay, a.weights[i], sum);
+    };
+    int rows[4], it = 0;
+    fetch(rows);
+    bool ok = true;
+    while (w.valid()) {
+        const int s = it % kStages;
+        if (!(ok = wait_or_abort(&ms.kv_empty[s], ((it / kStages) & 1) ^ 1, &ms.abort_flag))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&ms.kv_full[s], part < 4 ? 32 * 512 : 32 * 256);
+        __syncwarp();
+        uint8_t *st = sm + s * kStageBytes;
+        const int g8 = lane >> 1, half = lane & 1;
+        if (part < 4)
+            tc::gather4_hint(st + part * kLatBlock + g8 * 1024 + half * 512, mlat, part * 128, rows[0], rows[1],
+                             rows[2], rows[3], &ms.kv_full[s], pol);
+        else
+            tc::gather4_hint(st + kRopeOff + g8 * 512 + half * 256, mrope, 512, rows[0], rows[1], rows[2], rows[3],
+                             &ms.kv_full[s], pol);
+        ++it;
+        w.next(a);
+        fetch(rows);
+    }
+    if (!ok) {      // flagged: let the copies in flight land before the CTA ends
+        for (int k = it < kStages ? 0 : it - kStages; k < it; ++k) mbar_wait(&ms.kv_full[k % kStages], (k / kStages) & 1);
+    }
+}
+
+// ------------------------------------------------------------------ MMA issuer
+
+template <int NP, int TERMS>
+__device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms) {
+    using C = Cfg<NP, TERMS>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_u32(sm), tm = ms.tmem;
+    constexpr uint32_t kId = tc::idesc_e4m3(NP, false, false);
+    Walk w;
+    w.init(a, ms);
+    for (int it = 0; w.valid(); ++it, w.next(a)) {
+        const int s = it % kStages, d = it & 1;
+        if (w.first && !wait_or_abort(&ms.q_ready, w.unit & 1, &ms.abort_flag)) break;
+        if (!wait_or_abort(&ms.d_free[d], ((it >> 1) & 1) ^ 1, &ms.abort_flag)) break;
+        if (!wait_or_abort(&ms.kv_full[s], (it / kStages) & 1, &ms.abort_flag)) break;
+        tc::fence_after();
+        if (lane == 0) {
+            const uint32_t st = base + s * kStageBytes, dt = tm + d * NP;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int b = j >> 2, off = (j & 3) * 32;
+                tc::mma_e4m3(dt, tc::sdesc(st + b * kLatBlock + off, 16, 1024, tc::kSw128),
+                             tc::sdesc(base + kOffQ + b * C::QLatBlock + off, 16, 1024, tc::kSw128), kId, j > 0);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                tc::mma_e4m3(dt, tc::sdesc(st + kRopeOff + j * 32, 16, 512, tc::kSw64),
+                             tc::sdesc(base + kOffQ + C::QRope + j * 32, 16, 512, tc::kSw64), kId, true);
+            tc::commit(&ms.kv_empty[s]);
+            tc::commit(&ms.d_full[d]);
+            if (w.last()) tc::commit(&ms.q_free);
+        }
+        __syncwarp();
+    }
+    // Every MMA issued must be complete before TMEM is released.
+    if (lane == 0) tc::commit(&ms.fin);
+    __syncwarp();
+    mbar_wait(&ms.fin, 0);
+}
+
+// ------------------------------------------------------------------ query
+
+// Byte offset of column d of Q' row n.
+template <int NP, int TERMS>
+__device__ __forceinline__ uint32_t q_offset(int n, int d) {
+    using C = Cfg<NP, TERMS>;
+    return d < 512 ? kOffQ + (d >> 7) * C::QLatBlock + (n >> 3) * 1024 + tc::sw128(n, d & 127)
+                   : kOffQ + C::QRope + (n >> 3) * 512 + tc::sw64(n, d - 512);
+}
+
+// Request r's rows [grp * NQ, ...) as the B operand, a warp a row, and their
+// constants.
+template <int NP, int TERMS>
+__device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms, int r, int len, int grp, int unit) {
+    constexpr int NQ = NP / TERMS;
+    const int lane = threadIdx.x & 31, pw = (threadIdx.x >> 5) - kPrepWarp0, buf = unit % kConstBufs;
+    const int rows_total = a.qlen * a.heads;
+    if (pw == 0) {
+        int least = INT_MAX;
+        for (int n = lane; n < NQ; n += 32) {
+            const int rho = grp * NQ + n;
+            int vis = 0;
+            if (rho < rows_total) {
+                const int t = rho / a.heads;
+                const float lse = __ldg(a.lse + ((int64_t)r * a.qlen) * a.heads + rho);
+                vis = a.causal ? max(0, len - a.qlen + t + 1) : len;
+                if (lse == -INFINITY) vis = 0;
+                least = min(least, vis);
+            }
+            ms.vis[buf][n] = vis;
+        }
+        for (int d = 16; d >= 1; d >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
+        if (lane == 0) ms.all_vis[buf] = least;
+    }
+#pragma unroll 2
+    for (int n = pw; n < NQ; n += kPrepWarps) {
+        const int rho = grp * NQ + n;
+        const bool real = rho < rows_total;
+        const int t = rho / a.heads, h = rho - t * a.heads;
+        float back = 1.f;           // 2^-e
+        if (TERMS == 1) {
+            const uint8_t *src = static_cast<const uint8_t *>(a.q) + ((int64_t)r * a.qlen + t) * a.q_row_stride +
+                                 (int64_t)h * MLA_D_QK;
+            for (int ch = lane; ch < MLA_D_QK / 16; ch += 32) {
+                const uint4 v = real ? __ldg(reinterpret_cast<const uint4 *>(src) + ch) : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(sm + q_offset<NP, TERMS>(n, ch * 16)) = v;
+            }
+        } else {
+            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
+                                       ((int64_t)r * a.qlen + t) * a.q_row_stride + (int64_t)h * MLA_D_QK;
+            uint4 v[3];
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const int ch = lane + 32 * j;
+                v[j] = real && ch < MLA_D_QK / 8 ? __ldg(reinterpret_cast<const uint4 *>(src) + ch)
+                                                 : make_uint4(0, 0, 0, 0);
+                const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
+            }
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+            // amax = f * 2^(ex - 127), 1 <= f < 2: scaled by 2^e into [128, 256).
+            const int ex = min(max((int)(__float_as_uint(amax) >> 23), 40), 254);
+            const float up = __uint_as_float((uint32_t)(127 + 134 - ex) << 23);
+            back = __uint_as_float((uint32_t)(127 + ex - 134) << 23);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const int ch = lane + 32 * j;
+                if (ch >= MLA_D_QK / 8) continue;
+                const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // hi is x rounded to 4 bits; the difference, at most 4 bits more, and 16 times it are exact.
+                    const float2 f = make_float2(bf16_lo(x[e]) * up, bf16_hi(x[e]) * up);
+                    const __nv_fp8x2_storage_t h8 = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+                    const float2 hf = unpack_f16x2(e4m3x2_to_f16x2(h8));
+                    const __nv_fp8x2_storage_t l8 = __nv_cvt_float2_to_fp8x2(
+                        make_float2((f.x - hf.x) * 16.f, (f.y - hf.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+                    if (e & 1) {
+                        hi[e >> 1] |= (uint32_t)h8 << 16;
+                        lo[e >> 1] |= (uint32_t)l8 << 16;
+                    } else {
+                        hi[e >> 1] = h8;
+                        lo[e >> 1] = l8;
+                    }
+                }
+                *reinterpret_cast<uint2 *>(sm + q_offset<NP, TERMS>(n, ch * 8)) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(sm + q_offset<NP, TERMS>(NQ + n, ch * 8)) = make_uint2(lo[0], lo[1]);
+            }
+        }
+        if (lane == 0) {
+            // lse * log2(e) as a float pair (log2(e) itself as one).
+            const float lse = real ? __ldg(a.lse + ((int64_t)r * a.qlen) * a.heads + rho) : -INFINITY;
+            float4 c = make_float4(0.f, 0.f, INFINITY, 0.f);   // a row that counts nothing: 2^-inf
+            if (lse != -INFINITY) {
+                constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLo = 1.92596299112661746e-8f;
+                c.x = a.sc_hi * back;
+                c.y = a.sc_lo * back;
+                c.z = lse * kLog2e;
+                c.w = isinf(c.z) ? 0.f : fmaf(lse, kLog2e, -c.z) + lse * kLog2eLo;
+            }
+            ms.c[buf][n] = c;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ scores
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ void ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// One token's sum over the query rows; MASK: rows count tokens below their
+// vis only.
+template <int NP, int TERMS, bool MASK>
+__device__ __forceinline__ float token_sum(uint32_t taddr, const float4 *c, const int *vis, int j) {
+    constexpr int NQ = NP / TERMS;
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n0 = 0; n0 < NQ; n0 += 8) {
+        float acc[8], lo[8];
+        ld8(taddr + n0, acc);
+        if (TERMS == 2) ld8(taddr + NQ + n0, lo);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 k = c[n0 + i];
+            if (TERMS == 2) acc[i] = fmaf(lo[i], 0.0625f, acc[i]);
+            const float p = exp2_approx(fmaf(acc[i], k.x, -k.z) + fmaf(acc[i], k.y, -k.w));
+            if (!MASK || j < vis[n0 + i]) sum[i & 1] += p;
+        }
+    }
+    return sum[0] + sum[1];
+}
+
+template <int NP, int TERMS>
+__device__ void epilogue(const TokenArgs &a, Misc<NP / TERMS> &ms, int grp) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2, wq = warp & 3;
+    const uint32_t taddr = ms.tmem + wg * NP + ((uint32_t)(32 * wq) << 16);
+    float *out = a.out + (int64_t)grp * a.group_stride;
+    Walk w;
+    w.init(a, ms);
+    for (int it = 0; w.valid(); ++it, w.next(a)) {
+        if ((it & 1) != wg) continue;
+        const int j = w.t * kTile + 32 * wq + lane, buf = w.unit % kConstBufs;
+        const int64_t i = (int64_t)w.base + j;
+        const bool real = j < w.len;
+        float old = 0.f;
+        if (a.decay != 0.f && real) old = a.weights[i] * a.decay;
+        if (!wait_or_abort(&ms.d_full[wg], (it >> 1) & 1, &ms.abort_flag)) break;
+        tc::fence_after();
+        const bool whole = ms.all_vis[buf] >= min((w.t + 1) * kTile, w.len);
+        const float sum = whole ? token_sum<NP, TERMS, false>(taddr, ms.c[buf], ms.vis[buf], j)
+                                : token_sum<NP, TERMS, true>(taddr, ms.c[buf], ms.vis[buf], j);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.d_free[wg]);
+        if (real) out[i] = old + sum;
+    }
+}
+
+template <int NP, int TERMS>
+__global__ void __launch_bounds__(kThreads, 1)
+    token_weights_kernel(const __grid_constant__ CUtensorMap mlat, const __grid_constant__ CUtensorMap mrope,
+                         const TokenArgs a) {
+    using C = Cfg<NP, TERMS>;
+    constexpr int NQ = NP / TERMS;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Misc<NQ> &ms = *reinterpret_cast<Misc<NQ> *>(sm + C::OffMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int grp = blockIdx.x % a.groups;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ms.kv_full[s], kProdWarps);
+            mbar_init(&ms.kv_empty[s], 1);
+        }
+        for (int d = 0; d < 2; ++d) {
+            mbar_init(&ms.d_full[d], 1);
+            mbar_init(&ms.d_free[d], 4);
+        }
+        mbar_init(&ms.q_ready, kPrepWarps);
+        mbar_init(&ms.q_free, 1);
+        mbar_init(&ms.fin, 1);
+        ms.abort_flag = 0;
+        ms.start[0] = ms.start[1] = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) tc::tmem_alloc(&ms.tmem, C::TmemCols);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    find_start(a, ms, blockIdx.x / a.groups);
+    if (warp < kEpiWarps) {
+        epilogue<NP, TERMS>(a, ms, grp);
+    } else if (warp == kMmaWarp) {
+        mma_issuer<NP, TERMS>(a, sm, ms);
+    } else if (warp < kPrepWarp0) {
+        producer<NQ>(a, &mlat, &mrope, sm, ms);
+    } else {
+        Walk w;
+        w.init(a, ms);
+        for (; w.valid(); w.next(a)) {
+            if (!w.first) continue;
+            if (w.unit > 0 && !wait_or_abort(&ms.q_free, (w.unit - 1) & 1, &ms.abort_flag)) break;
+            prep_unit<NP, TERMS>(a, sm, ms, w.r, w.len, grp, w.unit);
+            tc::fence_async_smem();     // generic-proxy writes -> tensor-core reads
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.q_ready);
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == kMmaWarp) tc::tmem_free(ms.tmem, C::TmemCols);
+}
+
+// out[i] = decay * weights[i] + the groups' partial sums, in group order.
+__global__ void __launch_bounds__(256) join_kernel(const TokenArgs a, const float *__restrict__ parts, float *out,
+                                                   float decay) {
+    int base;
+    const int len = request_len(a.indptr, blockIdx.x, a.num_pages, &base);
+    for (int j = blockIdx.y * 256 + threadIdx.x; j < len; j += gridDim.y * 256) {
+        const int64_t i = (int64_t)base + j;
+        float sum = parts[i];
+        for (int g = 1; g < a.groups; ++g) sum += parts[i + g * a.group_stride];
+        out[i] = decay == 0.f ? sum : fmaf(a.weights[i], decay, sum);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// The cache as [pool_rows, 576] bytes, read in rows of `cols` bytes.
+bool encode_rows(CUtensorMap *m, const void *kv, int64_t pool_rows, cuuint32_t cols, CUtensorMapSwizzle swz) {
+    const cuuint64_t dim[2] = {(cuuint64_t)MLA_D_QK, (cuuint64_t)pool_rows}, stride[1] = {(cuuint64_t)MLA_D_QK};
+    const cuuint32_t box[2] = {cols, 1}, es[2] = {1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(kv), dim, stride, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Row groups and rows per group: the fewest groups of at most 128 MMA
+// columns, each as narrow as that allows (steps of 32 columns).
+void shape(int rows, int terms, int *groups, int *np) {
+    const int most = 128 / terms;
+    const int g = (rows + most - 1) / most, n = (rows + g - 1) / g * terms;
+    *groups = g;
+    *np = (n + 31) / 32 * 32;
+}
+
+template <int NP, int TERMS>
+cudaError_t launch(const CUtensorMap &ml, const CUtensorMap &mr, const TokenArgs &a, cudaStream_t st) {
+    constexpr int smem = Cfg<NP, TERMS>::OffMisc + sizeof(Misc<NP / TERMS>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+    cudaError_t e = smem_attr_once<token_weights_kernel<NP, TERMS>>(smem);
+    if (e != cudaSuccess) return e;
+    token_weights_kernel<NP, TERMS><<<a.virt * a.groups, kThreads, smem, st>>>(ml, mr, a);
+    return cudaGetLastError();
+}
+
+template <int TERMS>
+cudaError_t launch_np(int np, const CUtensorMap &ml, const CUtensorMap &mr, const TokenArgs &a, cudaStream_t st) {
+    switch (np) {
+        case 32: return launch<32, TERMS>(ml, mr, a, st);
+        case 64: return launch<64, TERMS>(ml, mr, a, st);
+        case 96: return launch<96, TERMS>(ml, mr, a, st);
+        default: return launch<128, TERMS>(ml, mr, a, st);
     }
 }
 
 }  // namespace
 
+int64_t token_weights_workspace(int rows, bool q8, int64_t num_pages) {
+    int groups, np;
+    shape(rows, q8 ? 1 : 2, &groups, &np);
+    return groups > 1 ? (int64_t)groups * num_pages * 4 : 0;
+}
+
 cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                                  const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
-                                 int heads, float sc, const float *lse, float decay, const float *weights, float *out,
-                                 bool causal, bool q8, int sms, cudaStream_t st) {
+                                 int heads, double sc, const float *lse, float decay, const float *weights, float *out,
+                                 bool causal, bool q8, void *workspace, int sms, cudaStream_t st) {
+    if (!encode_fn()) return cudaErrorNotSupported;
+    CUtensorMap ml, mr;
+    if (!encode_rows(&ml, kv, pool_rows, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_rows(&mr, kv, pool_rows, 64, CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
     TokenArgs a = {};
     a.q = q;
     a.q_row_stride = q_row_stride;
-    a.kv = static_cast<const uint8_t *>(kv);
     a.pool_rows = pool_rows;
-    a.pages = pages;
     a.num_pages = num_pages;
+    a.pages = pages;
     a.indptr = indptr;
+    a.lse = lse;
+    a.weights = weights;
     a.R = R;
     a.qlen = qlen;
     a.heads = heads;
-    a.sc = sc;
-    a.lse = lse;
-    a.decay = decay;
-    a.weights = weights;
-    a.out = out;
     a.causal = causal;
-    a.q8 = q8;
+    const double sc2 = sc * 1.4426950408889634;
+    a.sc_hi = (float)sc2;
+    a.sc_lo = (float)(sc2 - (double)a.sc_hi);
+    int np;
+    shape(qlen * heads, q8 ? 1 : 2, &a.groups, &np);
+    a.virt = sms / a.groups < 1 ? 1 : sms / a.groups;
+    a.out = a.groups > 1 ? static_cast<float *>(workspace) : out;
+    a.group_stride = num_pages;
+    a.decay = a.groups > 1 ? 0.f : decay;
+    cudaError_t e = q8 ? launch_np<1>(np, ml, mr, a, st) : launch_np<2>(np, ml, mr, a, st);
+    if (e != cudaSuccess || a.groups == 1) return e;
     const int chunks = (sms * 8 + R - 1) / R;
-    token_weights_kernel<<<dim3(R, chunks < 65535 ? chunks : 65535), kThreads, 0, st>>>(a);
+    join_kernel<<<dim3(R, chunks < 65535 ? chunks : 65535), 256, 0, st>>>(a, static_cast<const float *>(workspace), out,
+                                                                         decay);
     return cudaGetLastError();
 }
 

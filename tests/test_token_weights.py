@@ -12,7 +12,7 @@ import mla_decode_paged_gb300 as mla
 
 DEV = "cuda"
 A = 1 << 20
-B, C, D, E, F, G = (A + (i << 28) for i in range(1, 7))
+B, C, D, E, F, G, H = (A + (i << 28) for i in range(1, 8))
 
 
 @pytest.fixture(scope="module")
@@ -23,11 +23,11 @@ def lib():
 
 def _call(lib, **kw):
     a = dict(q=A, qs=12 * 576, kv=B, pool=100, pages=C, n=50, indptr=D, R=2, qlen=1, heads=12, scale=0.1,
-             kv_scale=1.0, q_scale=1.0, lse=E, decay=1.0, w=F, out=G, flags=0)
+             kv_scale=1.0, q_scale=1.0, lse=E, decay=1.0, w=F, out=G, flags=0, ws=None, wsn=0)
     a.update(kw)
     return lib.mla_token_weights(a["q"], a["qs"], a["kv"], a["pool"], a["pages"], a["n"], a["indptr"], a["R"],
                                  a["qlen"], a["heads"], a["scale"], a["kv_scale"], a["q_scale"], a["lse"], a["decay"],
-                                 a["w"], a["out"], a["flags"], None)
+                                 a["w"], a["out"], a["flags"], a["ws"], a["wsn"], None)
 
 
 @pytest.mark.parametrize("kw,msg", [
@@ -55,6 +55,12 @@ def _call(lib, **kw):
     (dict(out=G + 2), b"misaligned"),
     (dict(pool=0), b"empty"),
     (dict(out=F + 4), b"overlaps"),
+    (dict(scale=1e30, kv_scale=1e30), b"too large"),
+    (dict(qlen=16), b"workspace"),
+    (dict(qlen=16, ws=H, wsn=100), b"workspace"),
+    (dict(qlen=16, ws=H + 8, wsn=1 << 20), b"misaligned workspace"),
+    (dict(qlen=16, ws=G, wsn=1 << 20), b"workspace overlaps"),
+    (dict(qlen=16, ws=F, wsn=1 << 20), b"workspace overlaps"),
 ])
 def test_refusals(lib, kw, msg):
     assert _call(lib, **kw) == mla.MLA_ERR_INVALID
@@ -66,6 +72,14 @@ def test_unsupported_sizes_and_nothing_to_do(lib):
     assert _call(lib, n=1 << 31) == mla.MLA_ERR_UNSUPPORTED
     assert _call(lib, R=0) == mla.MLA_OK
     assert _call(lib, n=0, pages=None) == mla.MLA_OK
+
+
+def test_workspace(lib):
+    assert mla.token_weights_workspace(1, 12, 1000) == 0
+    assert mla.token_weights_workspace(1, 128, 1000, True) == 0
+    assert mla.token_weights_workspace(1, 96, 1000) > 0
+    with pytest.raises(mla.MlaError, match="qlen"):
+        mla.token_weights_workspace(17, 12, 1000)
 
 
 def test_binding_refusals():
@@ -273,6 +287,33 @@ def test_bad_pages_and_bad_page_lists_are_flagged():
                           out=out[:350])
         assert mla.device_status() == mla.DEV_BAD_INDPTR
         assert (out[350:] == -7).all()
+
+
+@pytest.mark.gpu
+def test_many_requests_of_all_lengths():
+    # more requests than threads of a CTA, most of one tile or none: every CTA changes requests at every tile
+    lengths = [(i * 37) % 150 if i % 5 else 0 for i in range(1500)] + [0] * 700 + [260]
+    for heads in (4, 70):
+        q, kv, pages, indptr = _make(lengths, 1, heads, heads, 12)
+        want, bound, lse = _formula(q, kv, pages, lengths, heads, 1, 0.05, False)
+        _check(mla.token_weights(q, kv, pages, indptr, 0.05, 1.0, lse.contiguous()), want, bound)
+    assert mla.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_given_workspace_and_overlapping_calls():
+    lengths = [900, 300]
+    q, kv, pages, indptr = _make(lengths, 2, 96, 96, 13)
+    _, _, lse = _formula(q, kv, pages, lengths, 96, 2, 0.05, False)
+    args, kw = (q, kv, pages, indptr, 0.05, 1.0, lse.contiguous()), dict(qlen=2)
+    want = mla.token_weights(*args, **kw)
+    ws = torch.empty(mla.token_weights_workspace(2, 96, 1200), dtype=torch.uint8, device=DEV)
+    assert torch.equal(mla.token_weights(*args, workspace=ws, **kw), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [mla.token_weights(*args, stream=s, **kw) for s in (side, None, side, None)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
 
 
 @pytest.mark.gpu
