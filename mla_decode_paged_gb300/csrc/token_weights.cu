@@ -45,7 +45,7 @@ namespace {
 
 constexpr int kEpiWarps = 8, kMmaWarp = 8, kProdWarp0 = 9, kProdWarps = 5, kPrepWarp0 = 14, kPrepWarps = 4;
 constexpr int kThreads = (kPrepWarp0 + kPrepWarps) * 32;
-constexpr int kStages = 2, kTile = 128;
+constexpr int kStages = 2, kTile = 128, kAhead = 8;
 constexpr int kLatBlock = (kTile / 8) * 1024;              // one 128-byte column block of a stage
 constexpr int kRopeOff = 4 * kLatBlock;
 constexpr int kStageBytes = kRopeOff + (kTile / 8) * 512;  // 73,728
@@ -207,10 +207,20 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
             }
         }
     };
+    // The page list, contiguous over a CTA's tiles, is brought to L2 kAhead
+    // tiles before its indices are read: an index that misses L2 waits behind
+    // the stream of rows for several thousand cycles.
+    const auto ahead = [&](int tiles) {
+        const int64_t at = (int64_t)w.base + (int64_t)(w.t + tiles) * kTile + 32 * lane;
+        if (lane < 5 && at < a.num_pages) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pages + at));
+    };
+    if (part == 4 && w.valid())
+        for (int k = 1; k < kAhead; ++k) ahead(k);
     int rows[4], it = 0;
     fetch(rows);
     bool ok = true;
     while (w.valid()) {
+        if (part == 4) ahead(kAhead);
         const int s = it % kStages;
         if (!(ok = wait_or_abort(&ms.kv_empty[s], ((it / kStages) & 1) ^ 1, &ms.abort_flag))) break;
         if (lane == 0) mbar_arrive_expect_tx(&ms.kv_full[s], part < 4 ? 32 * 512 : 32 * 256);
