@@ -436,6 +436,7 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
  *   weights      f32 [num_pages]; may be NULL when decay is 0.
  *   out          f32 [num_pages] (written); may be weights itself, otherwise
  *                must not overlap it.
+ * num_pages up to 2^31 - 65536, num_requests up to 2^24.
  *   workspace    device, 16-byte aligned, at least
  *                mla_token_weights_workspace() bytes (may be NULL for 0);
  *                holds nothing between calls, but two calls that may overlap
@@ -475,6 +476,7 @@ int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsi
  *   recent, sinks   >= 0.
  *   pages_out, weights_out  [num_pages], indptr_out [num_requests + 1]; no
  *                   output may overlap an input or another output.
+ * num_pages up to 2^31 - 65536, num_requests up to 2^24.
  * A bad indptr entry sets MLA_DEV_BAD_INDPTR and its request is empty.
  */
 mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,

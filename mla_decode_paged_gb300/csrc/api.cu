@@ -59,7 +59,7 @@ int64_t token_weights_workspace(int rows, bool q8, int64_t num_pages);
 cudaError_t token_weights_status(unsigned int *flags, bool clear);
 cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, const float *weights,
                             const int32_t *budgets, int budget, int recent, int sinks, int32_t *pages_out,
-                            int32_t *indptr_out, float *weights_out, cudaStream_t st);
+                            int32_t *indptr_out, float *weights_out, int sms, cudaStream_t st);
 cudaError_t evict_status(unsigned int *flags, bool clear);
 int64_t value_lora_workspace(int64_t rows, int heads, int rank);
 cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *gate, const int32_t *lengths,
@@ -82,6 +82,10 @@ mla_status cuda_fail(cudaError_t e, const char *where) {
     g_last_error = std::string(where) + ": " + cudaGetErrorString(e);
     return MLA_ERR_CUDA;
 }
+
+// Page-list sizes of the calls that walk it in 32-bit token positions (a
+// tile or a block's step past the last one still fits).
+constexpr int64_t kMaxPages = INT32_MAX - 65535, kMaxRequests = 1 << 24;
 
 // Whether two blocks of bytes share one.
 bool overlap(const void *p, int64_t pn, const void *q, int64_t qn) {
@@ -670,7 +674,8 @@ mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv
         return fail(MLA_ERR_INVALID, "misaligned pointer (q, kv need 16 bytes)");
     if (pool_rows == 0) return fail(MLA_ERR_INVALID, "empty KV pool");
     if (pool_rows > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "pool_rows above 2^31 - 1");
-    if (num_pages > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 1");
+    if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 65536");
+    if (num_requests > kMaxRequests) return fail(MLA_ERR_UNSUPPORTED, "num_requests above 2^24");
     if (out != weights && overlap(out, num_pages * 4, weights, num_pages * 4))
         return fail(MLA_ERR_INVALID, "out overlaps weights");
     const int64_t need = mla::token_weights_workspace(qlen * heads, q8, num_pages);
@@ -692,7 +697,7 @@ int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsi
     if (flags & ~(MLA_ATTEND_CAUSAL | MLA_ATTEND_Q_FP8)) return fail(MLA_ERR_INVALID, "unknown flag bits");
     if (qlen < 1 || qlen > MLA_MAX_QLEN) return fail(MLA_ERR_INVALID, "qlen outside 1..16");
     if (heads < 1 || heads > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID, "heads outside 1..128");
-    if (num_pages < 0 || num_pages > INT32_MAX) return fail(MLA_ERR_INVALID, "num_pages outside 0..2^31 - 1");
+    if (num_pages < 0 || num_pages > kMaxPages) return fail(MLA_ERR_INVALID, "num_pages outside 0..2^31 - 65536");
     return mla::token_weights_workspace(qlen * heads, (flags & MLA_ATTEND_Q_FP8) != 0, num_pages);
 }
 
@@ -706,7 +711,8 @@ mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *
     if (!aligned(pages, 4) || !aligned(indptr, 4) || !aligned(weights, 4) || !aligned(budgets, 4) ||
         !aligned(pages_out, 4) || !aligned(indptr_out, 4) || !aligned(weights_out, 4))
         return fail(MLA_ERR_INVALID, "misaligned pointer (4 bytes)");
-    if (num_pages > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 1");
+    if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 65536");
+    if (num_requests > kMaxRequests) return fail(MLA_ERR_UNSUPPORTED, "num_requests above 2^24");
     const int64_t n = num_pages * 4, r = (int64_t)num_requests * 4;
     const struct { const void *p; int64_t n; } in[4] = {{pages, n}, {weights, n}, {indptr, r + 4}, {budgets, r}},
                                                to[3] = {{pages_out, n}, {weights_out, n}, {indptr_out, r + 4}};
@@ -716,8 +722,10 @@ mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *
         for (int j = 0; j < i; ++j)
             if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return fail(MLA_ERR_INVALID, "two outputs overlap");
     }
+    const int sms = device_sms();
+    if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
     cudaError_t e = mla::kv_evict_launch(pages, num_pages, indptr, num_requests, weights, budgets, budget, recent, sinks,
-                                         pages_out, indptr_out, weights_out, static_cast<cudaStream_t>(stream));
+                                         pages_out, indptr_out, weights_out, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kv_evict launch");
     return MLA_OK;
 }

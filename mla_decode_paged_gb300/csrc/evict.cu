@@ -6,9 +6,23 @@
 // -inf, equal weights by the lowest position).  Kept tokens stay in order;
 // the page list becomes every request's kept rows, then the freed rows.
 //
-// The m-th largest weight is found by radix selection on an order-preserving
-// 32-bit key (11 + 11 + 10 bits, a shared histogram a pass), then one pass
-// in position order places every token by a block scan.
+// Bound by the 16 bytes a token that are read and written for many long
+// requests, by the chain of dependent steps for one.
+//
+// Design: a cluster of CS blocks per request, each with a contiguous slice
+// of its tokens and every warp with a contiguous part of that, whose keys
+// (order-preserving 32-bit images of the weights) stay in registers: 16 a
+// thread, 8,192 tokens a block.  A longer slice is taken in rounds of that
+// size, read again for every step.  The m-th largest key is found by radix
+// selection, 11 + 11 + 10 bits: every block counts its slice into a shared
+// histogram, sums one CS-th of the bins over the cluster through distributed
+// shared memory, and reads the others' sums (reading all CS histograms in
+// every block instead took 11,500 cycles a digit with 16 blocks, this 3,000;
+// a histogram per digit: none is reused).  What each warp keeps is counted
+// by ballots, the offsets of warps and blocks are exchanged once, and the
+// tokens are placed by the ballots again.
+#include <algorithm>
+
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -16,8 +30,11 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 2048, kDigits = 3, kOwn = kBins / kThreads;
+constexpr int kSteps = 16;         // tokens a thread holds
+constexpr int kRound = kSteps * kThreads;
+static_assert(kOwn == 4, "a thread reads its bins as one vector");
 
 struct EvictArgs {
     const int32_t *pages, *indptr, *budgets;
@@ -35,26 +52,68 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The weight of a key, where the key tells it (not of NaN or -inf, nor of a zero).
+__device__ __forceinline__ float key_weight(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+constexpr uint32_t kKeyZero = 0x80000000u, kKeyLowest = ~0xff800000u;
+
 __device__ __forceinline__ int kept_tokens(const EvictArgs &a, int r, int len) {
     const int b = a.budgets ? __ldg(a.budgets + r) : a.budget;
     return b < 0 ? 0 : b < len ? b : len;
 }
 
-// Sum of v over the block, to every thread.
-__device__ long long block_sum(long long v, long long *red) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    long long t = red[threadIdx.x & 31];
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-    return t;
+struct __align__(16) Shared {
+    uint32_t hist[kDigits][kBins];
+    uint32_t stage[kBins];          // one CS-th of the bins from every block
+    uint32_t sums[kDigits][kBins];  // and their sums (the first kBins / CS)
+    long long red64[3][kWarps];
+    uint32_t scan[kWarps];
+    uint32_t warp_kept[kWarps], warp_ties[kWarps];
+    uint32_t totals[2];             // this block's sure tokens and ties, for the cluster
+    uint32_t pick[3];
+};
+
+template <int CS>
+__device__ __forceinline__ uint32_t block_rank() {
+    if (CS == 1) return 0;
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
 
-// Exclusive prefix sum over the block of v; the block's sum in *total.
-__device__ uint32_t block_scan(uint32_t v, uint32_t *red, uint32_t *total) {
+// All blocks of the cluster, their shared-memory writes before it visible after it.
+template <int CS>
+__device__ __forceinline__ void cluster_sync() {
+    if (CS == 1) __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// What is at `p`'s place in the shared memory of block `rank`.
+template <int CS>
+__device__ __forceinline__ uint32_t remote(const uint32_t *p, uint32_t rank) {
+    if (CS == 1) return *p;
+    uint32_t addr, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+template <int CS>
+__device__ __forceinline__ uint4 remote4(const uint32_t *p, uint32_t rank) {
+    if (CS == 1) return *reinterpret_cast<const uint4 *>(p);
+    uint32_t addr;
+    uint4 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Exclusive prefix sum of v over the block's threads.
+__device__ uint32_t block_scan(uint32_t v, uint32_t *red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t x = v;
 #pragma unroll
@@ -65,130 +124,300 @@ __device__ uint32_t block_scan(uint32_t v, uint32_t *red, uint32_t *total) {
     __syncthreads();
     if (lane == 31) red[warp] = x;
     __syncthreads();
-    uint32_t w = red[lane], s = w;
+    const uint32_t w = lane < kWarps ? red[lane] : 0;
+    uint32_t s = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += y;
     }
-    *total = __shfl_sync(0xffffffffu, s, 31);
     return x - v + __shfl_sync(0xffffffffu, s - w, warp);
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t red[32];
-    __shared__ long long red64[32];
-    __shared__ uint32_t pick[2];
-    const int r = blockIdx.x, tid = threadIdx.x;
+template <int CS>
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
+    const int r = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = block_rank<CS>();
 
-    // Kept and freed tokens of the requests before this one, kept of all.
-    long long kept_before = 0, len_before = 0, kept_total = 0;
+    // Kept and all tokens of the requests before this one, kept of all.
+    long long sums[3] = {0, 0, 0};
     for (int i = tid; i < a.R; i += kThreads) {
         int base;
         const int len = request_len(a.indptr, i, a.num_pages, &base), k = kept_tokens(a, i, len);
-        kept_total += k;
+        sums[2] += k;
         if (i < r) {
-            kept_before += k;
-            len_before += len;
+            sums[0] += k;
+            sums[1] += len;
         }
     }
-    kept_before = block_sum(kept_before, red64);
-    len_before = block_sum(len_before, red64);
-    kept_total = block_sum(kept_total, red64);
+    for (int i = tid; i < kDigits * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], d);
+        if (lane == 0) sh.red64[j][warp] = sums[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        sums[j] = lane < kWarps ? sh.red64[j][lane] : 0;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], d);
+    }
     int base;
     const int len = request_len(a.indptr, r, a.num_pages, &base);
     const int kept = kept_tokens(a, r, len);
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
         if (r == 0) a.indptr_out[0] = 0;
-        a.indptr_out[r + 1] = (int32_t)(kept_before + kept);
+        a.indptr_out[r + 1] = (int32_t)(sums[0] + kept);
     }
     const int recent = a.recent < kept ? a.recent : kept;
     const int sinks = a.sinks < kept - recent ? a.sinks : kept - recent;
-    const int lo = sinks, hi = len - recent;   // the tokens that may go
-    int m = kept - recent - sinks;             // how many of them stay
+    const int lo = sinks, hi = len - recent;        // the tokens that may go
+    const int m = kept - recent - sinks;            // how many of them stay
     const float *w = a.weights + base;
+
+    // This block's slice, in rounds; a warp's part of a round, whole groups of
+    // 32 tokens.
+    const int slice = ((len + CS - 1) / CS + 31) / 32 * 32;
+    const int s0 = (int)min((int64_t)slice * rank, (int64_t)len), s1 = min(slice, len - s0) + s0;
+    const int rounds = (s1 - s0 + kRound - 1) / kRound;
+    uint32_t key[kSteps];
+    uint32_t valid = 0, free = 0;   // a bit a step: a token, one that may go
+    int first = 0, steps = 0;
+    const auto load = [&](int q) {
+        const int q0 = s0 + q * kRound, q1 = min(q0 + kRound, s1);
+        const int part = ((q1 - q0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+        first = q0 + warp * part + lane;
+        steps = part / 32;
+        valid = free = 0;
+        float x[kSteps];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const int i = first + 32 * j;
+            x[j] = 0.f;
+            if (j < steps && i < q1) {
+                x[j] = __ldg(w + i);
+                valid |= 1u << j;
+                if (i >= lo && i < hi) free |= 1u << j;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) key[j] = weight_key(x[j]);
+    };
+    if (rounds > 0) load(0);
 
     // The m-th largest key T of [lo, hi), and how many keys equal to T stay.
     uint32_t T = 0, ties = 0;
-    const bool all = m >= hi - lo;
-    if (m > 0 && !all) {
-        uint32_t need = (uint32_t)m, mask = 0;
-#pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const uint32_t bins = pass == 2 ? 1024u : 2048u;
-            for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-            __syncthreads();
-            for (int i = lo + tid; i < hi; i += kThreads) {
-                const uint32_t key = weight_key(__ldg(w + i));
-                if ((key & mask) == T) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+    const bool select = m > 0 && m < hi - lo;       // the same in every block of the cluster
+    bool tied = false;                              // some of the equal keys go
+    if (select) {
+        uint32_t need = (uint32_t)m;
+#pragma unroll
+        for (int digit = 0; digit < kDigits; ++digit) {
+            const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+            const uint32_t bins = digit == 2 ? 1024u : 2048u;
+            const int above_bits = digit == 0 ? 0 : digit == 1 ? 21 : 10;   // bits below the digits found
+            uint32_t *hist = sh.hist[digit];
+            for (int q = 0; q < rounds; ++q) {
+                if (rounds > 1) load(q);
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j)
+                    if (j < steps && (free >> j & 1) && (digit == 0 || (key[j] ^ T) >> above_bits == 0))
+                        atomicAdd(&hist[(key[j] >> shift) & (bins - 1)], 1u);
+            }
+            cluster_sync<CS>();
+            // Bins from the top: thread t holds the kOwn from kBins - 1 - kOwn * t down, summed over the cluster.
+            const uint32_t top = kBins - 1 - kOwn * tid;
+            uint32_t n[kOwn], sum = 0;
+            uint4 v;
+            if (CS == 1) {
+                v = *reinterpret_cast<const uint4 *>(hist + top - (kOwn - 1));
+            } else {
+                constexpr int kShare = kBins / CS;
+                const uint32_t c = (tid / (kShare / 4) + rank) % CS, at = tid % (kShare / 4) * 4;
+                *reinterpret_cast<uint4 *>(sh.stage + c * kShare + at) = remote4<CS>(hist + rank * kShare + at, c);
+                __syncthreads();
+                for (int i = tid; i < kShare; i += kThreads) {
+                    uint32_t s = 0;
+#pragma unroll
+                    for (int j = 0; j < CS; ++j) s += sh.stage[j * kShare + i];
+                    sh.sums[digit][i] = s;
+                }
+                cluster_sync<CS>();
+                const uint32_t low = top - (kOwn - 1);
+                v = remote4<CS>(sh.sums[digit] + low % kShare, low / kShare);
+            }
+            n[0] = v.w;
+            n[1] = v.z;
+            n[2] = v.y;
+            n[3] = v.x;
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) sum += n[j];
+            uint32_t above = block_scan(sum, sh.scan);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+                if (above < need && need <= above + n[j]) {
+                    sh.pick[0] = top - j;
+                    sh.pick[1] = need - above;
+                    sh.pick[2] = n[j];
+                }
+                above += n[j];
             }
             __syncthreads();
-            // Bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t.
-            const uint32_t b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
-            const uint32_t n1 = hist[b1], n0 = hist[b0];
-            uint32_t total;
-            const uint32_t above = block_scan(n1 + n0, red, &total);
-            if (above < need && need <= above + n1) {
-                pick[0] = b1;
-                pick[1] = need - above;
-            } else if (above + n1 < need && need <= above + n1 + n0) {
-                pick[0] = b0;
-                pick[1] = need - above - n1;
-            }
-            __syncthreads();
-            T |= pick[0] << shift;
-            need = pick[1];
-            mask |= (bins - 1) << shift;
+            T |= sh.pick[0] << shift;
+            need = sh.pick[1];
         }
         ties = need;
+        tied = need < sh.pick[2];
     }
 
-    // Placement, in position order.
-    long long out_kept = kept_before, out_freed = kept_total + (len_before - kept_before);
-    uint32_t ties_seen = 0;
-    for (int c = 0; c < len; c += kThreads) {
-        const int i = c + tid;
-        uint32_t sure = 0, tie = 0;
-        float wi = 0.f;
-        if (i < len) {
-            wi = __ldg(w + i);
-            if (i < lo || i >= hi || all) sure = 1;
-            else if (m > 0) {
-                const uint32_t key = weight_key(wi);
-                sure = key > T;
-                tie = key == T;
+    // A token outside [lo, hi), or any when all stay, is sure; between, those
+    // above T are, and those equal to T are ties (sure too when all of them stay).
+    const bool all = m >= hi - lo;
+    uint32_t sure = 0, tie = 0;     // a bit a step
+    const auto count = [&](uint32_t &nsure, uint32_t &nties) {
+        sure = all ? valid : valid & ~free;
+        tie = 0;
+        if (select) {
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+                if (key[j] >= T) sure |= free & 1u << j;
+                if (key[j] == T) tie |= free & 1u << j;
             }
+            if (tied) sure &= ~tie;
+            else tie = 0;
         }
-        uint32_t total;
-        const uint32_t before = block_scan(sure | tie << 16, red, &total);
-        const uint32_t sure_before = before & 0xffff, tie_before = ties_seen + (before >> 16);
-        const uint32_t ties_chunk0 = ties_seen < ties ? ties_seen : ties;
-        const uint32_t ties_here = tie_before < ties ? tie_before : ties;
-        const uint32_t rank = sure_before + ties_here - ties_chunk0;   // kept tokens of this chunk before i
-        const bool keep = sure || (tie && tie_before < ties);
-        if (i < len) {
-            const long long at = keep ? out_kept + rank : out_freed + (tid - rank);
-            if (at < a.num_pages) {
-                a.pages_out[at] = __ldg(a.pages + base + i);
-                a.weights_out[at] = keep ? wi : 0.f;
-            }
+        nsure += __reduce_add_sync(0xffffffffu, __popc(sure));
+        if (tied) nties += __reduce_add_sync(0xffffffffu, __popc(tie));
+    };
+    // Sums over the block (k, t) and over the warps before this one (kb, tb) of what every warp counted.
+    const auto exchange = [&](uint32_t nsure, uint32_t nties, uint32_t &k, uint32_t &t, uint32_t &kb, uint32_t &tb) {
+        __syncthreads();
+        if (lane == 0) {
+            sh.warp_kept[warp] = nsure;
+            sh.warp_ties[warp] = nties;
         }
-        ties_seen += total >> 16;
-        const uint32_t ties_now = ties_seen < ties ? ties_seen : ties;
-        const uint32_t chunk_kept = (total & 0xffff) + ties_now - ties_chunk0;
-        const int n = len - c < kThreads ? len - c : kThreads;
-        out_kept += chunk_kept;
-        out_freed += n - (int)chunk_kept;
+        __syncthreads();
+        k = lane < kWarps ? sh.warp_kept[lane] : 0;
+        t = lane < kWarps ? sh.warp_ties[lane] : 0;
+        kb = lane < warp ? k : 0;
+        tb = lane < warp ? t : 0;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) {
+            k += __shfl_xor_sync(0xffffffffu, k, d);
+            t += __shfl_xor_sync(0xffffffffu, t, d);
+            kb += __shfl_xor_sync(0xffffffffu, kb, d);
+            tb += __shfl_xor_sync(0xffffffffu, tb, d);
+        }
+    };
+    uint32_t nsure = 0, nties = 0, k, t, kb, tb;
+    for (int q = 0; q < rounds; ++q) {
+        if (rounds > 1) load(q);
+        count(nsure, nties);
     }
+    exchange(nsure, nties, k, t, kb, tb);
+    uint32_t block_kept = 0, block_ties = 0;        // sure tokens and ties of the blocks before this one
+    if (CS > 1) {
+        if (tid == 0) {
+            sh.totals[0] = k;
+            sh.totals[1] = t;
+        }
+        cluster_sync<CS>();
+        if (lane < rank) {
+            block_kept = remote<CS>(&sh.totals[0], lane);
+            block_ties = remote<CS>(&sh.totals[1], lane);
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) {
+            block_kept += __shfl_xor_sync(0xffffffffu, block_kept, d);
+            block_ties += __shfl_xor_sync(0xffffffffu, block_ties, d);
+        }
+    }
+
+    // Placement, in position order.  Places past the page list (only a bad
+    // indptr makes them) are dropped.
+    const uint32_t out_kept = (uint32_t)min(sums[0], 0x7fffffffll);
+    const uint32_t out_freed = (uint32_t)min(sums[2] + (sums[1] - sums[0]), 0x7fffffffll);
+    const uint32_t below = (1u << lane) - 1, limit = (uint32_t)a.num_pages;
+    for (int q = 0; q < rounds; ++q) {
+        if (rounds > 1) {
+            load(q);
+            nsure = nties = 0;
+            count(nsure, nties);
+            exchange(nsure, nties, k, t, kb, tb);
+        }
+        uint32_t kept_at = block_kept + kb, ties_at = block_ties + tb;
+        block_kept += k;
+        block_ties += t;
+        const int32_t *pages = a.pages + base + first;
+#pragma unroll
+        for (int j0 = 0; j0 < kSteps; j0 += 8) {
+            if (j0 >= steps) break;
+            int32_t page[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) page[j] = (valid >> (j0 + j) & 1) ? __ldg(pages + 32 * (j0 + j)) : 0;
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) {
+                const int j = j0 + jj;
+                if (j >= steps) break;
+                const uint32_t ms = __ballot_sync(0xffffffffu, sure >> j & 1);
+                // kept tokens of the request before this one: the sure ones and the ties among the first `ties`
+                uint32_t rank_i = kept_at + __popc(ms & below);
+                bool keep = sure >> j & 1;
+                if (tied) {
+                    const uint32_t mt = __ballot_sync(0xffffffffu, tie >> j & 1);
+                    const uint32_t tie_rank = ties_at + __popc(mt & below);
+                    keep = keep || ((tie >> j & 1) && tie_rank < ties);
+                    rank_i += min(tie_rank, ties);
+                    ties_at += __popc(mt);
+                }
+                kept_at += __popc(ms);
+                const uint32_t i = first + 32 * j;
+                const uint32_t at = keep ? out_kept + rank_i : out_freed + (i - rank_i);
+                float wi = 0.f;
+                if (keep) {
+                    wi = key_weight(key[j]);
+                    if (key[j] == kKeyZero || key[j] == kKeyLowest) wi = (valid >> j & 1) ? __ldg(w + i) : 0.f;
+                }
+                if ((valid >> j & 1) && at < limit) {
+                    a.pages_out[at] = page[jj];
+                    a.weights_out[at] = wi;
+                }
+            }
+        }
+    }
+    if (CS > 1) cluster_sync<CS>();                 // no block ends while another may read its shared memory
+}
+
+template <int CS>
+cudaError_t launch(const EvictArgs &a, cudaStream_t st) {
+    cudaError_t e = smem_attr_once<evict_kernel<CS>>((int)sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    if (CS > 8 && (e = cudaFuncSetAttribute(evict_kernel<CS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
+                      cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.R * CS, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = sizeof(Shared);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CS;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CS > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, evict_kernel<CS>, a);
 }
 
 }  // namespace
 
 cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, const float *weights,
                             const int32_t *budgets, int budget, int recent, int sinks, int32_t *pages_out,
-                            int32_t *indptr_out, float *weights_out, cudaStream_t st) {
+                            int32_t *indptr_out, float *weights_out, int sms, cudaStream_t st) {
     if (R == 0) return cudaMemsetAsync(indptr_out, 0, sizeof(int32_t), st);
     EvictArgs a = {};
     a.pages = pages;
@@ -203,8 +432,16 @@ cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32
     a.pages_out = pages_out;
     a.indptr_out = indptr_out;
     a.weights_out = weights_out;
-    evict_kernel<<<R, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    // The lengths are on the device; the mean length says how many blocks a
+    // request is worth (2,048 tokens each), the batch how many fit at once.
+    const int64_t mean = num_pages / R;
+    const int64_t room = 8 * (int64_t)sms / R;
+    const int64_t want = std::min(std::max<int64_t>(mean / 2048, 1), std::max<int64_t>(room, 1));
+    if (want >= 16) return launch<16>(a, st);
+    if (want >= 8) return launch<8>(a, st);
+    if (want >= 4) return launch<4>(a, st);
+    if (want >= 2) return launch<2>(a, st);
+    return launch<1>(a, st);
 }
 
 cudaError_t evict_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }
