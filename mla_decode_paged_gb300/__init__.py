@@ -465,6 +465,7 @@ def kv_append(kv, kv_c, k_pe, slots, k_scale, *, stream=None):
 
 _NORM_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NORM_QUANT = {None: 0, "row": 1, "group": 2, "static": 3}
+_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 
 
 def _empty(shape, dtype, device, stream):
@@ -479,10 +480,11 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _launch(fn, where, device, stream, *args):
-    """``fn(*args, stream)`` with ``device`` current (plain ints are passed
-    as pointers)."""
-    dev = device.index
+def _launch(fn, where, dev, stream, *args):
+    """``fn(*args, stream)`` with device number ``dev`` current (plain ints
+    are passed as pointers)."""
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             st = fn(*args, _stream(stream, dev))
@@ -492,11 +494,25 @@ def _launch(fn, where, device, stream, *args):
         _check(st, where)
 
 
-def _rows_of(t, name, dtypes, n, width):
-    _need(t.dtype in dtypes and t.dim() == 2 and t.shape[0] == n and t.shape[1] == width
-          and (t.stride(1) == 1 or width == 1), "%s must be %s [%d, %d] with contiguous rows"
-          % (name, " or ".join(str(d) for d in dtypes), n, width))
-    return t.stride(0) if n > 1 else width
+# Checks of the calls whose kernels take a few microseconds: the messages are
+# made only when one fails.
+
+
+def _dense(t, name, dtype, shape, dev):
+    """A contiguous tensor of this type and shape on device number ``dev``
+    (-1: the host, which the launch then refuses)."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on the first argument's device"
+                         % (name, dtype, list(shape)))
+
+
+def _rows_of(t, name, dtype, shape, dev):
+    """Row stride of a 2-D tensor of this type and shape whose rows are
+    contiguous, on device number ``dev``."""
+    if t.dtype != dtype or t.shape != shape or t.stride(1) != 1 or t.get_device() != dev:
+        raise ValueError("%s must be a %s tensor of shape %s with contiguous rows on the first argument's device"
+                         % (name, dtype, list(shape)))
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def add_rms_norm(x, weight, eps, residual=None, *, quant=None, scale=None, out=None, out_scales=None,
@@ -514,44 +530,53 @@ def add_rms_norm(x, weight, eps, residual=None, *, quant=None, scale=None, out=N
     ``[T, ceil(D / 128)]`` (128 columns each) or ``"static"`` (the float
     ``scale``; no scales returned): a code stands for code * scale.
     """
-    _need(x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float16), "x must be bf16 or fp16 [T, D]")
-    T, D = x.shape
-    dev = x.device
-    _same_device(dev, weight=weight, residual=residual, out=out, out_scales=out_scales, residual_out=residual_out)
-    xs = _rows_of(x, "x", (x.dtype,), T, D)
-    _need(weight.dtype == x.dtype and weight.shape == (D,) and weight.is_contiguous(),
-          "weight must be contiguous, x's type, [D]")
-    _need(quant in _NORM_QUANT, "quant must be None, 'row', 'group' or 'static'")
-    _need((scale is not None) == (quant == "static"), "scale goes with quant='static'")
-    rs = ros = 0
+    xtype = x.dtype
+    if x.dim() != 2 or xtype not in (_BF16, torch.float16):
+        raise ValueError("x must be bf16 or fp16 [T, D]")
+    shape = x.shape
+    T, D = shape
+    dev = x.get_device()
+    device = x.device
+    xs = _rows_of(x, "x", xtype, shape, dev)
+    _dense(weight, "weight", xtype, (D,), dev)
+    q = _NORM_QUANT.get(quant)
+    if q is None:
+        raise ValueError("quant must be None, 'row', 'group' or 'static'")
+    if (scale is not None) != (q == 3):
+        raise ValueError("scale goes with quant='static'")
+    rp = rop = sp = None
+    rs = ros = rt = 0
     if residual is not None:
-        rs = _rows_of(residual, "residual", (x.dtype, torch.float32), T, D)
+        rtype = residual.dtype
+        if rtype != xtype and rtype != _F32:
+            raise ValueError("residual must be x's type or float32")
+        rt = _NORM_TYPES[rtype]
+        rs = _rows_of(residual, "residual", rtype, shape, dev)
         if residual_out is None:
-            residual_out = _empty((T, D), residual.dtype, dev, stream)
+            residual_out = _empty(shape, rtype, device, stream)
             ros = D
         else:
-            ros = _rows_of(residual_out, "residual_out", (residual.dtype,), T, D)
-    else:
-        _need(residual_out is None, "residual_out needs a residual")
-    otype = x.dtype if quant is None else torch.float8_e4m3fn
+            ros = _rows_of(residual_out, "residual_out", rtype, shape, dev)
+        rp, rop = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    otype = _E4M3 if q else xtype
     if out is None:
-        out = _empty((T, D), otype, dev, stream)
+        out = _empty(shape, otype, device, stream)
         os_ = D
     else:
-        os_ = _rows_of(out, "out", (otype,) if quant is None else (otype, torch.uint8), T, D)
-    if quant in ("row", "group"):
-        shape = (T,) if quant == "row" else (T, (D + 127) // 128)
+        os_ = _rows_of(out, "out", _U8 if q and out.dtype == _U8 else otype, shape, dev)
+    if q == 1 or q == 2:
+        sshape = (T,) if q == 1 else (T, (D + 127) // 128)
         if out_scales is None:
-            out_scales = _empty(shape, torch.float32, dev, stream)
+            out_scales = _empty(sshape, _F32, device, stream)
         else:
-            _buffer(out_scales, "out_scales", torch.float32, shape)
-    else:
-        _need(out_scales is None, "out_scales goes with quant='row' or 'group'")
-    _launch(library().mla_add_rms_norm, "mla_add_rms_norm", dev, stream, x.data_ptr(), xs, _NORM_TYPES[x.dtype],
-            None if residual is None else residual.data_ptr(), rs,
-            0 if residual is None else _NORM_TYPES[residual.dtype], weight.data_ptr(), eps, T, D, _NORM_QUANT[quant],
-            0.0 if scale is None else scale, out.data_ptr(), os_, None if out_scales is None else out_scales.data_ptr(),
-            None if residual_out is None else residual_out.data_ptr(), ros)
+            _dense(out_scales, "out_scales", _F32, sshape, dev)
+        sp = out_scales.data_ptr()
+    elif out_scales is not None:
+        raise ValueError("out_scales goes with quant='row' or 'group'")
+    _launch(library().mla_add_rms_norm, "mla_add_rms_norm", dev, stream, x.data_ptr(), xs, _NORM_TYPES[xtype], rp, rs,
+            rt, weight.data_ptr(), eps, T, D, q, scale or 0.0, out.data_ptr(), os_, sp, rop, ros)
     return out, out_scales, residual_out
 
 
@@ -571,42 +596,46 @@ def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qle
     (allocated if not given and needed; not shared by calls that may
     overlap).
     """
-    kv = _as_u8(kv)
-    heads = q.shape[1] if heads is None else heads
-    R = indptr.numel() - 1
-    S = R * qlen
-    q8 = q.dtype in (torch.float8_e4m3fn, torch.uint8)
-    _need((q8 or q.dtype == torch.bfloat16) and q.dim() == 3 and q.shape[2] == D_QK,
-          "q must be bf16 or fp8 e4m3 [S, H, 576]")
-    _need(q.stride(2) == 1 and (q.stride(1) == D_QK or q.shape[1] == 1), "q rows must have contiguous [H, 576] heads")
-    _need(q.shape[0] == S and heads <= q.shape[1], "q shape does not match indptr / qlen / heads")
-    _need(kv.dim() == 2 and kv.shape[1] == D_QK and kv.is_contiguous(), "kv must be contiguous [pool, 576]")
-    _need(pages.dtype == torch.int32 and indptr.dtype == torch.int32 and pages.is_contiguous()
-          and indptr.is_contiguous(), "pages / indptr must be contiguous int32")
-    _need(lse.dtype == torch.float32 and lse.shape == (S, heads) and lse.is_contiguous(),
-          "lse must be contiguous f32 [S, heads]")
-    dev = q.device
-    _same_device(dev, kv=kv, pages=pages, indptr=indptr, lse=lse, weights=weights, out=out, workspace=workspace)
-    n = pages.numel()
+    qtype = q.dtype
+    q8 = qtype == _E4M3 or qtype == _U8
+    if not (q8 or qtype == _BF16) or q.dim() != 3 or q.shape[2] != D_QK:
+        raise ValueError("q must be bf16 or fp8 e4m3 [S, H, 576]")
+    dev = q.get_device()
+    S, hpad, _ = q.shape
+    if heads is None:
+        heads = hpad
+    R, n = indptr.numel() - 1, pages.numel()
+    if q.stride(2) != 1 or (hpad > 1 and q.stride(1) != D_QK):
+        raise ValueError("q rows must have contiguous [H, 576] heads")
+    if S != R * qlen or heads > hpad:
+        raise ValueError("q shape does not match indptr / qlen / heads")
+    if kv.dtype != _U8 and kv.dtype != _E4M3:
+        raise ValueError("kv must be uint8 codes or float8_e4m3fn")
+    pool = kv.shape[0]
+    _dense(kv, "kv", kv.dtype, (pool, D_QK), dev)
+    _dense(pages, "pages", _I32, (n,), dev)
+    _dense(indptr, "indptr", _I32, (R + 1,), dev)
+    _dense(lse, "lse", _F32, (S, heads), dev)
+    wp = None
     if weights is not None:
-        _buffer(weights, "weights", torch.float32, (n,))
+        _dense(weights, "weights", _F32, (n,), dev)
+        wp = weights.data_ptr()
     if out is None:
-        out = _empty((n,), torch.float32, dev, stream)
+        out = _empty((n,), _F32, q.device, stream)
     else:
-        _buffer(out, "out", torch.float32, (n,))
+        _dense(out, "out", _F32, (n,), dev)
+    wsp, wsn = None, 0
     if workspace is None:
         need = token_weights_workspace(qlen, heads, n, q8)
         if need:
-            workspace = _empty((need,), torch.uint8, dev, stream)
-    else:
-        _need(workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous(),
-              "workspace must be contiguous uint8")
+            workspace = _empty((need,), _U8, q.device, stream)
+    if workspace is not None:
+        wsp, wsn = workspace.data_ptr(), workspace.numel()
+        _dense(workspace, "workspace", _U8, (wsn,), dev)
     _launch(library().mla_token_weights, "mla_token_weights", dev, stream, q.data_ptr(),
-            q.stride(0) if S > 1 else heads * D_QK, kv.data_ptr(), kv.shape[0], pages.data_ptr(), n,
-            indptr.data_ptr(), R, qlen, heads, scale, kv_scale, q_scale, lse.data_ptr(),
-            0.0 if weights is None else decay, None if weights is None else weights.data_ptr(), out.data_ptr(),
-            (ATTEND_CAUSAL if causal else 0) | (ATTEND_Q_FP8 if q8 else 0),
-            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+            q.stride(0) if S > 1 else heads * D_QK, kv.data_ptr(), pool, pages.data_ptr(), n, indptr.data_ptr(), R,
+            qlen, heads, scale, kv_scale, q_scale, lse.data_ptr(), 0.0 if wp is None else decay, wp, out.data_ptr(),
+            (ATTEND_CAUSAL if causal else 0) | (ATTEND_Q_FP8 if q8 else 0), wsp, wsn)
     return out
 
 
@@ -615,7 +644,7 @@ def token_weights_workspace(qlen, heads, num_pages, fp8_query=False):
     n = library().mla_token_weights_workspace(qlen, heads, num_pages, ATTEND_Q_FP8 if fp8_query else 0)
     if n < 0:
         _check(int(n), "mla_token_weights_workspace")
-    return int(n)
+    return n
 
 
 def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=None, indptr_out=None, weights_out=None,
@@ -629,35 +658,35 @@ def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=Non
     are), then the freed rows; ``weights_out`` the kept tokens' weights,
     then zeros.  ``budget``: an int, or int32 ``[R]`` on the device.
     """
-    _need(pages.dtype == torch.int32 and indptr.dtype == torch.int32 and pages.dim() == 1 and indptr.dim() == 1
-          and indptr.numel() >= 1 and pages.is_contiguous() and indptr.is_contiguous(),
-          "pages / indptr must be contiguous int32")
-    n, R = pages.numel(), indptr.numel() - 1
-    _buffer(weights, "weights", torch.float32, (n,))
-    budgets = None
+    dev = pages.get_device()
+    device = pages.device
+    n, R1 = pages.numel(), indptr.numel()
+    if R1 < 1:
+        raise ValueError("indptr must have R + 1 entries")
+    _dense(pages, "pages", _I32, (n,), dev)
+    _dense(indptr, "indptr", _I32, (R1,), dev)
+    _dense(weights, "weights", _F32, (n,), dev)
+    bp = None
     if isinstance(budget, torch.Tensor):
-        _buffer(budget, "budget", torch.int32, (R,))
-        budgets, budget = budget, 0
-    dev = pages.device
-    _same_device(dev, indptr=indptr, weights=weights, budget=budgets, pages_out=pages_out, indptr_out=indptr_out,
-                 weights_out=weights_out)
+        _dense(budget, "budget", _I32, (R1 - 1,), dev)
+        bp, budget = budget.data_ptr(), 0
     if pages_out is None:
-        pages_out = _empty((n,), torch.int32, dev, stream)
+        pages_out = _empty((n,), _I32, device, stream)
     else:
-        _buffer(pages_out, "pages_out", torch.int32, (n,))
+        _dense(pages_out, "pages_out", _I32, (n,), dev)
     if indptr_out is None:
-        indptr_out = _empty((R + 1,), torch.int32, dev, stream)
+        indptr_out = _empty((R1,), _I32, device, stream)
     else:
-        _buffer(indptr_out, "indptr_out", torch.int32, (R + 1,))
+        _dense(indptr_out, "indptr_out", _I32, (R1,), dev)
     if weights_out is None:
-        weights_out = _empty((n,), torch.float32, dev, stream)
+        weights_out = _empty((n,), _F32, device, stream)
     else:
-        _buffer(weights_out, "weights_out", torch.float32, (n,))
-    _need(-2**31 <= budget < 2**31 and 0 <= recent < 2**31 and 0 <= sinks < 2**31,
-          "budget, recent, sinks must fit int32, recent and sinks >= 0")
-    _launch(library().mla_kv_evict, "mla_kv_evict", dev, stream, pages.data_ptr(), n, indptr.data_ptr(), R,
-            weights.data_ptr(), None if budgets is None else budgets.data_ptr(), budget, recent, sinks,
-            pages_out.data_ptr(), indptr_out.data_ptr(), weights_out.data_ptr())
+        _dense(weights_out, "weights_out", _F32, (n,), dev)
+    if not (-2**31 <= budget < 2**31 and 0 <= recent < 2**31 and 0 <= sinks < 2**31):
+        raise ValueError("budget, recent, sinks must fit int32, recent and sinks >= 0")
+    _launch(library().mla_kv_evict, "mla_kv_evict", dev, stream, pages.data_ptr(), n, indptr.data_ptr(), R1 - 1,
+            weights.data_ptr(), bp, budget, recent, sinks, pages_out.data_ptr(), indptr_out.data_ptr(),
+            weights_out.data_ptr())
     return pages_out, indptr_out, weights_out
 
 
@@ -673,40 +702,33 @@ def value_gate_lora(latent, w_uv, gate, lengths, lora_a, lora_b, adapters, lora_
     16-byte aligned (allocated if not given; not shared by calls that may
     overlap).
     """
-    _need(latent.dtype == torch.bfloat16 and latent.dim() == 3 and latent.shape[2] == D_LATENT
-          and latent.is_contiguous(), "latent must be contiguous bf16 [S, heads, 512]")
-    S, H = latent.shape[:2]
+    if latent.dim() != 3 or lora_a.dim() != 3:
+        raise ValueError("latent must be [S, heads, 512], lora_a [n, rank, 512]")
+    dev = latent.get_device()
+    S, H, _ = latent.shape
+    n, rank, _ = lora_a.shape
     R = lengths.numel()
-    _need(w_uv.dtype == torch.bfloat16 and w_uv.shape == (H, D_V, D_LATENT) and w_uv.is_contiguous(),
-          "w_uv must be contiguous bf16 [heads, 128, 512]")
-    _need(gate.dtype == torch.bfloat16 and gate.shape == (S, H * D_V) and gate.is_contiguous(),
-          "gate must be contiguous bf16 [S, heads*128]")
-    _need(lengths.dtype == torch.int32 and R * qlen == S and lengths.is_contiguous(),
-          "lengths must be contiguous int32 [S / qlen]")
-    _need(lora_a.dtype == torch.bfloat16 and lora_a.dim() == 3 and lora_a.shape[2] == D_LATENT
-          and lora_a.is_contiguous(), "lora_a must be contiguous bf16 [n, rank, 512]")
-    n, rank = lora_a.shape[:2]
-    _need(lora_b.dtype == torch.bfloat16 and lora_b.shape == (n, H * D_V, rank) and lora_b.is_contiguous(),
-          "lora_b must be contiguous bf16 [n, heads*128, rank]")
-    _need(adapters.dtype == torch.int32 and adapters.shape == (R,) and adapters.is_contiguous(),
-          "adapters must be contiguous int32 [R]")
-    _need(lora_scale.dtype == torch.float32 and lora_scale.shape == (n,) and lora_scale.is_contiguous(),
-          "lora_scale must be contiguous f32 [n]")
-    dev = latent.device
-    _same_device(dev, w_uv=w_uv, gate=gate, lengths=lengths, lora_a=lora_a, lora_b=lora_b, adapters=adapters,
-                 lora_scale=lora_scale, out=out, workspace=workspace)
+    if R * qlen != S:
+        raise ValueError("lengths must be [S / qlen]")
+    _dense(latent, "latent", _BF16, (S, H, D_LATENT), dev)
+    _dense(w_uv, "w_uv", _BF16, (H, D_V, D_LATENT), dev)
+    _dense(gate, "gate", _BF16, (S, H * D_V), dev)
+    _dense(lengths, "lengths", _I32, (R,), dev)
+    _dense(lora_a, "lora_a", _BF16, (n, rank, D_LATENT), dev)
+    _dense(lora_b, "lora_b", _BF16, (n, H * D_V, rank), dev)
+    _dense(adapters, "adapters", _I32, (R,), dev)
+    _dense(lora_scale, "lora_scale", _F32, (n,), dev)
     if out is None:
-        out = _empty((S, H * D_V), torch.bfloat16, dev, stream)
+        out = _empty((S, H * D_V), _BF16, latent.device, stream)
     else:
-        _buffer(out, "out", torch.bfloat16, (S, H * D_V))
+        _dense(out, "out", _BF16, (S, H * D_V), dev)
     if workspace is None:
-        workspace = _empty((value_gate_lora_workspace(R, qlen, H, rank),), torch.uint8, dev, stream)
-    else:
-        _need(workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous(),
-              "workspace must be contiguous uint8")
+        workspace = _empty((value_gate_lora_workspace(R, qlen, H, rank),), _U8, latent.device, stream)
+    wsn = workspace.numel()
+    _dense(workspace, "workspace", _U8, (wsn,), dev)
     _launch(library().mla_value_gate_lora, "mla_value_gate_lora", dev, stream, latent.data_ptr(), w_uv.data_ptr(),
             gate.data_ptr(), lengths.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
-            lora_scale.data_ptr(), n, rank, R, qlen, H, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+            lora_scale.data_ptr(), n, rank, R, qlen, H, out.data_ptr(), workspace.data_ptr(), wsn)
     return out
 
 
@@ -715,7 +737,7 @@ def value_gate_lora_workspace(requests, qlen, heads, rank):
     n = library().mla_value_gate_lora_workspace(requests, qlen, heads, rank)
     if n < 0:
         _check(int(n), "mla_value_gate_lora_workspace")
-    return int(n)
+    return n
 
 
 def debug_wait_timeout(stream=None):

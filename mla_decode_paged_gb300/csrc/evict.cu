@@ -9,8 +9,8 @@
 // Bound by the 16 bytes a token that are read and written for many long
 // requests, by the chain of dependent steps for one.
 //
-// Design: a cluster of CS blocks per request, each with a contiguous slice
-// of its tokens and every warp with a contiguous part of that, whose keys
+// Design: a cluster of blocks per request, as many of them as it takes to
+// hold it (the others end at once), each with a contiguous slice of its tokens and every warp with a contiguous part of that, whose keys
 // (order-preserving 32-bit images of the weights) stay in registers: 16 a
 // thread, 8,192 tokens a block.  A longer slice is taken in rounds of that
 // size, read again for every step.  The m-th largest key is found by radix
@@ -21,7 +21,7 @@
 // a histogram per digit: none is reused).  What each warp keeps is counted
 // by ballots, the offsets of warps and blocks are exchanged once, and the
 // tokens are placed by the ballots again.
-#include <algorithm>
+#include <atomic>
 
 #include <cuda_runtime.h>
 
@@ -74,34 +74,28 @@ struct __align__(16) Shared {
     uint32_t pick[3];
 };
 
-template <int CS>
 __device__ __forceinline__ uint32_t block_rank() {
-    if (CS == 1) return 0;
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
 
-// All blocks of the cluster, their shared-memory writes before it visible after it.
-template <int CS>
-__device__ __forceinline__ void cluster_sync() {
-    if (CS == 1) __syncthreads();
+// All running blocks of the cluster (one block: itself), their shared-memory
+// writes before it visible after it.
+__device__ __forceinline__ void cluster_sync(bool one) {
+    if (one) __syncthreads();
     else
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // What is at `p`'s place in the shared memory of block `rank`.
-template <int CS>
 __device__ __forceinline__ uint32_t remote(const uint32_t *p, uint32_t rank) {
-    if (CS == 1) return *p;
     uint32_t addr, v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-template <int CS>
 __device__ __forceinline__ uint4 remote4(const uint32_t *p, uint32_t rank) {
-    if (CS == 1) return *reinterpret_cast<const uint4 *>(p);
     uint32_t addr;
     uint4 v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
@@ -134,22 +128,30 @@ __device__ uint32_t block_scan(uint32_t v, uint32_t *red) {
     return x - v + __shfl_sync(0xffffffffu, s - w, warp);
 }
 
-template <int CS>
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
-    const int r = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = block_rank<CS>();
+// 2^log_cs blocks (a cluster) per request.
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, int log_cs) {
+    __shared__ Shared sh;
+    const int r = blockIdx.x >> log_cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = block_rank();
+    int base;
+    const int len = request_len(a.indptr, r, a.num_pages, &base);
+    // The blocks it takes to hold the request, 2^le of them; the others end
+    // (a cluster barrier waits for running threads only).
+    int le = 0;
+    while (le < log_cs && (len >> le) > kRound) ++le;
+    const uint32_t E = 1u << le;
+    if (rank >= E) return;
+    const bool one = le == 0;
 
     // Kept and all tokens of the requests before this one, kept of all.
     long long sums[3] = {0, 0, 0};
     for (int i = tid; i < a.R; i += kThreads) {
-        int base;
-        const int len = request_len(a.indptr, i, a.num_pages, &base), k = kept_tokens(a, i, len);
+        int at;
+        const int n = request_len(a.indptr, i, a.num_pages, &at), k = kept_tokens(a, i, n);
         sums[2] += k;
         if (i < r) {
             sums[0] += k;
-            sums[1] += len;
+            sums[1] += n;
         }
     }
     for (int i = tid; i < kDigits * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
@@ -166,8 +168,6 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], d);
     }
-    int base;
-    const int len = request_len(a.indptr, r, a.num_pages, &base);
     const int kept = kept_tokens(a, r, len);
     if (tid == 0 && rank == 0) {
         if (r == 0) a.indptr_out[0] = 0;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
 
     // This block's slice, in rounds; a warp's part of a round, whole groups of
     // 32 tokens.
-    const int slice = ((len + CS - 1) / CS + 31) / 32 * 32;
+    const int slice = (((len + (int)E - 1) >> le) + 31) / 32 * 32;
     const int s0 = (int)min((int64_t)slice * rank, (int64_t)len), s1 = min(slice, len - s0) + s0;
     const int rounds = (s1 - s0 + kRound - 1) / kRound;
     uint32_t key[kSteps];
@@ -228,27 +228,26 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
                     if (j < steps && (free >> j & 1) && (digit == 0 || (key[j] ^ T) >> above_bits == 0))
                         atomicAdd(&hist[(key[j] >> shift) & (bins - 1)], 1u);
             }
-            cluster_sync<CS>();
+            cluster_sync(one);
             // Bins from the top: thread t holds the kOwn from kBins - 1 - kOwn * t down, summed over the cluster.
             const uint32_t top = kBins - 1 - kOwn * tid;
             uint32_t n[kOwn], sum = 0;
             uint4 v;
-            if (CS == 1) {
+            if (one) {
                 v = *reinterpret_cast<const uint4 *>(hist + top - (kOwn - 1));
             } else {
-                constexpr int kShare = kBins / CS;
-                const uint32_t c = (tid / (kShare / 4) + rank) % CS, at = tid % (kShare / 4) * 4;
-                *reinterpret_cast<uint4 *>(sh.stage + c * kShare + at) = remote4<CS>(hist + rank * kShare + at, c);
+                const int share = kBins >> le, log_share = 11 - le;     // a block's bins
+                const uint32_t c = ((tid >> (log_share - 2)) + rank) & (E - 1), at = (tid & (share / 4 - 1)) * 4;
+                *reinterpret_cast<uint4 *>(sh.stage + c * share + at) = remote4(hist + rank * share + at, c);
                 __syncthreads();
-                for (int i = tid; i < kShare; i += kThreads) {
+                for (int i = tid; i < share; i += kThreads) {
                     uint32_t s = 0;
-#pragma unroll
-                    for (int j = 0; j < CS; ++j) s += sh.stage[j * kShare + i];
+                    for (uint32_t j = 0; j < E; ++j) s += sh.stage[j * share + i];
                     sh.sums[digit][i] = s;
                 }
-                cluster_sync<CS>();
+                cluster_sync(false);
                 const uint32_t low = top - (kOwn - 1);
-                v = remote4<CS>(sh.sums[digit] + low % kShare, low / kShare);
+                v = remote4(sh.sums[digit] + (low & (share - 1)), low >> log_share);
             }
             n[0] = v.w;
             n[1] = v.z;
@@ -320,15 +319,15 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
     }
     exchange(nsure, nties, k, t, kb, tb);
     uint32_t block_kept = 0, block_ties = 0;        // sure tokens and ties of the blocks before this one
-    if (CS > 1) {
+    if (!one) {
         if (tid == 0) {
             sh.totals[0] = k;
             sh.totals[1] = t;
         }
-        cluster_sync<CS>();
+        cluster_sync(false);
         if (lane < rank) {
-            block_kept = remote<CS>(&sh.totals[0], lane);
-            block_ties = remote<CS>(&sh.totals[1], lane);
+            block_kept = remote(&sh.totals[0], lane);
+            block_ties = remote(&sh.totals[1], lane);
         }
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) {
@@ -389,28 +388,33 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
             }
         }
     }
-    if (CS > 1) cluster_sync<CS>();                 // no block ends while another may read its shared memory
+    if (!one) cluster_sync(false);                  // no block ends while another may read its shared memory
 }
 
-template <int CS>
-cudaError_t launch(const EvictArgs &a, cudaStream_t st) {
-    cudaError_t e = smem_attr_once<evict_kernel<CS>>((int)sizeof(Shared));
-    if (e != cudaSuccess) return e;
-    if (CS > 8 && (e = cudaFuncSetAttribute(evict_kernel<CS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
-                      cudaSuccess)
-        return e;
+cudaError_t launch(const EvictArgs &a, int log_cs, cudaStream_t st) {
+    static std::atomic<unsigned long long> wide{0};     // devices where clusters of 16 have been allowed
+    if (log_cs > 3) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+        if (!(bit & wide.load(std::memory_order_acquire))) {
+            e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            wide.fetch_or(bit, std::memory_order_release);
+        }
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.R * CS, 1, 1);
+    cfg.gridDim = dim3((unsigned)a.R << log_cs, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CS;
+    attr[0].val.clusterDim.x = 1u << log_cs;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CS > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, evict_kernel<CS>, a);
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_kernel, a, log_cs);
 }
 
 }  // namespace
@@ -432,16 +436,12 @@ cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32
     a.pages_out = pages_out;
     a.indptr_out = indptr_out;
     a.weights_out = weights_out;
-    // The lengths are on the device; the mean length says how many blocks a
-    // request is worth (2,048 tokens each), the batch how many fit at once.
-    const int64_t mean = num_pages / R;
-    const int64_t room = 8 * (int64_t)sms / R;
-    const int64_t want = std::min(std::max<int64_t>(mean / 2048, 1), std::max<int64_t>(room, 1));
-    if (want >= 16) return launch<16>(a, st);
-    if (want >= 8) return launch<8>(a, st);
-    if (want >= 4) return launch<4>(a, st);
-    if (want >= 2) return launch<2>(a, st);
-    return launch<1>(a, st);
+    // The lengths are on the device: a cluster is made for the longest that
+    // the page list could hold, as far as the batch leaves room.
+    const int most = R <= 2 * sms ? 4 : R <= 16 * sms ? 3 : R <= 64 * sms ? 2 : 1;
+    int log_cs = 0;
+    while (log_cs < most && (num_pages >> log_cs) > kRound) ++log_cs;
+    return launch(a, log_cs, st);
 }
 
 cudaError_t evict_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }
