@@ -15,10 +15,10 @@
 // thread, 8,192 tokens a block.  A longer slice is taken in rounds of that
 // size, read again for every step.  The m-th largest key is found by radix
 // selection, 11 + 11 + 10 bits: every block counts its slice into a shared
-// histogram, sums one CS-th of the bins over the cluster through distributed
-// shared memory, and reads the others' sums (reading all CS histograms in
-// every block instead took 11,500 cycles a digit with 16 blocks, this 3,000;
-// a histogram per digit: none is reused).  What each warp keeps is counted
+// histogram, sums its share of the bins over the cluster through distributed
+// shared memory, and reads the others' sums (reading all histograms in every
+// block instead took 11,500 cycles a digit with 16 blocks, this 3,000; a
+// histogram per digit: none is reused).  What each warp keeps is counted
 // by ballots, the offsets of warps and blocks are exchanged once, and the
 // tokens are placed by the ballots again.
 #include <atomic>
@@ -65,8 +65,8 @@ __device__ __forceinline__ int kept_tokens(const EvictArgs &a, int r, int len) {
 
 struct __align__(16) Shared {
     uint32_t hist[kDigits][kBins];
-    uint32_t stage[kBins];          // one CS-th of the bins from every block
-    uint32_t sums[kDigits][kBins];  // and their sums (the first kBins / CS)
+    uint32_t stage[kBins];          // this block's share of the bins from every block
+    uint32_t sums[kDigits][kBins];  // and their sums
     long long red64[3][kWarps];
     uint32_t scan[kWarps];
     uint32_t warp_kept[kWarps], warp_ties[kWarps];
@@ -436,11 +436,14 @@ cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32
     a.pages_out = pages_out;
     a.indptr_out = indptr_out;
     a.weights_out = weights_out;
-    // The lengths are on the device: a cluster is made for the longest that
-    // the page list could hold, as far as the batch leaves room.
-    const int most = R <= 2 * sms ? 4 : R <= 16 * sms ? 3 : R <= 64 * sms ? 2 : 1;
+    // The lengths are on the device.  A cluster holds a request of twice the
+    // mean length in one round; more blocks than that mostly end unused, and
+    // each costs its launch (64 requests of 1K to 8K tokens: 10.8 us with 1
+    // or 2 blocks, 15 with 4 or 8, 25 with 16; one of 128K: 157 us with 1,
+    // 49 with 4, 30 with 8, 16 with 16).
+    const int64_t want = 2 * (num_pages / R);
     int log_cs = 0;
-    while (log_cs < most && (num_pages >> log_cs) > kRound) ++log_cs;
+    while (log_cs < 4 && (want >> log_cs) > kRound) ++log_cs;
     return launch(a, log_cs, st);
 }
 

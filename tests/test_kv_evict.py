@@ -132,6 +132,12 @@ def _rand(n, seed):
     ([40000], 1, 0, 0),
     ([70001, 3, 131072], 8192, 512, 4),
     ([300000], 1000, 100, 4),
+    ([8192, 8193, 8191, 0, 16385, 9000], 4000, 100, 4),
+    ([9000] * 12 + [100] * 300 + [50000, 20000], 4096, 64, 2),      # long requests with a part to select and without
+    ([9000] * 30, 9000, 0, 0),
+    ([9000, 40000], 0, 0, 0),
+    ([1500000, 10, 700000], 300000, 1000, 4),                       # several rounds a block
+    ([100] * 900 + [100000], 50, 5, 1),                             # one long request among many short
     ([7] * 700, 3, 1, 1),
     ([2500] * 40, 333, 10, 0),
 ])
@@ -193,6 +199,22 @@ def test_bad_indptr_is_flagged_and_stays_in_bounds():
         torch.cuda.synchronize()
         assert mla.device_status() == mla.DEV_BAD_INDPTR
         assert (guard[n:] == -7).all() and (wg[n:] == -7).all()
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams():
+    lengths = [30000, 9000, 12]
+    total = sum(lengths)
+    pages = torch.randperm(total, device=DEV).to(torch.int32)
+    indptr = torch.tensor([0, 30000, 39000, 39012], dtype=torch.int32, device=DEV)
+    w = torch.rand(total, device=DEV)
+    want = mla.kv_evict(pages, indptr, w, 1000)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [mla.kv_evict(pages, indptr, w, 1000, stream=s) for s in (side, None, side, None)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+    assert mla.device_status() == 0
 
 
 @pytest.mark.gpu
