@@ -14,6 +14,10 @@
 // maximum) is joined by shuffles and, where more than one warp holds the
 // row, through shared memory.  128 columns are 16 consecutive vectors, so a
 // group's maximum stays inside a half warp (T is a multiple of 16).
+//
+// Batches of many wide rows run a persistent form of the same: a block's next
+// rows arrive by bulk copies in a ring in shared memory while it works on
+// one, and its weights stay in registers.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -250,11 +254,210 @@ __global__ void __launch_bounds__(ONE_WARP ? 256 : 1024) norm_kernel(const NormA
     }
 }
 
+// ------------------------------------------------- many rows: a ring of rows
+
+constexpr int kMaxRing = 4;
+constexpr int kRingBytes = 110 * 1024;      // of shared memory, two blocks an SM
+
+struct RingArgs {
+    NormArgs n;
+    int x_bytes, row_bytes;     // of a row of x; of x and the residual
+    int depth;                  // rows in the ring
+};
+
+// blockDim.x threads hold a row, VPT vectors each, weights included; RES:
+// the residual's element size (0: none).
+template <typename T, int VPT, int RES>
+__global__ void __launch_bounds__(512, 2) norm_ring_kernel(const RingArgs ra) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float red[2][2][32];
+    __shared__ __align__(8) uint64_t full[kMaxRing];
+    const NormArgs &a = ra.n;
+    const int threads = blockDim.x, tid = threadIdx.x, warps = threads >> 5, lane = tid & 31, warp = tid >> 5;
+    const int64_t step = gridDim.x;
+    const int depth = ra.depth;
+    if (tid == 0) {
+        for (int s = 0; s < depth; ++s) mbar_init(&full[s], 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
+    const auto fetch = [&](int64_t row, int s) {
+        uint8_t *dst = ring + s * ra.row_bytes;
+        mbar_arrive_expect_tx(&full[s], ra.row_bytes);
+        bulk_g2s(dst, static_cast<const T *>(a.x) + row * a.x_stride, ra.x_bytes, &full[s]);
+        if (RES)
+            bulk_g2s(dst + ra.x_bytes, static_cast<const uint8_t *>(a.residual) + row * a.residual_stride * RES,
+                     ra.row_bytes - ra.x_bytes, &full[s]);
+    };
+    if (tid == 0)
+        for (int s = 0; s < depth; ++s)
+            if (blockIdx.x + s * step < a.rows) fetch(blockIdx.x + s * step, s);
+    uint4 w[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int v = tid + k * threads;
+        w[k] = v < a.vecs ? __ldg(static_cast<const uint4 *>(a.weight) + v) : make_uint4(0, 0, 0, 0);
+    }
+    int it = 0, s = 0, phase = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += step, ++it) {
+        const int buf = it & 1;
+        const bool ok = mbar_wait(&full[s], phase);
+        const uint4 *xs = reinterpret_cast<const uint4 *>(ring + s * ra.row_bytes);
+        const uint4 *rs = reinterpret_cast<const uint4 *>(ring + s * ra.row_bytes + ra.x_bytes);
+        float y[VPT][8], ssq = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * threads;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[k][i] = 0.f;
+            if (v < a.vecs) {
+                unpack8<T>(xs[v], y[k]);
+                if (RES == 4) {
+                    const uint4 r0 = rs[2 * v], r1 = rs[2 * v + 1];
+                    const uint32_t r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[k][i] += __uint_as_float(r[i]);
+                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.residual_out) +
+                                                           row * a.residual_out_stride) + 2 * v;
+                    o[0] = make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
+                    o[1] = make_float4(y[k][4], y[k][5], y[k][6], y[k][7]);
+                } else if (RES == 2) {
+                    float r[8];
+                    unpack8<T>(rs[v], r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[k][i] += r[i];
+                    reinterpret_cast<uint4 *>(static_cast<T *>(a.residual_out) + row * a.residual_out_stride)[v] =
+                        pack8<T>(y[k]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ssq = fmaf(y[k][i], y[k][i], ssq);
+            }
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, d);
+        if (lane == 0) red[buf][0][warp] = ssq;
+        if (!__syncthreads_and(ok)) {
+            // Flagged.  The rows in flight land before the block ends.
+            if (tid == 0)
+                for (int k = 0; k < depth; ++k) {
+                    if (row + k * step < a.rows) mbar_wait(&full[s], phase);
+                    if (++s == depth) s = 0, phase ^= 1;
+                }
+            return;
+        }
+        // The row has been read by all: its place takes the row `depth` further on.
+        if (tid == 0 && row + depth * step < a.rows) fetch(row + depth * step, s);
+        if (++s == depth) s = 0, phase ^= 1;
+        ssq = lane < warps ? red[buf][0][lane] : 0.f;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, d);
+        float rstd = rsqrtf(fmaf(ssq, a.inv_width, a.eps));
+        if (ssq == INFINITY) {      // as in norm_kernel
+            ssq = 0.f;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[k][i] *= 0x1p-80f;
+                    ssq = fmaf(y[k][i], y[k][i], ssq);
+                }
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, d);
+            __syncthreads();
+            if (lane == 0) red[buf][0][warp] = ssq;
+            __syncthreads();
+            ssq = lane < warps ? red[buf][0][lane] : 0.f;
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, d);
+            rstd = rsqrtf(ssq * a.inv_width);
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * threads;
+            if (v < a.vecs) {
+                float wt[8];
+                unpack8<T>(w[k], wt);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[k][i] = y[k][i] * rstd * wt[i];
+                    amax = max_nan(amax, fabsf(y[k][i]));
+                }
+            }
+            if (a.quant == MLA_QUANT_NONE) {
+                if (v < a.vecs)
+                    reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * a.out_stride)[v] = pack8<T>(y[k]);
+            } else if (a.quant == MLA_QUANT_GROUP) {
+#pragma unroll
+                for (int d = 8; d >= 1; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                if (v < a.vecs) {
+                    const float sc = block_scale(amax);
+                    if ((v & 15) == 0) a.scales[row * a.groups + (v >> 4)] = sc;
+                    reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.out_stride)[v] =
+                        pack8_e4m3(y[k], __fdiv_rn(1.f, sc));
+                }
+                amax = 0.f;
+            }
+        }
+        if (a.quant == MLA_QUANT_ROW || a.quant == MLA_QUANT_STATIC) {
+            float inv = a.inv_scale;
+            if (a.quant == MLA_QUANT_ROW) {
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                if (lane == 0) red[buf][1][warp] = amax;
+                __syncthreads();
+                amax = lane < warps ? red[buf][1][lane] : 0.f;
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                const float sc = block_scale(amax);
+                if (tid == 0) a.scales[row] = sc;
+                inv = __fdiv_rn(1.f, sc);
+            }
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = tid + k * threads;
+                if (v < a.vecs)
+                    reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.out_stride)[v] =
+                        pack8_e4m3(y[k], inv);
+            }
+        }
+    }
+}
+
+template <typename T, int VPT, int RES>
+cudaError_t launch_ring(const RingArgs &ra, int sms, cudaStream_t st) {
+    const int smem = ra.depth * ra.row_bytes;
+    cudaError_t e = smem_attr_once<norm_ring_kernel<T, VPT, RES>>(kRingBytes);
+    if (e != cudaSuccess) return e;
+    const int threads = ((ra.n.vecs + VPT - 1) / VPT + 31) / 32 * 32;
+    norm_ring_kernel<T, VPT, RES><<<2 * sms, threads, smem, st>>>(ra);
+    return cudaGetLastError();
+}
+
+template <typename T, int VPT>
+cudaError_t launch_ring_res(const RingArgs &ra, int sms, cudaStream_t st) {
+    switch (ra.n.residual_type) {
+        case -1: return launch_ring<T, VPT, 0>(ra, sms, st);
+        case MLA_TYPE_F32: return launch_ring<T, VPT, 4>(ra, sms, st);
+        default: return launch_ring<T, VPT, 2>(ra, sms, st);
+    }
+}
+
 template <typename T>
 cudaError_t launch(const NormArgs &a, int sms, cudaStream_t st) {
     // Up to 256 columns a warp holds a row in one vector a lane, up to 1,024
     // in two or four; wider rows take a block of up to 1,024 threads.
     const int64_t cap = (int64_t)sms * 64;
+    RingArgs ra;
+    ra.n = a;
+    ra.x_bytes = a.vecs * 16;
+    ra.row_bytes = ra.x_bytes * (a.residual_type < 0 ? 1 : a.residual_type == MLA_TYPE_F32 ? 3 : 2);
+    ra.depth = kRingBytes / ra.row_bytes < kMaxRing ? kRingBytes / ra.row_bytes : kMaxRing;
+    if (a.vecs > 128 && a.rows >= 8 * (int64_t)sms && ra.depth >= 2) {
+        if (a.vecs <= 512) return launch_ring_res<T, 1>(ra, sms, st);
+        if (a.vecs <= 1024) return launch_ring_res<T, 2>(ra, sms, st);
+        return launch_ring_res<T, 4>(ra, sms, st);
+    }
     if (a.vecs <= 128) {
         const int vpt = a.vecs <= 32 ? 1 : a.vecs <= 64 ? 2 : 4;
         const dim3 block(32, 4);

@@ -254,3 +254,44 @@ def test_uint8_codes_no_rows_own_stream_and_graph():
     again, asc, aro = mla.add_rms_norm(x, w, EPS, r, quant="group")
     assert torch.equal(gout.view(torch.uint8), again.view(torch.uint8)) and torch.equal(gsc, asc)
     assert torch.equal(gro, aro)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [None, "row", "group", "static"])
+@pytest.mark.parametrize("T,D,xt,rt,pad", [
+    (1300, 1032, torch.bfloat16, torch.bfloat16, 0),
+    (1217, 4096, torch.float16, None, 8),
+    (2500, 7168, torch.bfloat16, torch.bfloat16, 0),
+    (1300, 7168, torch.bfloat16, torch.float32, 8),
+    (1300, 8200, torch.bfloat16, torch.bfloat16, 0),
+    (1250, 16384, torch.float16, None, 0),
+])
+def test_many_wide_rows(T, D, xt, rt, pad, quant):
+    x, w, r = _inputs(T, D, xt, rt, T + D, pad, pad)
+    x[5] = 0
+    x[6] *= 2.0**15 if xt == torch.float16 else 2.0**90
+    x[7, 3] = float("nan")
+    x[8, D - 1] = float("inf")
+    if r is not None:
+        r[5] = 0
+    _, y = _formula(x, w, r)
+    out, scales, ro = mla.add_rms_norm(x, w, EPS, r, quant=quant, scale=0.013 if quant == "static" else None)
+    fine = torch.arange(T, device=DEV)
+    fine = fine[(fine != 7) & (fine != 8) & x.isfinite().all(1)]
+    if quant is None:
+        _check16(out[fine], y[fine], "out")
+        assert out[7].isnan().all() and out[8, D - 1].isnan() and (out[8, :D - 1] == 0).all()
+    else:
+        _check8(out[fine], None if scales is None else scales[fine], y[fine], quant, 0.013)
+        assert out[7].float().isnan().all() and out[8, D - 1].float().isnan()
+        if scales is not None:
+            assert scales.view(T, -1)[7].isnan().all() and scales.view(T, -1)[8, -1].isnan()
+    if r is not None:
+        small = mla.add_rms_norm(x[:64], w, EPS, r[:64])[2]
+        assert torch.equal(ro[:64].view(torch.int16 if rt != torch.float32 else torch.int32),
+                           small.view(torch.int16 if rt != torch.float32 else torch.int32))
+        keep = r.clone()
+        again = mla.add_rms_norm(x, w, EPS, keep, quant=quant, scale=0.013 if quant == "static" else None,
+                                 residual_out=keep)
+        assert torch.equal(again[0].view(torch.uint8), out.view(torch.uint8))
+        assert torch.equal(keep.view(torch.uint8), ro.contiguous().view(torch.uint8))
