@@ -10,19 +10,24 @@
 // Bound by bytes: the latent (1 KB a row and head), W_UV (128 KB a head), A
 // and B of every adapter in use; at a few rows by the two launches.
 //
-//   shrink: one block per request and tile of its (row, head) pairs, which
-//     share A: T = latent A^T * lora_scale by warp MMAs on fragments loaded
-//     straight from global memory (a lane's 16 bytes are two k-steps' worth:
-//     the products' order over k is free).  Eight warps take 64 latent
-//     columns each and are joined in shared memory.  T goes to the workspace
-//     as two bf16 terms, hi + lo (2^-17 of the product; one term would add
-//     2^-9, as much as the output's own rounding).
-//   project: one block per (rows, head).  W_UV[h] (M = 128 outputs) times the
-//     rows' latents (N) by tcgen05 MMAs on TMA tiles into TMEM, as in the
-//     plain projection; meanwhile the 16 warps form B T by warp MMAs into a
+//   shrink: the (row, head) pairs of a request share A: T = latent A^T *
+//     lora_scale.  Few pairs: warp MMAs on fragments loaded straight from
+//     global memory (a lane's 16 bytes are two k-steps' worth: the products'
+//     order over k is free), eight warps of 64 latent columns each, joined in
+//     shared memory.  Many: tcgen05 MMAs, A (M, its rows past the rank
+//     whatever follows in shared memory: unused lanes) times 96 pairs (N).
+//     T goes to the workspace as two bf16 terms, hi + lo (2^-17 of the
+//     product; one term would add 2^-9, as much as the output's own rounding).
+//   project: a persistent block per head (as many as fit), W_UV[h] (M = 128
+//     outputs) staying in shared memory, over the head's tiles of rows (N):
+//     tcgen05 MMAs into TMEM, the next tile's latents and products in flight
+//     during this one.  Meanwhile the 16 warps form B T by warp MMAs into a
 //     float32 tile, reading B[a, h] once per request of the tile (every
 //     column of a warp MMA is a row of its own, so rows of other requests
-//     need no mask).  The epilogue adds the two and gates.
+//     need no mask), four requests' loads in flight a warp.  The epilogue
+//     adds the two and gates.
+#include <algorithm>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -50,39 +55,45 @@ __device__ __forceinline__ int adapter_of(const LoraArgs &p, int r) {
     return -1;
 }
 
+// T[row][k] as its two terms.
+__device__ __forceinline__ void store_term(const LoraArgs &p, int64_t row, int k, float v) {
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    __nv_bfloat16 *dst = p.t + row * 2 * p.rank + k;
+    dst[0] = hi;
+    // no lo beside an infinite hi (inf - inf)
+    dst[p.rank] = __float2bfloat16_rn(isinf(__bfloat162float(hi)) ? 0.f : v - __bfloat162float(hi));
+}
+
 // ------------------------------------------------------------------ shrink
 
 constexpr int kShrinkWarps = 8;
 constexpr int kNChunk = 8;              // n-tiles (of 8 ranks) whose sums a warp holds at once
 
-// MT tiles of 16 (row, head) pairs per block.
-template <int MT>
+// 16 (row, head) pairs per block.
 __global__ void __launch_bounds__(kShrinkWarps * 32) shrink_kernel(const LoraArgs p, int tiles) {
-    extern __shared__ float part[];     // [warps][16 * MT][kNChunk * 8 + 1]
     constexpr int kCols = kNChunk * 8 + 1;
+    __shared__ float part[kShrinkWarps * 16 * kCols];
     asm volatile("griddepcontrol.launch_dependents;");
     const int r = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int a = adapter_of(p, r);
     if (a < 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int pairs = p.qlen * p.H, m0 = tile * 16 * MT;
+    const int pairs = p.qlen * p.H, m0 = tile * 16;
     const int64_t row0 = (int64_t)r * pairs;
     const float scale = __ldg(p.scale + a);
     const int c0 = warp * 64 + 8 * q;   // this lane's columns: c0 .. c0 + 7 and c0 + 32 ..
-    uint4 x[MT][2][2];                  // [tile][32-column block][row g, g + 8]
+    uint4 x[2][2];                      // [32-column block][row g, g + 8]
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < 2; ++i) {
+        const int row = min(m0 + 8 * i + g, pairs - 1);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.latent + (row0 + row) * MLA_D_LATENT + c0);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = min(m0 + 16 * m + 8 * i + g, pairs - 1);
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.latent + (row0 + row) * MLA_D_LATENT + c0);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) x[m][b][i] = __ldg(src + 4 * b);
-        }
+        for (int b = 0; b < 2; ++b) x[b][i] = __ldg(src + 4 * b);
+    }
     const int ntiles = p.rank / 8;
     for (int n0 = 0; n0 < ntiles; n0 += kNChunk) {
         const int nn = min(kNChunk, ntiles - n0);
-        float acc[MT][kNChunk][4] = {};
+        float acc[kNChunk][4] = {};
         uint4 w[kNChunk][2];
 #pragma unroll
         for (int n = 0; n < kNChunk; ++n)
@@ -96,61 +107,39 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) shrink_kernel(const LoraArg
         for (int n = 0; n < kNChunk; ++n)
             if (n < nn)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const uint4 u = x[m][b][0], v = x[m][b][1], k = w[n][b];
-                        const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
-                        mma_bf16(acc[m][n], a0, k.x, k.y);
-                        mma_bf16(acc[m][n], a1, k.z, k.w);
-                    }
+                for (int b = 0; b < 2; ++b) {
+                    const uint4 u = x[b][0], v = x[b][1], k = w[n][b];
+                    const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+                    mma_bf16(acc[n], a0, k.x, k.y);
+                    mma_bf16(acc[n], a1, k.z, k.w);
+                }
         if (n0 > 0) __syncthreads();
 #pragma unroll
         for (int n = 0; n < kNChunk; ++n)
             if (n < nn)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        part[(warp * 16 * MT + 16 * m + g + 8 * (i >> 1)) * kCols + 8 * n + 2 * q + (i & 1)] =
-                            acc[m][n][i];
+                for (int i = 0; i < 4; ++i)
+                    part[(warp * 16 + g + 8 * (i >> 1)) * kCols + 8 * n + 2 * q + (i & 1)] = acc[n][i];
         __syncthreads();
         const int cols = 8 * nn;
-        for (int e = threadIdx.x; e < 16 * MT * cols; e += kShrinkWarps * 32) {
+        for (int e = threadIdx.x; e < 16 * cols; e += kShrinkWarps * 32) {
             const int row = e / cols, k = e - row * cols;
             if (m0 + row >= pairs) break;
             float s = 0.f;
 #pragma unroll
-            for (int w8 = 0; w8 < kShrinkWarps; ++w8) s += part[(w8 * 16 * MT + row) * kCols + k];
-            s *= scale;
-            const __nv_bfloat16 hi = __float2bfloat16_rn(s);
-            __nv_bfloat16 *dst = p.t + (row0 + m0 + row) * 2 * p.rank + 8 * n0 + k;
-            dst[0] = hi;
-            // no lo beside an infinite hi (inf - inf)
-            dst[p.rank] = __float2bfloat16_rn(isinf(__bfloat162float(hi)) ? 0.f : s - __bfloat162float(hi));
+            for (int w8 = 0; w8 < kShrinkWarps; ++w8) s += part[(w8 * 16 + row) * kCols + k];
+            store_term(p, row0 + m0 + row, 8 * n0 + k, s * scale);
         }
     }
 }
 
-// ------------------------------------------------------------------ project
-
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+// The shape both tcgen05 kernels share.
 constexpr int kColBlocks = MLA_D_LATENT / 64;      // 128-byte column blocks of the K axis
-constexpr int kABlock = MLA_D_V * 128;             // one column block of W_UV[h]: 16 KB
-constexpr int kBOff = kColBlocks * kABlock;
-constexpr int kDStride = MLA_D_V + 4;              // float32 tile rows, a bank apart per row pair
 
-template <int NR>
-struct Tile {
-    static constexpr int kBBlock = NR * 128;
-    static constexpr int kDOff = kBOff + kColBlocks * kBBlock;
-    static constexpr int kSmem = kDOff + NR * kDStride * 4 + 1024;
-    static constexpr uint32_t kTmemCols = NR <= 32 ? 32 : 64;
-    static constexpr int kPairs = NR * (MLA_D_V / 2) / kThreads;     // gate / output words per thread
-    // kind::f16: bf16 A and B (K-major), f32 D, M = 128, N = NR.
-    static constexpr uint32_t kIdesc =
-        (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-};
+// kind::f16: bf16 A and B (K-major), f32 D, M = 128.
+constexpr uint32_t idesc_bf16(int n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
 
 __device__ __forceinline__ void mma_bf16_tc(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                             bool accumulate) {
@@ -158,6 +147,17 @@ __device__ __forceinline__ void mma_bf16_tc(uint32_t d_tmem, uint64_t a, uint64_
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+}
+
+// D = A[128 x 512] B[N x 512]^T, both in 128B-swizzled column blocks.
+__device__ __forceinline__ void mma_latent(uint32_t d_tmem, uint32_t a, uint32_t a_block, uint32_t b, uint32_t b_block,
+                                           uint32_t idesc) {
+#pragma unroll
+    for (int j = 0; j < MLA_D_LATENT / 16; ++j) {
+        const int kb = j >> 2, off = (j & 3) * 32;
+        mma_bf16_tc(d_tmem, tc::sdesc(a + kb * a_block + off, 16, 1024, tc::kSw128),
+                    tc::sdesc(b + kb * b_block + off, 16, 1024, tc::kSw128), idesc, j > 0);
+    }
 }
 
 __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
@@ -175,6 +175,124 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x,
         : "memory");
 }
 
+constexpr int kTcPairs = 96, kTcThreads = 256;
+constexpr int kTcBBlock = kTcPairs * 128;
+
+__host__ __device__ constexpr int shrink_tc_smem(int rank) {
+    return kColBlocks * (rank * 128 + kTcBBlock) + 1024;
+}
+
+// 96 pairs per block: ma maps lora_a as [n * rank, 512], mx the latent as
+// [S * H, 512].
+__global__ void __launch_bounds__(kTcThreads, 1)
+    shrink_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mx, const LoraArgs p,
+                     int tiles) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full, done;
+    __shared__ uint32_t tmem;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int r = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int a = adapter_of(p, r);
+    if (a < 0) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int pairs = p.qlen * p.H, m0 = tile * kTcPairs;
+    const int64_t row0 = (int64_t)r * pairs + m0;
+    const int a_block = p.rank * 128, b_off = kColBlocks * a_block;
+    if (tid == 0) {
+        mbar_init(&full, 1);
+        mbar_init(&done, 1);
+        mbar_fence_init();
+        mbar_arrive_expect_tx(&full, kColBlocks * (a_block + kTcBBlock));
+        for (int kb = 0; kb < kColBlocks; ++kb) {
+            tma_2d(sm + kb * a_block, &ma, 64 * kb, a * p.rank, &full);
+            tma_2d(sm + b_off + kb * kTcBBlock, &mx, 64 * kb, (int)row0, &full);
+        }
+    }
+    if (warp == 0) tc::tmem_alloc(&tmem, 128);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    bool ok = true, issued = false;
+    if (tid == 0) {
+        ok = mbar_wait(&full, 0);
+        if (ok) {
+            issued = true;
+            tc::fence_after();
+            mma_latent(tmem, smem_u32(sm), a_block, smem_u32(sm) + b_off, kTcBBlock, idesc_bf16(kTcPairs));
+            tc::commit(&done);
+        }
+    }
+    ok = __syncthreads_and(ok);
+    if (ok) ok = mbar_wait(&done, 0);
+    ok = __syncthreads_and(ok);
+    if (ok) {
+        tc::fence_after();
+        // Lane = rank index; the block's two warpgroups take half of the pairs each.
+        const int k = 32 * (warp & 3) + lane, c0 = (warp >> 2) * (kTcPairs / 2);
+        const float scale = __ldg(p.scale + a);
+        if (32 * (warp & 3) < p.rank) {
+#pragma unroll
+            for (int c = 0; c < kTcPairs / 2; c += 16) {
+                float d[16];
+                tc::ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c0 + c, d);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (k < p.rank && m0 + c0 + c + i < pairs) store_term(p, row0 + c0 + c + i, k, d[i] * scale);
+            }
+        }
+    } else if (tid == 0) {
+        // Flagged.  What is in flight finishes before TMEM is released.
+        mbar_wait(&full, 0);
+        if (issued) mbar_wait(&done, 0);
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::tmem_free(tmem, 128);
+}
+
+// ------------------------------------------------------------------ project
+
+constexpr int kThreads = 512;                      // and a warp that issues copies and products
+constexpr int kABlock = MLA_D_V * 128;             // one column block of W_UV[h]: 16 KB
+constexpr int kBOff = kColBlocks * kABlock;
+constexpr int kDStride = MLA_D_V + 4;              // float32 tile rows, a bank apart per row pair
+constexpr int kBatch = 2;                          // items a warp expands at once
+
+// NR rows a tile; two tiles' latents.
+template <int NR>
+struct Tile {
+    static constexpr int kBBlock = NR * 128, kBBytes = kColBlocks * kBBlock;
+    static constexpr int kDOff = kBOff + 2 * kBBytes;
+    static constexpr int kSmem = kDOff + NR * kDStride * 4 + 1024;
+    static constexpr int kRows = NR / 4;            // rows per thread in the epilogue
+};
+
+// N consecutive f32 TMEM columns of this warp's lanes.
+template <int N>
+__device__ __forceinline__ void ld_rows(uint32_t taddr, float (&v)[N]) {
+    static_assert(N == 4 || N == 8, "rows of a 16- or 32-row tile");
+    uint32_t r[8];
+    if (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Up to eight rows [n0, e) of a tile that share a request, and B[a, h] of its
+// adapter (null: none).
+struct Item {
+    const __nv_bfloat16 *b;
+    int n0, e;
+};
+
 // 1 / (1 + e^-x); e^-x = inf gives 0.
 __device__ __forceinline__ float sigmoid_f32(float x) {
     float r;
@@ -182,156 +300,200 @@ __device__ __forceinline__ float sigmoid_f32(float x) {
     return r;
 }
 
-// B[a, h] T of the tile's rows [t0, t0 + nrows) -> delta[row][v].  Warp w
-// takes outputs 16 (w % 8) .. + 15 of every second request.
-__device__ void expand(const LoraArgs &p, float *delta, int t0, int nrows, int h) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int v0 = 16 * (warp & 7);
-    const int r_end = (t0 + nrows - 1) / p.qlen;
-    for (int r = t0 / p.qlen + (warp >> 3); r <= r_end; r += 2) {
+// The tile's items, one thread each; their number.
+__device__ __forceinline__ int make_items(const LoraArgs &p, Item *items, int t0, int nrows, int h) {
+    const int per = (p.qlen + 7) / 8;
+    const int r0 = t0 / p.qlen, n = ((t0 + nrows - 1) / p.qlen - r0 + 1) * per;
+    if (threadIdx.x < n) {
+        const int i = threadIdx.x, r = r0 + i / per, first = r * p.qlen + i % per * 8;
         const int a = adapter_of(p, r);
-        if (a < 0) continue;
-        const int s = max(r * p.qlen, t0), e = min((r + 1) * p.qlen, t0 + nrows);
-        const __nv_bfloat16 *bsrc = p.b + (((int64_t)a * p.H + h) * MLA_D_V + v0 + g) * p.rank + 8 * q;
-        for (int n0 = s; n0 < e; n0 += 8) {
-            const int row = min(n0 + g, e - 1);        // columns past the request are not kept
-            const __nv_bfloat16 *tsrc = p.t + ((int64_t)row * p.H + h) * 2 * p.rank + 8 * q;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-            for (int k = 0; k < p.rank; k += 32) {
-                uint4 u = make_uint4(0, 0, 0, 0), v = u, hi = u, lo = u;
-                if (k + 8 * q < p.rank) {
-                    u = __ldg(reinterpret_cast<const uint4 *>(bsrc + k));
-                    v = __ldg(reinterpret_cast<const uint4 *>(bsrc + 8 * p.rank + k));
-                    hi = *reinterpret_cast<const uint4 *>(tsrc + k);
-                    lo = *reinterpret_cast<const uint4 *>(tsrc + p.rank + k);
+        Item x;
+        x.n0 = max(first, t0) - t0;
+        x.e = min(min(first + 8, (r + 1) * p.qlen), t0 + nrows) - t0;
+        x.b = a < 0 || x.e <= x.n0 ? nullptr : p.b + ((int64_t)a * p.H + h) * MLA_D_V * p.rank;
+        items[i] = x;
+    }
+    return n;
+}
+
+// B[a, h] T of the tile's rows -> delta[row][v].  Warp w takes outputs
+// 16 (w % 8) .. + 15 of every second item.
+__device__ __forceinline__ void expand(const LoraArgs &p, float *delta, const Item *items, int nitems, int t0, int h) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int v0 = 16 * (warp & 7), rank = p.rank;
+    const int b_lane = (v0 + g) * rank + 8 * q, t_row = p.H * 2 * rank;
+    const __nv_bfloat16 *t_lane = p.t + ((int64_t)t0 * p.H + h) * 2 * rank + 8 * q;
+    for (int i0 = warp >> 3; i0 < nitems; i0 += 2 * kBatch) {
+        const __nv_bfloat16 *b[kBatch], *t[kBatch];
+        int n0[kBatch], e[kBatch];
+        float acc[kBatch][4] = {};
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + 2 * u;
+            e[u] = n0[u] = 0;
+            b[u] = nullptr;
+            if (i < nitems) {
+                const Item x = items[i];
+                if (x.b) {
+                    b[u] = x.b + b_lane;
+                    n0[u] = x.n0;
+                    e[u] = x.e;
                 }
-                const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
-                mma_bf16(acc, a0, hi.x, hi.y);
-                mma_bf16(acc, a1, hi.z, hi.w);
-                mma_bf16(acc, a0, lo.x, lo.y);
-                mma_bf16(acc, a1, lo.z, lo.w);
+            }
+            t[u] = t_lane + (int64_t)t_row * max(min(n0[u] + g, e[u] - 1), 0);    // columns past the request are not kept
+        }
+        for (int k = 0; k < rank; k += 32) {
+            const bool in = k + 8 * q < rank;
+            uint4 x[kBatch], y[kBatch], hi[kBatch], lo[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                x[u] = y[u] = hi[u] = lo[u] = make_uint4(0, 0, 0, 0);
+                if (in && e[u]) {
+                    x[u] = __ldg(reinterpret_cast<const uint4 *>(b[u] + k));
+                    y[u] = __ldg(reinterpret_cast<const uint4 *>(b[u] + 8 * rank + k));
+                    hi[u] = *reinterpret_cast<const uint4 *>(t[u] + k);
+                    lo[u] = *reinterpret_cast<const uint4 *>(t[u] + rank + k);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = n0 + 2 * q + (i & 1);
-                if (n < e) delta[(n - t0) * kDStride + v0 + g + 8 * (i >> 1)] = acc[i];
+            for (int u = 0; u < kBatch; ++u) {
+                const uint32_t a0[4] = {x[u].x, y[u].x, x[u].y, y[u].y}, a1[4] = {x[u].z, y[u].z, x[u].w, y[u].w};
+                mma_bf16(acc[u], a0, hi[u].x, hi[u].y);
+                mma_bf16(acc[u], a1, hi[u].z, hi[u].w);
+                mma_bf16(acc[u], a0, lo[u].x, lo[u].y);
+                mma_bf16(acc[u], a1, lo[u].z, lo[u].w);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int n = n0[u] + 2 * q;
+            float *d = delta + n * kDStride + v0 + g;
+            if (n < e[u]) {
+                d[0] = acc[u][0];
+                d[8] = acc[u][2];
+            }
+            if (n + 1 < e[u]) {
+                d[kDStride] = acc[u][1];
+                d[kDStride + 8] = acc[u][3];
             }
         }
     }
 }
 
 template <int NR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads + 32, 1)
     project_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap ml, const LoraArgs p) {
     using T = Tile<NR>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *delta = reinterpret_cast<float *>(sm + T::kDOff);
-    __shared__ uint64_t full, done;
+    __shared__ uint64_t full[2], done[2];
     __shared__ uint32_t tmem;
     __shared__ uint8_t active[NR], adapted[NR];
+    __shared__ Item items[NR];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int t0 = blockIdx.x * NR, h = blockIdx.y;
-    const int nrows = min(NR, p.S - t0);
+    const int h = blockIdx.y, tiles = (p.S + NR - 1) / NR, step = gridDim.x;
+    const bool issuer = tid == kThreads;
 
     if (tid == 0) {
-        mbar_init(&full, 1);
-        mbar_init(&done, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&done[s], 1);
+        }
         mbar_fence_init();
     }
-    if (warp == 0) tc::tmem_alloc(&tmem, T::kTmemCols);
+    if (warp == 0) tc::tmem_alloc(&tmem, 2 * NR);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (tid == 0) {
-        // Nothing here but the low-rank products is written by the kernel
-        // before this one: W_UV and the latent are fetched first.  Rows past
-        // S read as zeros (their outputs are not written).
-        mbar_arrive_expect_tx(&full, kColBlocks * (kABlock + T::kBBlock));
-        for (int kb = 0; kb < kColBlocks; ++kb) {
-            tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &full);
-            tma_3d(sm + kBOff + kb * T::kBBlock, &ml, 64 * kb, h, t0, &full);
-        }
-    }
-    for (int i = tid; i < NR; i += kThreads) {
-        const int r = (t0 + i) / p.qlen;
-        active[i] = i < nrows && __ldg(p.lengths + r) > 0;
-        adapted[i] = i < nrows && adapter_of(p, r) >= 0;
-    }
-    // This thread's gate words (bf16 pairs w = tid + 512 k: row w / 64, pair
-    // w % 64), in flight during the copies and the products.
-    uint32_t gw[T::kPairs];
-#pragma unroll
-    for (int k = 0; k < T::kPairs; ++k) {
-        const int w = tid + kThreads * k, r = w / (MLA_D_V / 2), i = w - r * (MLA_D_V / 2);
-        gw[k] = r < nrows ? __ldg(reinterpret_cast<const uint32_t *>(p.gate + ((int64_t)(t0 + r) * p.H + h) * MLA_D_V +
-                                                                     2 * i))
-                          : 0u;
-    }
     const uint32_t base = smem_u32(sm), tm = tmem;
-    bool ok = true, issued = false;
-    if (tid == 0) {
-        ok = mbar_wait(&full, 0);
-        if (ok) {
-            issued = true;
-            tc::fence_after();
-#pragma unroll
-            for (int j = 0; j < MLA_D_LATENT / 16; ++j) {
-                const int kb = j >> 2, off = (j & 3) * 32;
-                mma_bf16_tc(tm, tc::sdesc(base + kb * kABlock + off, 16, 1024, tc::kSw128),
-                            tc::sdesc(base + kBOff + kb * T::kBBlock + off, 16, 1024, tc::kSw128), T::kIdesc, j > 0);
-            }
-            tc::commit(&done);
-        }
+    // Rows past S read as zeros (their outputs are not written).
+    const auto fetch = [&](int tile, int s, uint32_t with) {
+        mbar_arrive_expect_tx(&full[s], with + T::kBBytes);
+        for (int kb = 0; kb < kColBlocks; ++kb)
+            tma_3d(sm + kBOff + s * T::kBBytes + kb * T::kBBlock, &ml, 64 * kb, h, tile * NR, &full[s]);
+    };
+    if (issuer) {
+        // Nothing here but the low-rank products is written by the kernel
+        // before this one: W_UV and the latent are fetched at once.
+        fetch(blockIdx.x, 0, kBOff);
+        for (int kb = 0; kb < kColBlocks; ++kb) tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &full[0]);
+        if (blockIdx.x + step < tiles) fetch(blockIdx.x + step, 1, 0);
     }
-    __syncwarp();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    expand(p, delta, t0, nrows, h);
-    ok = __syncthreads_and(ok);
-    if (ok) ok = mbar_wait(&done, 0);
-    ok = __syncthreads_and(ok);
-    if (!ok) {
-        // Flagged.  The copies and MMAs in flight finish (one more bounded
-        // wait each) before TMEM is released and the CTA ends.
-        if (tid == 0) {
-            mbar_wait(&full, 0);
-            if (issued) mbar_wait(&done, 0);
+    bool ok = true;
+    int issued = 0, it = 0;                         // issuer: tiles whose products are issued
+    const auto multiply = [&](int n) {              // the n-th tile of this block
+        ok = ok && mbar_wait(&full[n & 1], (n >> 1) & 1);
+        if (!ok) return;
+        tc::fence_after();
+        mma_latent(tm + (n & 1) * NR, base, kABlock, base + kBOff + (n & 1) * T::kBBytes, T::kBBlock, idesc_bf16(NR));
+        tc::commit(&done[n & 1]);
+        ++issued;
+    };
+    for (int tile = blockIdx.x; tile < tiles; tile += step, ++it) {
+        const int t0 = tile * NR, nrows = min(NR, p.S - t0);
+        if (tid < NR) {
+            const int r = (t0 + tid) / p.qlen;
+            active[tid] = tid < nrows && __ldg(p.lengths + r) > 0;
+            adapted[tid] = tid < nrows && adapter_of(p, r) >= 0;
         }
-        tc::fence_before();
+        const int nitems = make_items(p, items, t0, nrows, h);
+        // This thread's gates (output v of rows first .. first + kRows - 1),
+        // in flight during the products.
+        const int v = 32 * (warp & 3) + lane, first = (warp >> 2) * T::kRows;
+        const int64_t at = ((int64_t)(t0 + first) * p.H + h) * MLA_D_V + v;
+        const int row_step = p.H * MLA_D_V;
+        uint16_t gate[T::kRows];
+#pragma unroll
+        for (int i = 0; i < T::kRows; ++i)
+            gate[i] = first + i < nrows
+                          ? __ldg(reinterpret_cast<const uint16_t *>(p.gate) + at + (int64_t)i * row_step)
+                          : 0;
         __syncthreads();
-        if (warp == 0) tc::tmem_free(tm, T::kTmemCols);
-        return;
-    }
-    tc::fence_after();
-    if (warp < 4) {
-        const int v = 32 * warp + lane;
-#pragma unroll
-        for (int c = 0; c < NR; c += 16) {
-            float d[16];
-            tc::ld16(tm + ((uint32_t)(32 * warp) << 16) + c, d);
+        if (it == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (tid < kThreads) expand(p, delta, items, nitems, t0, h);
+        if (issuer) {
+            if (it == 0) multiply(0);
+            if (tile + step < tiles) multiply(it + 1);     // D and latents are double-buffered
+        }
+        __syncwarp();
+        ok = __syncthreads_and(ok);
+        if (ok) ok = mbar_wait(&done[it & 1], (it >> 1) & 1);
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        tc::fence_after();
+        // The latents of this tile have been multiplied: their place takes the tile after the next.
+        if (issuer && tile + 2 * step < tiles) fetch(tile + 2 * step, it & 1, 0);
+        if (tid < kThreads) {
+            float d[T::kRows];
+            ld_rows<T::kRows>(tm + ((uint32_t)(32 * (warp & 3)) << 16) + (it & 1) * NR + first, d);
             tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float *x = delta + (c + i) * kDStride + v;
-                *x = adapted[c + i] ? d[i] + *x : d[i];
+            for (int i = 0; i < T::kRows; ++i) {
+                const int n = first + i;
+                if (n >= nrows) break;
+                float x = 0.f;      // a select, so that nothing of an empty request is seen
+                if (active[n]) {
+                    x = adapted[n] ? d[i] + delta[n * kDStride + v] : d[i];
+                    x *= sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16));
+                }
+                p.out[at + (int64_t)i * row_step] = __float2bfloat16_rn(x);
             }
+        }
+        tc::fence_before();
+        __syncthreads();            // the tile's shared arrays are read
+    }
+    if (!ok && issuer) {
+        // Flagged.  What is in flight finishes (one more bounded wait each)
+        // before TMEM is released and the CTA ends.
+        for (int n = it; n < it + 2 && blockIdx.x + n * step < tiles; ++n) {
+            mbar_wait(&full[n & 1], (n >> 1) & 1);
+            if (n < issued) mbar_wait(&done[n & 1], (n >> 1) & 1);
         }
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 0) tc::tmem_free(tm, T::kTmemCols);
-#pragma unroll
-    for (int k = 0; k < T::kPairs; ++k) {
-        const int w = tid + kThreads * k, r = w / (MLA_D_V / 2), i = w - r * (MLA_D_V / 2);
-        if (r >= nrows) break;
-        uint32_t res = 0u;      // a select, so that nothing of an empty request is seen
-        if (active[r]) {
-            const float2 val = *reinterpret_cast<const float2 *>(delta + r * kDStride + 2 * i);
-            res = pack_bf16x2(val.x * sigmoid_f32(bf16_lo(gw[k])), val.y * sigmoid_f32(bf16_hi(gw[k])));
-        }
-        *reinterpret_cast<uint32_t *>(p.out + ((int64_t)(t0 + r) * p.H + h) * MLA_D_V + 2 * i) = res;
-    }
+    if (warp == 0) tc::tmem_free(tm, 2 * NR);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -354,28 +516,46 @@ bool encode_bf16(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *di
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MT>
-cudaError_t shrink(const LoraArgs &p, int R, cudaStream_t st) {
-    constexpr int smem = kShrinkWarps * 16 * MT * (kNChunk * 8 + 1) * 4;
-    cudaError_t e = smem_attr_once<shrink_kernel<MT>>(smem);
-    if (e != cudaSuccess) return e;
-    const int tiles = (p.qlen * p.H + 16 * MT - 1) / (16 * MT);
-    shrink_kernel<MT><<<(unsigned)R * tiles, kShrinkWarps * 32, smem, st>>>(p, tiles);
+// `map` over `rows` rows of the latent width, in boxes of box_rows.
+bool encode_rows(CUtensorMap *m, const void *ptr, int64_t rows, int box_rows) {
+    const cuuint64_t dim[2] = {(cuuint64_t)MLA_D_LATENT, (cuuint64_t)rows};
+    const cuuint64_t stride[1] = {(cuuint64_t)MLA_D_LATENT * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    return encode_bf16(m, ptr, 2, dim, stride, box);
+}
+
+cudaError_t shrink(const LoraArgs &p, int R, int sms, cudaStream_t st) {
+    const int pairs = p.qlen * p.H;
+    // With more 16-pair blocks than the GPU holds at once, A's repeated reads
+    // cost more than the taller tiles' start.
+    if ((int64_t)R * ((pairs + 15) / 16) > 4 * (int64_t)sms && pairs > 16 && (int64_t)p.S * p.H <= INT32_MAX) {
+        CUtensorMap ma, mx;
+        if (!encode_rows(&ma, p.a, (int64_t)p.n * p.rank, p.rank) ||
+            !encode_rows(&mx, p.latent, (int64_t)p.S * p.H, kTcPairs))
+            return cudaErrorInvalidValue;
+        cudaError_t e = smem_attr_once<shrink_tc_kernel>(shrink_tc_smem(MLA_MAX_LORA_RANK));
+        if (e != cudaSuccess) return e;
+        const int tiles = (pairs + kTcPairs - 1) / kTcPairs;
+        shrink_tc_kernel<<<(unsigned)R * tiles, kTcThreads, shrink_tc_smem(p.rank), st>>>(ma, mx, p, tiles);
+        return cudaGetLastError();
+    }
+    const int tiles = (pairs + 15) / 16;
+    shrink_kernel<<<(unsigned)R * tiles, kShrinkWarps * 32, 0, st>>>(p, tiles);
     return cudaGetLastError();
 }
 
 template <int NR>
-cudaError_t project(const CUtensorMap &mw, const void *latent, const LoraArgs &p, cudaStream_t st) {
+cudaError_t project(const CUtensorMap &mw, const LoraArgs &p, int sms, cudaStream_t st) {
     const cuuint64_t dim[3] = {(cuuint64_t)MLA_D_LATENT, (cuuint64_t)p.H, (cuuint64_t)p.S};
     const cuuint64_t stride[2] = {(cuuint64_t)MLA_D_LATENT * 2, (cuuint64_t)p.H * MLA_D_LATENT * 2};
     const cuuint32_t box[3] = {64, 1, (cuuint32_t)NR};
     CUtensorMap ml;
-    if (!encode_bf16(&ml, latent, 3, dim, stride, box)) return cudaErrorInvalidValue;
+    if (!encode_bf16(&ml, p.latent, 3, dim, stride, box)) return cudaErrorInvalidValue;
     cudaError_t e = smem_attr_once<project_kernel<NR>>(Tile<NR>::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((p.S + NR - 1) / NR, p.H, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.gridDim = dim3(std::min((p.S + NR - 1) / NR, std::max(1, sms / p.H)), p.H, 1);
+    cfg.blockDim = dim3(kThreads + 32, 1, 1);
     cfg.dynamicSmemBytes = Tile<NR>::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -410,19 +590,13 @@ cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *
     p.H = H;
     p.rank = rank;
     p.n = num_adapters;
-    const cuuint64_t dim[2] = {(cuuint64_t)MLA_D_LATENT, (cuuint64_t)H * MLA_D_V};
-    const cuuint64_t stride[1] = {(cuuint64_t)MLA_D_LATENT * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)MLA_D_V};
     CUtensorMap mw;
-    if (!encode_bf16(&mw, w_uv, 2, dim, stride, box)) return cudaErrorInvalidValue;
-    // A block's adapter is read once per tile: taller tiles where there are enough of them.
-    cudaError_t e = (int64_t)R * ((qlen * H + 31) / 32) > 2 * (int64_t)sms ? shrink<3>(p, R, st) : shrink<1>(p, R, st);
+    if (!encode_rows(&mw, w_uv, (int64_t)H * MLA_D_V, MLA_D_V)) return cudaErrorInvalidValue;
+    cudaError_t e = shrink(p, R, sms, st);
     if (e != cudaSuccess) return e;
-    // Rows per CTA (one CTA per SM): the fewest that still leave at most two waves.
-    const auto ctas = [&](int nr) { return (int64_t)((p.S + nr - 1) / nr) * H; };
-    if (ctas(16) <= 2 * (int64_t)sms) return project<16>(mw, latent, p, st);
-    if (ctas(32) <= 2 * (int64_t)sms) return project<32>(mw, latent, p, st);
-    return project<64>(mw, latent, p, st);
+    // 32-row tiles, unless 16-row ones leave no block of a head with two.
+    if ((p.S + 15) / 16 <= std::max(1, sms / H)) return project<16>(mw, p, sms, st);
+    return project<32>(mw, p, sms, st);
 }
 
 cudaError_t value_lora_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }

@@ -140,6 +140,10 @@ def _check(out, s):
     (300, 1, 4, 8, 300),
     (256, 8, 12, 64, 32),
     (40, 2, 128, 104, 5),
+    (300, 3, 12, 16, 5),         # several tiles a block, requests across tiles
+    (130, 16, 7, 128, 9),
+    (3, 16, 128, 64, 3),
+    (90, 9, 20, 48, 90),
 ])
 def test_against_the_formula(R, qlen, heads, rank, n):
     s = _make(R, qlen, heads, rank, n, R + rank)
