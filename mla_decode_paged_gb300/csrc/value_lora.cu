@@ -14,8 +14,9 @@
 //     lora_scale.  Few pairs: warp MMAs on fragments loaded straight from
 //     global memory (a lane's 16 bytes are two k-steps' worth: the products'
 //     order over k is free), eight warps of 64 latent columns each, joined in
-//     shared memory.  Many: tcgen05 MMAs, A (M, its rows past the rank
-//     whatever follows in shared memory: unused lanes) times 96 pairs (N).
+//     shared memory.  Many: tcgen05 MMAs, 48 pairs (M, the rows past them
+//     whatever follows in shared memory: unused lanes) times A (N), two
+//     blocks an SM.
 //     T goes to the workspace as two bf16 terms, hi + lo (2^-17 of the
 //     product; one term would add 2^-9, as much as the output's own rounding).
 //   project: a persistent block per head (as many as fit), W_UV[h] (M = 128
@@ -55,13 +56,11 @@ __device__ __forceinline__ int adapter_of(const LoraArgs &p, int r) {
     return -1;
 }
 
-// T[row][k] as its two terms.
-__device__ __forceinline__ void store_term(const LoraArgs &p, int64_t row, int k, float v) {
-    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-    __nv_bfloat16 *dst = p.t + row * 2 * p.rank + k;
-    dst[0] = hi;
-    // no lo beside an infinite hi (inf - inf)
-    dst[p.rank] = __float2bfloat16_rn(isinf(__bfloat162float(hi)) ? 0.f : v - __bfloat162float(hi));
+// Two values as bf16 pairs hi + lo; no lo beside an infinite hi (inf - inf).
+__device__ __forceinline__ void two_terms(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16x2(a, b);
+    const float ha = bf16_lo(hi), hb = bf16_hi(hi);
+    lo = pack_bf16x2(isinf(ha) ? 0.f : a - ha, isinf(hb) ? 0.f : b - hb);
 }
 
 // ------------------------------------------------------------------ shrink
@@ -121,14 +120,20 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) shrink_kernel(const LoraArg
                 for (int i = 0; i < 4; ++i)
                     part[(warp * 16 + g + 8 * (i >> 1)) * kCols + 8 * n + 2 * q + (i & 1)] = acc[n][i];
         __syncthreads();
-        const int cols = 8 * nn;
+        const int cols = 4 * nn;        // pairs of columns
         for (int e = threadIdx.x; e < 16 * cols; e += kShrinkWarps * 32) {
-            const int row = e / cols, k = e - row * cols;
+            const int row = e / cols, k = 2 * (e - row * cols);
             if (m0 + row >= pairs) break;
-            float s = 0.f;
+            float s[2] = {0.f, 0.f};
 #pragma unroll
-            for (int w8 = 0; w8 < kShrinkWarps; ++w8) s += part[(w8 * 16 + row) * kCols + k];
-            store_term(p, row0 + m0 + row, 8 * n0 + k, s * scale);
+            for (int w8 = 0; w8 < kShrinkWarps; ++w8) {
+                s[0] += part[(w8 * 16 + row) * kCols + k];
+                s[1] += part[(w8 * 16 + row) * kCols + k + 1];
+            }
+            uint32_t hi, lo, *dst = reinterpret_cast<uint32_t *>(p.t + (row0 + m0 + row) * 2 * p.rank + 8 * n0 + k);
+            two_terms(s[0] * scale, s[1] * scale, hi, lo);
+            dst[0] = hi;
+            dst[p.rank / 2] = lo;
         }
     }
 }
@@ -175,20 +180,22 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x,
         : "memory");
 }
 
-constexpr int kTcPairs = 96, kTcThreads = 256;
-constexpr int kTcBBlock = kTcPairs * 128;
+constexpr int kTcPairs = 48, kTcThreads = 128;
+constexpr int kTcXBlock = kTcPairs * 128;
 
+// The last block's reads of 128 rows of pairs, and of 16 of A where the rank
+// ends at 8, stay inside too.
 __host__ __device__ constexpr int shrink_tc_smem(int rank) {
-    return kColBlocks * (rank * 128 + kTcBBlock) + 1024;
+    const int all = kColBlocks * (kTcXBlock + rank * 128) + (rank % 16 ? 1024 : 0), pairs = (kColBlocks - 1) * kTcXBlock + 128 * 128;
+    return all > pairs ? all : pairs;
 }
 
-// 96 pairs per block: ma maps lora_a as [n * rank, 512], mx the latent as
+// 48 pairs per block: ma maps lora_a as [n * rank, 512], mx the latent as
 // [S * H, 512].
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads)
     shrink_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mx, const LoraArgs p,
                      int tiles) {
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];
     __shared__ uint64_t full, done;
     __shared__ uint32_t tmem;
     asm volatile("griddepcontrol.launch_dependents;");
@@ -198,15 +205,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pairs = p.qlen * p.H, m0 = tile * kTcPairs;
     const int64_t row0 = (int64_t)r * pairs + m0;
-    const int a_block = p.rank * 128, b_off = kColBlocks * a_block;
+    const int a_block = p.rank * 128, a_off = kColBlocks * kTcXBlock;
     if (tid == 0) {
         mbar_init(&full, 1);
         mbar_init(&done, 1);
         mbar_fence_init();
-        mbar_arrive_expect_tx(&full, kColBlocks * (a_block + kTcBBlock));
+        mbar_arrive_expect_tx(&full, kColBlocks * (kTcXBlock + a_block));
         for (int kb = 0; kb < kColBlocks; ++kb) {
-            tma_2d(sm + kb * a_block, &ma, 64 * kb, a * p.rank, &full);
-            tma_2d(sm + b_off + kb * kTcBBlock, &mx, 64 * kb, (int)row0, &full);
+            tma_2d(sm + kb * kTcXBlock, &mx, 64 * kb, (int)row0, &full);
+            tma_2d(sm + a_off + kb * a_block, &ma, 64 * kb, a * p.rank, &full);
         }
     }
     if (warp == 0) tc::tmem_alloc(&tmem, 128);
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (ok) {
             issued = true;
             tc::fence_after();
-            mma_latent(tmem, smem_u32(sm), a_block, smem_u32(sm) + b_off, kTcBBlock, idesc_bf16(kTcPairs));
+            mma_latent(tmem, smem_u32(sm), kTcXBlock, smem_u32(sm) + a_off, a_block, idesc_bf16((p.rank + 15) / 16 * 16));
             tc::commit(&done);
         }
     }
@@ -228,20 +235,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     ok = __syncthreads_and(ok);
     if (ok) {
         tc::fence_after();
-        // Lane = rank index; the block's two warpgroups take half of the pairs each.
-        const int k = 32 * (warp & 3) + lane, c0 = (warp >> 2) * (kTcPairs / 2);
+        const int m = tid;      // TMEM lane = pair
         const float scale = __ldg(p.scale + a);
-        if (32 * (warp & 3) < p.rank) {
-#pragma unroll
-            for (int c = 0; c < kTcPairs / 2; c += 16) {
+        uint4 *dst = reinterpret_cast<uint4 *>(p.t + (row0 + m) * 2 * p.rank);
+        const int vecs = p.rank / 8;
+        if (32 * warp < kTcPairs)
+            for (int c = 0; c < p.rank; c += 16) {
                 float d[16];
-                tc::ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c0 + c, d);
+                tc::ld16(tmem + ((uint32_t)(32 * warp) << 16) + c, d);
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (k < p.rank && m0 + c0 + c + i < pairs) store_term(p, row0 + c0 + c + i, k, d[i] * scale);
+                for (int v = 0; v < 2; ++v) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) two_terms(d[8 * v + 2 * i] * scale, d[8 * v + 2 * i + 1] * scale, hi[i], lo[i]);
+                    if (m < kTcPairs && m0 + m < pairs && c / 8 + v < vecs) {
+                        dst[c / 8 + v] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        dst[vecs + c / 8 + v] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
             }
-        }
     } else if (tid == 0) {
         // Flagged.  What is in flight finishes before TMEM is released.
         mbar_wait(&full, 0);
