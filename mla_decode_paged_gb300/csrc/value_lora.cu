@@ -19,14 +19,22 @@
 //     blocks an SM.
 //     T goes to the workspace as two bf16 terms, hi + lo (2^-17 of the
 //     product; one term would add 2^-9, as much as the output's own rounding).
-//   project: a persistent block per head (as many as fit), W_UV[h] (M = 128
-//     outputs) staying in shared memory, over the head's tiles of rows (N):
-//     tcgen05 MMAs into TMEM, the next tile's latents and products in flight
-//     during this one.  Meanwhile the 16 warps form B T by warp MMAs into a
-//     float32 tile, reading B[a, h] once per request of the tile (every
-//     column of a warp MMA is a row of its own, so rows of other requests
-//     need no mask), four requests' loads in flight a warp.  The epilogue
-//     adds the two and gates.
+//   project: persistent blocks, each on one head: W_UV[h] (M = 128 outputs)
+//     stays in shared memory over the head's tiles of rows (N), whose latents
+//     stream past it into tcgen05 MMAs.  B[a, h] T in one of two ways.
+//     One row a request: 16 warps form it by warp MMAs from global memory
+//     into a float32 tile (every column of a warp MMA is a row of its own).
+//     More: through a ring, an entry being B[a, h] (M, by TMA) and the T rows
+//     of up to eight rows of one request (its place in a 16-row window, N),
+//     two MMAs per 16 ranks into 16 TMEM columns of its own, of which the
+//     request's rows are added to the projection's.  (Added into the
+//     projection's columns with the other rows zero, one tenant's infinite B
+//     would be everyone's NaN.)
+//       warps 0..7   epilogue: the sum from TMEM, gated, while the next
+//                    tile's projection runs (its D is double-buffered)
+//       warps 8..13  one ring slot each: T rows and B into it
+//       warp 14      latents and W_UV
+//       warp 15      MMA issuer
 #include <algorithm>
 
 #include <cuda.h>
@@ -146,23 +154,31 @@ constexpr uint32_t idesc_bf16(int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_bf16_tc(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                            bool accumulate) {
+// Run by a whole warp, its arguments the same in every lane; `one` (0 or 1)
+// set in the lane that issues.  A branch around it instead would keep the
+// descriptors out of the uniform registers.
+__device__ __forceinline__ void mma_bf16_tc(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate,
+                                            uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(one));
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
 
 // D = A[128 x 512] B[N x 512]^T, both in 128B-swizzled column blocks.
 __device__ __forceinline__ void mma_latent(uint32_t d_tmem, uint32_t a, uint32_t a_block, uint32_t b, uint32_t b_block,
-                                           uint32_t idesc) {
+                                           uint32_t idesc, uint32_t one) {
+    const uint64_t ad = tc::sdesc(a, 16, 1024, tc::kSw128), bd = tc::sdesc(b, 16, 1024, tc::kSw128);
 #pragma unroll
-    for (int j = 0; j < MLA_D_LATENT / 16; ++j) {
-        const int kb = j >> 2, off = (j & 3) * 32;
-        mma_bf16_tc(d_tmem, tc::sdesc(a + kb * a_block + off, 16, 1024, tc::kSw128),
-                    tc::sdesc(b + kb * b_block + off, 16, 1024, tc::kSw128), idesc, j > 0);
-    }
+    for (int j = 0; j < MLA_D_LATENT / 16; ++j)
+        mma_bf16_tc(d_tmem, ad + (j >> 2) * (a_block >> 4) + (j & 3) * 2, bd + (j >> 2) * (b_block >> 4) + (j & 3) * 2,
+                    idesc, j > 0, one);
 }
 
 __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
@@ -202,7 +218,7 @@ __global__ void __launch_bounds__(kTcThreads)
     const int r = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int a = adapter_of(p, r);
     if (a < 0) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int pairs = p.qlen * p.H, m0 = tile * kTcPairs;
     const int64_t row0 = (int64_t)r * pairs + m0;
     const int a_block = p.rank * 128, a_off = kColBlocks * kTcXBlock;
@@ -221,13 +237,16 @@ __global__ void __launch_bounds__(kTcThreads)
     __syncthreads();
     tc::fence_after();
     bool ok = true, issued = false;
-    if (tid == 0) {
-        ok = mbar_wait(&full, 0);
+    if (warp == 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full, 0));
         if (ok) {
             issued = true;
             tc::fence_after();
-            mma_latent(tmem, smem_u32(sm), kTcXBlock, smem_u32(sm) + a_off, a_block, idesc_bf16((p.rank + 15) / 16 * 16));
-            tc::commit(&done);
+            const uint32_t one = elect_one();
+            mma_latent(tmem, smem_u32(sm), kTcXBlock, smem_u32(sm) + a_off, a_block, idesc_bf16((p.rank + 15) / 16 * 16),
+                       one);
+            if (one) tc::commit(&done);
+            __syncwarp();
         }
     }
     ok = __syncthreads_and(ok);
@@ -267,17 +286,27 @@ __global__ void __launch_bounds__(kTcThreads)
 
 // ------------------------------------------------------------------ project
 
-constexpr int kThreads = 512;                      // and a warp that issues copies and products
 constexpr int kABlock = MLA_D_V * 128;             // one column block of W_UV[h]: 16 KB
-constexpr int kBOff = kColBlocks * kABlock;
+constexpr int kXOff = kColBlocks * kABlock;        // the tile's latents
+
+// 1 / (1 + e^-x); e^-x = inf gives 0.
+__device__ __forceinline__ float sigmoid_f32(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+    return r;
+}
+
+// --------------------------------- project: B T by warp MMAs (one row a request)
+
+constexpr int kFewThreads = 512;                   // and a warp that issues copies and products
 constexpr int kDStride = MLA_D_V + 4;              // float32 tile rows, a bank apart per row pair
 constexpr int kBatch = 2;                          // items a warp expands at once
 
 // NR rows a tile; two tiles' latents.
 template <int NR>
-struct Tile {
+struct FewTile {
     static constexpr int kBBlock = NR * 128, kBBytes = kColBlocks * kBBlock;
-    static constexpr int kDOff = kBOff + 2 * kBBytes;
+    static constexpr int kDOff = kXOff + 2 * kBBytes;
     static constexpr int kSmem = kDOff + NR * kDStride * 4 + 1024;
     static constexpr int kRows = NR / 4;            // rows per thread in the epilogue
 };
@@ -305,13 +334,6 @@ struct Item {
     const __nv_bfloat16 *b;
     int n0, e;
 };
-
-// 1 / (1 + e^-x); e^-x = inf gives 0.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
-    return r;
-}
 
 // The tile's items, one thread each; their number.
 __device__ __forceinline__ int make_items(const LoraArgs &p, Item *items, int t0, int nrows, int h) {
@@ -394,9 +416,9 @@ __device__ __forceinline__ void expand(const LoraArgs &p, float *delta, const It
 }
 
 template <int NR>
-__global__ void __launch_bounds__(kThreads + 32, 1)
-    project_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap ml, const LoraArgs p) {
-    using T = Tile<NR>;
+__global__ void __launch_bounds__(kFewThreads + 32, 1)
+    project_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap ml, const LoraArgs p) {
+    using T = FewTile<NR>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *delta = reinterpret_cast<float *>(sm + T::kDOff);
@@ -406,7 +428,8 @@ __global__ void __launch_bounds__(kThreads + 32, 1)
     __shared__ Item items[NR];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y, tiles = (p.S + NR - 1) / NR, step = gridDim.x;
-    const bool issuer = tid == kThreads;
+    const bool issuer = warp == kFewThreads / 32;   // a whole warp; one lane copies and commits
+    const uint32_t one = elect_one();
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -424,23 +447,24 @@ __global__ void __launch_bounds__(kThreads + 32, 1)
     const auto fetch = [&](int tile, int s, uint32_t with) {
         mbar_arrive_expect_tx(&full[s], with + T::kBBytes);
         for (int kb = 0; kb < kColBlocks; ++kb)
-            tma_3d(sm + kBOff + s * T::kBBytes + kb * T::kBBlock, &ml, 64 * kb, h, tile * NR, &full[s]);
+            tma_3d(sm + kXOff + s * T::kBBytes + kb * T::kBBlock, &ml, 64 * kb, h, tile * NR, &full[s]);
     };
-    if (issuer) {
+    if (issuer && one) {
         // Nothing here but the low-rank products is written by the kernel
         // before this one: W_UV and the latent are fetched at once.
-        fetch(blockIdx.x, 0, kBOff);
+        fetch(blockIdx.x, 0, kXOff);
         for (int kb = 0; kb < kColBlocks; ++kb) tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &full[0]);
         if (blockIdx.x + step < tiles) fetch(blockIdx.x + step, 1, 0);
     }
     bool ok = true;
-    int issued = 0, it = 0;                         // issuer: tiles whose products are issued
+    int issued = 0, it = 0;                         // issuing warp: tiles whose products are issued
     const auto multiply = [&](int n) {              // the n-th tile of this block
-        ok = ok && mbar_wait(&full[n & 1], (n >> 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[n & 1], (n >> 1) & 1));
         if (!ok) return;
         tc::fence_after();
-        mma_latent(tm + (n & 1) * NR, base, kABlock, base + kBOff + (n & 1) * T::kBBytes, T::kBBlock, idesc_bf16(NR));
-        tc::commit(&done[n & 1]);
+        mma_latent(tm + (n & 1) * NR, base, kABlock, base + kXOff + (n & 1) * T::kBBytes, T::kBBlock, idesc_bf16(NR), one);
+        if (one) tc::commit(&done[n & 1]);
+        __syncwarp();
         ++issued;
     };
     for (int tile = blockIdx.x; tile < tiles; tile += step, ++it) {
@@ -464,7 +488,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1)
                           : 0;
         __syncthreads();
         if (it == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (tid < kThreads) expand(p, delta, items, nitems, t0, h);
+        if (tid < kFewThreads) expand(p, delta, items, nitems, t0, h);
         if (issuer) {
             if (it == 0) multiply(0);
             if (tile + step < tiles) multiply(it + 1);     // D and latents are double-buffered
@@ -476,8 +500,8 @@ __global__ void __launch_bounds__(kThreads + 32, 1)
         if (!ok) break;
         tc::fence_after();
         // The latents of this tile have been multiplied: their place takes the tile after the next.
-        if (issuer && tile + 2 * step < tiles) fetch(tile + 2 * step, it & 1, 0);
-        if (tid < kThreads) {
+        if (issuer && one && tile + 2 * step < tiles) fetch(tile + 2 * step, it & 1, 0);
+        if (tid < kFewThreads) {
             float d[T::kRows];
             ld_rows<T::kRows>(tm + ((uint32_t)(32 * (warp & 3)) << 16) + (it & 1) * NR + first, d);
             tc::wait_ld();
@@ -509,6 +533,329 @@ __global__ void __launch_bounds__(kThreads + 32, 1)
     if (warp == 0) tc::tmem_free(tm, 2 * NR);
 }
 
+// ------------------------------------------- project: B T through a ring of tcgen05 MMAs
+
+constexpr int kEpiWarps = 8, kSlotWarp0 = 8, kMaxSlots = 6, kLoadWarp = 14, kIssueWarp = 15;
+constexpr int kThreads = 16 * 32;
+constexpr int kWin = 16;                           // rows of a window
+
+// NR rows a tile; RB ranks of a ring entry (its rows are 2 * RB bytes, the
+// swizzle's span).
+template <int NR, int RB>
+struct Tile {
+    static_assert(RB == 32 || RB == 64, "64- or 128-byte swizzle");
+    static constexpr int kXBlock = NR * 128, kXBytes = kColBlocks * kXBlock;
+    static constexpr int kSlotOff = kXOff + kXBytes;
+    static constexpr int kBBytes = MLA_D_V * 2 * RB, kTBytes = kWin * 2 * RB;   // of a slot: B, then T hi, T lo
+    static constexpr int kSlot = kBBytes + 2 * kTBytes;
+    static constexpr int kSlots = RB == 32 ? kMaxSlots : 3;
+    static constexpr int kSmem = kSlotOff + kSlots * kSlot + 1024;
+    static constexpr int kRows = NR / 2;           // rows per thread in the epilogue
+    // TMEM columns: two tiles' projections, then one tile's entries.
+    static constexpr int kAddCols = 2 * NR, kMaxItems = (512 - kAddCols) / kWin;
+    static_assert(kMaxItems >= (NR == 16 ? 16 : 2 * 9), "the entries of a tile (NR 32: two rows a request or more)");
+    static constexpr uint32_t kSwz = RB == 32 ? tc::kSw64 : tc::kSw128, kSbo = 16 * RB;
+};
+
+// 8 consecutive f32 TMEM columns of this warp's lanes.
+__device__ __forceinline__ void ld8(uint32_t taddr, float *v) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ float ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    return __uint_as_float(r);
+}
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t par, int *abort_flag) {
+    if (*(volatile int *)abort_flag) return false;
+    if (!mbar_wait(bar, par)) {
+        *(volatile int *)abort_flag = 1;
+        return false;
+    }
+    return true;
+}
+
+// A block's ring entries in order: tile, 16-row window, eight rows (or the
+// request's rest) of a request there, chunk of RB ranks.
+template <int NR, int RB>
+struct Entries {
+    int tile, win, item, chunk, items, r0, t0, nrows, chunks;
+
+    __device__ void open(const LoraArgs &p) {       // the window's items
+        t0 = tile * NR + win * kWin;
+        nrows = min(kWin, p.S - t0);
+        const int per = (p.qlen + 7) / 8;
+        r0 = t0 / p.qlen;
+        items = nrows <= 0 ? 0 : ((t0 + nrows - 1) / p.qlen - r0 + 1) * per;
+    }
+    __device__ void init(const LoraArgs &p) {
+        tile = blockIdx.x;
+        win = item = chunk = 0;
+        chunks = (p.rank + RB - 1) / RB;
+        open(p);
+    }
+    __device__ int in_window() const { return items * chunks; }
+};
+
+template <int NR, int RB>
+struct Shared {
+    uint64_t w_full, x_full, x_empty, d_full[2], d_free[2], add_free, s_full[kMaxSlots], s_empty[kMaxSlots], fin;
+    uint32_t tmem;
+    int abort_flag;
+    uint8_t used[kMaxSlots];        // a slot's entry has an adapter
+};
+
+// Fills slot s with entries s, s + slots, ... of the block.
+template <int NR, int RB>
+__device__ void slot_filler(const LoraArgs &p, const CUtensorMap *mb, uint8_t *sm, Shared<NR, RB> &sh, int s, int h,
+                            int tiles) {
+    using T = Tile<NR, RB>;
+    const int lane = threadIdx.x & 31;
+    uint8_t *slot = sm + T::kSlotOff + s * T::kSlot;
+    const int per = (p.qlen + 7) / 8;
+    Entries<NR, RB> e;
+    e.init(p);
+    int n = 0, skip = s;            // uses of the slot; entries to pass by first
+    while (e.tile < tiles) {
+        if (skip >= e.in_window()) {
+            skip -= e.in_window();
+            if (++e.win == NR / kWin) {
+                e.win = 0;
+                e.tile += gridDim.x;
+            }
+            if (e.tile < tiles) e.open(p);
+            continue;
+        }
+        const int item = skip / e.chunks, k0 = (skip - item * e.chunks) * RB;
+        skip += T::kSlots;
+        const int r = e.r0 + item / per, first = r * p.qlen + item % per * 8;
+        const int lo = max(first, e.t0), hi = min(min(first + 8, (r + 1) * p.qlen), e.t0 + e.nrows);
+        const int a = lo < hi ? adapter_of(p, r) : -1;
+        // T's rows of the window as the B operand, 16-byte chunks: hi, then
+        // lo; other rows and ranks zero.  On their way while the slot is waited for.
+        constexpr int kChunks = RB / 8, kPer = kWin * 2 * kChunks / 32;
+        uint4 v[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int c = lane + 32 * j, row = c / (2 * kChunks), half = c / kChunks % 2, k = k0 + c % kChunks * 8;
+            const int t = e.t0 + row;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (a >= 0 && t >= lo && t < hi && k < p.rank)
+                v[j] = *reinterpret_cast<const uint4 *>(p.t + (((int64_t)t * p.H + h) * 2 + half) * p.rank + k);
+        }
+        if (!wait_or_abort(&sh.s_empty[s], (n & 1) ^ 1, &sh.abort_flag)) break;
+        ++n;
+        if (lane == 0) {
+            sh.used[s] = a >= 0;
+            if (a >= 0) {
+                mbar_arrive_expect_tx(&sh.s_full[s], T::kBBytes);
+                tma_2d(slot, mb, k0, (a * p.H + h) * MLA_D_V, &sh.s_full[s]);
+            } else {
+                mbar_arrive(&sh.s_full[s]);
+            }
+        }
+        __syncwarp();
+        if (a >= 0) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int c = lane + 32 * j, row = c / (2 * kChunks), half = c / kChunks % 2, byte = c % kChunks * 16;
+                uint8_t *d = slot + T::kBBytes + half * T::kTBytes + (row >> 3) * T::kSbo +
+                             (RB == 32 ? tc::sw64(row, byte) : tc::sw128(row, byte));
+                *reinterpret_cast<uint4 *>(d) = v[j];
+            }
+            tc::fence_async_smem();     // generic-proxy writes -> tensor-core reads
+            __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&sh.s_full[s]);
+    }
+    // Flagged elsewhere: let a copy of this slot's land before the block ends.
+    if (*(volatile int *)&sh.abort_flag && n > 0) mbar_wait(&sh.s_full[s], (n - 1) & 1);
+}
+
+template <int NR, int RB>
+__global__ void __launch_bounds__(kThreads, 1)
+    project_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap ml,
+                   const __grid_constant__ CUtensorMap mb, const LoraArgs p) {
+    using T = Tile<NR, RB>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ Shared<NR, RB> sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.y, tiles = (p.S + NR - 1) / NR, step = gridDim.x;
+    if (tid == 0) {
+        mbar_init(&sh.w_full, 1);
+        mbar_init(&sh.x_full, 1);
+        mbar_init(&sh.x_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.d_full[i], 1);
+            mbar_init(&sh.d_free[i], kEpiWarps);
+        }
+        for (int i = 0; i < T::kSlots; ++i) {
+            mbar_init(&sh.s_full[i], 2);
+            mbar_init(&sh.s_empty[i], 1);
+        }
+        mbar_init(&sh.add_free, kEpiWarps);
+        mbar_init(&sh.fin, 1);
+        sh.abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == kIssueWarp) tc::tmem_alloc(&sh.tmem, 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t base = smem_u32(sm), tm = sh.tmem;
+    if (warp == kLoadWarp) {
+        // Neither W_UV nor the latent is written by the kernel before this
+        // one.  Rows past S read as zeros (their outputs are not written).
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.w_full, kXOff);
+            for (int kb = 0; kb < kColBlocks; ++kb) tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &sh.w_full);
+            int it = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < tiles; tile += step, ++it) {
+                if (!(ok = wait_or_abort(&sh.x_empty, (it & 1) ^ 1, &sh.abort_flag))) break;
+                mbar_arrive_expect_tx(&sh.x_full, T::kXBytes);
+                for (int kb = 0; kb < kColBlocks; ++kb)
+                    tma_3d(sm + kXOff + kb * T::kXBlock, &ml, 64 * kb, h, tile * NR, &sh.x_full);
+            }
+            if (!ok) {      // flagged: the copies in flight land before the block ends
+                mbar_wait(&sh.w_full, 0);
+                if (it > 0) mbar_wait(&sh.x_full, (it - 1) & 1);
+            }
+        }
+    } else if (warp == kIssueWarp) {
+        bool ok = wait_or_abort(&sh.w_full, 0, &sh.abort_flag);
+        const uint32_t one = elect_one();
+        int it = 0, s = 0, s_phase = 0;
+        const uint64_t b_desc = tc::sdesc(base + T::kSlotOff, 16, T::kSbo, T::kSwz);
+        const uint64_t t_desc = tc::sdesc(base + T::kSlotOff + T::kBBytes, 16, T::kSbo, T::kSwz);
+        Entries<NR, RB> e;
+        e.init(p);
+        for (int tile = blockIdx.x; ok && tile < tiles; tile += step, ++it) {
+            const uint32_t d = tm + (it & 1) * NR;
+            if (!(ok = wait_or_abort(&sh.x_full, it & 1, &sh.abort_flag))) break;
+            if (!(ok = wait_or_abort(&sh.d_free[it & 1], ((it >> 1) & 1) ^ 1, &sh.abort_flag))) break;
+            tc::fence_after();
+            mma_latent(d, base, kABlock, base + kXOff, T::kXBlock, idesc_bf16(NR), one);
+            if (one) tc::commit(&sh.x_empty);
+            __syncwarp();
+            e.tile = tile;
+            if (!(ok = wait_or_abort(&sh.add_free, (it & 1) ^ 1, &sh.abort_flag))) break;
+            tc::fence_after();
+            int before = 0;     // items of the windows before
+            for (e.win = 0; ok && e.win < NR / kWin; before += e.items, ++e.win) {
+                e.open(p);
+                for (int i = 0; ok && i < e.items; ++i) {
+                    const uint32_t add = tm + T::kAddCols + (before + i) * kWin;
+                    for (int k0 = 0; k0 < p.rank; k0 += RB) {
+                        if (!(ok = wait_or_abort(&sh.s_full[s], s_phase, &sh.abort_flag))) break;
+                        tc::fence_after();
+                        if (__any_sync(0xffffffffu, sh.used[s])) {
+                            // 32 bytes of the ranks a step: 2 in a descriptor's address field
+                            const uint64_t b = b_desc + s * (T::kSlot >> 4), x = t_desc + s * (T::kSlot >> 4);
+#pragma unroll
+                            for (int j = 0; j < RB / 16; ++j)
+                                if (k0 + 16 * j < p.rank) {
+                                    mma_bf16_tc(add, b + 2 * j, x + 2 * j, idesc_bf16(kWin), k0 > 0 || j > 0, one);
+                                    mma_bf16_tc(add, b + 2 * j, x + (T::kTBytes >> 4) + 2 * j, idesc_bf16(kWin), true,
+                                                one);
+                                }
+                            if (one) tc::commit(&sh.s_empty[s]);
+                        } else if (one) {
+                            mbar_arrive(&sh.s_empty[s]);
+                        }
+                        __syncwarp();
+                        if (++s == T::kSlots) s = 0, s_phase ^= 1;
+                    }
+                }
+            }
+            if (ok && one) tc::commit(&sh.d_full[it & 1]);
+            __syncwarp();
+        }
+        // Every MMA issued must be complete before TMEM is released.
+        if (one) tc::commit(&sh.fin);
+        __syncwarp();
+        mbar_wait(&sh.fin, 0);
+    } else if (warp >= kSlotWarp0) {
+        if (warp - kSlotWarp0 < T::kSlots) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            slot_filler<NR, RB>(p, &mb, sm, sh, warp - kSlotWarp0, h, tiles);
+        }
+    } else {
+        // Output v of rows first .. first + kRows - 1 of the tile.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int v = 32 * (warp & 3) + lane, first = (warp >> 2) * T::kRows;
+        const int64_t row_step = (int64_t)p.H * MLA_D_V;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        int it = 0;
+        for (int tile = blockIdx.x; tile < tiles; tile += step, ++it) {
+            const int t0 = tile * NR + first, nrows = min(T::kRows, p.S - t0);
+            const int64_t at = ((int64_t)t0 * p.H + h) * MLA_D_V + v;
+            uint32_t live = 0;
+            uint16_t gate[T::kRows];
+#pragma unroll
+            for (int i = 0; i < T::kRows; ++i)
+                gate[i] = i < nrows ? __ldg(reinterpret_cast<const uint16_t *>(p.gate) + at + i * row_step) : 0;
+            // Lane i: the column of row i's low-rank part (-1: none).
+            int col = -1;
+            {
+                const int t = t0 + lane, r = t / p.qlen;
+                live = __ballot_sync(0xffffffffu, lane < nrows && __ldg(p.lengths + min(r, p.S / p.qlen - 1)) > 0);
+                if (lane < nrows && adapter_of(p, r) >= 0) {
+                    Entries<NR, RB> e;
+                    e.tile = tile;
+                    int item = 0;
+                    const int win = (first + lane) / kWin;
+                    for (e.win = 0; e.win <= win; ++e.win) {
+                        e.open(p);
+                        if (e.win < win) item += e.items;
+                    }
+                    item += (r - e.r0) * ((p.qlen + 7) / 8) + (t - r * p.qlen) / 8;
+                    col = T::kAddCols + item * kWin + (first + lane) % kWin;
+                }
+            }
+            if (!wait_or_abort(&sh.d_full[it & 1], (it >> 1) & 1, &sh.abort_flag)) break;
+            tc::fence_after();
+            float d[T::kRows];
+#pragma unroll
+            for (int c = 0; c < T::kRows; c += 8)
+                ld8(tm + lanes + (it & 1) * NR + first + c, d + c);
+            float add[T::kRows];
+#pragma unroll
+            for (int i = 0; i < T::kRows; ++i) {
+                const int c = __shfl_sync(0xffffffffu, col, i);
+                add[i] = ld1(tm + lanes + (c < 0 ? T::kAddCols : c));
+            }
+            const uint32_t adapted = __ballot_sync(0xffffffffu, col >= 0);
+            tc::wait_ld();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.d_free[it & 1]);
+                mbar_arrive(&sh.add_free);
+            }
+#pragma unroll
+            for (int i = 0; i < T::kRows; ++i) {
+                if (i >= nrows) break;
+                // a select, so that nothing of an empty request is seen
+                const float x = live >> i & 1 ? (adapted >> i & 1 ? d[i] + add[i] : d[i]) * sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16)) : 0.f;
+                p.out[at + i * row_step] = __float2bfloat16_rn(x);
+            }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == kIssueWarp) tc::tmem_free(tm, 512);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         cudaDriverEntryPointQueryResult q;
@@ -522,10 +869,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 bool encode_bf16(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dim, const cuuint64_t *stride,
-                 const cuuint32_t *box) {
+                 const cuuint32_t *box, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
     const cuuint32_t es[3] = {1, 1, 1};
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), dim, stride, box, es,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -557,26 +904,52 @@ cudaError_t shrink(const LoraArgs &p, int R, int sms, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int NR>
-cudaError_t project(const CUtensorMap &mw, const LoraArgs &p, int sms, cudaStream_t st) {
-    const cuuint64_t dim[3] = {(cuuint64_t)MLA_D_LATENT, (cuuint64_t)p.H, (cuuint64_t)p.S};
-    const cuuint64_t stride[2] = {(cuuint64_t)MLA_D_LATENT * 2, (cuuint64_t)p.H * MLA_D_LATENT * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)NR};
-    CUtensorMap ml;
-    if (!encode_bf16(&ml, p.latent, 3, dim, stride, box)) return cudaErrorInvalidValue;
-    cudaError_t e = smem_attr_once<project_kernel<NR>>(Tile<NR>::kSmem);
-    if (e != cudaSuccess) return e;
+template <class... Args>
+cudaError_t launch_project(void (*kernel)(Args...), int nr, int threads, int smem, const LoraArgs &p, int sms,
+                           cudaStream_t st, const Args &...args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(std::min((p.S + NR - 1) / NR, std::max(1, sms / p.H)), p.H, 1);
-    cfg.blockDim = dim3(kThreads + 32, 1, 1);
-    cfg.dynamicSmemBytes = Tile<NR>::kSmem;
+    cfg.gridDim = dim3(std::min((p.S + nr - 1) / nr, std::max(1, sms / p.H)), p.H, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, project_kernel<NR>, mw, ml, p);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The latent as [S][H][512], NR rows a box.
+bool encode_latent(CUtensorMap *m, const LoraArgs &p, int nr) {
+    const cuuint64_t dim[3] = {(cuuint64_t)MLA_D_LATENT, (cuuint64_t)p.H, (cuuint64_t)p.S};
+    const cuuint64_t stride[2] = {(cuuint64_t)MLA_D_LATENT * 2, (cuuint64_t)p.H * MLA_D_LATENT * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)nr};
+    return encode_bf16(m, p.latent, 3, dim, stride, box);
+}
+
+template <int NR>
+cudaError_t project_few(const CUtensorMap &mw, const LoraArgs &p, int sms, cudaStream_t st) {
+    CUtensorMap ml;
+    if (!encode_latent(&ml, p, NR)) return cudaErrorInvalidValue;
+    cudaError_t e = smem_attr_once<project_few_kernel<NR>>(FewTile<NR>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_project(project_few_kernel<NR>, NR, kFewThreads + 32, FewTile<NR>::kSmem, p, sms, st, mw, ml, p);
+}
+
+template <int NR, int RB>
+cudaError_t project(const CUtensorMap &mw, const LoraArgs &p, int sms, cudaStream_t st) {
+    // lora_b as [n * H * 128, rank]; columns past the rank read as zeros.
+    const cuuint64_t bdim[2] = {(cuuint64_t)p.rank, (cuuint64_t)p.n * p.H * MLA_D_V};
+    const cuuint64_t bstride[1] = {(cuuint64_t)p.rank * 2};
+    const cuuint32_t bbox[2] = {(cuuint32_t)RB, (cuuint32_t)MLA_D_V};
+    CUtensorMap ml, mb;
+    if (!encode_latent(&ml, p, NR) ||
+        !encode_bf16(&mb, p.b, 2, bdim, bstride, bbox, RB == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    cudaError_t e = smem_attr_once<project_kernel<NR, RB>>(Tile<NR, RB>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_project(project_kernel<NR, RB>, NR, kThreads, Tile<NR, RB>::kSmem, p, sms, st, mw, ml, mb, p);
 }
 
 }  // namespace
@@ -608,8 +981,16 @@ cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *
     cudaError_t e = shrink(p, R, sms, st);
     if (e != cudaSuccess) return e;
     // 32-row tiles, unless 16-row ones leave no block of a head with two.
-    if ((p.S + 15) / 16 <= std::max(1, sms / H)) return project<16>(mw, p, sms, st);
-    return project<32>(mw, p, sms, st);
+    const bool low = (p.S + 15) / 16 <= std::max(1, sms / H);
+    // With one row a request every row has an entry of its own, whose way
+    // through the ring (~600 cycles) costs more than its warp MMAs: 64
+    // requests of rank 16, 12 heads 9.1 us by warp MMAs and 10.6 through the
+    // ring, 32 of rank 32, 96 heads 14.2 and 18.1 (and a 32-row tile's
+    // entries would not fit TMEM).  With eight rows a request (256 of rank
+    // 64) 46 and 37 us, with four 29 and 23.
+    if (qlen == 1) return low ? project_few<16>(mw, p, sms, st) : project_few<32>(mw, p, sms, st);
+    if (rank <= 32) return low ? project<16, 32>(mw, p, sms, st) : project<32, 32>(mw, p, sms, st);
+    return low ? project<16, 64>(mw, p, sms, st) : project<32, 64>(mw, p, sms, st);
 }
 
 cudaError_t value_lora_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }
