@@ -28,10 +28,14 @@
 //                gather4 (four cache rows) a lane and tile, two 72 KB stages
 //   warps 14..17 convert the next request's query rows once the last MMA on
 //                the previous ones has completed
-// Requests of more rows than one CTA's Q' buffer (64, or 128 of an fp8
-// query) are cut into row groups on neighbouring CTAs, which read the same
-// tiles at about the same time (the later ones from L2); each writes its
-// partial sums to the workspace, joined in group order by a small kernel.
+// Up to 64 rows (128 of an fp8 query) fit one CTA's Q' buffer.  Up to 128
+// bf16 rows take a pair of CTAs: each holds half of Q' and a 128-token tile
+// of its own, and cta_group::2 MMAs give both their tokens' scores with all
+// rows, so a cache row still crosses L2 once.  (Two CTAs reading every tile
+// for half of the rows each took 213 us against @PAIR@ for 32 x 96 heads, 32K
+// tokens: L2 then delivers the cache twice.)  More rows are cut into groups
+// on neighbouring CTAs (pairs), each writing its partial sums to the
+// workspace, joined in group order by a small kernel.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
@@ -67,20 +71,26 @@ struct TokenArgs {
 // (acc * c.x - c.z) + (acc * c.y - c.w), its two halves each a float pair.
 constexpr int kConstBufs = 3;   // a unit's constants outlive two more units' (one-tile units in flight)
 
-// NP MMA columns, TERMS of them per query row.
-template <int NP, int TERMS>
+// NP columns of Q' in a CTA, TERMS of them per query row; PAIR: two CTAs'
+// columns make the MMA's N (CTA 0's first), two tiles its M.
+template <int NP, int TERMS, bool PAIR>
 struct Cfg {
-    static constexpr int NQ = NP / TERMS;
+    static constexpr int NQ = NP / TERMS;               // query rows in this CTA's Q'
+    static constexpr int Rows = PAIR ? 2 * NQ : NQ;     // query rows of the MMA
+    static constexpr int N = PAIR ? 2 * NP : NP;
+    static constexpr int Tokens = PAIR ? 2 * kTile : kTile;
     static constexpr int QLatBlock = (NP / 8) * 1024;
     static constexpr int QRope = 4 * QLatBlock;
     static constexpr int OffMisc = kOffQ + NP * MLA_D_QK;
-    static constexpr uint32_t TmemCols = 2 * NP <= 64 ? 64 : 2 * NP <= 128 ? 128 : 256;
+    static constexpr uint32_t TmemCols = 2 * N <= 64 ? 64 : 2 * N <= 128 ? 128 : 2 * N <= 256 ? 256 : 512;
+    // Instruction descriptor: e4m3 operands, f32 sums, M = 128 or 256.
+    static constexpr uint32_t Idesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)((PAIR ? 256 : 128) >> 4) << 24);
 };
 
-template <int NQ>
+template <class C>
 struct Misc {
-    float4 c[kConstBufs][NQ];
-    int vis[kConstBufs][NQ];    // tokens of the request that the row counts (0: a skipped row)
+    float4 c[kConstBufs][C::Rows];
+    int vis[kConstBufs][C::Rows];   // tokens of the request that the row counts (0: a skipped row)
     int all_vis[kConstBufs];    // smallest of them over the real rows
     uint64_t kv_full[kStages], kv_empty[kStages], d_full[2], d_free[2], q_ready, q_free, fin;
     uint32_t tmem;
@@ -97,13 +107,15 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t par, int *
     return true;
 }
 
-// A CTA's tiles in order; every role walks them on its own (uniform loads).
+// A CTA's (a pair's) tiles of TOKENS in order; every role walks them on its
+// own (uniform loads).
+template <int TOKENS>
 struct Walk {
     int r, t, ntiles, len, base, left, unit;
     bool first;     // the tile is its unit's first in this CTA
 
-    template <int NQ>
-    __device__ void init(const TokenArgs &a, const Misc<NQ> &ms) {
+    template <class C>
+    __device__ void init(const TokenArgs &a, const Misc<C> &ms) {
         r = ms.start[0];
         t = ms.start[1];
         left = ms.start[2];
@@ -113,11 +125,10 @@ struct Walk {
     }
     __device__ void open(const TokenArgs &a) {
         len = request_len(a.indptr, r, a.num_pages, &base);
-        ntiles = (len + kTile - 1) / kTile;
+        ntiles = (len + TOKENS - 1) / TOKENS;
     }
     __device__ bool valid() const { return left > 0; }
     __device__ bool last() const { return left == 1 || t + 1 == ntiles; }
-    __device__ int ntok() const { return min(kTile, len - t * kTile); }
     __device__ void next(const TokenArgs &a) {
         --left;
         first = false;
@@ -133,13 +144,13 @@ struct Walk {
 };
 
 // This CTA's range of the batch's tiles -> ms.start.
-template <int NQ>
-__device__ void find_start(const TokenArgs &a, Misc<NQ> &ms, int v) {
+template <class C>
+__device__ void find_start(const TokenArgs &a, Misc<C> &ms, int v) {
     __shared__ int part[kThreads / 32 + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const auto tiles_of = [&](int r) {
         int base;
-        return (request_len(a.indptr, r, a.num_pages, &base) + kTile - 1) / kTile;
+        return (request_len(a.indptr, r, a.num_pages, &base) + C::Tokens - 1) / C::Tokens;
     };
     int mine = 0, sum = 0;
     for (int r = tid; r < a.R; r += kThreads) {
@@ -184,21 +195,20 @@ __device__ void find_start(const TokenArgs &a, Misc<NQ> &ms, int v) {
 
 // ------------------------------------------------------------------ producers
 
-template <int NQ>
+template <class C>
 __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUtensorMap *mrope, uint8_t *sm,
-                         Misc<NQ> &ms) {
+                         Misc<C> &ms, int rank) {
     const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kProdWarp0;
-    Walk w;
+    Walk<C::Tokens> w;
     w.init(a, ms);
     const uint64_t pol = tc::l2_policy(true);   // the rows stream through L2; the query and the outputs stay
     const auto fetch = [&](int (&rows)[4]) {
-        const int ntok = w.valid() ? w.ntok() : 0;
+        const int tok0 = w.t * C::Tokens + rank * kTile + 4 * lane, len = w.valid() ? w.len : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int tok = 4 * lane + i;
-            rows[i] = -1;                       // past the tile: the copy fills zeros
-            if (tok < ntok) {
-                const int p = __ldg(a.pages + (int64_t)w.base + w.t * kTile + tok);
+            rows[i] = -1;                       // past the request: the copy fills zeros
+            if (tok0 + i < len) {
+                const int p = __ldg(a.pages + (int64_t)w.base + tok0 + i);
                 rows[i] = p;
                 if (p < 0 || p >= a.pool_rows) {
                     flag(MLA_DEV_BAD_PAGE);
@@ -211,7 +221,7 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
     // tiles before its indices are read: an index that misses L2 waits behind
     // the stream of rows for several thousand cycles.
     const auto ahead = [&](int tiles) {
-        const int64_t at = (int64_t)w.base + (int64_t)(w.t + tiles) * kTile + 32 * lane;
+        const int64_t at = (int64_t)w.base + (int64_t)(w.t + tiles) * C::Tokens + rank * kTile + 32 * lane;
         if (lane < 5 && at < a.num_pages) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pages + at));
     };
     if (part == 4 && w.valid())
@@ -244,40 +254,124 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
 
 // ------------------------------------------------------------------ MMA issuer
 
-template <int NP, int TERMS>
-__device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms) {
-    using C = Cfg<NP, TERMS>;
-    const int lane = threadIdx.x & 31;
+// Run by the whole warp, its arguments the same in every lane; `one` set in
+// the lane that issues (a branch around it would keep the descriptors out of
+// the uniform registers).
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate,
+                                    uint32_t one) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(one));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(one));
+}
+
+// Arrive on `bar` (PAIR: in both CTAs) once this thread's MMAs so far have completed.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        tc::commit(bar);
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// Arrive on CTA 0's `bar`, from either CTA of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_lead(uint64_t *bar) {
+    if (!PAIR) {
+        mbar_arrive(bar);
+        return;
+    }
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// wait_or_abort for what the other CTA has written too.
+template <bool PAIR>
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t par, int *abort_flag) {
+    if (!PAIR) return wait_or_abort(bar, par, abort_flag);
+    if (*(volatile int *)abort_flag) return false;
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(par)
+            : "memory");
+        if (ok) return true;
+        if (clock64() - t0 > kWaitCycles) {
+            flag(MLA_DEV_TIMEOUT);
+            *(volatile int *)abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+// CTA 0 issues; CTA 1 of a pair passes its tiles' arrival on to it.
+template <int NP, int TERMS, bool PAIR>
+__device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, PAIR>> &ms, int rank) {
+    using C = Cfg<NP, TERMS, PAIR>;
     const uint32_t base = smem_u32(sm), tm = ms.tmem;
-    constexpr uint32_t kId = tc::idesc_e4m3(NP, false, false);
-    Walk w;
+    const uint32_t one = elect_one();
+    const uint64_t lat0 = tc::sdesc(base, 16, 1024, tc::kSw128), rope0 = tc::sdesc(base + kRopeOff, 16, 512, tc::kSw64);
+    const uint64_t q0 = tc::sdesc(base + kOffQ, 16, 1024, tc::kSw128);
+    const uint64_t qr0 = tc::sdesc(base + kOffQ + C::QRope, 16, 512, tc::kSw64);
+    Walk<C::Tokens> w;
     w.init(a, ms);
+    if (PAIR && rank > 0) {
+        for (int it = 0; w.valid(); ++it, w.next(a)) {
+            const int s = it % kStages;
+            if (!wait_or_abort(&ms.kv_full[s], (it / kStages) & 1, &ms.abort_flag)) break;
+            if (one) arrive_lead<PAIR>(&ms.kv_full[s]);
+            __syncwarp();
+        }
+        return;
+    }
     for (int it = 0; w.valid(); ++it, w.next(a)) {
         const int s = it % kStages, d = it & 1;
-        if (w.first && !wait_or_abort(&ms.q_ready, w.unit & 1, &ms.abort_flag)) break;
-        if (!wait_or_abort(&ms.d_free[d], ((it >> 1) & 1) ^ 1, &ms.abort_flag)) break;
-        if (!wait_or_abort(&ms.kv_full[s], (it / kStages) & 1, &ms.abort_flag)) break;
+        if (w.first && !wait_pair<PAIR>(&ms.q_ready, w.unit & 1, &ms.abort_flag)) break;
+        if (!wait_pair<PAIR>(&ms.d_free[d], ((it >> 1) & 1) ^ 1, &ms.abort_flag)) break;
+        if (!wait_pair<PAIR>(&ms.kv_full[s], (it / kStages) & 1, &ms.abort_flag)) break;
         tc::fence_after();
-        if (lane == 0) {
-            const uint32_t st = base + s * kStageBytes, dt = tm + d * NP;
+        // Column blocks of 128 bytes, 32 bytes a step (an address counts 16).
+        const uint32_t dt = tm + d * C::N;
+        const uint64_t lat = lat0 + s * (kStageBytes >> 4), rope = rope0 + s * (kStageBytes >> 4);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int b = j >> 2, off = (j & 3) * 32;
-                tc::mma_e4m3(dt, tc::sdesc(st + b * kLatBlock + off, 16, 1024, tc::kSw128),
-                             tc::sdesc(base + kOffQ + b * C::QLatBlock + off, 16, 1024, tc::kSw128), kId, j > 0);
-            }
+        for (int j = 0; j < 16; ++j)
+            mma<PAIR>(dt, lat + (j >> 2) * (kLatBlock >> 4) + (j & 3) * 2,
+                      q0 + (j >> 2) * (C::QLatBlock >> 4) + (j & 3) * 2, C::Idesc, j > 0, one);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                tc::mma_e4m3(dt, tc::sdesc(st + kRopeOff + j * 32, 16, 512, tc::kSw64),
-                             tc::sdesc(base + kOffQ + C::QRope + j * 32, 16, 512, tc::kSw64), kId, true);
-            tc::commit(&ms.kv_empty[s]);
-            tc::commit(&ms.d_full[d]);
-            if (w.last()) tc::commit(&ms.q_free);
+        for (int j = 0; j < 2; ++j) mma<PAIR>(dt, rope + j * 2, qr0 + j * 2, C::Idesc, true, one);
+        if (one) {
+            commit<PAIR>(&ms.kv_empty[s]);
+            commit<PAIR>(&ms.d_full[d]);
+            if (w.last()) commit<PAIR>(&ms.q_free);
         }
         __syncwarp();
     }
     // Every MMA issued must be complete before TMEM is released.
-    if (lane == 0) tc::commit(&ms.fin);
+    if (one) commit<PAIR>(&ms.fin);
     __syncwarp();
     mbar_wait(&ms.fin, 0);
 }
@@ -285,24 +379,25 @@ __device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms
 // ------------------------------------------------------------------ query
 
 // Byte offset of column d of Q' row n.
-template <int NP, int TERMS>
+template <class C>
 __device__ __forceinline__ uint32_t q_offset(int n, int d) {
-    using C = Cfg<NP, TERMS>;
     return d < 512 ? kOffQ + (d >> 7) * C::QLatBlock + (n >> 3) * 1024 + tc::sw128(n, d & 127)
                    : kOffQ + C::QRope + (n >> 3) * 512 + tc::sw64(n, d - 512);
 }
 
-// Request r's rows [grp * NQ, ...) as the B operand, a warp a row, and their
-// constants.
-template <int NP, int TERMS>
-__device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms, int r, int len, int grp, int unit) {
-    constexpr int NQ = NP / TERMS;
+// The constants of request r's rows [grp * Rows, ...), and this CTA's half of
+// them (all without a pair) as the B operand, a warp a row.
+template <int NP, int TERMS, bool PAIR>
+__device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, PAIR>> &ms, int r, int len, int grp,
+                          int unit, int rank) {
+    using C = Cfg<NP, TERMS, PAIR>;
+    constexpr int NQ = C::NQ;
     const int lane = threadIdx.x & 31, pw = (threadIdx.x >> 5) - kPrepWarp0, buf = unit % kConstBufs;
     const int rows_total = a.qlen * a.heads;
     if (pw == 0) {
         int least = INT_MAX;
-        for (int n = lane; n < NQ; n += 32) {
-            const int rho = grp * NQ + n;
+        for (int n = lane; n < C::Rows; n += 32) {
+            const int rho = grp * C::Rows + n;
             int vis = 0;
             if (rho < rows_total) {
                 const int t = rho / a.heads;
@@ -317,17 +412,19 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms,
         if (lane == 0) ms.all_vis[buf] = least;
     }
 #pragma unroll 2
-    for (int n = pw; n < NQ; n += kPrepWarps) {
-        const int rho = grp * NQ + n;
+    for (int row = pw; row < C::Rows; row += kPrepWarps) {
+        const int rho = grp * C::Rows + row;
+        const int n = row - rank * NQ;      // row of this CTA's Q'
+        const bool mine = !PAIR || (n >= 0 && n < NQ);
         const bool real = rho < rows_total;
         const int t = rho / a.heads, h = rho - t * a.heads;
         float back = 1.f;           // 2^-e
         if (TERMS == 1) {
             const uint8_t *src = static_cast<const uint8_t *>(a.q) + ((int64_t)r * a.qlen + t) * a.q_row_stride +
                                  (int64_t)h * MLA_D_QK;
-            for (int ch = lane; ch < MLA_D_QK / 16; ch += 32) {
+            for (int ch = lane; mine && ch < MLA_D_QK / 16; ch += 32) {
                 const uint4 v = real ? __ldg(reinterpret_cast<const uint4 *>(src) + ch) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(sm + q_offset<NP, TERMS>(n, ch * 16)) = v;
+                *reinterpret_cast<uint4 *>(sm + q_offset<C>(n, ch * 16)) = v;
             }
         } else {
             const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
@@ -352,7 +449,7 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms,
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
                 const int ch = lane + 32 * j;
-                if (ch >= MLA_D_QK / 8) continue;
+                if (ch >= MLA_D_QK / 8 || !mine) continue;
                 const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
                 uint32_t hi[2], lo[2];
 #pragma unroll
@@ -371,8 +468,8 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms,
                         lo[e >> 1] = l8;
                     }
                 }
-                *reinterpret_cast<uint2 *>(sm + q_offset<NP, TERMS>(n, ch * 8)) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2 *>(sm + q_offset<NP, TERMS>(NQ + n, ch * 8)) = make_uint2(lo[0], lo[1]);
+                *reinterpret_cast<uint2 *>(sm + q_offset<C>(n, ch * 8)) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(sm + q_offset<C>(NQ + n, ch * 8)) = make_uint2(lo[0], lo[1]);
             }
         }
         if (lane == 0) {
@@ -386,7 +483,7 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<NP / TERMS> &ms,
                 c.z = lse * kLog2e;
                 c.w = isinf(c.z) ? 0.f : fmaf(lse, kLog2e, -c.z) + lse * kLog2eLo;
             }
-            ms.c[buf][n] = c;
+            ms.c[buf][row] = c;
         }
     }
 }
@@ -431,86 +528,121 @@ __device__ __forceinline__ float token_sum(uint32_t taddr, const float4 *c, cons
     return sum[0] + sum[1];
 }
 
-template <int NP, int TERMS>
-__device__ void epilogue(const TokenArgs &a, Misc<NP / TERMS> &ms, int grp) {
+template <int NP, int TERMS, bool PAIR>
+__device__ void epilogue(const TokenArgs &a, Misc<Cfg<NP, TERMS, PAIR>> &ms, int grp, int rank) {
+    using C = Cfg<NP, TERMS, PAIR>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2, wq = warp & 3;
-    const uint32_t taddr = ms.tmem + wg * NP + ((uint32_t)(32 * wq) << 16);
+    const uint32_t taddr = ms.tmem + wg * C::N + ((uint32_t)(32 * wq) << 16);
     float *out = a.out + (int64_t)grp * a.group_stride;
-    Walk w;
+    Walk<C::Tokens> w;
     w.init(a, ms);
     for (int it = 0; w.valid(); ++it, w.next(a)) {
         if ((it & 1) != wg) continue;
-        const int j = w.t * kTile + 32 * wq + lane, buf = w.unit % kConstBufs;
+        const int j0 = w.t * C::Tokens + rank * kTile, j = j0 + 32 * wq + lane, buf = w.unit % kConstBufs;
         const int64_t i = (int64_t)w.base + j;
         const bool real = j < w.len;
         float old = 0.f;
         if (a.decay != 0.f && real) old = a.weights[i] * a.decay;
         if (!wait_or_abort(&ms.d_full[wg], (it >> 1) & 1, &ms.abort_flag)) break;
         tc::fence_after();
-        const bool whole = ms.all_vis[buf] >= min((w.t + 1) * kTile, w.len);
-        const float sum = whole ? token_sum<NP, TERMS, false>(taddr, ms.c[buf], ms.vis[buf], j)
-                                : token_sum<NP, TERMS, true>(taddr, ms.c[buf], ms.vis[buf], j);
+        const bool whole = ms.all_vis[buf] >= min(j0 + kTile, w.len);
+        float sum = 0.f;
+#pragma unroll
+        for (int half = 0; half < (PAIR ? 2 : 1); ++half) {
+            const float4 *c = ms.c[buf] + half * C::NQ;
+            const int *vis = ms.vis[buf] + half * C::NQ;
+            sum += whole ? token_sum<NP, TERMS, false>(taddr + half * NP, c, vis, j)
+                         : token_sum<NP, TERMS, true>(taddr + half * NP, c, vis, j);
+        }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.d_free[wg]);
+        if (lane == 0) arrive_lead<PAIR>(&ms.d_free[wg]);
         if (real) out[i] = old + sum;
     }
 }
 
-template <int NP, int TERMS>
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols) {
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        tc::tmem_alloc(dst, cols);
+    }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+    if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+    else tc::tmem_free(base, cols);
+}
+
+// All threads of the CTA, or of both.
+template <bool PAIR>
+__device__ __forceinline__ void sync_all() {
+    if (PAIR)
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+        __syncthreads();
+}
+
+template <int NP, int TERMS, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     token_weights_kernel(const __grid_constant__ CUtensorMap mlat, const __grid_constant__ CUtensorMap mrope,
                          const TokenArgs a) {
-    using C = Cfg<NP, TERMS>;
-    constexpr int NQ = NP / TERMS;
+    using C = Cfg<NP, TERMS, PAIR>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Misc<NQ> &ms = *reinterpret_cast<Misc<NQ> *>(sm + C::OffMisc);
+    Misc<C> &ms = *reinterpret_cast<Misc<C> *>(sm + C::OffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int grp = blockIdx.x % a.groups;
+    // A pair's blocks are neighbours (a cluster), and so are a tile's row groups.
+    const int rank = PAIR ? blockIdx.x & 1 : 0, unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, grp = unit % a.groups;
     if (tid == 0) {
+        const int more = PAIR && rank == 0;         // CTA 0 also hears of CTA 1's
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&ms.kv_full[s], kProdWarps);
+            mbar_init(&ms.kv_full[s], kProdWarps + more);
             mbar_init(&ms.kv_empty[s], 1);
         }
         for (int d = 0; d < 2; ++d) {
             mbar_init(&ms.d_full[d], 1);
-            mbar_init(&ms.d_free[d], 4);
+            mbar_init(&ms.d_free[d], 4 + 4 * more);
         }
-        mbar_init(&ms.q_ready, kPrepWarps);
+        mbar_init(&ms.q_ready, kPrepWarps + kPrepWarps * more);
         mbar_init(&ms.q_free, 1);
         mbar_init(&ms.fin, 1);
         ms.abort_flag = 0;
         ms.start[0] = ms.start[1] = 0;
         mbar_fence_init();
     }
-    if (warp == kMmaWarp) tc::tmem_alloc(&ms.tmem, C::TmemCols);
+    if (warp == kMmaWarp) tmem_alloc<PAIR>(&ms.tmem, C::TmemCols);
     tc::fence_before();
-    __syncthreads();
+    sync_all<PAIR>();
     tc::fence_after();
-    find_start(a, ms, blockIdx.x / a.groups);
+    find_start<C>(a, ms, unit / a.groups);
     if (warp < kEpiWarps) {
-        epilogue<NP, TERMS>(a, ms, grp);
+        epilogue<NP, TERMS, PAIR>(a, ms, grp, rank);
     } else if (warp == kMmaWarp) {
-        mma_issuer<NP, TERMS>(a, sm, ms);
+        mma_issuer<NP, TERMS, PAIR>(a, sm, ms, rank);
     } else if (warp < kPrepWarp0) {
-        producer<NQ>(a, &mlat, &mrope, sm, ms);
+        producer<C>(a, &mlat, &mrope, sm, ms, rank);
     } else {
-        Walk w;
+        Walk<C::Tokens> w;
         w.init(a, ms);
         for (; w.valid(); w.next(a)) {
             if (!w.first) continue;
             if (w.unit > 0 && !wait_or_abort(&ms.q_free, (w.unit - 1) & 1, &ms.abort_flag)) break;
-            prep_unit<NP, TERMS>(a, sm, ms, w.r, w.len, grp, w.unit);
+            prep_unit<NP, TERMS, PAIR>(a, sm, ms, w.r, w.len, grp, w.unit, rank);
             tc::fence_async_smem();     // generic-proxy writes -> tensor-core reads
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.q_ready);
+            if (lane == 0) arrive_lead<PAIR>(&ms.q_ready);
         }
     }
+    // Neither CTA of a pair ends while the other may still reach it.
     tc::fence_before();
-    __syncthreads();
+    __syncwarp();
+    sync_all<PAIR>();
     tc::fence_after();
-    if (warp == kMmaWarp) tc::tmem_free(ms.tmem, C::TmemCols);
+    if (warp == kMmaWarp) tmem_free<PAIR>(ms.tmem, C::TmemCols);
 }
 
 // out[i] = decay * weights[i] + the groups' partial sums, in group order.
@@ -547,40 +679,61 @@ bool encode_rows(CUtensorMap *m, const void *kv, int64_t pool_rows, cuuint32_t c
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Row groups and rows per group: the fewest groups of at most 128 MMA
-// columns, each as narrow as that allows (steps of 32 columns).
-void shape(int rows, int terms, int *groups, int *np) {
-    const int most = 128 / terms;
-    const int g = (rows + most - 1) / most, n = (rows + g - 1) / g * terms;
-    *groups = g;
-    *np = (n + 31) / 32 * 32;
+// How a request's query rows are laid out: `groups` of CTAs (or pairs), np
+// columns of Q' in each CTA.
+struct Shape {
+    int groups, np;
+    bool pair;
+};
+
+// The fewest groups of at most 128 columns a CTA, each as narrow as that
+// allows (steps of 32 columns); bf16 rows above one CTA's 64 take pairs.
+Shape shape(int rows, int terms) {
+    Shape s;
+    s.pair = terms == 2 && rows > 64;
+    const int most = (s.pair ? 256 : 128) / terms;
+    s.groups = (rows + most - 1) / most;
+    const int n = (rows + s.groups - 1) / s.groups * terms;     // columns of a group
+    s.np = ((s.pair ? (n + 1) / 2 : n) + 31) / 32 * 32;
+    return s;
 }
 
-template <int NP, int TERMS>
+template <int NP, int TERMS, bool PAIR>
 cudaError_t launch(const CUtensorMap &ml, const CUtensorMap &mr, const TokenArgs &a, cudaStream_t st) {
-    constexpr int smem = Cfg<NP, TERMS>::OffMisc + sizeof(Misc<NP / TERMS>) + 1024;
-    static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-    cudaError_t e = smem_attr_once<token_weights_kernel<NP, TERMS>>(smem);
+    using C = Cfg<NP, TERMS, PAIR>;
+    constexpr int smem = C::OffMisc + sizeof(Misc<C>) + 1024;
+    static_assert(smem <= 226 * 1024, "shared memory of one CTA");
+    cudaError_t e = smem_attr_once<token_weights_kernel<NP, TERMS, PAIR>>(smem);
     if (e != cudaSuccess) return e;
-    token_weights_kernel<NP, TERMS><<<a.virt * a.groups, kThreads, smem, st>>>(ml, mr, a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.virt * a.groups * (PAIR ? 2 : 1), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, token_weights_kernel<NP, TERMS, PAIR>, ml, mr, a);
 }
 
-template <int TERMS>
-cudaError_t launch_np(int np, const CUtensorMap &ml, const CUtensorMap &mr, const TokenArgs &a, cudaStream_t st) {
-    switch (np) {
-        case 32: return launch<32, TERMS>(ml, mr, a, st);
-        case 64: return launch<64, TERMS>(ml, mr, a, st);
-        case 96: return launch<96, TERMS>(ml, mr, a, st);
-        default: return launch<128, TERMS>(ml, mr, a, st);
+cudaError_t launch_shape(const Shape &s, bool q8, const CUtensorMap &ml, const CUtensorMap &mr, const TokenArgs &a,
+                         cudaStream_t st) {
+    if (s.pair) return s.np <= 96 ? launch<96, 2, true>(ml, mr, a, st) : launch<128, 2, true>(ml, mr, a, st);
+    switch (s.np) {
+        case 32: return q8 ? launch<32, 1, false>(ml, mr, a, st) : launch<32, 2, false>(ml, mr, a, st);
+        case 64: return q8 ? launch<64, 1, false>(ml, mr, a, st) : launch<64, 2, false>(ml, mr, a, st);
+        case 96: return q8 ? launch<96, 1, false>(ml, mr, a, st) : launch<96, 2, false>(ml, mr, a, st);
+        default: return q8 ? launch<128, 1, false>(ml, mr, a, st) : launch<128, 2, false>(ml, mr, a, st);
     }
 }
 
 }  // namespace
 
 int64_t token_weights_workspace(int rows, bool q8, int64_t num_pages) {
-    int groups, np;
-    shape(rows, q8 ? 1 : 2, &groups, &np);
+    const int groups = shape(rows, q8 ? 1 : 2).groups;
     return groups > 1 ? (int64_t)groups * num_pages * 4 : 0;
 }
 
@@ -609,13 +762,14 @@ cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void
     const double sc2 = sc * 1.4426950408889634;
     a.sc_hi = (float)sc2;
     a.sc_lo = (float)(sc2 - (double)a.sc_hi);
-    int np;
-    shape(qlen * heads, q8 ? 1 : 2, &a.groups, &np);
-    a.virt = sms / a.groups < 1 ? 1 : sms / a.groups;
+    const Shape s = shape(qlen * heads, q8 ? 1 : 2);
+    a.groups = s.groups;
+    const int ctas = a.groups * (s.pair ? 2 : 1);
+    a.virt = sms / ctas < 1 ? 1 : sms / ctas;
     a.out = a.groups > 1 ? static_cast<float *>(workspace) : out;
     a.group_stride = num_pages;
     a.decay = a.groups > 1 ? 0.f : decay;
-    cudaError_t e = q8 ? launch_np<1>(np, ml, mr, a, st) : launch_np<2>(np, ml, mr, a, st);
+    cudaError_t e = launch_shape(s, q8, ml, mr, a, st);
     if (e != cudaSuccess || a.groups == 1) return e;
     const int chunks = (sms * 8 + R - 1) / R;
     join_kernel<<<dim3(R, chunks < 65535 ? chunks : 65535), 256, 0, st>>>(a, static_cast<const float *>(workspace), out,

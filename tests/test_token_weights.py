@@ -77,7 +77,8 @@ def test_unsupported_sizes_and_nothing_to_do(lib):
 def test_workspace(lib):
     assert mla.token_weights_workspace(1, 12, 1000) == 0
     assert mla.token_weights_workspace(1, 128, 1000, True) == 0
-    assert mla.token_weights_workspace(1, 96, 1000) > 0
+    assert mla.token_weights_workspace(1, 128, 1000) == 0
+    assert mla.token_weights_workspace(2, 96, 1000) > 0
     with pytest.raises(mla.MlaError, match="qlen"):
         mla.token_weights_workspace(17, 12, 1000)
 
