@@ -38,6 +38,7 @@
 // workspace, joined in group order by a small kernel.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <climits>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -202,20 +203,22 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
     Walk<C::Tokens> w;
     w.init(a, ms);
     const uint64_t pol = tc::l2_policy(true);   // the rows stream through L2; the query and the outputs stay
-    const auto fetch = [&](int (&rows)[4]) {
-        const int tok0 = w.t * C::Tokens + rank * kTile + 4 * lane, len = w.valid() ? w.len : 0;
+    // The page indices of this lane's four tokens; how many of them the request has.
+    const auto load = [&](int (&rows)[4]) {
+        const int tok0 = w.t * C::Tokens + rank * kTile + 4 * lane;
+        const int n = w.valid() ? min(max(w.len - tok0, 0), 4) : 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            rows[i] = -1;                       // past the request: the copy fills zeros
-            if (tok0 + i < len) {
-                const int p = __ldg(a.pages + (int64_t)w.base + tok0 + i);
-                rows[i] = p;
-                if (p < 0 || p >= a.pool_rows) {
-                    flag(MLA_DEV_BAD_PAGE);
-                    rows[i] = 0;
-                }
+        for (int i = 0; i < 4; ++i) rows[i] = i < n ? __ldg(a.pages + (int64_t)w.base + tok0 + i) : -1;
+        return n;
+    };
+    // Past the request the copy fills zeros (row -1).
+    const auto check = [&](int (&rows)[4], int n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n && (rows[i] < 0 || rows[i] >= a.pool_rows)) {
+                flag(MLA_DEV_BAD_PAGE);
+                rows[i] = 0;
             }
-        }
     };
     // The page list, contiguous over a CTA's tiles, is brought to L2 kAhead
     // tiles before its indices are read: an index that misses L2 waits behind
@@ -227,10 +230,17 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
     if (part == 4 && w.valid())
         for (int k = 1; k < kAhead; ++k) ahead(k);
     int rows[4], it = 0;
-    fetch(rows);
+    {
+        const int n = load(rows);
+        check(rows, n);
+    }
     bool ok = true;
     while (w.valid()) {
         if (part == 4) ahead(kAhead);
+        // The next tile's indices are on their way while this one's copies are issued.
+        int next[4];
+        w.next(a);
+        const int n = load(next);
         const int s = it % kStages;
         if (!(ok = wait_or_abort(&ms.kv_empty[s], ((it / kStages) & 1) ^ 1, &ms.abort_flag))) break;
         if (lane == 0) mbar_arrive_expect_tx(&ms.kv_full[s], part < 4 ? 32 * 512 : 32 * 256);
@@ -244,8 +254,9 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
             tc::gather4_hint(st + kRopeOff + g8 * 512 + half * 256, mrope, 512, rows[0], rows[1], rows[2], rows[3],
                              &ms.kv_full[s], pol);
         ++it;
-        w.next(a);
-        fetch(rows);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows[i] = next[i];
+        check(rows, n);
     }
     if (!ok) {      // flagged: let the copies in flight land before the CTA ends
         for (int k = it < kStages ? 0 : it - kStages; k < it; ++k) mbar_wait(&ms.kv_full[k % kStages], (k / kStages) & 1);
@@ -411,70 +422,86 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, P
         for (int d = 16; d >= 1; d >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
         if (lane == 0) ms.all_vis[buf] = least;
     }
-#pragma unroll 2
-    for (int row = pw; row < C::Rows; row += kPrepWarps) {
-        const int rho = grp * C::Rows + row;
-        const int n = row - rank * NQ;      // row of this CTA's Q'
-        const bool mine = !PAIR || (n >= 0 && n < NQ);
-        const bool real = rho < rows_total;
-        const int t = rho / a.heads, h = rho - t * a.heads;
-        float back = 1.f;           // 2^-e
-        if (TERMS == 1) {
-            const uint8_t *src = static_cast<const uint8_t *>(a.q) + ((int64_t)r * a.qlen + t) * a.q_row_stride +
-                                 (int64_t)h * MLA_D_QK;
-            for (int ch = lane; mine && ch < MLA_D_QK / 16; ch += 32) {
-                const uint4 v = real ? __ldg(reinterpret_cast<const uint4 *>(src) + ch) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(sm + q_offset<C>(n, ch * 16)) = v;
-            }
-        } else {
-            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
-                                       ((int64_t)r * a.qlen + t) * a.q_row_stride + (int64_t)h * MLA_D_QK;
-            uint4 v[3];
-            float amax = 0.f;
+    // Lane i: the LSE of the warp's i-th row.
+    float lses = -INFINITY;
+    static_assert(C::Rows <= 32 * kPrepWarps, "a lane per row of a warp");
+    {
+        const int rho = grp * C::Rows + pw + kPrepWarps * lane;
+        if (pw + kPrepWarps * lane < C::Rows && rho < rows_total) lses = __ldg(a.lse + (int64_t)r * rows_total + rho);
+    }
+    // Four rows' loads in flight a warp.
+    constexpr int kBatch = 4, kVecs = TERMS == 1 ? 2 : 3;   // 16-byte vectors of a row a lane
+    static_assert(C::Rows % (kBatch * kPrepWarps) == 0, "whole batches");
+#pragma unroll 1
+    for (int i0 = 0; i0 < C::Rows / kPrepWarps; i0 += kBatch) {
+        uint4 v[kBatch][kVecs];
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
+        for (int i = 0; i < kBatch; ++i) {
+            const int row = pw + kPrepWarps * (i0 + i), rho = grp * C::Rows + row;
+            const int t = rho / a.heads, h = rho - t * a.heads;
+            const uint8_t *src = static_cast<const uint8_t *>(a.q) +
+                                 (((int64_t)r * a.qlen + t) * a.q_row_stride + (int64_t)h * MLA_D_QK) * TERMS;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
                 const int ch = lane + 32 * j;
-                v[j] = real && ch < MLA_D_QK / 8 ? __ldg(reinterpret_cast<const uint4 *>(src) + ch)
-                                                 : make_uint4(0, 0, 0, 0);
-                const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
-            }
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-            // amax = f * 2^(ex - 127), 1 <= f < 2: scaled by 2^e into [128, 256).
-            const int ex = min(max((int)(__float_as_uint(amax) >> 23), 40), 254);
-            const float up = __uint_as_float((uint32_t)(127 + 134 - ex) << 23);
-            back = __uint_as_float((uint32_t)(127 + ex - 134) << 23);
-#pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const int ch = lane + 32 * j;
-                if (ch >= MLA_D_QK / 8 || !mine) continue;
-                const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // hi is x rounded to 4 bits; the difference, at most 4 bits more, and 16 times it are exact.
-                    const float2 f = make_float2(bf16_lo(x[e]) * up, bf16_hi(x[e]) * up);
-                    const __nv_fp8x2_storage_t h8 = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-                    const float2 hf = unpack_f16x2(e4m3x2_to_f16x2(h8));
-                    const __nv_fp8x2_storage_t l8 = __nv_cvt_float2_to_fp8x2(
-                        make_float2((f.x - hf.x) * 16.f, (f.y - hf.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
-                    if (e & 1) {
-                        hi[e >> 1] |= (uint32_t)h8 << 16;
-                        lo[e >> 1] |= (uint32_t)l8 << 16;
-                    } else {
-                        hi[e >> 1] = h8;
-                        lo[e >> 1] = l8;
-                    }
-                }
-                *reinterpret_cast<uint2 *>(sm + q_offset<C>(n, ch * 8)) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2 *>(sm + q_offset<C>(NQ + n, ch * 8)) = make_uint2(lo[0], lo[1]);
+                v[i][j] = rho < rows_total && ch < MLA_D_QK * TERMS / 16 ? __ldg(reinterpret_cast<const uint4 *>(src) + ch)
+                                                                         : make_uint4(0, 0, 0, 0);
             }
         }
-        if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int row = pw + kPrepWarps * (i0 + i);
+            const int n = row - rank * NQ;      // row of this CTA's Q'
+            const bool mine = !PAIR || (n >= 0 && n < NQ);
+            float back = 1.f;                   // 2^-e
+            if (TERMS == 1) {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    const int ch = lane + 32 * j;
+                    if (mine && ch < MLA_D_QK / 16) *reinterpret_cast<uint4 *>(sm + q_offset<C>(n, ch * 16)) = v[i][j];
+                }
+            } else {
+                float amax = 0.f;
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    const uint32_t x[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
+                }
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                // amax = f * 2^(ex - 127), 1 <= f < 2: scaled by 2^e into [128, 256).
+                const int ex = min(max((int)(__float_as_uint(amax) >> 23), 40), 254);
+                const float up = __uint_as_float((uint32_t)(127 + 134 - ex) << 23);
+                back = __uint_as_float((uint32_t)(127 + ex - 134) << 23);
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    const int ch = lane + 32 * j;
+                    if (ch >= MLA_D_QK / 8 || !mine) continue;
+                    const uint32_t x[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // hi is x rounded to 4 bits; the difference, at most 4 bits more, and 16 times it are exact.
+                        const float2 f = make_float2(bf16_lo(x[e]) * up, bf16_hi(x[e]) * up);
+                        const __nv_fp8x2_storage_t h8 = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+                        const float2 hf = unpack_f16x2(e4m3x2_to_f16x2(h8));
+                        const __nv_fp8x2_storage_t l8 = __nv_cvt_float2_to_fp8x2(
+                            make_float2((f.x - hf.x) * 16.f, (f.y - hf.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+                        if (e & 1) {
+                            hi[e >> 1] |= (uint32_t)h8 << 16;
+                            lo[e >> 1] |= (uint32_t)l8 << 16;
+                        } else {
+                            hi[e >> 1] = h8;
+                            lo[e >> 1] = l8;
+                        }
+                    }
+                    *reinterpret_cast<uint2 *>(sm + q_offset<C>(n, ch * 8)) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(sm + q_offset<C>(NQ + n, ch * 8)) = make_uint2(lo[0], lo[1]);
+                }
+            }
             // lse * log2(e) as a float pair (log2(e) itself as one).
-            const float lse = real ? __ldg(a.lse + ((int64_t)r * a.qlen) * a.heads + rho) : -INFINITY;
+            const float lse = __shfl_sync(0xffffffffu, lses, i0 + i);
             float4 c = make_float4(0.f, 0.f, INFINITY, 0.f);   // a row that counts nothing: 2^-inf
             if (lse != -INFINITY) {
                 constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLo = 1.92596299112661746e-8f;
@@ -483,8 +510,23 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, P
                 c.z = lse * kLog2e;
                 c.w = isinf(c.z) ? 0.f : fmaf(lse, kLog2e, -c.z) + lse * kLog2eLo;
             }
-            ms.c[buf][row] = c;
+            if (lane == 0) ms.c[buf][row] = c;
         }
+    }
+}
+
+// A request's rows of this group into L2, ahead of their conversion.
+template <class C, int TERMS>
+__device__ void prefetch_rows(const TokenArgs &a, int r, int grp) {
+    const int rows_total = a.qlen * a.heads;
+    const uint64_t keep = tc::l2_policy_last();
+    for (int row = threadIdx.x - kPrepWarp0 * 32; row < C::Rows; row += kPrepWarps * 32) {
+        const int rho = grp * C::Rows + row;
+        if (rho >= rows_total) break;
+        const int t = rho / a.heads, h = rho - t * a.heads;
+        tc::bulk_prefetch_l2(static_cast<const uint8_t *>(a.q) +
+                                 (((int64_t)r * a.qlen + t) * a.q_row_stride + (int64_t)h * MLA_D_QK) * TERMS,
+                             MLA_D_QK * TERMS, keep);
     }
 }
 
@@ -635,6 +677,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_async_smem();     // generic-proxy writes -> tensor-core reads
             __syncwarp();
             if (lane == 0) arrive_lead<PAIR>(&ms.q_ready);
+            // The next request's (empty ones passed over), if this CTA gets to it.
+            if (w.left > w.ntiles - w.t) {
+                int r = w.r + 1, base;
+                while (r < a.R && request_len(a.indptr, r, a.num_pages, &base) == 0) ++r;
+                if (r < a.R) prefetch_rows<C, TERMS>(a, r, grp);
+            }
         }
     }
     // Neither CTA of a pair ends while the other may still reach it.

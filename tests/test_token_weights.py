@@ -276,9 +276,9 @@ def test_bad_pages_and_bad_page_lists_are_flagged():
     want, bound, lse = _formula(q, kv, pages, lengths, 12, 1, 0.05, False)
     lse = lse.contiguous()
     bad = pages.clone()
-    bad[3], bad[130], bad[220] = -1, kv.shape[0], 2**31 - 1
+    bad[3], bad[130], bad[220], bad[221] = -1, kv.shape[0], 2**31 - 1, -2**31
     fixed = pages.clone()
-    fixed[3] = fixed[130] = fixed[220] = 0
+    fixed[3] = fixed[130] = fixed[220] = fixed[221] = 0
     got = mla.token_weights(q, kv, bad, indptr, 0.05, 1.0, lse)
     assert mla.device_status() == mla.DEV_BAD_PAGE
     assert torch.equal(got, mla.token_weights(q, kv, fixed, indptr, 0.05, 1.0, lse))     # read as row 0
