@@ -548,24 +548,40 @@ __device__ __forceinline__ void ld8(uint32_t taddr, float (&v)[8]) {
 }
 
 // One token's sum over the query rows; MASK: rows count tokens below their
-// vis only.
-template <int NP, int TERMS, bool MASK>
+// vis only.  HALVES blocks of NP columns, each its rows' hi then lo terms.
+// Eight rows' scores leave TMEM while the eight before are summed.  A loop,
+// not unrolled over all rows: 96 rows of straight code per warp do not stay
+// in the instruction cache.
+template <int NP, int TERMS, int HALVES, bool MASK>
 __device__ __forceinline__ float token_sum(uint32_t taddr, const float4 *c, const int *vis, int j) {
-    constexpr int NQ = NP / TERMS;
+    constexpr int NQ = NP / TERMS, kGroups = NQ * HALVES / 8;
+    static_assert(kGroups % 2 == 0, "groups in pairs");
     float sum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int n0 = 0; n0 < NQ; n0 += 8) {
-        float acc[8], lo[8];
-        ld8(taddr + n0, acc);
-        if (TERMS == 2) ld8(taddr + NQ + n0, lo);
-        tc::wait_ld();
+    float acc[2][8], lo[2][8];
+    const auto load = [&](int b, int g) {
+        const uint32_t at = taddr + g * 8 + (HALVES == 2 && g >= kGroups / 2 ? NP - NQ : 0);
+        ld8(at, acc[b]);
+        if (TERMS == 2) ld8(at + NQ, lo[b]);
+    };
+    const auto add = [&](int b, int g) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float4 k = c[n0 + i];
-            if (TERMS == 2) acc[i] = fmaf(lo[i], 0.0625f, acc[i]);
-            const float p = exp2_approx(fmaf(acc[i], k.x, -k.z) + fmaf(acc[i], k.y, -k.w));
-            if (!MASK || j < vis[n0 + i]) sum[i & 1] += p;
+            const float4 k = c[8 * g + i];
+            const float x = TERMS == 2 ? fmaf(lo[b][i], 0.0625f, acc[b][i]) : acc[b][i];
+            const float p = exp2_approx(fmaf(x, k.x, -k.z) + fmaf(x, k.y, -k.w));
+            if (!MASK || j < vis[8 * g + i]) sum[i & 1] += p;
         }
+    };
+    load(0, 0);
+    tc::wait_ld();
+#pragma unroll 1
+    for (int g = 0; g < kGroups; g += 2) {
+        load(1, g + 1);
+        add(0, g);
+        tc::wait_ld();
+        if (g + 2 < kGroups) load(0, g + 2);
+        add(1, g + 1);
+        tc::wait_ld();
     }
     return sum[0] + sum[1];
 }
@@ -588,14 +604,9 @@ __device__ void epilogue(const TokenArgs &a, Misc<Cfg<NP, TERMS, PAIR>> &ms, int
         if (!wait_or_abort(&ms.d_full[wg], (it >> 1) & 1, &ms.abort_flag)) break;
         tc::fence_after();
         const bool whole = ms.all_vis[buf] >= min(j0 + kTile, w.len);
-        float sum = 0.f;
-#pragma unroll
-        for (int half = 0; half < (PAIR ? 2 : 1); ++half) {
-            const float4 *c = ms.c[buf] + half * C::NQ;
-            const int *vis = ms.vis[buf] + half * C::NQ;
-            sum += whole ? token_sum<NP, TERMS, false>(taddr + half * NP, c, vis, j)
-                         : token_sum<NP, TERMS, true>(taddr + half * NP, c, vis, j);
-        }
+        constexpr int kHalves = PAIR ? 2 : 1;
+        const float sum = whole ? token_sum<NP, TERMS, kHalves, false>(taddr, ms.c[buf], ms.vis[buf], j)
+                                : token_sum<NP, TERMS, kHalves, true>(taddr, ms.c[buf], ms.vis[buf], j);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) arrive_lead<PAIR>(&ms.d_free[wg]);
