@@ -302,17 +302,24 @@ __device__ __forceinline__ uint32_t elect_one() {
     return r;
 }
 
-// Arrive on CTA 0's `bar`, from either CTA of a pair.
-template <bool PAIR>
-__device__ __forceinline__ void arrive_lead(uint64_t *bar) {
-    if (!PAIR) {
+// Arrive on CTA 0's `bar`, from either CTA of a pair.  RELAXED: where only
+// TMEM reads (fenced by the caller) go before it; a release at cluster scope
+// would wait for this thread's global stores, several thousand cycles under
+// the stream of rows.
+template <bool PAIR, bool RELAXED = false>
+__device__ __forceinline__ void arrive_lead(uint64_t *bar, int rank) {
+    if (!PAIR || rank == 0)
         mbar_arrive(bar);
-        return;
-    }
-    asm volatile(
-        "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
-        : "memory");
+    else if (RELAXED)
+        asm volatile(
+            "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+            "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+            "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+            : "memory");
 }
 
 // wait_or_abort for what the other CTA has written too.
@@ -354,7 +361,7 @@ __device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, 
         for (int it = 0; w.valid(); ++it, w.next(a)) {
             const int s = it % kStages;
             if (!wait_or_abort(&ms.kv_full[s], (it / kStages) & 1, &ms.abort_flag)) break;
-            if (one) arrive_lead<PAIR>(&ms.kv_full[s]);
+            if (one) arrive_lead<PAIR>(&ms.kv_full[s], rank);
             __syncwarp();
         }
         return;
@@ -609,7 +616,7 @@ __device__ void epilogue(const TokenArgs &a, Misc<Cfg<NP, TERMS, PAIR>> &ms, int
                                 : token_sum<NP, TERMS, kHalves, true>(taddr, ms.c[buf], ms.vis[buf], j);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) arrive_lead<PAIR>(&ms.d_free[wg]);
+        if (lane == 0) arrive_lead<PAIR, true>(&ms.d_free[wg], rank);
         if (real) out[i] = old + sum;
     }
 }
@@ -687,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             prep_unit<NP, TERMS, PAIR>(a, sm, ms, w.r, w.len, grp, w.unit, rank);
             tc::fence_async_smem();     // generic-proxy writes -> tensor-core reads
             __syncwarp();
-            if (lane == 0) arrive_lead<PAIR>(&ms.q_ready);
+            if (lane == 0) arrive_lead<PAIR>(&ms.q_ready, rank);
             // The next request's (empty ones passed over), if this CTA gets to it.
             if (w.left > w.ntiles - w.t) {
                 int r = w.r + 1, base;
