@@ -10,7 +10,8 @@ The three calls of one decode step of a Multi-head Latent Attention layer:
 and the operators around them: ``kv_append``, ``add_rms_norm``,
 ``token_weights`` / ``kv_evict`` and ``value_gate_lora``.
 
-This module only marshals arguments: it checks dtypes / shapes, allocates
+This module only marshals arguments (for the last four calls through a
+compiled module, ``csrc/binding.cpp``): it checks dtypes / shapes, allocates
 outputs with torch (device memory), passes raw pointers and the current CUDA
 stream to the native library, and turns error codes into exceptions.  Every
 step of the computation runs in the library's CUDA kernels; there is no
@@ -21,6 +22,8 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -463,56 +466,28 @@ def kv_append(kv, kv_c, k_pe, slots, k_scale, *, stream=None):
     return kv
 
 
-_NORM_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NORM_QUANT = {None: 0, "row": 1, "group": 2, "static": 3}
-_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_ops_module = None
 
 
-def _empty(shape, dtype, device, stream):
-    """An output on ``device``; one that a call launches on a ``stream`` of
-    its own is allocated there, so that its memory is not still in use by
-    work of the current stream."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _launch(fn, where, dev, stream, *args):
-    """``fn(*args, stream)`` with device number ``dev`` current (plain ints
-    are passed as pointers)."""
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    if torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream, dev))
-    else:
-        st = fn(*args, _stream(stream, dev))
-    if st != MLA_OK:
-        _check(st, where)
-
-
-# Checks of the calls whose kernels take a few microseconds: the messages are
-# made only when one fails.
-
-
-def _dense(t, name, dtype, shape, dev):
-    """A contiguous tensor of this type and shape on device number ``dev``
-    (-1: the host, which the launch then refuses)."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on the first argument's device"
-                         % (name, dtype, list(shape)))
-
-
-def _rows_of(t, name, dtype, shape, dev):
-    """Row stride of a 2-D tensor of this type and shape whose rows are
-    contiguous, on device number ``dev``."""
-    if t.dtype != dtype or t.shape != shape or t.stride(1) != 1 or t.get_device() != dev:
-        raise ValueError("%s must be a %s tensor of shape %s with contiguous rows on the first argument's device"
-                         % (name, dtype, list(shape)))
-    return t.stride(0) if shape[0] > 1 else shape[1]
+def _ops():
+    """The compiled Python module (``csrc/binding.cpp``) of the calls below:
+    it checks the arguments (ValueError), allocates the outputs and calls the
+    library with the tensors' device current, on ``stream`` or the device's
+    current stream; raises if it has not been built."""
+    global _ops_module
+    if _ops_module is None:
+        library()
+        path = _build.ops_path()
+        if not os.path.exists(path):
+            raise RuntimeError("mla_decode_paged_gb300: native module %s is missing; run "
+                               "mla_decode_paged_gb300.build() first (no fallback exists)" % path)
+        loader = importlib.machinery.ExtensionFileLoader("mla_ops", path)
+        spec = importlib.util.spec_from_file_location("mla_ops", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _ops_module = module
+    return _ops_module
 
 
 def add_rms_norm(x, weight, eps, residual=None, *, quant=None, scale=None, out=None, out_scales=None,
@@ -530,54 +505,13 @@ def add_rms_norm(x, weight, eps, residual=None, *, quant=None, scale=None, out=N
     ``[T, ceil(D / 128)]`` (128 columns each) or ``"static"`` (the float
     ``scale``; no scales returned): a code stands for code * scale.
     """
-    xtype = x.dtype
-    if x.dim() != 2 or xtype not in (_BF16, torch.float16):
-        raise ValueError("x must be bf16 or fp16 [T, D]")
-    shape = x.shape
-    T, D = shape
-    dev = x.get_device()
-    device = x.device
-    xs = _rows_of(x, "x", xtype, shape, dev)
-    _dense(weight, "weight", xtype, (D,), dev)
     q = _NORM_QUANT.get(quant)
     if q is None:
         raise ValueError("quant must be None, 'row', 'group' or 'static'")
-    if (scale is not None) != (q == 3):
-        raise ValueError("scale goes with quant='static'")
-    rp = rop = sp = None
-    rs = ros = rt = 0
-    if residual is not None:
-        rtype = residual.dtype
-        if rtype != xtype and rtype != _F32:
-            raise ValueError("residual must be x's type or float32")
-        rt = _NORM_TYPES[rtype]
-        rs = _rows_of(residual, "residual", rtype, shape, dev)
-        if residual_out is None:
-            residual_out = _empty(shape, rtype, device, stream)
-            ros = D
-        else:
-            ros = _rows_of(residual_out, "residual_out", rtype, shape, dev)
-        rp, rop = residual.data_ptr(), residual_out.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    otype = _E4M3 if q else xtype
-    if out is None:
-        out = _empty(shape, otype, device, stream)
-        os_ = D
-    else:
-        os_ = _rows_of(out, "out", _U8 if q and out.dtype == _U8 else otype, shape, dev)
-    if q == 1 or q == 2:
-        sshape = (T,) if q == 1 else (T, (D + 127) // 128)
-        if out_scales is None:
-            out_scales = _empty(sshape, _F32, device, stream)
-        else:
-            _dense(out_scales, "out_scales", _F32, sshape, dev)
-        sp = out_scales.data_ptr()
-    elif out_scales is not None:
-        raise ValueError("out_scales goes with quant='row' or 'group'")
-    _launch(library().mla_add_rms_norm, "mla_add_rms_norm", dev, stream, x.data_ptr(), xs, _NORM_TYPES[xtype], rp, rs,
-            rt, weight.data_ptr(), eps, T, D, q, scale or 0.0, out.data_ptr(), os_, sp, rop, ros)
-    return out, out_scales, residual_out
+    r = (_ops_module or _ops()).add_rms_norm(x, weight, eps, residual, q, scale, out, out_scales, residual_out, stream)
+    if type(r) is int:
+        _check(r, "mla_add_rms_norm")
+    return r
 
 
 def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qlen=1, weights=None, decay=1.0,
@@ -596,47 +530,11 @@ def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qle
     (allocated if not given and needed; not shared by calls that may
     overlap).
     """
-    qtype = q.dtype
-    q8 = qtype == _E4M3 or qtype == _U8
-    if not (q8 or qtype == _BF16) or q.dim() != 3 or q.shape[2] != D_QK:
-        raise ValueError("q must be bf16 or fp8 e4m3 [S, H, 576]")
-    dev = q.get_device()
-    S, hpad, _ = q.shape
-    if heads is None:
-        heads = hpad
-    R, n = indptr.numel() - 1, pages.numel()
-    if q.stride(2) != 1 or (hpad > 1 and q.stride(1) != D_QK):
-        raise ValueError("q rows must have contiguous [H, 576] heads")
-    if S != R * qlen or heads > hpad:
-        raise ValueError("q shape does not match indptr / qlen / heads")
-    if kv.dtype != _U8 and kv.dtype != _E4M3:
-        raise ValueError("kv must be uint8 codes or float8_e4m3fn")
-    pool = kv.shape[0]
-    _dense(kv, "kv", kv.dtype, (pool, D_QK), dev)
-    _dense(pages, "pages", _I32, (n,), dev)
-    _dense(indptr, "indptr", _I32, (R + 1,), dev)
-    _dense(lse, "lse", _F32, (S, heads), dev)
-    wp = None
-    if weights is not None:
-        _dense(weights, "weights", _F32, (n,), dev)
-        wp = weights.data_ptr()
-    if out is None:
-        out = _empty((n,), _F32, q.device, stream)
-    else:
-        _dense(out, "out", _F32, (n,), dev)
-    wsp, wsn = None, 0
-    if workspace is None:
-        need = token_weights_workspace(qlen, heads, n, q8)
-        if need:
-            workspace = _empty((need,), _U8, q.device, stream)
-    if workspace is not None:
-        wsp, wsn = workspace.data_ptr(), workspace.numel()
-        _dense(workspace, "workspace", _U8, (wsn,), dev)
-    _launch(library().mla_token_weights, "mla_token_weights", dev, stream, q.data_ptr(),
-            q.stride(0) if S > 1 else heads * D_QK, kv.data_ptr(), pool, pages.data_ptr(), n, indptr.data_ptr(), R,
-            qlen, heads, scale, kv_scale, q_scale, lse.data_ptr(), 0.0 if wp is None else decay, wp, out.data_ptr(),
-            (ATTEND_CAUSAL if causal else 0) | (ATTEND_Q_FP8 if q8 else 0), wsp, wsn)
-    return out
+    r = (_ops_module or _ops()).token_weights(q, kv, pages, indptr, scale, kv_scale, lse, heads, qlen, weights, decay,
+                                              causal, q_scale, out, workspace, stream)
+    if type(r) is int:
+        _check(r, "mla_token_weights")
+    return r
 
 
 def token_weights_workspace(qlen, heads, num_pages, fp8_query=False):
@@ -658,36 +556,11 @@ def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=Non
     are), then the freed rows; ``weights_out`` the kept tokens' weights,
     then zeros.  ``budget``: an int, or int32 ``[R]`` on the device.
     """
-    dev = pages.get_device()
-    device = pages.device
-    n, R1 = pages.numel(), indptr.numel()
-    if R1 < 1:
-        raise ValueError("indptr must have R + 1 entries")
-    _dense(pages, "pages", _I32, (n,), dev)
-    _dense(indptr, "indptr", _I32, (R1,), dev)
-    _dense(weights, "weights", _F32, (n,), dev)
-    bp = None
-    if isinstance(budget, torch.Tensor):
-        _dense(budget, "budget", _I32, (R1 - 1,), dev)
-        bp, budget = budget.data_ptr(), 0
-    if pages_out is None:
-        pages_out = _empty((n,), _I32, device, stream)
-    else:
-        _dense(pages_out, "pages_out", _I32, (n,), dev)
-    if indptr_out is None:
-        indptr_out = _empty((R1,), _I32, device, stream)
-    else:
-        _dense(indptr_out, "indptr_out", _I32, (R1,), dev)
-    if weights_out is None:
-        weights_out = _empty((n,), _F32, device, stream)
-    else:
-        _dense(weights_out, "weights_out", _F32, (n,), dev)
-    if not (-2**31 <= budget < 2**31 and 0 <= recent < 2**31 and 0 <= sinks < 2**31):
-        raise ValueError("budget, recent, sinks must fit int32, recent and sinks >= 0")
-    _launch(library().mla_kv_evict, "mla_kv_evict", dev, stream, pages.data_ptr(), n, indptr.data_ptr(), R1 - 1,
-            weights.data_ptr(), bp, budget, recent, sinks, pages_out.data_ptr(), indptr_out.data_ptr(),
-            weights_out.data_ptr())
-    return pages_out, indptr_out, weights_out
+    r = (_ops_module or _ops()).kv_evict(pages, indptr, weights, budget, recent, sinks, pages_out, indptr_out,
+                                         weights_out, stream)
+    if type(r) is int:
+        _check(r, "mla_kv_evict")
+    return r
 
 
 def value_gate_lora(latent, w_uv, gate, lengths, lora_a, lora_b, adapters, lora_scale, qlen=1, *, out=None,
@@ -702,34 +575,11 @@ def value_gate_lora(latent, w_uv, gate, lengths, lora_a, lora_b, adapters, lora_
     16-byte aligned (allocated if not given; not shared by calls that may
     overlap).
     """
-    if latent.dim() != 3 or lora_a.dim() != 3:
-        raise ValueError("latent must be [S, heads, 512], lora_a [n, rank, 512]")
-    dev = latent.get_device()
-    S, H, _ = latent.shape
-    n, rank, _ = lora_a.shape
-    R = lengths.numel()
-    if R * qlen != S:
-        raise ValueError("lengths must be [S / qlen]")
-    _dense(latent, "latent", _BF16, (S, H, D_LATENT), dev)
-    _dense(w_uv, "w_uv", _BF16, (H, D_V, D_LATENT), dev)
-    _dense(gate, "gate", _BF16, (S, H * D_V), dev)
-    _dense(lengths, "lengths", _I32, (R,), dev)
-    _dense(lora_a, "lora_a", _BF16, (n, rank, D_LATENT), dev)
-    _dense(lora_b, "lora_b", _BF16, (n, H * D_V, rank), dev)
-    _dense(adapters, "adapters", _I32, (R,), dev)
-    _dense(lora_scale, "lora_scale", _F32, (n,), dev)
-    if out is None:
-        out = _empty((S, H * D_V), _BF16, latent.device, stream)
-    else:
-        _dense(out, "out", _BF16, (S, H * D_V), dev)
-    if workspace is None:
-        workspace = _empty((value_gate_lora_workspace(R, qlen, H, rank),), _U8, latent.device, stream)
-    wsn = workspace.numel()
-    _dense(workspace, "workspace", _U8, (wsn,), dev)
-    _launch(library().mla_value_gate_lora, "mla_value_gate_lora", dev, stream, latent.data_ptr(), w_uv.data_ptr(),
-            gate.data_ptr(), lengths.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
-            lora_scale.data_ptr(), n, rank, R, qlen, H, out.data_ptr(), workspace.data_ptr(), wsn)
-    return out
+    r = (_ops_module or _ops()).value_gate_lora(latent, w_uv, gate, lengths, lora_a, lora_b, adapters, lora_scale, qlen,
+                                                out, workspace, stream)
+    if type(r) is int:
+        _check(r, "mla_value_gate_lora")
+    return r
 
 
 def value_gate_lora_workspace(requests, qlen, heads, rank):

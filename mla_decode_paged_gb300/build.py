@@ -3,6 +3,9 @@
 Every ``csrc/*.cu`` translation unit is compiled in parallel for sm_103a
 only, then linked into one shared library (CUDA runtime linked statically,
 so the library carries no dependency on a particular libcudart build).
+``csrc/binding.cpp``, the Python module over part of it, is compiled beside
+them with the host compiler against the installed torch (its version is in
+the module's file name) and linked to the library.
 """
 
 from __future__ import annotations
@@ -11,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +24,39 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmla_decode.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
+
+
+def _torch_dir() -> str:
+    import torch
+
+    return os.path.dirname(torch.__file__)
+
+
+def ops_path() -> str:
+    """The Python module's file, for the installed torch and Python."""
+    import torch
+
+    tag = "%s-%s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+    return os.path.join(BUILD, "mla_ops-%s.so" % "".join(c if c.isalnum() or c in ".-" else "_" for c in tag))
+
+
+def _cuda_include() -> str:
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+
+
+def _ops_compile(obj: str):
+    t = os.path.join(_torch_dir(), "include")
+    import torch
+
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+            "-I" + t, "-I" + os.path.join(t, "torch", "csrc", "api", "include"), "-I" + _cuda_include(),
+            "-I" + sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+
+
+def _ops_link(obj: str, out: str):
+    lib = os.path.join(_torch_dir(), "lib")
+    return ["g++", "-shared", "-o", out, obj, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-L" + BUILD, "-lmla_decode", "-Wl,-rpath,$ORIGIN"]
 
 
 def nvcc() -> str:
@@ -53,13 +90,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [s] + deps):
             jobs.append([cc, *ARCH, *NVCC_FLAGS, "-c", s, "-o", obj])
+    ops = ops_path()
+    ops_obj = ops[:-3] + ".o"
+    ops_stale = force or _stale(ops_obj, [os.path.join(CSRC, "binding.cpp")] + deps)
+    if ops_stale:
+        jobs.append(_ops_compile(ops_obj))
 
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+            raise RuntimeError("%s failed:\n%s\n%s" % (os.path.basename(cmd[0]), " ".join(cmd), r.stderr))
         return r.stderr
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
@@ -70,6 +112,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + ".tmp%d" % os.getpid()
         run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"])
         os.replace(tmp, LIB)
+    if ops_stale or _stale(ops, [ops_obj, LIB]):
+        tmp = ops + ".tmp%d" % os.getpid()
+        run(_ops_link(ops_obj, tmp))
+        os.replace(tmp, ops)
     return LIB
 
 
