@@ -338,7 +338,7 @@ def _own_norm(s):
                                                  quant=s["quant"], scale=s["scale"])
     if scales is None:
         return {"out": out, "residual_out": residual_out}
-    return {"out": out, "scales": scales, "residual_out": residual_out}
+    return {"out": out, "scales": scales.view(out.shape[0], -1), "residual_out": residual_out}
 
 
 def _own_weights(s):
