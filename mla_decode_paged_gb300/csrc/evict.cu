@@ -34,6 +34,8 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kDigits = 3, kOwn = kBins / kThreads;
 constexpr int kSteps = 16;         // tokens a thread holds
 constexpr int kRound = kSteps * kThreads;
+constexpr int kClasses = 6;        // powers of two of blocks, 0 to 4, and more than one round
+constexpr int kInOrder = 32;       // clusters that all run at once
 static_assert(kOwn == 4, "a thread reads its bins as one vector");
 
 struct EvictArgs {
@@ -67,7 +69,9 @@ struct __align__(16) Shared {
     uint32_t hist[kDigits][kBins];
     uint32_t stage[kBins];          // this block's share of the bins from every block
     uint32_t sums[kDigits][kBins];  // and their sums
-    long long red64[3][kWarps];
+    uint32_t red[3][kWarps];
+    uint32_t classes[kWarps][kClasses];     // a warp's requests by the blocks they take
+    int own[4];                             // the cluster's request, its tokens, first entry, kept tokens
     uint32_t scan[kWarps];
     uint32_t warp_kept[kWarps], warp_ties[kWarps];
     uint32_t totals[2];             // this block's sure tokens and ties, for the cluster
@@ -128,51 +132,70 @@ __device__ uint32_t block_scan(uint32_t v, uint32_t *red) {
     return x - v + __shfl_sync(0xffffffffu, s - w, warp);
 }
 
+// Blocks it takes to hold a request, as a power of two; above log_cs where a
+// cluster of 2^log_cs needs more than one round for it.
+__device__ __forceinline__ int blocks_for(int len, int log_cs) {
+    int le = 0;
+    while (le <= log_cs && (len >> le) > kRound) ++le;
+    return le;
+}
+
 // 2^log_cs blocks (a cluster) per request.
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, int log_cs) {
     __shared__ Shared sh;
-    const int r = blockIdx.x >> log_cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = block_rank();
-    int base;
-    const int len = request_len(a.indptr, r, a.num_pages, &base);
-    // The blocks it takes to hold the request, 2^le of them; the others end
-    // (a cluster barrier waits for running threads only).
-    int le = 0;
-    while (le < log_cs && (len >> le) > kRound) ++le;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t below = (1u << lane) - 1, rank = block_rank();
+    // The cluster's request.  Clusters start in order of their number: with
+    // more of them than run at once, the requests of most blocks go first.
+    int r = blockIdx.x >> log_cs, len, base, kept;
+    uint32_t sums[3] = {0, 0, 0};   // kept and all tokens of the requests before it, kept of all (mod 2^32)
+    if (a.R <= kThreads) {
+        int my_base = 0, my_len = 0, my_kept = 0;
+        if (tid < a.R) {
+            my_len = request_len(a.indptr, tid, a.num_pages, &my_base);
+            my_kept = kept_tokens(a, tid, my_len);
+        }
+        int place = tid;
+        if (log_cs > 0 && a.R > kInOrder) {
+            const int mine = tid < a.R ? blocks_for(my_len, log_cs) : -1;
+            uint32_t same = 0;
+#pragma unroll
+            for (int c = 0; c < kClasses; ++c) {
+                const uint32_t m = __ballot_sync(0xffffffffu, mine == c);
+                if (mine == c) same = m;
+                if (lane == 0) sh.classes[warp][c] = __popc(m);
+            }
+            __syncthreads();
+            place = __popc(same & below);
+            for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+                for (int c = 0; c < kClasses; ++c)
+                    if (c > mine || (c == mine && w < warp)) place += sh.classes[w][c];
+        }
+        if (tid < a.R && place == r) {
+            sh.own[0] = tid;
+            sh.own[1] = my_len;
+            sh.own[2] = my_base;
+            sh.own[3] = my_kept;
+        }
+        __syncthreads();
+        r = sh.own[0];
+        len = sh.own[1];
+        base = sh.own[2];
+        kept = sh.own[3];
+        sums[0] = tid < r ? my_kept : 0;
+        sums[1] = tid < r ? my_len : 0;
+        sums[2] = my_kept;
+    } else {
+        len = request_len(a.indptr, r, a.num_pages, &base);
+        kept = kept_tokens(a, r, len);
+    }
+    // The blocks past those that hold the request end (a cluster barrier
+    // waits for running threads only).
+    const int le = min(blocks_for(len, log_cs), log_cs);
     const uint32_t E = 1u << le;
     if (rank >= E) return;
     const bool one = le == 0;
-
-    // Kept and all tokens of the requests before this one, kept of all.
-    long long sums[3] = {0, 0, 0};
-    for (int i = tid; i < a.R; i += kThreads) {
-        int at;
-        const int n = request_len(a.indptr, i, a.num_pages, &at), k = kept_tokens(a, i, n);
-        sums[2] += k;
-        if (i < r) {
-            sums[0] += k;
-            sums[1] += n;
-        }
-    }
-    for (int i = tid; i < kDigits * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], d);
-        if (lane == 0) sh.red64[j][warp] = sums[j];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        sums[j] = lane < kWarps ? sh.red64[j][lane] : 0;
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], d);
-    }
-    const int kept = kept_tokens(a, r, len);
-    if (tid == 0 && rank == 0) {
-        if (r == 0) a.indptr_out[0] = 0;
-        a.indptr_out[r + 1] = (int32_t)(sums[0] + kept);
-    }
     const int recent = a.recent < kept ? a.recent : kept;
     const int sinks = a.sinks < kept - recent ? a.sinks : kept - recent;
     const int lo = sinks, hi = len - recent;        // the tokens that may go
@@ -187,27 +210,58 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
     uint32_t key[kSteps];
     uint32_t valid = 0, free = 0;   // a bit a step: a token, one that may go
     int first = 0, steps = 0;
-    const auto load = [&](int q) {
+    const auto fetch = [&](int q) {                 // weights into key, as they are
         const int q0 = s0 + q * kRound, q1 = min(q0 + kRound, s1);
         const int part = ((q1 - q0 + kWarps - 1) / kWarps + 31) / 32 * 32;
         first = q0 + warp * part + lane;
         steps = part / 32;
         valid = free = 0;
-        float x[kSteps];
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
             const int i = first + 32 * j;
-            x[j] = 0.f;
+            key[j] = 0;
             if (j < steps && i < q1) {
-                x[j] = __ldg(w + i);
+                key[j] = __float_as_uint(__ldg(w + i));
                 valid |= 1u << j;
                 if (i >= lo && i < hi) free |= 1u << j;
             }
         }
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) key[j] = weight_key(x[j]);
     };
-    if (rounds > 0) load(0);
+    const auto convert = [&] {
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) key[j] = weight_key(__uint_as_float(key[j]));
+    };
+    const auto load = [&](int q) {
+        fetch(q);
+        convert();
+    };
+    // On their way during the sums over the requests.
+    if (rounds > 0) fetch(0);
+    for (int i = tid; i < kDigits * kBins / 4; i += kThreads)
+        reinterpret_cast<uint4 *>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+    if (a.R > kThreads)
+        for (int i = tid; i < a.R; i += kThreads) {
+            int at;
+            const int n = request_len(a.indptr, i, a.num_pages, &at), k = kept_tokens(a, i, n);
+            sums[2] += k;
+            if (i < r) {
+                sums[0] += k;
+                sums[1] += n;
+            }
+        }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const uint32_t s = __reduce_add_sync(0xffffffffu, sums[j]);
+        if (lane == 0) sh.red[j][warp] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) sums[j] = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red[j][lane] : 0);
+    if (tid == 0 && rank == 0) {
+        if (r == 0) a.indptr_out[0] = 0;
+        a.indptr_out[r + 1] = (int32_t)(sums[0] + kept);
+    }
+    if (rounds > 0) convert();
 
     // The m-th largest key T of [lo, hi), and how many keys equal to T stay.
     uint32_t T = 0, ties = 0;
@@ -302,15 +356,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
         __syncthreads();
         k = lane < kWarps ? sh.warp_kept[lane] : 0;
         t = lane < kWarps ? sh.warp_ties[lane] : 0;
-        kb = lane < warp ? k : 0;
-        tb = lane < warp ? t : 0;
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) {
-            k += __shfl_xor_sync(0xffffffffu, k, d);
-            t += __shfl_xor_sync(0xffffffffu, t, d);
-            kb += __shfl_xor_sync(0xffffffffu, kb, d);
-            tb += __shfl_xor_sync(0xffffffffu, tb, d);
-        }
+        kb = __reduce_add_sync(0xffffffffu, lane < warp ? k : 0);
+        tb = __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
+        k = __reduce_add_sync(0xffffffffu, k);
+        t = __reduce_add_sync(0xffffffffu, t);
     };
     uint32_t nsure = 0, nties = 0, k, t, kb, tb;
     for (int q = 0; q < rounds; ++q) {
@@ -329,18 +378,14 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
             block_kept = remote(&sh.totals[0], lane);
             block_ties = remote(&sh.totals[1], lane);
         }
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) {
-            block_kept += __shfl_xor_sync(0xffffffffu, block_kept, d);
-            block_ties += __shfl_xor_sync(0xffffffffu, block_ties, d);
-        }
+        block_kept = __reduce_add_sync(0xffffffffu, block_kept);
+        block_ties = __reduce_add_sync(0xffffffffu, block_ties);
     }
 
     // Placement, in position order.  Places past the page list (only a bad
     // indptr makes them) are dropped.
-    const uint32_t out_kept = (uint32_t)min(sums[0], 0x7fffffffll);
-    const uint32_t out_freed = (uint32_t)min(sums[2] + (sums[1] - sums[0]), 0x7fffffffll);
-    const uint32_t below = (1u << lane) - 1, limit = (uint32_t)a.num_pages;
+    const uint32_t out_kept = sums[0], out_freed = sums[2] + (sums[1] - sums[0]);
+    const uint32_t limit = (uint32_t)a.num_pages;
     for (int q = 0; q < rounds; ++q) {
         if (rounds > 1) {
             load(q);
