@@ -481,14 +481,15 @@ cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32
     a.pages_out = pages_out;
     a.indptr_out = indptr_out;
     a.weights_out = weights_out;
-    // The lengths are on the device.  A cluster holds a request of twice the
-    // mean length in one round; more blocks than that mostly end unused, and
-    // each costs its launch (64 requests of 1K to 8K tokens: 10.8 us with 1
-    // or 2 blocks, 15 with 4 or 8, 25 with 16; one of 128K: 157 us with 1,
-    // 49 with 4, 30 with 8, 16 with 16).
-    const int64_t want = 2 * (num_pages / R);
+    // The lengths are on the device.  A cluster holds a request of the mean
+    // length in one round.  Fewer blocks take a long request in rounds (one of
+    // 128K: 157 us with 1, 49 with 4, 28 with 8, 15 with 16); more mostly end
+    // unused, and each costs its launch (64 requests of 1K to 8K: 10.1 us with
+    // 1, 11 with 2, 16 with 4, 18 with 8; 128 of 8K to 32K: 39 with 4, 45 with
+    // 8, 92 with 16; 256 of 128 to 128K: 97 with 4, 80 with 8, 125 with 16).
+    const int64_t mean = (num_pages + R - 1) / R;
     int log_cs = 0;
-    while (log_cs < 4 && (want >> log_cs) > kRound) ++log_cs;
+    while (log_cs < 4 && (mean >> log_cs) > kRound) ++log_cs;
     return launch(a, log_cs, st);
 }
 
