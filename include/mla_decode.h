@@ -434,12 +434,13 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
  *   lse          f32 [num_requests * qlen, heads].
  *   decay        finite; 0 does not read weights.
  *   weights      f32 [num_pages]; may be NULL when decay is 0.
- *   out          f32 [num_pages] (written); may be weights itself, otherwise
- *                must not overlap it.
+ *   out          f32 [num_pages] (written); may be weights itself, no other
+ *                overlap with what is read.
  * num_pages up to 2^31 - 65536, num_requests up to 2^24.
  *   workspace    device, 16-byte aligned, at least
  *                mla_token_weights_workspace() bytes (may be NULL for 0);
- *                holds nothing between calls, but two calls that may overlap
+ *                holds nothing between calls and overlaps no other
+ *                argument; two calls (or captured graphs) that may overlap
  *                on the GPU need one each.
  * A page outside the pool reads as row 0 of the pool and sets
  * MLA_DEV_BAD_PAGE; a bad indptr entry sets MLA_DEV_BAD_INDPTR and leaves
@@ -469,7 +470,9 @@ int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsi
  *   pages_out[K .. N)     freed rows, request by request, in order
  *   weights_out[0 .. K)   the kept tokens' weights; [K .. N) zeros
  * Entries from N on are left as they were.  The cache itself is not touched
- * and pages are not looked up: a row is only an index here.
+ * and pages are not looked up: a row is only an index here, and one that
+ * several requests hold (a shared prefix) may be kept by one and freed by
+ * another.
  *
  *   pages, weights  int32 / f32 [num_pages]; indptr int32 [num_requests + 1].
  *   budgets         int32 [num_requests], device; NULL: `budget` for all.
@@ -506,8 +509,9 @@ mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *
  *   adapters     int32 [num_requests], lora_scale f32 [num_adapters], device
  *   workspace    device, 16-byte aligned, at least
  *                mla_value_gate_lora_workspace() bytes; holds nothing
- *                between calls, but two calls that may overlap on the GPU
- *                need one each.
+ *                between calls; two calls (or captured graphs) that may
+ *                overlap on the GPU need one each.
+ * Neither out nor the workspace overlaps another argument.
  */
 #define MLA_MAX_LORA_RANK 128
 mla_status mla_value_gate_lora(const void *latent, const void *w_uv, const void *gate, const int32_t *lengths,

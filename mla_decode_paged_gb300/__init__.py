@@ -554,7 +554,9 @@ def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=Non
     weights_out)``: ``pages_out`` holds the kept rows of every request in
     order (``indptr_out`` counts them; both go to :func:`attend` as they
     are), then the freed rows; ``weights_out`` the kept tokens' weights,
-    then zeros.  ``budget``: an int, or int32 ``[R]`` on the device.
+    then zeros.  A row that several requests hold (a shared prefix) may be
+    kept by one and freed by another.  ``budget``: an int, or int32 ``[R]``
+    on the device.
     """
     r = (_ops_module or _ops()).kv_evict(pages, indptr, weights, budget, recent, sinks, pages_out, indptr_out,
                                          weights_out, stream)

@@ -93,6 +93,18 @@ bool overlap(const void *p, int64_t pn, const void *q, int64_t qn) {
     return p && q && pn > 0 && qn > 0 && a < b + (uintptr_t)qn && b < a + (uintptr_t)pn;
 }
 
+struct Span {
+    const void *p;
+    int64_t n;
+};
+
+template <int N>
+bool overlaps(const Span &w, const Span (&in)[N]) {
+    for (const Span &x : in)
+        if (overlap(w.p, w.n, x.p, x.n)) return true;
+    return false;
+}
+
 // Rows of `width` bytes every `stride` bytes.
 struct Rows {
     const void *p;
@@ -676,13 +688,18 @@ mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv
     if (pool_rows > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "pool_rows above 2^31 - 1");
     if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 65536");
     if (num_requests > kMaxRequests) return fail(MLA_ERR_UNSUPPORTED, "num_requests above 2^24");
-    if (out != weights && overlap(out, num_pages * 4, weights, num_pages * 4))
-        return fail(MLA_ERR_INVALID, "out overlaps weights");
+    if (q_row_stride > INT64_MAX / 2 / MLA_MAX_QLEN / kMaxRequests)
+        return fail(MLA_ERR_INVALID, "q_row_stride too large");
+    const int64_t rows = (int64_t)num_requests * qlen, n = num_pages * 4;
+    const Span in[5] = {{q, ((rows - 1) * q_row_stride + heads * MLA_D_QK) * (q8 ? 1 : 2)}, {kv, pool_rows * MLA_D_QK},
+                        {pages, n}, {indptr, ((int64_t)num_requests + 1) * 4}, {lse, rows * heads * 4}};
+    if (out != weights && overlap(out, n, weights, n)) return fail(MLA_ERR_INVALID, "out overlaps weights");
+    if (overlaps({out, n}, in)) return fail(MLA_ERR_INVALID, "out overlaps an input");
     const int64_t need = mla::token_weights_workspace(qlen * heads, q8, num_pages);
     if (workspace_bytes < need || (need > 0 && !workspace)) return fail(MLA_ERR_INVALID, "workspace too small");
     if (need > 0 && !aligned(workspace, 16)) return fail(MLA_ERR_INVALID, "misaligned workspace (16 bytes)");
-    if (overlap(workspace, need, out, num_pages * 4) || overlap(workspace, need, weights, num_pages * 4))
-        return fail(MLA_ERR_INVALID, "workspace overlaps weights or out");
+    if (overlap(workspace, need, out, n) || overlap(workspace, need, weights, n) || overlaps({workspace, need}, in))
+        return fail(MLA_ERR_INVALID, "workspace overlaps weights, out or an input");
     const int sms = device_sms();
     if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
     cudaError_t e = mla::token_weights_launch(q, q_row_stride, kv, pool_rows, pages, num_pages, indptr, num_requests,
@@ -714,11 +731,10 @@ mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *
     if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 65536");
     if (num_requests > kMaxRequests) return fail(MLA_ERR_UNSUPPORTED, "num_requests above 2^24");
     const int64_t n = num_pages * 4, r = (int64_t)num_requests * 4;
-    const struct { const void *p; int64_t n; } in[4] = {{pages, n}, {weights, n}, {indptr, r + 4}, {budgets, r}},
-                                               to[3] = {{pages_out, n}, {weights_out, n}, {indptr_out, r + 4}};
+    const Span in[4] = {{pages, n}, {weights, n}, {indptr, r + 4}, {budgets, r}};
+    const Span to[3] = {{pages_out, n}, {weights_out, n}, {indptr_out, r + 4}};
     for (int i = 0; i < 3; ++i) {
-        for (const auto &x : in)
-            if (overlap(to[i].p, to[i].n, x.p, x.n)) return fail(MLA_ERR_INVALID, "an output overlaps an input");
+        if (overlaps(to[i], in)) return fail(MLA_ERR_INVALID, "an output overlaps an input");
         for (int j = 0; j < i; ++j)
             if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return fail(MLA_ERR_INVALID, "two outputs overlap");
     }
@@ -763,6 +779,14 @@ mla_status mla_value_gate_lora(const void *latent, const void *w_uv, const void 
     if ((int64_t)num_adapters * heads * MLA_D_V > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "too many adapters");
     const int64_t need = mla::value_lora_workspace(S, heads, rank);
     if (workspace_bytes < need || (need > 0 && !workspace)) return fail(MLA_ERR_INVALID, "workspace too small");
+    const int64_t row = (int64_t)heads * MLA_D_V * 2;
+    const Span in[8] = {{latent, S * heads * MLA_D_LATENT * 2}, {w_uv, row * MLA_D_LATENT}, {gate, S * row},
+                        {lengths, (int64_t)num_requests * 4}, {lora_a, (int64_t)num_adapters * rank * MLA_D_LATENT * 2},
+                        {lora_b, num_adapters * row * rank}, {adapters, (int64_t)num_requests * 4},
+                        {lora_scale, (int64_t)num_adapters * 4}};
+    if (overlaps({out, S * row}, in)) return fail(MLA_ERR_INVALID, "out overlaps an input");
+    if (overlap(workspace, need, out, S * row) || overlaps({workspace, need}, in))
+        return fail(MLA_ERR_INVALID, "workspace overlaps out or an input");
     const int sms = device_sms();
     if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
     cudaError_t e = mla::value_lora_launch(latent, w_uv, gate, lengths, lora_a, lora_b, adapters, lora_scale,

@@ -144,16 +144,18 @@ struct Walk {
     }
 };
 
-// This CTA's range of the batch's tiles -> ms.start.
+// This CTA's range of the batch's tiles -> ms.start.  Requests that share
+// entries (a bad indptr only) count up to what the page list could hold.
 template <class C>
 __device__ void find_start(const TokenArgs &a, Misc<C> &ms, int v) {
-    __shared__ int part[kThreads / 32 + 1];
+    __shared__ long long part[kThreads / 32 + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const auto tiles_of = [&](int r) {
         int base;
         return (request_len(a.indptr, r, a.num_pages, &base) + C::Tokens - 1) / C::Tokens;
     };
-    int mine = 0, sum = 0;
+    int mine = 0;
+    long long sum = 0;
     for (int r = tid; r < a.R; r += kThreads) {
         const int n = tiles_of(r);
         if (r == tid) mine = n;
@@ -162,9 +164,10 @@ __device__ void find_start(const TokenArgs &a, Misc<C> &ms, int v) {
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) part[warp] = sum;
     __syncthreads();
-    int total = 0;
+    long long total = 0;
     for (int w = 0; w < kThreads / 32; ++w) total += part[w];
-    const int64_t lo = (int64_t)total * v / a.virt, hi = (int64_t)total * (v + 1) / a.virt;
+    total = min(total, (long long)(a.num_pages / C::Tokens + a.R));
+    const int64_t lo = total * v / a.virt, hi = total * (v + 1) / a.virt;
     if (tid == 0) ms.start[2] = (int)(hi - lo);
     int64_t before = 0;   // tiles of the requests before this chunk
     for (int r0 = 0; r0 < a.R && before <= lo; r0 += kThreads) {
@@ -179,7 +182,7 @@ __device__ void find_start(const TokenArgs &a, Misc<C> &ms, int v) {
         if (lane == 31) part[warp] = incl;
         __syncthreads();
         int64_t at = before;
-        int all = 0;
+        int64_t all = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) at += part[w];
             all += part[w];

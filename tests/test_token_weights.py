@@ -61,6 +61,13 @@ def _call(lib, **kw):
     (dict(qlen=16, ws=H + 8, wsn=1 << 20), b"misaligned workspace"),
     (dict(qlen=16, ws=G, wsn=1 << 20), b"workspace overlaps"),
     (dict(qlen=16, ws=F, wsn=1 << 20), b"workspace overlaps"),
+    (dict(qlen=16, ws=B, wsn=1 << 20), b"workspace overlaps"),
+    (dict(qs=1 << 61), b"q_row_stride"),
+    (dict(out=A + 12 * 576 * 4 - 4), b"out overlaps"),
+    (dict(out=B + 99 * 576), b"out overlaps"),
+    (dict(out=C), b"out overlaps"),
+    (dict(out=D + 8), b"out overlaps"),
+    (dict(out=E + 2 * 12 * 4 - 4), b"out overlaps"),
 ])
 def test_refusals(lib, kw, msg):
     assert _call(lib, **kw) == mla.MLA_ERR_INVALID
@@ -288,6 +295,22 @@ def test_bad_pages_and_bad_page_lists_are_flagged():
                           out=out[:350])
         assert mla.device_status() == mla.DEV_BAD_INDPTR
         assert (out[350:] == -7).all()
+
+
+@pytest.mark.gpu
+def test_page_list_named_again_and_again():
+    # every other entry of indptr goes back to 0: the requests in between are bad, the others all tokens each,
+    # thousands of times the list's tiles
+    q, kv, pages, indptr = _make([300], 1, 12, 12, 10)
+    _, _, lse = _formula(q, kv, pages, [300], 12, 1, 0.05, False)
+    R = 3001
+    ind = torch.zeros(R + 1, dtype=torch.int32, device=DEV)
+    ind[1::2] = 300
+    out = torch.full((300 + 64,), -7.0, device=DEV)
+    mla.token_weights(q.expand(R, -1, -1).contiguous(), kv, pages, ind, 0.05, 1.0, lse.expand(R, -1).contiguous(),
+                      out=out[:300])
+    assert mla.device_status() == mla.DEV_BAD_INDPTR
+    assert (out[300:] == -7).all()
 
 
 @pytest.mark.gpu

@@ -45,6 +45,12 @@ def _call(lib, **kw):
     (dict(la=E + 8), b"misaligned"),
     (dict(ws=J + 8), b"misaligned"),
     (dict(gate=C + 2), b"misaligned"),
+    (dict(out=C), b"out overlaps"),
+    (dict(out=A + 8 * 12 * 1024 - 4), b"out overlaps"),
+    (dict(out=H + 8), b"out overlaps"),
+    (dict(ws=I), b"workspace overlaps"),
+    (dict(ws=B + 12 * 128 * 1024 - 16), b"workspace overlaps"),
+    (dict(ws=G), b"workspace overlaps"),
 ])
 def test_refusals(lib, kw, msg):
     assert _call(lib, **kw) == mla.MLA_ERR_INVALID
