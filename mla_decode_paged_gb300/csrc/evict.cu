@@ -10,7 +10,8 @@
 // requests, by the chain of dependent steps for one.
 //
 // Design: a cluster of blocks per request, as many of them as it takes to
-// hold it (the others end at once), each with a contiguous slice of its tokens and every warp with a contiguous part of that, whose keys
+// hold it (the others end at once), each with a contiguous slice of its
+// tokens and every warp with a contiguous part of that, whose keys
 // (order-preserving 32-bit images of the weights) stay in registers: 16 a
 // thread, 8,192 tokens a block.  A longer slice is taken in rounds of that
 // size, read again for every step.  The m-th largest key is found by radix
@@ -21,6 +22,11 @@
 // histogram per digit: none is reused).  What each warp keeps is counted
 // by ballots, the offsets of warps and blocks are exchanged once, and the
 // tokens are placed by the ballots again.
+//
+// Measured: 15.0 us for one request of 128K tokens, 10.1 for 64 of 1K to 8K,
+// 80 for 256 of 128 to 128K (log-uniform, 5.0 M tokens, 1.0 TB/s: its counts
+// and placements are bound by instructions, 1.7 a cycle and SM, and by how
+// many clusters an SM holds).
 #include <atomic>
 
 #include <cuda_runtime.h>
@@ -483,13 +489,17 @@ cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32
     a.weights_out = weights_out;
     // The lengths are on the device.  A cluster holds a request of the mean
     // length in one round.  Fewer blocks take a long request in rounds (one of
-    // 128K: 157 us with 1, 49 with 4, 28 with 8, 15 with 16); more mostly end
-    // unused, and each costs its launch (64 requests of 1K to 8K: 10.1 us with
-    // 1, 11 with 2, 16 with 4, 18 with 8; 128 of 8K to 32K: 39 with 4, 45 with
-    // 8, 92 with 16; 256 of 128 to 128K: 97 with 4, 80 with 8, 125 with 16).
+    // 128K: 149 us with 1, 82 with 2, 46 with 4, 28 with 8, 15 with 16); more
+    // mostly end unused, and each costs its launch (64 requests of 1K to 8K:
+    // 10.1 us with 1, 11 with 2, 16 with 4, 18 with 8; 128 of 8K to 32K: 39
+    // with 4, 45 with 8, 92 with 16; 256 of 128 to 128K: 97 with 4, 80 with 8,
+    // 125 with 16).  A few requests take the blocks that half the SMs hold:
+    // these cost nothing (8 of 4K: 8.2 us with 1 to 8, 11.4 with 16), and one
+    // request may be much longer than the mean (15 of 1K and one of 128K: 46
+    // us with 4, 83 with the mean's 2).
     const int64_t mean = (num_pages + R - 1) / R;
     int log_cs = 0;
-    while (log_cs < 4 && (mean >> log_cs) > kRound) ++log_cs;
+    while (log_cs < 4 && ((mean >> log_cs) > kRound || ((int64_t)R << (log_cs + 1)) <= sms / 2)) ++log_cs;
     return launch(a, log_cs, st);
 }
 
