@@ -775,7 +775,7 @@ mla_status mla_value_gate_lora(const void *latent, const void *w_uv, const void 
         !aligned(adapters, 4) || !aligned(lora_scale, 4))
         return fail(MLA_ERR_INVALID, "misaligned pointer (latent, w_uv, lora_a, lora_b, workspace need 16 bytes)");
     const int64_t S = (int64_t)num_requests * qlen;
-    if (S > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "too many rows");
+    if (S > 1 << 29) return fail(MLA_ERR_UNSUPPORTED, "too many rows");
     if ((int64_t)num_adapters * heads * MLA_D_V > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "too many adapters");
     const int64_t need = mla::value_lora_workspace(S, heads, rank);
     if (workspace_bytes < need || (need > 0 && !workspace)) return fail(MLA_ERR_INVALID, "workspace too small");

@@ -33,8 +33,8 @@
 //       warps 0..7   epilogue: the sum from TMEM, gated, while the next
 //                    tile's projection runs (its D is double-buffered)
 //       warps 8..13  one ring slot each: T rows and B into it
-//       warp 14      latents and W_UV
-//       warp 15      MMA issuer
+//       warp 14      latents and W_UV, and their MMAs
+//       warp 15      the entries' MMAs
 #include <algorithm>
 
 #include <cuda.h>
@@ -53,16 +53,24 @@ struct LoraArgs {
     const float *scale;
     __nv_bfloat16 *t;       // [S * H, 2, rank]: hi, lo
     __nv_bfloat16 *out;
+    uint64_t inv_qlen;
+    int add_both;           // the ring's kernel: 1, two tiles' low-rank products fit TMEM
     int S, qlen, H, rank, n;
 };
 
-// Request r's adapter, -1 for none (and, flagged, for an index outside).
-__device__ __forceinline__ int adapter_of(const LoraArgs &p, int r) {
-    const int a = __ldg(p.adapters + r);
+// t / qlen for 0 <= t < 2^29: with inv_qlen = ceil(2^35 / qlen) the quotient
+// is too large by less than t / 2^35 < 1 / qlen.
+__device__ __forceinline__ int request_of(const LoraArgs &p, int t) { return (int)((uint64_t)t * p.inv_qlen >> 35); }
+
+// An adapter index; -1 for none and, flagged, for one outside.
+__device__ __forceinline__ int valid_adapter(const LoraArgs &p, int a) {
     if (a >= -1 && a < p.n) return a;
     flag(MLA_DEV_BAD_ADAPTER);
     return -1;
 }
+
+// Request r's.
+__device__ __forceinline__ int adapter_of(const LoraArgs &p, int r) { return valid_adapter(p, __ldg(p.adapters + r)); }
 
 // Two values as bf16 pairs hi + lo; no lo beside an infinite hi (inf - inf).
 __device__ __forceinline__ void two_terms(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -535,7 +543,7 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
 
 // ------------------------------------------- project: B T through a ring of tcgen05 MMAs
 
-constexpr int kEpiWarps = 8, kSlotWarp0 = 8, kMaxSlots = 6, kLoadWarp = 14, kIssueWarp = 15;
+constexpr int kEpiWarps = 8, kSlotWarp0 = 8, kMaxSlots = 6, kLatentWarp = 14, kItemWarp = 15;
 constexpr int kThreads = 16 * 32;
 constexpr int kWin = 16;                           // rows of a window
 
@@ -551,11 +559,23 @@ struct Tile {
     static constexpr int kSlots = RB == 32 ? kMaxSlots : 3;
     static constexpr int kSmem = kSlotOff + kSlots * kSlot + 1024;
     static constexpr int kRows = NR / 2;           // rows per thread in the epilogue
-    // TMEM columns: two tiles' projections, then one tile's entries.
-    static constexpr int kAddCols = 2 * NR, kMaxItems = (512 - kAddCols) / kWin;
-    static_assert(kMaxItems >= (NR == 16 ? 16 : 2 * 9), "the entries of a tile (NR 32: two rows a request or more)");
+    // TMEM columns: two tiles' projections, then the entries of one tile or,
+    // in halves of kAddBuf, of two.
+    static constexpr int kAddCols = 2 * NR, kAddBuf = (512 - kAddCols) / 2 / kWin * kWin;
+    static_assert((512 - kAddCols) / kWin >= NR / kWin * 9, "the entries of a tile, at two rows a request or more");
     static constexpr uint32_t kSwz = RB == 32 ? tc::kSw64 : tc::kSw128, kSbo = 16 * RB;
 };
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok;
+}
 
 // 8 consecutive f32 TMEM columns of this warp's lanes.
 __device__ __forceinline__ void ld8(uint32_t taddr, float *v) {
@@ -591,9 +611,8 @@ struct Entries {
     __device__ void open(const LoraArgs &p) {       // the window's items
         t0 = tile * NR + win * kWin;
         nrows = min(kWin, p.S - t0);
-        const int per = (p.qlen + 7) / 8;
-        r0 = t0 / p.qlen;
-        items = nrows <= 0 ? 0 : ((t0 + nrows - 1) / p.qlen - r0 + 1) * per;
+        r0 = request_of(p, t0);
+        items = nrows <= 0 ? 0 : (request_of(p, t0 + nrows - 1) - r0 + 1) << (p.qlen > 8);
     }
     __device__ void init(const LoraArgs &p) {
         tile = blockIdx.x;
@@ -606,10 +625,9 @@ struct Entries {
 
 template <int NR, int RB>
 struct Shared {
-    uint64_t w_full, x_full, x_empty, d_full[2], d_free[2], add_free, s_full[kMaxSlots], s_empty[kMaxSlots], fin;
+    uint64_t w_full, x_full, x_empty, d_full[2], d_free[2], add_free[2], s_full[kMaxSlots], s_empty[kMaxSlots], fin;
     uint32_t tmem;
     int abort_flag;
-    uint8_t used[kMaxSlots];        // a slot's entry has an adapter
 };
 
 // Fills slot s with entries s, s + slots, ... of the block.
@@ -619,7 +637,7 @@ __device__ void slot_filler(const LoraArgs &p, const CUtensorMap *mb, uint8_t *s
     using T = Tile<NR, RB>;
     const int lane = threadIdx.x & 31;
     uint8_t *slot = sm + T::kSlotOff + s * T::kSlot;
-    const int per = (p.qlen + 7) / 8;
+    const int log_per = p.qlen > 8;     // a request's items, as a power of two
     Entries<NR, RB> e;
     e.init(p);
     int n = 0, skip = s;            // uses of the slot; entries to pass by first
@@ -633,27 +651,30 @@ __device__ void slot_filler(const LoraArgs &p, const CUtensorMap *mb, uint8_t *s
             if (e.tile < tiles) e.open(p);
             continue;
         }
-        const int item = skip / e.chunks, k0 = (skip - item * e.chunks) * RB;
+        const int item = e.chunks == 2 ? skip >> 1 : skip / e.chunks, k0 = (skip - item * e.chunks) * RB;
         skip += T::kSlots;
-        const int r = e.r0 + item / per, first = r * p.qlen + item % per * 8;
+        const int r = e.r0 + (item >> log_per), first = r * p.qlen + (item & log_per) * 8;
         const int lo = max(first, e.t0), hi = min(min(first + 8, (r + 1) * p.qlen), e.t0 + e.nrows);
-        const int a = lo < hi ? adapter_of(p, r) : -1;
+        const int index = lo < hi ? __ldg(p.adapters + r) : -1;
         // T's rows of the window as the B operand, 16-byte chunks: hi, then
-        // lo; other rows and ranks zero.  On their way while the slot is waited for.
+        // lo; other rows and ranks zero (without an adapter whatever is there,
+        // unused).  On their way while the slot is waited for.
         constexpr int kChunks = RB / 8, kPer = kWin * 2 * kChunks / 32;
         uint4 v[kPer];
+        const auto load = [&] {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int c = lane + 32 * j, row = c / (2 * kChunks), half = c / kChunks % 2, k = k0 + c % kChunks * 8;
-            const int t = e.t0 + row;
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (a >= 0 && t >= lo && t < hi && k < p.rank)
-                v[j] = *reinterpret_cast<const uint4 *>(p.t + (((int64_t)t * p.H + h) * 2 + half) * p.rank + k);
-        }
+            for (int j = 0; j < kPer; ++j) {
+                const int c = lane + 32 * j, row = c / (2 * kChunks), half = c / kChunks % 2, k = k0 + c % kChunks * 8;
+                const int t = e.t0 + row;
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (t >= lo && t < hi && k < p.rank)
+                    v[j] = *reinterpret_cast<const uint4 *>(p.t + (((int64_t)t * p.H + h) * 2 + half) * p.rank + k);
+            }
+        };
+        if (n > 0) load();
         if (!wait_or_abort(&sh.s_empty[s], (n & 1) ^ 1, &sh.abort_flag)) break;
-        ++n;
+        const int a = valid_adapter(p, index);
         if (lane == 0) {
-            sh.used[s] = a >= 0;
             if (a >= 0) {
                 mbar_arrive_expect_tx(&sh.s_full[s], T::kBBytes);
                 tma_2d(slot, mb, k0, (a * p.H + h) * MLA_D_V, &sh.s_full[s]);
@@ -662,6 +683,10 @@ __device__ void slot_filler(const LoraArgs &p, const CUtensorMap *mb, uint8_t *s
             }
         }
         __syncwarp();
+        if (n++ == 0) {     // T is written by the kernel before this one, B is not
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            load();
+        }
         if (a >= 0) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
@@ -694,98 +719,118 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.x_full, 1);
         mbar_init(&sh.x_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.d_full[i], 1);
+            mbar_init(&sh.d_full[i], 2);
             mbar_init(&sh.d_free[i], kEpiWarps);
+            mbar_init(&sh.add_free[i], kEpiWarps);
         }
         for (int i = 0; i < T::kSlots; ++i) {
             mbar_init(&sh.s_full[i], 2);
             mbar_init(&sh.s_empty[i], 1);
         }
-        mbar_init(&sh.add_free, kEpiWarps);
-        mbar_init(&sh.fin, 1);
+        mbar_init(&sh.fin, 2);
         sh.abort_flag = 0;
         mbar_fence_init();
     }
-    if (warp == kIssueWarp) tc::tmem_alloc(&sh.tmem, 512);
+    if (warp == kLatentWarp) tc::tmem_alloc(&sh.tmem, 512);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t base = smem_u32(sm), tm = sh.tmem;
-    if (warp == kLoadWarp) {
+    // A whole warp's wait; its result, and with it what the loops count, is uniform.
+    const auto wait_warp = [&](uint64_t *bar, uint32_t par) {
+        return __all_sync(0xffffffffu, wait_or_abort(bar, par, &sh.abort_flag)) != 0;
+    };
+    if (warp == kLatentWarp) {
         // Neither W_UV nor the latent is written by the kernel before this
         // one.  Rows past S read as zeros (their outputs are not written).
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&sh.w_full, kXOff);
-            for (int kb = 0; kb < kColBlocks; ++kb) tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &sh.w_full);
-            int it = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles; tile += step, ++it) {
-                if (!(ok = wait_or_abort(&sh.x_empty, (it & 1) ^ 1, &sh.abort_flag))) break;
+        const uint32_t one = elect_one();
+        int fetched = 0;
+        const auto fetch = [&](int tile) {
+            if (one) {
                 mbar_arrive_expect_tx(&sh.x_full, T::kXBytes);
                 for (int kb = 0; kb < kColBlocks; ++kb)
                     tma_3d(sm + kXOff + kb * T::kXBlock, &ml, 64 * kb, h, tile * NR, &sh.x_full);
             }
-            if (!ok) {      // flagged: the copies in flight land before the block ends
-                mbar_wait(&sh.w_full, 0);
-                if (it > 0) mbar_wait(&sh.x_full, (it - 1) & 1);
+            __syncwarp();
+            ++fetched;
+        };
+        if (one) {
+            mbar_arrive_expect_tx(&sh.w_full, kXOff);
+            for (int kb = 0; kb < kColBlocks; ++kb) tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &sh.w_full);
+        }
+        fetch(blockIdx.x);
+        bool ok = wait_warp(&sh.w_full, 0);
+        int it = 0;
+        for (int tile = blockIdx.x; ok && tile < tiles; tile += step, ++it) {
+            if (!(ok = wait_warp(&sh.x_full, it & 1))) break;
+            if (!(ok = wait_warp(&sh.d_free[it & 1], ((it >> 1) & 1) ^ 1))) break;
+            tc::fence_after();
+            mma_latent(tm + (it & 1) * NR, base, kABlock, base + kXOff, T::kXBlock, idesc_bf16(NR), one);
+            if (one) {
+                tc::commit(&sh.x_empty);
+                tc::commit(&sh.d_full[it & 1]);
+            }
+            __syncwarp();
+            if (tile + step < tiles) {
+                if (!(ok = wait_warp(&sh.x_empty, it & 1))) break;
+                fetch(tile + step);
             }
         }
-    } else if (warp == kIssueWarp) {
-        bool ok = wait_or_abort(&sh.w_full, 0, &sh.abort_flag);
+        if (!ok) {          // flagged: the copies in flight land before the block ends
+            mbar_wait(&sh.w_full, 0);
+            mbar_wait(&sh.x_full, (fetched - 1) & 1);
+        }
+        // Every MMA issued must be complete before TMEM is released.
+        if (one) tc::commit(&sh.fin);
+        __syncwarp();
+        mbar_wait(&sh.fin, 0);
+    } else if (warp == kItemWarp) {
         const uint32_t one = elect_one();
+        bool ok = true, ready = false;      // the next slot is known to be full
         int it = 0, s = 0, s_phase = 0;
         const uint64_t b_desc = tc::sdesc(base + T::kSlotOff, 16, T::kSbo, T::kSwz);
         const uint64_t t_desc = tc::sdesc(base + T::kSlotOff + T::kBBytes, 16, T::kSbo, T::kSwz);
         Entries<NR, RB> e;
         e.init(p);
         for (int tile = blockIdx.x; ok && tile < tiles; tile += step, ++it) {
-            const uint32_t d = tm + (it & 1) * NR;
-            if (!(ok = wait_or_abort(&sh.x_full, it & 1, &sh.abort_flag))) break;
-            if (!(ok = wait_or_abort(&sh.d_free[it & 1], ((it >> 1) & 1) ^ 1, &sh.abort_flag))) break;
-            tc::fence_after();
-            mma_latent(d, base, kABlock, base + kXOff, T::kXBlock, idesc_bf16(NR), one);
-            if (one) tc::commit(&sh.x_empty);
-            __syncwarp();
+            int items = 0;
             e.tile = tile;
-            if (!(ok = wait_or_abort(&sh.add_free, (it & 1) ^ 1, &sh.abort_flag))) break;
-            tc::fence_after();
-            int before = 0;     // items of the windows before
-            for (e.win = 0; ok && e.win < NR / kWin; before += e.items, ++e.win) {
+            for (e.win = 0; e.win < NR / kWin; ++e.win) {
                 e.open(p);
-                for (int i = 0; ok && i < e.items; ++i) {
-                    const uint32_t add = tm + T::kAddCols + (before + i) * kWin;
-                    for (int k0 = 0; k0 < p.rank; k0 += RB) {
-                        if (!(ok = wait_or_abort(&sh.s_full[s], s_phase, &sh.abort_flag))) break;
-                        tc::fence_after();
-                        if (__any_sync(0xffffffffu, sh.used[s])) {
-                            // 32 bytes of the ranks a step: 2 in a descriptor's address field
-                            const uint64_t b = b_desc + s * (T::kSlot >> 4), x = t_desc + s * (T::kSlot >> 4);
-#pragma unroll
-                            for (int j = 0; j < RB / 16; ++j)
-                                if (k0 + 16 * j < p.rank) {
-                                    mma_bf16_tc(add, b + 2 * j, x + 2 * j, idesc_bf16(kWin), k0 > 0 || j > 0, one);
-                                    mma_bf16_tc(add, b + 2 * j, x + (T::kTBytes >> 4) + 2 * j, idesc_bf16(kWin), true,
-                                                one);
-                                }
-                            if (one) tc::commit(&sh.s_empty[s]);
-                        } else if (one) {
-                            mbar_arrive(&sh.s_empty[s]);
-                        }
-                        __syncwarp();
-                        if (++s == T::kSlots) s = 0, s_phase ^= 1;
-                    }
-                }
+                items += e.items;
             }
+            const int buf = it & p.add_both, use = it >> p.add_both;
+            if (!(ok = wait_warp(&sh.add_free[buf], (use & 1) ^ 1))) break;
+            tc::fence_after();
+            uint32_t add = tm + T::kAddCols + buf * T::kAddBuf;
+            for (int i = 0; ok && i < items; ++i, add += kWin)
+                for (int k0 = 0; k0 < p.rank; k0 += RB) {
+                    if (!ready && !(ok = wait_warp(&sh.s_full[s], s_phase))) break;
+                    tc::fence_after();
+                    // 32 bytes of the ranks a step: 2 in a descriptor's address field
+                    const uint64_t b = b_desc + s * (T::kSlot >> 4), x = t_desc + s * (T::kSlot >> 4);
+                    uint64_t *empty = &sh.s_empty[s];
+                    if (++s == T::kSlots) s = 0, s_phase ^= 1;
+                    const uint32_t next = mbar_test(&sh.s_full[s], s_phase);    // the answer comes during the MMAs
+                    // (An entry without an adapter multiplies what the slot
+                    // holds into columns that nothing reads.)
+#pragma unroll
+                    for (int j = 0; j < RB / 16; ++j)
+                        if (k0 + 16 * j < p.rank) {
+                            mma_bf16_tc(add, b + 2 * j, x + 2 * j, idesc_bf16(kWin), k0 > 0 || j > 0, one);
+                            mma_bf16_tc(add, b + 2 * j, x + (T::kTBytes >> 4) + 2 * j, idesc_bf16(kWin), true, one);
+                        }
+                    if (one) tc::commit(empty);
+                    ready = __all_sync(0xffffffffu, next);
+                }
             if (ok && one) tc::commit(&sh.d_full[it & 1]);
             __syncwarp();
         }
-        // Every MMA issued must be complete before TMEM is released.
         if (one) tc::commit(&sh.fin);
         __syncwarp();
         mbar_wait(&sh.fin, 0);
     } else if (warp >= kSlotWarp0) {
         if (warp - kSlotWarp0 < T::kSlots) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
             slot_filler<NR, RB>(p, &mb, sm, sh, warp - kSlotWarp0, h, tiles);
         }
     } else {
@@ -794,33 +839,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int v = 32 * (warp & 3) + lane, first = (warp >> 2) * T::kRows;
         const int64_t row_step = (int64_t)p.H * MLA_D_V;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        // Gates and, of row `lane`, length and adapter: the next tile's are
+        // loaded before this one's results are stored.
+        struct Inputs {
+            uint16_t gate[T::kRows];
+            int len, adapter;
+        };
+        const auto load = [&](Inputs &x, int tile) {
+            const int t0 = tile * NR + first, nrows = min(T::kRows, p.S - t0);
+            const uint16_t *gate = reinterpret_cast<const uint16_t *>(p.gate) + ((int64_t)t0 * p.H + h) * MLA_D_V + v;
+#pragma unroll
+            for (int i = 0; i < T::kRows; ++i) x.gate[i] = i < nrows ? __ldg(gate + i * row_step) : 0;
+            x.len = 0;
+            x.adapter = -1;
+            if (lane < nrows) {
+                const int r = request_of(p, t0 + lane);
+                x.len = __ldg(p.lengths + r);
+                x.adapter = __ldg(p.adapters + r);
+            }
+        };
+        Inputs in, next;
+        load(in, blockIdx.x);
         int it = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += step, ++it) {
+        for (int tile = blockIdx.x; tile < tiles; tile += step, ++it, in = next) {
             const int t0 = tile * NR + first, nrows = min(T::kRows, p.S - t0);
             const int64_t at = ((int64_t)t0 * p.H + h) * MLA_D_V + v;
-            uint32_t live = 0;
-            uint16_t gate[T::kRows];
-#pragma unroll
-            for (int i = 0; i < T::kRows; ++i)
-                gate[i] = i < nrows ? __ldg(reinterpret_cast<const uint16_t *>(p.gate) + at + i * row_step) : 0;
-            // Lane i: the column of row i's low-rank part (-1: none).
-            int col = -1;
-            {
-                const int t = t0 + lane, r = t / p.qlen;
-                live = __ballot_sync(0xffffffffu, lane < nrows && __ldg(p.lengths + min(r, p.S / p.qlen - 1)) > 0);
-                if (lane < nrows && adapter_of(p, r) >= 0) {
-                    Entries<NR, RB> e;
-                    e.tile = tile;
-                    int item = 0;
-                    const int win = (first + lane) / kWin;
-                    for (e.win = 0; e.win <= win; ++e.win) {
-                        e.open(p);
-                        if (e.win < win) item += e.items;
-                    }
-                    item += (r - e.r0) * ((p.qlen + 7) / 8) + (t - r * p.qlen) / 8;
-                    col = T::kAddCols + item * kWin + (first + lane) % kWin;
-                }
-            }
+            const uint32_t live = __ballot_sync(0xffffffffu, in.len > 0);
+            const uint32_t adapted = __ballot_sync(0xffffffffu, in.adapter >= 0 && in.adapter < p.n);
+            // Lane i: the column of row i's low-rank part.
+            const int w0 = tile * NR, win = first / kWin * kWin, log_per = p.qlen > 8;
+            int item = win ? (request_of(p, w0 + kWin - 1) - request_of(p, w0) + 1) << log_per : 0;
+            const int r = request_of(p, t0 + lane);
+            item += ((r - request_of(p, w0 + win)) << log_per) + ((t0 + lane - r * p.qlen) >> 3);
+            const int col = T::kAddCols + (it & p.add_both) * T::kAddBuf + item * kWin + (first + lane) % kWin;
             if (!wait_or_abort(&sh.d_full[it & 1], (it >> 1) & 1, &sh.abort_flag)) break;
             tc::fence_after();
             float d[T::kRows];
@@ -831,21 +882,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < T::kRows; ++i) {
                 const int c = __shfl_sync(0xffffffffu, col, i);
-                add[i] = ld1(tm + lanes + (c < 0 ? T::kAddCols : c));
+                add[i] = ld1(tm + lanes + (adapted >> i & 1 ? c : T::kAddCols));
             }
-            const uint32_t adapted = __ballot_sync(0xffffffffu, col >= 0);
+            if (tile + step < tiles) load(next, tile + step);
             tc::wait_ld();
             tc::fence_before();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sh.d_free[it & 1]);
-                mbar_arrive(&sh.add_free);
+                mbar_arrive(&sh.add_free[it & p.add_both]);
             }
 #pragma unroll
             for (int i = 0; i < T::kRows; ++i) {
                 if (i >= nrows) break;
                 // a select, so that nothing of an empty request is seen
-                const float x = live >> i & 1 ? (adapted >> i & 1 ? d[i] + add[i] : d[i]) * sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16)) : 0.f;
+                float x = 0.f;
+                if (live >> i & 1)
+                    x = (adapted >> i & 1 ? d[i] + add[i] : d[i]) * sigmoid_f32(__uint_as_float((uint32_t)in.gate[i] << 16));
                 p.out[at + i * row_step] = __float2bfloat16_rn(x);
             }
         }
@@ -853,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == kIssueWarp) tc::tmem_free(tm, 512);
+    if (warp == kLatentWarp) tc::tmem_free(tm, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -949,7 +1002,10 @@ cudaError_t project(const CUtensorMap &mw, const LoraArgs &p, int sms, cudaStrea
         return cudaErrorInvalidValue;
     cudaError_t e = smem_attr_once<project_kernel<NR, RB>>(Tile<NR, RB>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_project(project_kernel<NR, RB>, NR, kThreads, Tile<NR, RB>::kSmem, p, sms, st, mw, ml, mb, p);
+    LoraArgs q = p;
+    const int items = ((kWin + p.qlen - 2) / p.qlen + 1) << (p.qlen > 8);      // of a window, at most
+    q.add_both = items * (NR / kWin) * kWin <= Tile<NR, RB>::kAddBuf;
+    return launch_project(project_kernel<NR, RB>, NR, kThreads, Tile<NR, RB>::kSmem, p, sms, st, mw, ml, mb, q);
 }
 
 }  // namespace
@@ -973,6 +1029,7 @@ cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.S = R * qlen;
     p.qlen = qlen;
+    p.inv_qlen = ((1ull << 35) + qlen - 1) / qlen;
     p.H = H;
     p.rank = rank;
     p.n = num_adapters;
@@ -987,7 +1044,7 @@ cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *
     // requests of rank 16, 12 heads 9.1 us by warp MMAs and 10.6 through the
     // ring, 32 of rank 32, 96 heads 14.2 and 18.1 (and a 32-row tile's
     // entries would not fit TMEM).  With eight rows a request (256 of rank
-    // 64) 46 and 37 us, with four 29 and 23.
+    // 64) 46 and 29 us, with four 29 and 20.
     if (qlen == 1) return low ? project_few<16>(mw, p, sms, st) : project_few<32>(mw, p, sms, st);
     if (rank <= 32) return low ? project<16, 32>(mw, p, sms, st) : project<32, 32>(mw, p, sms, st);
     return low ? project<16, 64>(mw, p, sms, st) : project<32, 64>(mw, p, sms, st);
