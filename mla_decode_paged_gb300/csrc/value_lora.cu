@@ -8,7 +8,13 @@
 //   out[t, h*128 + v] = lengths[r] > 0 ? bf16(val * sigmoid(gate)) : 0
 //
 // Bound by bytes: the latent (1 KB a row and head), W_UV (128 KB a head), A
-// and B of every adapter in use; at a few rows by the two launches.
+// and B of every adapter in use; at a few rows by the two launches and the
+// chain A -> T -> B T.
+//
+// Measured: 64 single-row requests of 12 heads, rank 16, in 6.7 us; 32 of 96
+// heads, rank 32, in 12.8 (their bytes: 3.5); 256 requests of eight rows, 12
+// heads, rank 64, in 29.3 (47.7 MB, 7.0): 8.8 until the last T, then 5.3
+// tiles a block of ~3,600 cycles, bound by the chain of the ring's entries.
 //
 //   shrink: the (row, head) pairs of a request share A: T = latent A^T *
 //     lora_scale.  Few pairs: warp MMAs on fragments loaded straight from
@@ -23,7 +29,8 @@
 //     stays in shared memory over the head's tiles of rows (N), whose latents
 //     stream past it into tcgen05 MMAs.  B[a, h] T in one of two ways.
 //     One row a request: 16 warps form it by warp MMAs from global memory
-//     into a float32 tile (every column of a warp MMA is a row of its own).
+//     into a float32 tile, each row from its own B (the MMA's other columns
+//     are copies); the first rows' B is on its way while T is still formed.
 //     More: through a ring, an entry being B[a, h] (M, by TMA) and the T rows
 //     of up to eight rows of one request (its place in a 16-row window, N),
 //     two MMAs per 16 ranks into 16 TMEM columns of its own, of which the
@@ -54,6 +61,7 @@ struct LoraArgs {
     __nv_bfloat16 *t;       // [S * H, 2, rank]: hi, lo
     __nv_bfloat16 *out;
     uint64_t inv_qlen;
+    int tile_rows;          // warp MMAs' kernel: rows of a tile
     int add_both;           // the ring's kernel: 1, two tiles' low-rank products fit TMEM
     int S, qlen, H, rank, n;
 };
@@ -79,6 +87,39 @@ __device__ __forceinline__ void two_terms(float a, float b, uint32_t &hi, uint32
     lo = pack_bf16x2(isinf(ha) ? 0.f : a - ha, isinf(hb) ? 0.f : b - hb);
 }
 
+// N 4-byte words, 4 N bytes aligned.
+template <int N>
+struct Words {
+    uint32_t w[N];
+};
+
+// Read-only loads that stay where they are: ahead of what follows them.
+template <int N>
+__device__ __forceinline__ Words<N> load_now(const void *p) {
+    static_assert(N == 2 || N == 4, "8 or 16 bytes");
+    Words<N> x;
+    if constexpr (N == 4)
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3])
+                     : "l"(p));
+    else
+        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(x.w[0]), "=r"(x.w[1]) : "l"(p));
+    return x;
+}
+
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const void *p) {
+    Words<N> x;
+    if constexpr (N == 4) {
+        const uint4 v = *static_cast<const uint4 *>(p);
+        x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
+    } else {
+        const uint2 v = *static_cast<const uint2 *>(p);
+        x.w[0] = v.x, x.w[1] = v.y;
+    }
+    return x;
+}
+
 // ------------------------------------------------------------------ shrink
 
 constexpr int kShrinkWarps = 8;
@@ -90,21 +131,22 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) shrink_kernel(const LoraArg
     __shared__ float part[kShrinkWarps * 16 * kCols];
     asm volatile("griddepcontrol.launch_dependents;");
     const int r = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-    const int a = adapter_of(p, r);
-    if (a < 0) return;
+    const int index = __ldg(p.adapters + r);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int pairs = p.qlen * p.H, m0 = tile * 16;
     const int64_t row0 = (int64_t)r * pairs;
-    const float scale = __ldg(p.scale + a);
     const int c0 = warp * 64 + 8 * q;   // this lane's columns: c0 .. c0 + 7 and c0 + 32 ..
-    uint4 x[2][2];                      // [32-column block][row g, g + 8]
+    Words<4> x[2][2];                   // [32-column block][row g, g + 8], on its way with the index
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = min(m0 + 8 * i + g, pairs - 1);
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.latent + (row0 + row) * MLA_D_LATENT + c0);
+        const __nv_bfloat16 *src = p.latent + (row0 + row) * MLA_D_LATENT + c0;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) x[b][i] = __ldg(src + 4 * b);
+        for (int b = 0; b < 2; ++b) x[b][i] = load_now<4>(src + 32 * b);
     }
+    const int a = valid_adapter(p, index);
+    if (a < 0) return;
+    const float scale = __ldg(p.scale + a);
     const int ntiles = p.rank / 8;
     for (int n0 = 0; n0 < ntiles; n0 += kNChunk) {
         const int nn = min(kNChunk, ntiles - n0);
@@ -123,8 +165,9 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) shrink_kernel(const LoraArg
             if (n < nn)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const uint4 u = x[b][0], v = x[b][1], k = w[n][b];
-                    const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+                    const Words<4> u = x[b][0], v = x[b][1];
+                    const uint4 k = w[n][b];
+                    const uint32_t a0[4] = {u.w[0], v.w[0], u.w[1], v.w[1]}, a1[4] = {u.w[2], v.w[2], u.w[3], v.w[3]};
                     mma_bf16(acc[n], a0, k.x, k.y);
                     mma_bf16(acc[n], a1, k.z, k.w);
                 }
@@ -308,7 +351,6 @@ __device__ __forceinline__ float sigmoid_f32(float x) {
 
 constexpr int kFewThreads = 512;                   // and a warp that issues copies and products
 constexpr int kDStride = MLA_D_V + 4;              // float32 tile rows, a bank apart per row pair
-constexpr int kBatch = 2;                          // items a warp expands at once
 
 // NR rows a tile; two tiles' latents.
 template <int NR>
@@ -336,93 +378,65 @@ __device__ __forceinline__ void ld_rows(uint32_t taddr, float (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Up to eight rows [n0, e) of a tile that share a request, and B[a, h] of its
-// adapter (null: none).
-struct Item {
-    const __nv_bfloat16 *b;
-    int n0, e;
-};
-
-// The tile's items, one thread each; their number.
-__device__ __forceinline__ int make_items(const LoraArgs &p, Item *items, int t0, int nrows, int h) {
-    const int per = (p.qlen + 7) / 8;
-    const int r0 = t0 / p.qlen, n = ((t0 + nrows - 1) / p.qlen - r0 + 1) * per;
-    if (threadIdx.x < n) {
-        const int i = threadIdx.x, r = r0 + i / per, first = r * p.qlen + i % per * 8;
-        const int a = adapter_of(p, r);
-        Item x;
-        x.n0 = max(first, t0) - t0;
-        x.e = min(min(first + 8, (r + 1) * p.qlen), t0 + nrows) - t0;
-        x.b = a < 0 || x.e <= x.n0 ? nullptr : p.b + ((int64_t)a * p.H + h) * MLA_D_V * p.rank;
-        items[i] = x;
-    }
-    return n;
-}
-
-// B[a, h] T of the tile's rows -> delta[row][v].  Warp w takes outputs
-// 16 (w % 8) .. + 15 of every second item.
-__device__ __forceinline__ void expand(const LoraArgs &p, float *delta, const Item *items, int nitems, int t0, int h) {
+// B[a, h] T of the tile's rows (row n: B[n] its adapter's, null for none) ->
+// delta[n][v].  Warp w takes outputs 16 (w % 8) .. + 15 of every second row,
+// BATCH rows at once, 8 W ranks a step: a lane's W words of B and of T are
+// W / 2 k-steps' worth.  FIRST: T is waited for once the first rows' B is on
+// its way.
+template <int W, int BATCH, bool FIRST>
+__device__ __forceinline__ void expand(const LoraArgs &p, float *delta, const __nv_bfloat16 *const *B, int nrows,
+                                       int t0, int h) {
+    bool wait = FIRST;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int v0 = 16 * (warp & 7), rank = p.rank;
-    const int b_lane = (v0 + g) * rank + 8 * q, t_row = p.H * 2 * rank;
-    const __nv_bfloat16 *t_lane = p.t + ((int64_t)t0 * p.H + h) * 2 * rank + 8 * q;
-    for (int i0 = warp >> 3; i0 < nitems; i0 += 2 * kBatch) {
-        const __nv_bfloat16 *b[kBatch], *t[kBatch];
-        int n0[kBatch], e[kBatch];
-        float acc[kBatch][4] = {};
+    const int b_lane = (v0 + g) * rank + 2 * W * q, t_row = p.H * 2 * rank;
+    const __nv_bfloat16 *t_lane = p.t + ((int64_t)t0 * p.H + h) * 2 * rank + 2 * W * q;
+    for (int i0 = warp >> 3; i0 < nrows; i0 += 2 * BATCH) {
+        const __nv_bfloat16 *b[BATCH];
+        float acc[BATCH][4] = {};
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int i = i0 + 2 * u;
-            e[u] = n0[u] = 0;
-            b[u] = nullptr;
-            if (i < nitems) {
-                const Item x = items[i];
-                if (x.b) {
-                    b[u] = x.b + b_lane;
-                    n0[u] = x.n0;
-                    e[u] = x.e;
+        for (int u = 0; u < BATCH; ++u) b[u] = i0 + 2 * u < nrows ? B[i0 + 2 * u] : nullptr;
+        for (int k = 0; k < rank; k += 8 * W) {
+            const bool in = k + 2 * W * q < rank;
+            Words<W> x[BATCH] = {}, y[BATCH] = {}, hi[BATCH] = {}, lo[BATCH] = {};
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                if (in && b[u]) {
+                    const __nv_bfloat16 *at = b[u] + b_lane + k;
+                    x[u] = FIRST ? load_now<W>(at) : load_words<W>(at);
+                    y[u] = FIRST ? load_now<W>(at + 8 * rank) : load_words<W>(at + 8 * rank);
                 }
-            }
-            t[u] = t_lane + (int64_t)t_row * max(min(n0[u] + g, e[u] - 1), 0);    // columns past the request are not kept
-        }
-        for (int k = 0; k < rank; k += 32) {
-            const bool in = k + 8 * q < rank;
-            uint4 x[kBatch], y[kBatch], hi[kBatch], lo[kBatch];
+            if (FIRST && wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+            wait = false;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                x[u] = y[u] = hi[u] = lo[u] = make_uint4(0, 0, 0, 0);
-                if (in && e[u]) {
-                    x[u] = __ldg(reinterpret_cast<const uint4 *>(b[u] + k));
-                    y[u] = __ldg(reinterpret_cast<const uint4 *>(b[u] + 8 * rank + k));
-                    hi[u] = *reinterpret_cast<const uint4 *>(t[u] + k);
-                    lo[u] = *reinterpret_cast<const uint4 *>(t[u] + rank + k);
+            for (int u = 0; u < BATCH; ++u)
+                if (in && b[u]) {
+                    const __nv_bfloat16 *t = t_lane + (int64_t)t_row * (i0 + 2 * u) + k;
+                    hi[u] = load_words<W>(t);
+                    lo[u] = load_words<W>(t + rank);
                 }
-            }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const uint32_t a0[4] = {x[u].x, y[u].x, x[u].y, y[u].y}, a1[4] = {x[u].z, y[u].z, x[u].w, y[u].w};
-                mma_bf16(acc[u], a0, hi[u].x, hi[u].y);
-                mma_bf16(acc[u], a1, hi[u].z, hi[u].w);
-                mma_bf16(acc[u], a0, lo[u].x, lo[u].y);
-                mma_bf16(acc[u], a1, lo[u].z, lo[u].w);
-            }
+            for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+                for (int j = 0; j < W; j += 2) {
+                    const uint32_t a[4] = {x[u].w[j], y[u].w[j], x[u].w[j + 1], y[u].w[j + 1]};
+                    mma_bf16(acc[u], a, hi[u].w[j], hi[u].w[j + 1]);
+                    mma_bf16(acc[u], a, lo[u].w[j], lo[u].w[j + 1]);
+                }
         }
+        // The eight columns are equal.
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int n = n0[u] + 2 * q;
-            float *d = delta + n * kDStride + v0 + g;
-            if (n < e[u]) {
+        for (int u = 0; u < BATCH; ++u)
+            if (q == 0 && b[u]) {
+                float *d = delta + (i0 + 2 * u) * kDStride + v0 + g;
                 d[0] = acc[u][0];
                 d[8] = acc[u][2];
             }
-            if (n + 1 < e[u]) {
-                d[kDStride] = acc[u][1];
-                d[kDStride + 8] = acc[u][3];
-            }
-        }
     }
+    if (FIRST && wait) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// NR rows a tile at most, p.tile_rows of them.
 template <int NR>
 __global__ void __launch_bounds__(kFewThreads + 32, 1)
     project_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap ml, const LoraArgs p) {
@@ -432,10 +446,10 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
     float *delta = reinterpret_cast<float *>(sm + T::kDOff);
     __shared__ uint64_t full[2], done[2];
     __shared__ uint32_t tmem;
-    __shared__ uint8_t active[NR], adapted[NR];
-    __shared__ Item items[NR];
+    __shared__ uint8_t active[NR];
+    __shared__ const __nv_bfloat16 *adapter_b[NR];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.y, tiles = (p.S + NR - 1) / NR, step = gridDim.x;
+    const int h = blockIdx.y, rows = p.tile_rows, tiles = (p.S + rows - 1) / rows, step = gridDim.x;
     const bool issuer = warp == kFewThreads / 32;   // a whole warp; one lane copies and commits
     const uint32_t one = elect_one();
 
@@ -455,7 +469,7 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
     const auto fetch = [&](int tile, int s, uint32_t with) {
         mbar_arrive_expect_tx(&full[s], with + T::kBBytes);
         for (int kb = 0; kb < kColBlocks; ++kb)
-            tma_3d(sm + kXOff + s * T::kBBytes + kb * T::kBBlock, &ml, 64 * kb, h, tile * NR, &full[s]);
+            tma_3d(sm + kXOff + s * T::kBBytes + kb * T::kBBlock, &ml, 64 * kb, h, tile * rows, &full[s]);
     };
     if (issuer && one) {
         // Nothing here but the low-rank products is written by the kernel
@@ -476,13 +490,12 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
         ++issued;
     };
     for (int tile = blockIdx.x; tile < tiles; tile += step, ++it) {
-        const int t0 = tile * NR, nrows = min(NR, p.S - t0);
+        const int t0 = tile * rows, nrows = min(rows, p.S - t0);
         if (tid < NR) {
-            const int r = (t0 + tid) / p.qlen;
-            active[tid] = tid < nrows && __ldg(p.lengths + r) > 0;
-            adapted[tid] = tid < nrows && adapter_of(p, r) >= 0;
+            const int a = tid < nrows ? adapter_of(p, t0 + tid) : -1;
+            active[tid] = tid < nrows && __ldg(p.lengths + t0 + tid) > 0;
+            adapter_b[tid] = a < 0 ? nullptr : p.b + ((int64_t)a * p.H + h) * MLA_D_V * p.rank;
         }
-        const int nitems = make_items(p, items, t0, nrows, h);
         // This thread's gates (output v of rows first .. first + kRows - 1),
         // in flight during the products.
         const int v = 32 * (warp & 3) + lane, first = (warp >> 2) * T::kRows;
@@ -495,8 +508,15 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
                           ? __ldg(reinterpret_cast<const uint16_t *>(p.gate) + at + (int64_t)i * row_step)
                           : 0;
         __syncthreads();
-        if (it == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (tid < kFewThreads) expand(p, delta, items, nitems, t0, h);
+        if (tid < kFewThreads) {
+            if (p.rank <= 16) {
+                if (it == 0) expand<2, 4, true>(p, delta, adapter_b, nrows, t0, h);
+                else expand<2, 4, false>(p, delta, adapter_b, nrows, t0, h);
+            } else {
+                if (it == 0) expand<4, 2, true>(p, delta, adapter_b, nrows, t0, h);
+                else expand<4, 2, false>(p, delta, adapter_b, nrows, t0, h);
+            }
+        }
         if (issuer) {
             if (it == 0) multiply(0);
             if (tile + step < tiles) multiply(it + 1);     // D and latents are double-buffered
@@ -519,7 +539,7 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
                 if (n >= nrows) break;
                 float x = 0.f;      // a select, so that nothing of an empty request is seen
                 if (active[n]) {
-                    x = adapted[n] ? d[i] + delta[n * kDStride + v] : d[i];
+                    x = adapter_b[n] ? d[i] + delta[n * kDStride + v] : d[i];
                     x *= sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16));
                 }
                 p.out[at + (int64_t)i * row_step] = __float2bfloat16_rn(x);
@@ -987,7 +1007,8 @@ cudaError_t project_few(const CUtensorMap &mw, const LoraArgs &p, int sms, cudaS
     if (!encode_latent(&ml, p, NR)) return cudaErrorInvalidValue;
     cudaError_t e = smem_attr_once<project_few_kernel<NR>>(FewTile<NR>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_project(project_few_kernel<NR>, NR, kFewThreads + 32, FewTile<NR>::kSmem, p, sms, st, mw, ml, p);
+    return launch_project(project_few_kernel<NR>, p.tile_rows, kFewThreads + 32, FewTile<NR>::kSmem, p, sms, st, mw, ml,
+                          p);
 }
 
 template <int NR, int RB>
@@ -1040,12 +1061,19 @@ cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *
     // 32-row tiles, unless 16-row ones leave no block of a head with two.
     const bool low = (p.S + 15) / 16 <= std::max(1, sms / H);
     // With one row a request every row has an entry of its own, whose way
-    // through the ring (~600 cycles) costs more than its warp MMAs: 64
-    // requests of rank 16, 12 heads 9.1 us by warp MMAs and 10.6 through the
-    // ring, 32 of rank 32, 96 heads 14.2 and 18.1 (and a 32-row tile's
-    // entries would not fit TMEM).  With eight rows a request (256 of rank
-    // 64) 46 and 29 us, with four 29 and 20.
-    if (qlen == 1) return low ? project_few<16>(mw, p, sms, st) : project_few<32>(mw, p, sms, st);
+    // through the ring costs more than its warp MMAs: 64 requests of 12 heads
+    // 6.7 us by warp MMAs and 7.9 through the ring at rank 16, 9.7 and 11.7 at
+    // rank 64 (and a 32-row tile's entries would not fit TMEM).  With eight
+    // rows a request (256 of rank 64) 46 and 29 us, with four 29 and 20.
+    if (qlen == 1) {
+        p.tile_rows = low ? 16 : 32;
+        // Down to four rows while every tile has a block of its own: a row's
+        // expansion takes its block's time (64 requests of rank 64 12.3 us
+        // with 16 rows, 9.7 with eight; 16 of them 11.5, and 6.9 with four).
+        const auto tiles = [&](int rows) { return (p.S + rows - 1) / rows; };
+        while (low && p.tile_rows > 4 && tiles(p.tile_rows / 2) <= std::max(1, sms / H)) p.tile_rows /= 2;
+        return low ? project_few<16>(mw, p, sms, st) : project_few<32>(mw, p, sms, st);
+    }
     if (rank <= 32) return low ? project<16, 32>(mw, p, sms, st) : project<32, 32>(mw, p, sms, st);
     return low ? project<16, 64>(mw, p, sms, st) : project<32, 64>(mw, p, sms, st);
 }
