@@ -15,18 +15,18 @@
 // (order-preserving 32-bit images of the weights) stay in registers: 16 a
 // thread, 8,192 tokens a block.  A longer slice is taken in rounds of that
 // size, read again for every step.  The m-th largest key is found by radix
-// selection, 11 + 11 + 10 bits: every block counts its slice into a shared
-// histogram, sums its share of the bins over the cluster through distributed
-// shared memory, and reads the others' sums (reading all histograms in every
-// block instead took 11,500 cycles a digit with 16 blocks, this 3,000; a
-// histogram per digit: none is reused).  What each warp keeps is counted
+// selection, 11 + 11 + 10 bits, ended by the digits whose keys all stay: every
+// block counts its slice into a shared histogram, adds the bins that are not
+// empty to their sums over the cluster, which the blocks hold in equal shares,
+// and reads these through distributed shared memory (reading all histograms in
+// every block instead took 11,500 cycles a digit with 16 blocks; a histogram
+// per digit: none is reused).  What each warp keeps is counted
 // by ballots, the offsets of warps and blocks are exchanged once, and the
 // tokens are placed by the ballots again.
 //
-// Measured: 15.0 us for one request of 128K tokens, 10.1 for 64 of 1K to 8K,
-// 80 for 256 of 128 to 128K (log-uniform, 5.0 M tokens, 1.0 TB/s: its counts
-// and placements are bound by instructions, 1.7 a cycle and SM, and by how
-// many clusters an SM holds).
+// Measured: 12.8 us for one request of 128K tokens, 9.4 for 64 of 1K to 8K, 77
+// for 256 of 128 to 128K (log-uniform, 5.0 M tokens, 1.0 TB/s: its counts and
+// placements are bound by instructions, and by how many clusters an SM holds).
 #include <atomic>
 
 #include <cuda_runtime.h>
@@ -64,7 +64,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 __device__ __forceinline__ float key_weight(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
-constexpr uint32_t kKeyZero = 0x80000000u, kKeyLowest = ~0xff800000u;
+constexpr uint32_t kKeyZero = 0x80000000u, kKeyLowest = ~0xff800000u;     // no key is below kKeyLowest
 
 __device__ __forceinline__ int kept_tokens(const EvictArgs &a, int r, int len) {
     const int b = a.budgets ? __ldg(a.budgets + r) : a.budget;
@@ -73,8 +73,7 @@ __device__ __forceinline__ int kept_tokens(const EvictArgs &a, int r, int len) {
 
 struct __align__(16) Shared {
     uint32_t hist[kDigits][kBins];
-    uint32_t stage[kBins];          // this block's share of the bins from every block
-    uint32_t sums[kDigits][kBins];  // and their sums
+    uint32_t sums[kDigits][kBins];  // of this block's share of the bins, over the cluster
     uint32_t red[3][kWarps];
     uint32_t classes[kWarps][kClasses];     // a warp's requests by the blocks they take
     int own[4];                             // the cluster's request, its tokens, first entry, kept tokens
@@ -90,12 +89,13 @@ __device__ __forceinline__ uint32_t block_rank() {
     return r;
 }
 
-// All running blocks of the cluster (one block: itself), their shared-memory
-// writes before it visible after it.
-__device__ __forceinline__ void cluster_sync(bool one) {
-    if (one) __syncthreads();
-    else
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// All running blocks of the cluster, their shared-memory writes before it
+// visible after it.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
 }
 
 // What is at `p`'s place in the shared memory of block `rank`.
@@ -114,6 +114,15 @@ __device__ __forceinline__ uint4 remote4(const uint32_t *p, uint32_t rank) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+// Adds v at `p`'s place in the shared memory of block `rank`.
+__device__ __forceinline__ void remote_add(uint32_t *p, uint32_t rank, uint32_t v) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tred.relaxed.cluster.shared::cluster.add.u32 [a], %2;\n\t}" ::"r"(
+            smem_u32(p)),
+        "r"(rank), "r"(v)
+        : "memory");
 }
 
 // Exclusive prefix sum of v over the block's threads.
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
     const float *w = a.weights + base;
 
     // This block's slice, in rounds; a warp's part of a round, whole groups of
-    // 32 tokens.
+    // 32 tokens.  Key 0: no token that may go.
     const int slice = (((len + (int)E - 1) >> le) + 31) / 32 * 32;
     const int s0 = (int)min((int64_t)slice * rank, (int64_t)len), s1 = min(slice, len - s0) + s0;
     const int rounds = (s1 - s0 + kRound - 1) / kRound;
@@ -242,9 +251,18 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
         convert();
     };
     // On their way during the sums over the requests.
-    if (rounds > 0) fetch(0);
+    if (rounds > 0) {
+        fetch(0);
+        const int line = first - lane + 32 * lane;      // 32 rows of the page list, read at the placement
+        if (lane < steps && line < s1) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pages + base + line));
+    }
     for (int i = tid; i < kDigits * kBins / 4; i += kThreads)
         reinterpret_cast<uint4 *>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+    if (!one) {
+        for (int i = tid; i < kDigits * kBins / 4; i += kThreads)
+            reinterpret_cast<uint4 *>(&sh.sums[0][0])[i] = make_uint4(0, 0, 0, 0);
+        cluster_arrive();       // waited for before the first sums are added to
+    }
     if (a.R > kThreads)
         for (int i = tid; i < a.R; i += kThreads) {
             int at;
@@ -273,10 +291,13 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
     uint32_t T = 0, ties = 0;
     const bool select = m > 0 && m < hi - lo;       // the same in every block of the cluster
     bool tied = false;                              // some of the equal keys go
+    if (!select && !one) cluster_wait();
     if (select) {
         uint32_t need = (uint32_t)m;
+        bool found = false;                         // the keys that begin with T's digits so far all stay
 #pragma unroll
         for (int digit = 0; digit < kDigits; ++digit) {
+            if (found) break;
             const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
             const uint32_t bins = digit == 2 ? 1024u : 2048u;
             const int above_bits = digit == 0 ? 0 : digit == 1 ? 21 : 10;   // bits below the digits found
@@ -288,26 +309,21 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
                     if (j < steps && (free >> j & 1) && (digit == 0 || (key[j] ^ T) >> above_bits == 0))
                         atomicAdd(&hist[(key[j] >> shift) & (bins - 1)], 1u);
             }
-            cluster_sync(one);
+            __syncthreads();
             // Bins from the top: thread t holds the kOwn from kBins - 1 - kOwn * t down, summed over the cluster.
-            const uint32_t top = kBins - 1 - kOwn * tid;
+            const uint32_t top = kBins - 1 - kOwn * tid, low = top - (kOwn - 1);
             uint32_t n[kOwn], sum = 0;
-            uint4 v;
-            if (one) {
-                v = *reinterpret_cast<const uint4 *>(hist + top - (kOwn - 1));
-            } else {
-                const int share = kBins >> le, log_share = 11 - le;     // a block's bins
-                const uint32_t c = ((tid >> (log_share - 2)) + rank) & (E - 1), at = (tid & (share / 4 - 1)) * 4;
-                *reinterpret_cast<uint4 *>(sh.stage + c * share + at) = remote4(hist + rank * share + at, c);
-                __syncthreads();
-                for (int i = tid; i < share; i += kThreads) {
-                    uint32_t s = 0;
-                    for (uint32_t j = 0; j < E; ++j) s += sh.stage[j * share + i];
-                    sh.sums[digit][i] = s;
-                }
-                cluster_sync(false);
-                const uint32_t low = top - (kOwn - 1);
-                v = remote4(sh.sums[digit] + (low & (share - 1)), low >> log_share);
+            uint4 v = *reinterpret_cast<const uint4 *>(hist + low);
+            if (!one) {
+                const uint32_t share = kBins >> le, owner = low >> (11 - le);       // a block's bins; these bins' block
+                uint32_t *at = sh.sums[digit] + (low & (share - 1));
+                if (digit == 0) cluster_wait();
+                if (v.x) remote_add(at, owner, v.x);
+                if (v.y) remote_add(at + 1, owner, v.y);
+                if (v.z) remote_add(at + 2, owner, v.z);
+                if (v.w) remote_add(at + 3, owner, v.w);
+                cluster_sync();
+                v = remote4(at, owner);
             }
             n[0] = v.w;
             n[1] = v.z;
@@ -328,9 +344,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
             __syncthreads();
             T |= sh.pick[0] << shift;
             need = sh.pick[1];
+            found = need == sh.pick[2];
         }
         ties = need;
-        tied = need < sh.pick[2];
+        tied = !found;
     }
 
     // A token outside [lo, hi), or any when all stay, is sure; between, those
@@ -344,10 +361,9 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
                 if (key[j] >= T) sure |= free & 1u << j;
-                if (key[j] == T) tie |= free & 1u << j;
+                if (tied && key[j] == T) tie |= free & 1u << j;
             }
-            if (tied) sure &= ~tie;
-            else tie = 0;
+            sure &= ~tie;
         }
         nsure += __reduce_add_sync(0xffffffffu, __popc(sure));
         if (tied) nties += __reduce_add_sync(0xffffffffu, __popc(tie));
@@ -379,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
             sh.totals[0] = k;
             sh.totals[1] = t;
         }
-        cluster_sync(false);
+        cluster_sync();
         if (lane < rank) {
             block_kept = remote(&sh.totals[0], lane);
             block_ties = remote(&sh.totals[1], lane);
@@ -439,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
             }
         }
     }
-    if (!one) cluster_sync(false);                  // no block ends while another may read its shared memory
+    if (!one) cluster_sync();                  // no block ends while another may read its shared memory
 }
 
 cudaError_t launch(const EvictArgs &a, int log_cs, cudaStream_t st) {
@@ -489,14 +505,14 @@ cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32
     a.weights_out = weights_out;
     // The lengths are on the device.  A cluster holds a request of the mean
     // length in one round.  Fewer blocks take a long request in rounds (one of
-    // 128K: 149 us with 1, 82 with 2, 46 with 4, 28 with 8, 15 with 16); more
+    // 128K: 136 us with 1, 75 with 2, 42 with 4, 25 with 8, 12.8 with 16); more
     // mostly end unused, and each costs its launch (64 requests of 1K to 8K:
-    // 10.1 us with 1, 11 with 2, 16 with 4, 18 with 8; 128 of 8K to 32K: 39
-    // with 4, 45 with 8, 92 with 16; 256 of 128 to 128K: 97 with 4, 80 with 8,
-    // 125 with 16).  A few requests take the blocks that half the SMs hold:
-    // these cost nothing (8 of 4K: 8.2 us with 1 to 8, 11.4 with 16), and one
-    // request may be much longer than the mean (15 of 1K and one of 128K: 46
-    // us with 4, 83 with the mean's 2).
+    // 9.4 us with 1, 10.5 with 2, 15 with 4, 17 with 8; 128 of 8K to 32K: 44
+    // with 2, 34 with 4, 40 with 8; 256 of 128 to 128K: 96 with 2, 77 with 4,
+    // 74 with 8, 114 with 16).  A few requests take the blocks that half the
+    // SMs hold: these cost nothing (8 of 4K: 7.4 us with 1 to 8, 10 with 16),
+    // and one request may be much longer than the mean (15 of 1K and one of
+    // 128K: 47 us with 4, 82 with the mean's 2).
     const int64_t mean = (num_pages + R - 1) / R;
     int log_cs = 0;
     while (log_cs < 4 && ((mean >> log_cs) > kRound || ((int64_t)R << (log_cs + 1)) <= sms / 2)) ++log_cs;
