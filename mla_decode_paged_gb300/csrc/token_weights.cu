@@ -32,11 +32,17 @@
 // bf16 rows take a pair of CTAs: each holds half of Q' and a 128-token tile
 // of its own, and cta_group::2 MMAs give both their tokens' scores with all
 // rows, so a cache row still crosses L2 once.  (Two CTAs reading every tile
-// for half of the rows each took 213 us against 165 us for 32 x 96 heads, 32K
-// tokens: L2 then delivers the cache twice.)  More rows are cut into groups
-// on neighbouring CTAs (pairs), each writing its partial sums to the
-// workspace, joined in group order by a small kernel.
-#include <cuda.h>
+// for half of the rows each took 213 us against 128 us for 32 x 96 heads, 32K
+// tokens: L2 then delivers the cache twice.)  Both CTAs' copies count at CTA
+// 0's barriers (a warp of CTA 1 that passed its tiles' arrival on: 164 us).
+// More rows are cut into groups on neighbouring CTAs (pairs), each writing
+// its partial sums to the workspace, joined in group order by a small kernel.
+//
+// Measured (12 heads, bf16 query): 64 requests of 1K to 8K tokens, one row
+// each, in 34.5 us, 5.0 TB/s of cache rows; 128 of 4K to 32K, four rows each,
+// in 256 us, 5.7 TB/s (the attention kernel's loads alone reach 5.8 at this
+// random order of 576-byte rows); 32 of 32K, 96 heads, in 128 us, 4.9 TB/s:
+// two stages' copies do not cover their latency and the MMAs' 1,940 cycles.
 #include <cudaTypedefs.h>
 #include <climits>
 #include <cuda_fp8.h>
@@ -96,6 +102,7 @@ struct Misc {
     uint64_t kv_full[kStages], kv_empty[kStages], d_full[2], d_free[2], q_ready, q_free, fin;
     uint32_t tmem;
     int abort_flag;
+    int issued[kProdWarps];     // PAIR: tiles whose copies each producer has issued
     int start[3];               // this CTA's first request, its first tile there, tiles in all
 };
 
@@ -199,7 +206,32 @@ __device__ void find_start(const TokenArgs &a, Misc<C> &ms, int v) {
 
 // ------------------------------------------------------------------ producers
 
-template <class C>
+// The place of `p` in the shared memory of the pair's block `rank`.
+__device__ __forceinline__ uint32_t in_block(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ int load_in_block(const int *p, uint32_t rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(in_block(p, rank)) : "memory");
+    return v;
+}
+
+// tc::gather4_hint whose bytes count at a barrier of either CTA of the pair
+// (`bar`: its shared::cluster address).
+__device__ __forceinline__ void gather4_pair(void *dst, const CUtensorMap *map, int x, const int (&rows)[4],
+                                             uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(rows[0]), "r"(rows[1]), "r"(rows[2]), "r"(rows[3]), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+constexpr int part_bytes(int part) { return part < 4 ? 32 * 512 : 32 * 256; }      // of a producer and tile
+
+template <class C, bool PAIR>
 __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUtensorMap *mrope, uint8_t *sm,
                          Misc<C> &ms, int rank) {
     const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kProdWarp0;
@@ -246,23 +278,46 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
         const int n = load(next);
         const int s = it % kStages;
         if (!(ok = wait_or_abort(&ms.kv_empty[s], ((it / kStages) & 1) ^ 1, &ms.abort_flag))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&ms.kv_full[s], part < 4 ? 32 * 512 : 32 * 256);
+        // A pair's tiles are both counted by CTA 0's barrier.
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&ms.kv_full[s], (PAIR ? 2 : 1) * part_bytes(part));
         __syncwarp();
         uint8_t *st = sm + s * kStageBytes;
         const int g8 = lane >> 1, half = lane & 1;
-        if (part < 4)
-            tc::gather4_hint(st + part * kLatBlock + g8 * 1024 + half * 512, mlat, part * 128, rows[0], rows[1],
-                             rows[2], rows[3], &ms.kv_full[s], pol);
-        else
-            tc::gather4_hint(st + kRopeOff + g8 * 512 + half * 256, mrope, 512, rows[0], rows[1], rows[2], rows[3],
-                             &ms.kv_full[s], pol);
+        void *dst = st + (part < 4 ? part * kLatBlock + g8 * 1024 + half * 512 : kRopeOff + g8 * 512 + half * 256);
+        const CUtensorMap *map = part < 4 ? mlat : mrope;
+        if (PAIR) gather4_pair(dst, map, part * 128, rows, in_block(&ms.kv_full[s], 0), pol);
+        else tc::gather4_hint(dst, map, part * 128, rows[0], rows[1], rows[2], rows[3], &ms.kv_full[s], pol);
         ++it;
 #pragma unroll
         for (int i = 0; i < 4; ++i) rows[i] = next[i];
         check(rows, n);
     }
-    if (!ok) {      // flagged: let the copies in flight land before the CTA ends
+    if (PAIR) {
+        if (lane == 0) ms.issued[part] = it;        // see land
+    } else if (!ok) {       // flagged: let the copies in flight land before the CTA ends
         for (int k = it < kStages ? 0 : it - kStages; k < it; ++k) mbar_wait(&ms.kv_full[k % kStages], (k / kStages) & 1);
+    }
+}
+
+// A pair that gave up (flagged): run by one thread of CTA 0 once neither CTA
+// issues any more, lets the copies of both land.  The barriers' last phases
+// may lack a producer's arrival or one CTA's bytes, which never come.
+template <class C>
+__device__ void land(Misc<C> &ms) {
+    int most = 0;
+    for (int j = 0; j < kProdWarps; ++j) most = max(most, max(ms.issued[j], load_in_block(&ms.issued[j], 1)));
+    for (int k = max(most - kStages, 0); k < most; ++k) {
+        uint64_t *bar = &ms.kv_full[k % kStages];
+        for (int j = 0; j < kProdWarps; ++j) {
+            const bool here = k < ms.issued[j], there = k < load_in_block(&ms.issued[j], 1);
+            if (!here)
+                mbar_arrive_expect_tx(bar, there ? part_bytes(j) : 0);
+            else if (!there)
+                asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                             "r"(part_bytes(j))
+                             : "memory");
+        }
+        mbar_wait(bar, (k / kStages) & 1);
     }
 }
 
@@ -349,7 +404,7 @@ __device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t par, int *abor
     }
 }
 
-// CTA 0 issues; CTA 1 of a pair passes its tiles' arrival on to it.
+// CTA 0 issues a pair's.
 template <int NP, int TERMS, bool PAIR>
 __device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, PAIR>> &ms, int rank) {
     using C = Cfg<NP, TERMS, PAIR>;
@@ -360,15 +415,7 @@ __device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, 
     const uint64_t qr0 = tc::sdesc(base + kOffQ + C::QRope, 16, 512, tc::kSw64);
     Walk<C::Tokens> w;
     w.init(a, ms);
-    if (PAIR && rank > 0) {
-        for (int it = 0; w.valid(); ++it, w.next(a)) {
-            const int s = it % kStages;
-            if (!wait_or_abort(&ms.kv_full[s], (it / kStages) & 1, &ms.abort_flag)) break;
-            if (one) arrive_lead<PAIR>(&ms.kv_full[s], rank);
-            __syncwarp();
-        }
-        return;
-    }
+    if (PAIR && rank > 0) return;
     for (int it = 0; w.valid(); ++it, w.next(a)) {
         const int s = it % kStages, d = it & 1;
         if (w.first && !wait_pair<PAIR>(&ms.q_ready, w.unit & 1, &ms.abort_flag)) break;
@@ -663,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         const int more = PAIR && rank == 0;         // CTA 0 also hears of CTA 1's
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&ms.kv_full[s], kProdWarps + more);
+            mbar_init(&ms.kv_full[s], kProdWarps);
             mbar_init(&ms.kv_empty[s], 1);
         }
         for (int d = 0; d < 2; ++d) {
@@ -687,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
         mma_issuer<NP, TERMS, PAIR>(a, sm, ms, rank);
     } else if (warp < kPrepWarp0) {
-        producer<C>(a, &mlat, &mrope, sm, ms, rank);
+        producer<C, PAIR>(a, &mlat, &mrope, sm, ms, rank);
     } else {
         Walk<C::Tokens> w;
         w.init(a, ms);
@@ -710,6 +757,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();
     __syncwarp();
     sync_all<PAIR>();
+    if (PAIR && (ms.abort_flag || load_in_block(&ms.abort_flag, rank ^ 1))) {
+        if (tid == 0 && rank == 0) land(ms);
+    }
+    if (PAIR) sync_all<PAIR>();
     tc::fence_after();
     if (warp == kMmaWarp) tmem_free<PAIR>(ms.tmem, C::TmemCols);
 }
