@@ -40,7 +40,7 @@
 //
 // Measured (12 heads, bf16 query): 64 requests of 1K to 8K tokens, one row
 // each, in 34.5 us, 5.0 TB/s of cache rows; 128 of 4K to 32K, four rows each,
-// in 256 us, 5.7 TB/s (the attention kernel's loads alone reach 5.8 at this
+// in 256 us, 5.7 TB/s (loads alone top out at 5.3 to 5.7 at this
 // random order of 576-byte rows); 32 of 32K, 96 heads, in 128 us, 4.9 TB/s:
 // two stages' copies do not cover their latency and the MMAs' 1,940 cycles.
 #include <cudaTypedefs.h>

@@ -11,8 +11,8 @@
 // and B of every adapter in use; at a few rows by the two launches and the
 // chain A -> T -> B T.
 //
-// Measured: 64 single-row requests of 12 heads, rank 16, in 6.7 us; 32 of 96
-// heads, rank 32, in 12.8 (their bytes: 3.5); 256 requests of eight rows, 12
+// Measured: 64 single-row requests of 12 heads, rank 16, in 6.8 us; 32 of 96
+// heads, rank 32, in 9.7 (their bytes: 3.5); 256 requests of eight rows, 12
 // heads, rank 64, in 29.3 (47.7 MB, 7.0): 8.8 until the last T, then 5.3
 // tiles a block of ~3,600 cycles, bound by the chain of the ring's entries.
 //
@@ -29,8 +29,9 @@
 //     stays in shared memory over the head's tiles of rows (N), whose latents
 //     stream past it into tcgen05 MMAs.  B[a, h] T in one of two ways.
 //     One row a request: 16 warps form it by warp MMAs from global memory
-//     into a float32 tile, each row from its own B (the MMA's other columns
-//     are copies); the first rows' B is on its way while T is still formed.
+//     into a float32 tile, an MMA's eight columns being rows that share an
+//     adapter (32 requests of 96 heads on eight adapters 9.7 us, with a row an
+//     MMA 12.3); the first ones' B is on its way while T is still formed.
 //     More: through a ring, an entry being B[a, h] (M, by TMA) and the T rows
 //     of up to eight rows of one request (its place in a 16-row window, N),
 //     two MMAs per 16 ranks into 16 TMEM columns of its own, of which the
@@ -104,6 +105,12 @@ __device__ __forceinline__ Words<N> load_now(const void *p) {
                      : "l"(p));
     else
         asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(x.w[0]), "=r"(x.w[1]) : "l"(p));
+    return x;
+}
+
+__device__ __forceinline__ int load_int(const int *p) {
+    int x;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(x) : "l"(p));
     return x;
 }
 
@@ -350,14 +357,19 @@ __device__ __forceinline__ float sigmoid_f32(float x) {
 // --------------------------------- project: B T by warp MMAs (one row a request)
 
 constexpr int kFewThreads = 512;                   // and a warp that issues copies and products
+constexpr int kBatch = 4;                          // items a warp expands at once
 constexpr int kDStride = MLA_D_V + 4;              // float32 tile rows, a bank apart per row pair
+
+// A row of T, hi and lo, in shared memory (its 16 bytes more spread rows over the banks).
+__host__ __device__ constexpr int t_stride(int rank) { return 2 * rank + 8; }
 
 // NR rows a tile; two tiles' latents.
 template <int NR>
 struct FewTile {
     static constexpr int kBBlock = NR * 128, kBBytes = kColBlocks * kBBlock;
     static constexpr int kDOff = kXOff + 2 * kBBytes;
-    static constexpr int kSmem = kDOff + NR * kDStride * 4 + 1024;
+    static constexpr int kTOff = kDOff + NR * kDStride * 4;         // the rows' T
+    static constexpr int kSmem = kTOff + NR * t_stride(MLA_MAX_LORA_RANK) * 2 + 1024;
     static constexpr int kRows = NR / 4;            // rows per thread in the epilogue
 };
 
@@ -378,62 +390,101 @@ __device__ __forceinline__ void ld_rows(uint32_t taddr, float (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// B[a, h] T of the tile's rows (row n: B[n] its adapter's, null for none) ->
-// delta[n][v].  Warp w takes outputs 16 (w % 8) .. + 15 of every second row,
-// BATCH rows at once, 8 W ranks a step: a lane's W words of B and of T are
-// W / 2 k-steps' worth.  FIRST: T is waited for once the first rows' B is on
-// its way.
+// Up to eight rows of a tile that share an adapter, and its B[a, h].
+struct Item {
+    const __nv_bfloat16 *b;
+    int n;
+    uint8_t row[8];     // past the n-th: the first again
+};
+
+// Run by a warp, lane i with row i's adapter (-1: none): the tile's items; their number.
+__device__ __forceinline__ int make_items(const LoraArgs &p, Item *items, int a, int h) {
+    const uint32_t lane = threadIdx.x & 31, below = (1u << lane) - 1;
+    const uint32_t same = __match_any_sync(0xffffffffu, a);
+    const int before = __popc(same & below);
+    const bool lead = a >= 0 && before % 8 == 0;
+    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    if (lead) {
+        Item x;
+        x.b = p.b + ((int64_t)a * p.H + h) * MLA_D_V * p.rank;
+        x.n = min(8, __popc(same) - before);
+        uint32_t rest = same & ~below;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            x.row[c] = (uint8_t)(c < x.n ? __ffs(rest) - 1 : lane);
+            rest &= rest - 1;
+        }
+        items[__popc(leads & below)] = x;
+    }
+    return __popc(leads);
+}
+
+// B[a, h] T of the tile's items -> delta[row][v], T staged in `ts`.  Warp w
+// takes outputs 16 (w % 8) .. + 15 of every second item, BATCH items at once,
+// 8 W ranks a step: a lane's W words of B and of T are W / 2 k-steps' worth.
+// FIRST: T is waited for once the first items' B is on its way.
 template <int W, int BATCH, bool FIRST>
-__device__ __forceinline__ void expand(const LoraArgs &p, float *delta, const __nv_bfloat16 *const *B, int nrows,
-                                       int t0, int h) {
-    bool wait = FIRST;
+__device__ __forceinline__ void expand(const LoraArgs &p, float *delta, __nv_bfloat16 *ts, const Item *items,
+                                       int nitems, int nrows, int t0, int h) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int v0 = 16 * (warp & 7), rank = p.rank;
-    const int b_lane = (v0 + g) * rank + 2 * W * q, t_row = p.H * 2 * rank;
-    const __nv_bfloat16 *t_lane = p.t + ((int64_t)t0 * p.H + h) * 2 * rank + 2 * W * q;
-    for (int i0 = warp >> 3; i0 < nrows; i0 += 2 * BATCH) {
-        const __nv_bfloat16 *b[BATCH];
+    const int v0 = 16 * (warp & 7), rank = p.rank, stride = t_stride(rank);
+    const int b_lane = (v0 + g) * rank + 2 * W * q;
+    Words<W> x[BATCH], y[BATCH];
+    const auto load = [&](int i0, int k) {
+        const bool in = k + 2 * W * q < rank;
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            x[u] = y[u] = {};
+            if (in && i0 + 2 * u < nitems) {
+                const __nv_bfloat16 *b = items[i0 + 2 * u].b + b_lane + k;
+                x[u] = load_now<W>(b);
+                y[u] = load_now<W>(b + 8 * rank);
+            }
+        }
+    };
+    const int first = warp >> 3;
+    load(first, 0);
+    if (FIRST) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int row = warp; row < nrows; row += kFewThreads / 32)
+        if (lane < rank / 4)
+            reinterpret_cast<uint4 *>(ts + row * stride)[lane] =
+                reinterpret_cast<const uint4 *>(p.t + ((int64_t)(t0 + row) * p.H + h) * 2 * rank)[lane];
+    asm volatile("bar.sync 1, %0;" ::"n"(kFewThreads) : "memory");
+    for (int i0 = first; i0 < nitems; i0 += 2 * BATCH) {
         float acc[BATCH][4] = {};
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u) b[u] = i0 + 2 * u < nrows ? B[i0 + 2 * u] : nullptr;
         for (int k = 0; k < rank; k += 8 * W) {
+            if (i0 > first || k > 0) load(i0, k);
             const bool in = k + 2 * W * q < rank;
-            Words<W> x[BATCH] = {}, y[BATCH] = {}, hi[BATCH] = {}, lo[BATCH] = {};
 #pragma unroll
-            for (int u = 0; u < BATCH; ++u)
-                if (in && b[u]) {
-                    const __nv_bfloat16 *at = b[u] + b_lane + k;
-                    x[u] = FIRST ? load_now<W>(at) : load_words<W>(at);
-                    y[u] = FIRST ? load_now<W>(at + 8 * rank) : load_words<W>(at + 8 * rank);
+            for (int u = 0; u < BATCH; ++u) {
+                if (i0 + 2 * u >= nitems) break;
+                Words<W> hi = {}, lo = {};
+                if (in) {
+                    const __nv_bfloat16 *s = ts + items[i0 + 2 * u].row[g] * stride + k + 2 * W * q;
+                    hi = load_words<W>(s);
+                    lo = load_words<W>(s + rank);
                 }
-            if (FIRST && wait) asm volatile("griddepcontrol.wait;" ::: "memory");
-            wait = false;
-#pragma unroll
-            for (int u = 0; u < BATCH; ++u)
-                if (in && b[u]) {
-                    const __nv_bfloat16 *t = t_lane + (int64_t)t_row * (i0 + 2 * u) + k;
-                    hi[u] = load_words<W>(t);
-                    lo[u] = load_words<W>(t + rank);
-                }
-#pragma unroll
-            for (int u = 0; u < BATCH; ++u)
 #pragma unroll
                 for (int j = 0; j < W; j += 2) {
                     const uint32_t a[4] = {x[u].w[j], y[u].w[j], x[u].w[j + 1], y[u].w[j + 1]};
-                    mma_bf16(acc[u], a, hi[u].w[j], hi[u].w[j + 1]);
-                    mma_bf16(acc[u], a, lo[u].w[j], lo[u].w[j + 1]);
+                    mma_bf16(acc[u], a, hi.w[j], hi.w[j + 1]);
+                    mma_bf16(acc[u], a, lo.w[j], lo.w[j + 1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            if (i0 + 2 * u >= nitems) break;
+            const Item &it = items[i0 + 2 * u];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                if (2 * q + c < it.n) {
+                    float *d = delta + it.row[2 * q + c] * kDStride + v0 + g;
+                    d[0] = acc[u][c];
+                    d[8] = acc[u][2 + c];
                 }
         }
-        // The eight columns are equal.
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u)
-            if (q == 0 && b[u]) {
-                float *d = delta + (i0 + 2 * u) * kDStride + v0 + g;
-                d[0] = acc[u][0];
-                d[8] = acc[u][2];
-            }
     }
-    if (FIRST && wait) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // NR rows a tile at most, p.tile_rows of them.
@@ -444,15 +495,27 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *delta = reinterpret_cast<float *>(sm + T::kDOff);
+    __nv_bfloat16 *ts = reinterpret_cast<__nv_bfloat16 *>(sm + T::kTOff);
     __shared__ uint64_t full[2], done[2];
     __shared__ uint32_t tmem;
     __shared__ uint8_t active[NR];
-    __shared__ const __nv_bfloat16 *adapter_b[NR];
+    __shared__ uint8_t adapted[NR];
+    __shared__ Item items[NR];
+    __shared__ int nitems;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y, rows = p.tile_rows, tiles = (p.S + rows - 1) / rows, step = gridDim.x;
     const bool issuer = warp == kFewThreads / 32;   // a whole warp; one lane copies and commits
     const uint32_t one = elect_one();
 
+    // Row `tid`'s adapter and length; the first tile's on their way during the set-up.
+    int index = -1, len = 0;
+    const auto look = [&](int tile) {
+        const int t = tile * rows + tid;
+        const bool is = tid < rows && t < p.S;
+        index = is ? load_int(p.adapters + t) : -1;
+        len = is ? load_int(p.lengths + t) : 0;
+    };
+    look(blockIdx.x);
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&full[s], 1);
@@ -491,10 +554,14 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
     };
     for (int tile = blockIdx.x; tile < tiles; tile += step, ++it) {
         const int t0 = tile * rows, nrows = min(rows, p.S - t0);
-        if (tid < NR) {
-            const int a = tid < nrows ? adapter_of(p, t0 + tid) : -1;
-            active[tid] = tid < nrows && __ldg(p.lengths + t0 + tid) > 0;
-            adapter_b[tid] = a < 0 ? nullptr : p.b + ((int64_t)a * p.H + h) * MLA_D_V * p.rank;
+        if (it > 0) look(tile);
+        if (warp == 0) {        // NR <= 32
+            const int a = valid_adapter(p, index), n = make_items(p, items, a, h);
+            if (lane < NR) {
+                active[lane] = len > 0;
+                adapted[lane] = a >= 0;
+            }
+            if (lane == 0) nitems = n;
         }
         // This thread's gates (output v of rows first .. first + kRows - 1),
         // in flight during the products.
@@ -510,11 +577,11 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
         __syncthreads();
         if (tid < kFewThreads) {
             if (p.rank <= 16) {
-                if (it == 0) expand<2, 4, true>(p, delta, adapter_b, nrows, t0, h);
-                else expand<2, 4, false>(p, delta, adapter_b, nrows, t0, h);
+                if (it == 0) expand<2, kBatch, true>(p, delta, ts, items, nitems, nrows, t0, h);
+                else expand<2, kBatch, false>(p, delta, ts, items, nitems, nrows, t0, h);
             } else {
-                if (it == 0) expand<4, 2, true>(p, delta, adapter_b, nrows, t0, h);
-                else expand<4, 2, false>(p, delta, adapter_b, nrows, t0, h);
+                if (it == 0) expand<4, kBatch, true>(p, delta, ts, items, nitems, nrows, t0, h);
+                else expand<4, kBatch, false>(p, delta, ts, items, nitems, nrows, t0, h);
             }
         }
         if (issuer) {
@@ -539,7 +606,7 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
                 if (n >= nrows) break;
                 float x = 0.f;      // a select, so that nothing of an empty request is seen
                 if (active[n]) {
-                    x = adapter_b[n] ? d[i] + delta[n * kDStride + v] : d[i];
+                    x = adapted[n] ? d[i] + delta[n * kDStride + v] : d[i];
                     x *= sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16));
                 }
                 p.out[at + (int64_t)i * row_step] = __float2bfloat16_rn(x);
@@ -1062,14 +1129,14 @@ cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *
     const bool low = (p.S + 15) / 16 <= std::max(1, sms / H);
     // With one row a request every row has an entry of its own, whose way
     // through the ring costs more than its warp MMAs: 64 requests of 12 heads
-    // 6.7 us by warp MMAs and 7.9 through the ring at rank 16, 9.7 and 11.7 at
+    // 6.8 us by warp MMAs and 7.9 through the ring at rank 16, 9.4 and 11.7 at
     // rank 64 (and a 32-row tile's entries would not fit TMEM).  With eight
     // rows a request (256 of rank 64) 46 and 29 us, with four 29 and 20.
     if (qlen == 1) {
         p.tile_rows = low ? 16 : 32;
         // Down to four rows while every tile has a block of its own: a row's
-        // expansion takes its block's time (64 requests of rank 64 12.3 us
-        // with 16 rows, 9.7 with eight; 16 of them 11.5, and 6.9 with four).
+        // expansion takes its block's time (64 requests of rank 64 11.3 us
+        // with 16 rows, 9.4 with eight; 16 of them 11.0, and 7.4 with four).
         const auto tiles = [&](int rows) { return (p.S + rows - 1) / rows; };
         while (low && p.tile_rows > 4 && tiles(p.tile_rows / 2) <= std::max(1, sms / H)) p.tile_rows /= 2;
         return low ? project_few<16>(mw, p, sms, st) : project_few<32>(mw, p, sms, st);

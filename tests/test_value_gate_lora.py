@@ -252,3 +252,19 @@ def test_without_adapters_it_is_value_gate_up_to_one_rounding():
     ref = mla.value_gate(s["latent"], s["w_uv"], s["gate"], s["lengths"], 2).double()
     # value_gate rounds the value and the product (2^-8 each), this one the product: 3 half steps apart at most
     assert ((out - ref).abs() <= 3.02 * 2.0**-8 * out.abs() + 1e-30).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,heads,rank", [(40, 12, 24), (150, 5, 16), (70, 3, 128)])
+def test_rows_that_share_adapters_in_no_order(R, heads, rank):
+    # an adapter of more rows than a product holds, some of a few, some of one, and none
+    s = _make(R, 1, heads, rank, 6, 31)
+    ad = [0 if i % 3 else (i * 7) % 9 - 1 for i in range(R)]
+    s["adapters"] = torch.tensor([a if a < 6 else -1 for a in ad], dtype=torch.int32, device=DEV)
+    want = mla.value_gate_lora(**s)
+    _check(want, s)
+    s["latent"][4] = float("nan")       # a row's own only, whoever shares its adapter
+    got = mla.value_gate_lora(**s)
+    others = torch.arange(R, device=DEV) != 4
+    assert torch.equal(got[others], want[others])
+    assert got[4].isnan().any()
