@@ -12,8 +12,8 @@
 // Design: a cluster of blocks per request, as many of them as it takes to
 // hold it (the others end at once), each with a contiguous slice of its
 // tokens and every warp with a contiguous part of that, whose keys
-// (order-preserving 32-bit images of the weights) stay in registers: 16 a
-// thread, 8,192 tokens a block.  A longer slice is taken in rounds of that
+// (order-preserving 32-bit images of the weights) stay in registers: 8,192
+// tokens a block.  A longer slice is taken in rounds of that
 // size, read again for every step.  The m-th largest key is found by radix
 // selection, 11 + 11 + 10 bits, ended by the digits whose keys all stay: every
 // block counts its slice into a shared histogram, adds the bins that are not
@@ -24,7 +24,7 @@
 // by ballots, the offsets of warps and blocks are exchanged once, and the
 // tokens are placed by the ballots again.
 //
-// Measured: 12.8 us for one request of 128K tokens, 9.4 for 64 of 1K to 8K, 77
+// Measured: 12.8 us for one request of 128K tokens, 8.7 for 64 of 1K to 8K, 77
 // for 256 of 128 to 128K (log-uniform, 5.0 M tokens, 1.0 TB/s: its counts and
 // placements are bound by instructions, and by how many clusters an SM holds).
 #include <atomic>
@@ -36,13 +36,10 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048, kDigits = 3, kOwn = kBins / kThreads;
-constexpr int kSteps = 16;         // tokens a thread holds
-constexpr int kRound = kSteps * kThreads;
+constexpr int kBins = 2048, kDigits = 3;
+constexpr int kRound = 8192;       // tokens a block holds
 constexpr int kClasses = 6;        // powers of two of blocks, 0 to 4, and more than one round
 constexpr int kInOrder = 32;       // clusters that all run at once
-static_assert(kOwn == 4, "a thread reads its bins as one vector");
 
 struct EvictArgs {
     const int32_t *pages, *indptr, *budgets;
@@ -71,14 +68,15 @@ __device__ __forceinline__ int kept_tokens(const EvictArgs &a, int r, int len) {
     return b < 0 ? 0 : b < len ? b : len;
 }
 
+template <int WARPS>
 struct __align__(16) Shared {
     uint32_t hist[kDigits][kBins];
     uint32_t sums[kDigits][kBins];  // of this block's share of the bins, over the cluster
-    uint32_t red[3][kWarps];
-    uint32_t classes[kWarps][kClasses];     // a warp's requests by the blocks they take
+    uint32_t red[3][WARPS];
+    uint32_t classes[WARPS][kClasses];     // a warp's requests by the blocks they take
     int own[4];                             // the cluster's request, its tokens, first entry, kept tokens
-    uint32_t scan[kWarps];
-    uint32_t warp_kept[kWarps], warp_ties[kWarps];
+    uint32_t scan[WARPS];
+    uint32_t warp_kept[WARPS], warp_ties[WARPS];
     uint32_t totals[2];             // this block's sure tokens and ties, for the cluster
     uint32_t pick[3];
 };
@@ -105,15 +103,37 @@ __device__ __forceinline__ uint32_t remote(const uint32_t *p, uint32_t rank) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ uint4 remote4(const uint32_t *p, uint32_t rank) {
+// A thread's bins.
+template <int N>
+struct Bins {
+    static_assert(N == 2 || N == 4, "one vector");
+    uint32_t n[N];
+};
+template <int N>
+__device__ __forceinline__ Bins<N> local_bins(const uint32_t *p) {
+    Bins<N> b;
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        b.n[0] = v.x, b.n[1] = v.y, b.n[2] = v.z, b.n[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        b.n[0] = v.x, b.n[1] = v.y;
+    }
+    return b;
+}
+template <int N>
+__device__ __forceinline__ Bins<N> remote_bins(const uint32_t *p, uint32_t rank) {
     uint32_t addr;
-    uint4 v;
+    Bins<N> b;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+    if constexpr (N == 4)
+        asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(b.n[0]), "=r"(b.n[1]), "=r"(b.n[2]), "=r"(b.n[3])
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(b.n[0]), "=r"(b.n[1]) : "r"(addr) : "memory");
+    return b;
 }
 
 // Adds v at `p`'s place in the shared memory of block `rank`.
@@ -126,6 +146,7 @@ __device__ __forceinline__ void remote_add(uint32_t *p, uint32_t rank, uint32_t 
 }
 
 // Exclusive prefix sum of v over the block's threads.
+template <int WARPS>
 __device__ uint32_t block_scan(uint32_t v, uint32_t *red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t x = v;
@@ -137,7 +158,7 @@ __device__ uint32_t block_scan(uint32_t v, uint32_t *red) {
     __syncthreads();
     if (lane == 31) red[warp] = x;
     __syncthreads();
-    const uint32_t w = lane < kWarps ? red[lane] : 0;
+    const uint32_t w = lane < WARPS ? red[lane] : 0;
     uint32_t s = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -156,8 +177,11 @@ __device__ __forceinline__ int blocks_for(int len, int log_cs) {
 }
 
 // 2^log_cs blocks (a cluster) per request.
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, int log_cs) {
-    __shared__ Shared sh;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_kernel(const EvictArgs a, int log_cs) {
+    constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+    constexpr int kSteps = kRound / THREADS, kOwn = kBins / THREADS;    // tokens a thread holds; bins it sums
+    __shared__ Shared<kWarps> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t below = (1u << lane) - 1, rank = block_rank();
     // The cluster's request.  Clusters start in order of their number: with
@@ -312,34 +336,30 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
             __syncthreads();
             // Bins from the top: thread t holds the kOwn from kBins - 1 - kOwn * t down, summed over the cluster.
             const uint32_t top = kBins - 1 - kOwn * tid, low = top - (kOwn - 1);
-            uint32_t n[kOwn], sum = 0;
-            uint4 v = *reinterpret_cast<const uint4 *>(hist + low);
+            uint32_t sum = 0;
+            Bins<kOwn> bin = local_bins<kOwn>(hist + low);
             if (!one) {
                 const uint32_t share = kBins >> le, owner = low >> (11 - le);       // a block's bins; these bins' block
                 uint32_t *at = sh.sums[digit] + (low & (share - 1));
                 if (digit == 0) cluster_wait();
-                if (v.x) remote_add(at, owner, v.x);
-                if (v.y) remote_add(at + 1, owner, v.y);
-                if (v.z) remote_add(at + 2, owner, v.z);
-                if (v.w) remote_add(at + 3, owner, v.w);
-                cluster_sync();
-                v = remote4(at, owner);
-            }
-            n[0] = v.w;
-            n[1] = v.z;
-            n[2] = v.y;
-            n[3] = v.x;
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) sum += n[j];
-            uint32_t above = block_scan(sum, sh.scan);
+                for (int j = 0; j < kOwn; ++j)
+                    if (bin.n[j]) remote_add(at + j, owner, bin.n[j]);
+                cluster_sync();
+                bin = remote_bins<kOwn>(at, owner);
+            }
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) sum += bin.n[j];
+            uint32_t above = block_scan<kWarps>(sum, sh.scan);
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
-                if (above < need && need <= above + n[j]) {
+                const uint32_t n = bin.n[kOwn - 1 - j];
+                if (above < need && need <= above + n) {
                     sh.pick[0] = top - j;
                     sh.pick[1] = need - above;
-                    sh.pick[2] = n[j];
+                    sh.pick[2] = n;
                 }
-                above += n[j];
+                above += n;
             }
             __syncthreads();
             T |= sh.pick[0] << shift;
@@ -458,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a, i
     if (!one) cluster_sync();                  // no block ends while another may read its shared memory
 }
 
+template <int THREADS>
 cudaError_t launch(const EvictArgs &a, int log_cs, cudaStream_t st) {
     static std::atomic<unsigned long long> wide{0};     // devices where clusters of 16 have been allowed
     if (log_cs > 3) {
@@ -466,14 +487,14 @@ cudaError_t launch(const EvictArgs &a, int log_cs, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
         if (!(bit & wide.load(std::memory_order_acquire))) {
-            e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            e = cudaFuncSetAttribute(evict_kernel<THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
             wide.fetch_or(bit, std::memory_order_release);
         }
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.R << log_cs, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -481,7 +502,7 @@ cudaError_t launch(const EvictArgs &a, int log_cs, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, a, log_cs);
+    return cudaLaunchKernelEx(&cfg, evict_kernel<THREADS>, a, log_cs);
 }
 
 }  // namespace
@@ -507,7 +528,7 @@ cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32
     // length in one round.  Fewer blocks take a long request in rounds (one of
     // 128K: 136 us with 1, 75 with 2, 42 with 4, 25 with 8, 12.8 with 16); more
     // mostly end unused, and each costs its launch (64 requests of 1K to 8K:
-    // 9.4 us with 1, 10.5 with 2, 15 with 4, 17 with 8; 128 of 8K to 32K: 44
+    // 9.2 us with 1, 10.5 with 2, 15 with 4, 17 with 8; 128 of 8K to 32K: 44
     // with 2, 34 with 4, 40 with 8; 256 of 128 to 128K: 96 with 2, 77 with 4,
     // 74 with 8, 114 with 16).  A few requests take the blocks that half the
     // SMs hold: these cost nothing (8 of 4K: 7.4 us with 1 to 8, 10 with 16),
@@ -516,7 +537,11 @@ cudaError_t kv_evict_launch(const int32_t *pages, int64_t num_pages, const int32
     const int64_t mean = (num_pages + R - 1) / R;
     int log_cs = 0;
     while (log_cs < 4 && ((mean >> log_cs) > kRound || ((int64_t)R << (log_cs + 1)) <= sms / 2)) ++log_cs;
-    return launch(a, log_cs, st);
+    // One block a request and an SM for each: 1,024 threads (64 of 1K to 8K
+    // 8.7 us, 9.2 with 512; 63 of 1K and one of 128K 133 and 147).  Elsewhere
+    // two blocks of 512 an SM (256 of 512 to 2K 9.9, 12.2 with 1,024; one of
+    // 128K 12.8 and 13.7; 128 of 8K to 32K 34 and 57).
+    return log_cs == 0 && R <= sms ? launch<1024>(a, log_cs, st) : launch<512>(a, log_cs, st);
 }
 
 cudaError_t evict_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }
