@@ -229,12 +229,13 @@ __device__ __forceinline__ uint32_t elect_one() {
     return r;
 }
 
-// D = A[128 x 512] B[N x 512]^T, both in 128B-swizzled column blocks.
+// D (+)= A[128 x 64 (kb1 - kb0)] B[N x ..]^T: column blocks kb0 .. kb1 - 1 of
+// the latent's, both 128B-swizzled.
 __device__ __forceinline__ void mma_latent(uint32_t d_tmem, uint32_t a, uint32_t a_block, uint32_t b, uint32_t b_block,
-                                           uint32_t idesc, uint32_t one) {
+                                           uint32_t idesc, uint32_t one, int kb0 = 0, int kb1 = kColBlocks) {
     const uint64_t ad = tc::sdesc(a, 16, 1024, tc::kSw128), bd = tc::sdesc(b, 16, 1024, tc::kSw128);
 #pragma unroll
-    for (int j = 0; j < MLA_D_LATENT / 16; ++j)
+    for (int j = 4 * kb0; j < 4 * kb1; ++j)
         mma_bf16_tc(d_tmem, ad + (j >> 2) * (a_block >> 4) + (j & 3) * 2, bd + (j >> 2) * (b_block >> 4) + (j & 3) * 2,
                     idesc, j > 0, one);
 }
@@ -254,7 +255,7 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x,
         : "memory");
 }
 
-constexpr int kTcPairs = 48, kTcThreads = 128;
+constexpr int kTcPairs = 48, kTcThreads = 128, kParts = 4;
 constexpr int kTcXBlock = kTcPairs * 128;
 
 // The last block's reads of 128 rows of pairs, and of 16 of A where the rank
@@ -270,42 +271,52 @@ __global__ void __launch_bounds__(kTcThreads)
     shrink_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mx, const LoraArgs p,
                      int tiles) {
     extern __shared__ __align__(1024) uint8_t sm[];
-    __shared__ uint64_t full, done;
+    __shared__ uint64_t full[kParts], done;     // a part: column blocks that arrive and are multiplied together
     __shared__ uint32_t tmem;
     asm volatile("griddepcontrol.launch_dependents;");
     const int r = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-    const int a = adapter_of(p, r);
-    if (a < 0) return;
+    const int index = load_int(p.adapters + r);
     const int tid = threadIdx.x, warp = tid >> 5;
     const int pairs = p.qlen * p.H, m0 = tile * kTcPairs;
     const int64_t row0 = (int64_t)r * pairs + m0;
     const int a_block = p.rank * 128, a_off = kColBlocks * kTcXBlock;
     if (tid == 0) {
-        mbar_init(&full, 1);
+        for (int i = 0; i < kParts; ++i) mbar_init(&full[i], 1);
         mbar_init(&done, 1);
         mbar_fence_init();
-        mbar_arrive_expect_tx(&full, kColBlocks * (kTcXBlock + a_block));
-        for (int kb = 0; kb < kColBlocks; ++kb) {
-            tma_2d(sm + kb * kTcXBlock, &mx, 64 * kb, (int)row0, &full);
-            tma_2d(sm + a_off + kb * a_block, &ma, 64 * kb, a * p.rank, &full);
-        }
     }
-    if (warp == 0) tc::tmem_alloc(&tmem, 128);
+    if (warp == 1) tc::tmem_alloc(&tmem, 128);
+    const int a = valid_adapter(p, index);
+    if (tid == 0 && a >= 0)
+        for (int i = 0; i < kParts; ++i) {
+            constexpr int kPer = kColBlocks / kParts;
+            mbar_arrive_expect_tx(&full[i], kPer * (kTcXBlock + a_block));
+            for (int kb = i * kPer; kb < (i + 1) * kPer; ++kb) {
+                tma_2d(sm + kb * kTcXBlock, &mx, 64 * kb, (int)row0, &full[i]);
+                tma_2d(sm + a_off + kb * a_block, &ma, 64 * kb, a * p.rank, &full[i]);
+            }
+        }
+    __syncwarp();
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    bool ok = true, issued = false;
+    if (a < 0) {
+        if (warp == 1) tc::tmem_free(tmem, 128);
+        return;
+    }
+    bool ok = true;
     if (warp == 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&full, 0));
-        if (ok) {
-            issued = true;
+        const uint32_t one = elect_one(), idesc = idesc_bf16((p.rank + 15) / 16 * 16);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            constexpr int kPer = kColBlocks / kParts;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[i], 0));
+            if (!ok) break;
             tc::fence_after();
-            const uint32_t one = elect_one();
-            mma_latent(tmem, smem_u32(sm), kTcXBlock, smem_u32(sm) + a_off, a_block, idesc_bf16((p.rank + 15) / 16 * 16),
-                       one);
-            if (one) tc::commit(&done);
-            __syncwarp();
+            mma_latent(tmem, smem_u32(sm), kTcXBlock, smem_u32(sm) + a_off, a_block, idesc, one, i * kPer, (i + 1) * kPer);
         }
+        if (one) tc::commit(&done);     // of those issued
+        __syncwarp();
     }
     ok = __syncthreads_and(ok);
     if (ok) ok = mbar_wait(&done, 0);
@@ -334,12 +345,12 @@ __global__ void __launch_bounds__(kTcThreads)
             }
     } else if (tid == 0) {
         // Flagged.  What is in flight finishes before TMEM is released.
-        mbar_wait(&full, 0);
-        if (issued) mbar_wait(&done, 0);
+        for (int i = 0; i < kParts; ++i) mbar_wait(&full[i], 0);
+        mbar_wait(&done, 0);
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 0) tc::tmem_free(tmem, 128);
+    if (warp == 1) tc::tmem_free(tmem, 128);
 }
 
 // ------------------------------------------------------------------ project
