@@ -12,9 +12,11 @@
 // chain A -> T -> B T.
 //
 // Measured: 64 single-row requests of 12 heads, rank 16, in 6.8 us; 32 of 96
-// heads, rank 32, in 9.7 (their bytes: 3.5); 256 requests of eight rows, 12
-// heads, rank 64, in 29.3 (47.7 MB, 7.0): 8.8 until the last T, then 5.3
-// tiles a block of ~3,600 cycles, bound by the chain of the ring's entries.
+// heads, rank 32, in 9.5 (their bytes: 3.5); 256 requests of eight rows, 12
+// heads, rank 64, in 27.6 (47.7 MB, 7.0): 8.8 until the last T, then six
+// tiles a block of ~3,300 cycles, in which the ring's entries, the latents'
+// products (their copies wait for the tile before) and the epilogue take
+// about as long as each other.
 //
 //   shrink: the (row, head) pairs of a request share A: T = latent A^T *
 //     lora_scale.  Few pairs: warp MMAs on fragments loaded straight from
@@ -611,17 +613,19 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
             float d[T::kRows];
             ld_rows<T::kRows>(tm + ((uint32_t)(32 * (warp & 3)) << 16) + (it & 1) * NR + first, d);
             tc::wait_ld();
+            uint16_t x[T::kRows];
 #pragma unroll
             for (int i = 0; i < T::kRows; ++i) {
                 const int n = first + i;
-                if (n >= nrows) break;
-                float x = 0.f;      // a select, so that nothing of an empty request is seen
-                if (active[n]) {
-                    x = adapted[n] ? d[i] + delta[n * kDStride + v] : d[i];
-                    x *= sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16));
-                }
-                p.out[at + (int64_t)i * row_step] = __float2bfloat16_rn(x);
+                const float val = adapted[n] ? d[i] + delta[n * kDStride + v] : d[i];
+                const float y = val * sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16));
+                // a select, so that nothing of an empty request is seen
+                x[i] = active[n] ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : 0;
             }
+            uint16_t *out = reinterpret_cast<uint16_t *>(p.out) + at;
+#pragma unroll
+            for (int i = 0; i < T::kRows; ++i)
+                if (first + i < nrows) out[(int64_t)i * row_step] = x[i];
         }
         tc::fence_before();
         __syncthreads();            // the tile's shared arrays are read
@@ -982,7 +986,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int c = __shfl_sync(0xffffffffu, col, i);
                 add[i] = ld1(tm + lanes + (adapted >> i & 1 ? c : T::kAddCols));
             }
-            if (tile + step < tiles) load(next, tile + step);
             tc::wait_ld();
             tc::fence_before();
             __syncwarp();
@@ -990,15 +993,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&sh.d_free[it & 1]);
                 mbar_arrive(&sh.add_free[it & p.add_both]);
             }
+            if (tile + step < tiles) load(next, tile + step);
+            // (Without branches between the rows: one at a time they would
+            // take 2,400 cycles.)
+            uint16_t x[T::kRows];
 #pragma unroll
             for (int i = 0; i < T::kRows; ++i) {
-                if (i >= nrows) break;
+                const float val = adapted >> i & 1 ? d[i] + add[i] : d[i];
+                const float y = val * sigmoid_f32(__uint_as_float((uint32_t)in.gate[i] << 16));
                 // a select, so that nothing of an empty request is seen
-                float x = 0.f;
-                if (live >> i & 1)
-                    x = (adapted >> i & 1 ? d[i] + add[i] : d[i]) * sigmoid_f32(__uint_as_float((uint32_t)in.gate[i] << 16));
-                p.out[at + i * row_step] = __float2bfloat16_rn(x);
+                x[i] = live >> i & 1 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : 0;
             }
+            uint16_t *out = reinterpret_cast<uint16_t *>(p.out) + at;
+#pragma unroll
+            for (int i = 0; i < T::kRows; ++i)
+                if (i < nrows) out[i * row_step] = x[i];
         }
     }
     tc::fence_before();
@@ -1142,7 +1151,7 @@ cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *
     // through the ring costs more than its warp MMAs: 64 requests of 12 heads
     // 6.8 us by warp MMAs and 7.9 through the ring at rank 16, 9.4 and 11.7 at
     // rank 64 (and a 32-row tile's entries would not fit TMEM).  With eight
-    // rows a request (256 of rank 64) 46 and 29 us, with four 29 and 20.
+    // rows a request (256 of rank 64) 46 and 28 us, with four 29 and 20.
     if (qlen == 1) {
         p.tile_rows = low ? 16 : 32;
         // Down to four rows while every tile has a block of its own: a row's
