@@ -55,8 +55,8 @@ def _ops_compile(obj: str):
 
 def _ops_link(obj: str, out: str):
     lib = os.path.join(_torch_dir(), "lib")
-    return ["g++", "-shared", "-o", out, obj, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
-            "-L" + BUILD, "-lmla_decode", "-Wl,-rpath,$ORIGIN"]
+    return ["g++", "-shared", "-o", out, obj, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+            "-ltorch_python", "-L" + BUILD, "-lmla_decode", "-Wl,-rpath,$ORIGIN"]
 
 
 def nvcc() -> str:
