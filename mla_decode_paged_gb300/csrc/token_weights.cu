@@ -32,17 +32,20 @@
 // bf16 rows take a pair of CTAs: each holds half of Q' and a 128-token tile
 // of its own, and cta_group::2 MMAs give both their tokens' scores with all
 // rows, so a cache row still crosses L2 once.  (Two CTAs reading every tile
-// for half of the rows each took 213 us against 128 us for 32 x 96 heads, 32K
+// for half of the rows each took 213 us against 121 us for 32 x 96 heads, 32K
 // tokens: L2 then delivers the cache twice.)  Both CTAs' copies count at CTA
-// 0's barriers (a warp of CTA 1 that passed its tiles' arrival on: 164 us).
+// 0's barriers (a warp of CTA 1 that passed its tiles' arrival on: 164 us to
+// 128), and each converts its half of the query only (from both: 128 to 121).
 // More rows are cut into groups on neighbouring CTAs (pairs), each writing
 // its partial sums to the workspace, joined in group order by a small kernel.
 //
 // Measured (12 heads, bf16 query): 64 requests of 1K to 8K tokens, one row
 // each, in 34.5 us, 5.0 TB/s of cache rows; 128 of 4K to 32K, four rows each,
 // in 256 us, 5.7 TB/s (loads alone top out at 5.3 to 5.7 at this
-// random order of 576-byte rows); 32 of 32K, 96 heads, in 128 us, 4.9 TB/s:
+// random order of 576-byte rows); 32 of 32K, 96 heads, in 121 us, 5.1 TB/s:
 // two stages' copies do not cover their latency and the MMAs' 1,940 cycles.
+// A new request costs the conversion of its query, about 3,400 cycles for 16
+// rows (100 requests of 384 rows and 9 to 65 tokens: 62 us).
 #include <cudaTypedefs.h>
 #include <climits>
 #include <cuda_fp8.h>
@@ -453,8 +456,9 @@ __device__ __forceinline__ uint32_t q_offset(int n, int d) {
                    : kOffQ + C::QRope + (n >> 3) * 512 + tc::sw64(n, d - 512);
 }
 
-// The constants of request r's rows [grp * Rows, ...), and this CTA's half of
-// them (all without a pair) as the B operand, a warp a row.
+// The constants of request r's rows [grp * Rows, ...) and the rows as the B
+// operand, a warp a row; a pair's CTAs take half of them each and write the
+// constants to both.
 template <int NP, int TERMS, bool PAIR>
 __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, PAIR>> &ms, int r, int len, int grp,
                           int unit, int rank) {
@@ -481,20 +485,20 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, P
     }
     // Lane i: the LSE of the warp's i-th row.
     float lses = -INFINITY;
-    static_assert(C::Rows <= 32 * kPrepWarps, "a lane per row of a warp");
+    static_assert(NQ <= 32 * kPrepWarps, "a lane per row of a warp");
     {
-        const int rho = grp * C::Rows + pw + kPrepWarps * lane;
-        if (pw + kPrepWarps * lane < C::Rows && rho < rows_total) lses = __ldg(a.lse + (int64_t)r * rows_total + rho);
+        const int rho = grp * C::Rows + rank * NQ + pw + kPrepWarps * lane;
+        if (pw + kPrepWarps * lane < NQ && rho < rows_total) lses = __ldg(a.lse + (int64_t)r * rows_total + rho);
     }
     // Four rows' loads in flight a warp.
     constexpr int kBatch = 4, kVecs = TERMS == 1 ? 2 : 3;   // 16-byte vectors of a row a lane
-    static_assert(C::Rows % (kBatch * kPrepWarps) == 0, "whole batches");
+    static_assert(NQ % (kBatch * kPrepWarps) == 0, "whole batches");
 #pragma unroll 1
-    for (int i0 = 0; i0 < C::Rows / kPrepWarps; i0 += kBatch) {
+    for (int i0 = 0; i0 < NQ / kPrepWarps; i0 += kBatch) {
         uint4 v[kBatch][kVecs];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int row = pw + kPrepWarps * (i0 + i), rho = grp * C::Rows + row;
+            const int rho = grp * C::Rows + rank * NQ + pw + kPrepWarps * (i0 + i);
             const int t = rho / a.heads, h = rho - t * a.heads;
             const uint8_t *src = static_cast<const uint8_t *>(a.q) +
                                  (((int64_t)r * a.qlen + t) * a.q_row_stride + (int64_t)h * MLA_D_QK) * TERMS;
@@ -507,15 +511,13 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, P
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int row = pw + kPrepWarps * (i0 + i);
-            const int n = row - rank * NQ;      // row of this CTA's Q'
-            const bool mine = !PAIR || (n >= 0 && n < NQ);
+            const int n = pw + kPrepWarps * (i0 + i), row = rank * NQ + n;     // of this CTA's Q', of the group
             float back = 1.f;                   // 2^-e
             if (TERMS == 1) {
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
                     const int ch = lane + 32 * j;
-                    if (mine && ch < MLA_D_QK / 16) *reinterpret_cast<uint4 *>(sm + q_offset<C>(n, ch * 16)) = v[i][j];
+                    if (ch < MLA_D_QK / 16) *reinterpret_cast<uint4 *>(sm + q_offset<C>(n, ch * 16)) = v[i][j];
                 }
             } else {
                 float amax = 0.f;
@@ -534,7 +536,7 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, P
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
                     const int ch = lane + 32 * j;
-                    if (ch >= MLA_D_QK / 8 || !mine) continue;
+                    if (ch >= MLA_D_QK / 8) continue;
                     const uint32_t x[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
                     uint32_t hi[2], lo[2];
 #pragma unroll
@@ -567,18 +569,24 @@ __device__ void prep_unit(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, P
                 c.z = lse * kLog2e;
                 c.w = isinf(c.z) ? 0.f : fmaf(lse, kLog2e, -c.z) + lse * kLog2eLo;
             }
-            if (lane == 0) ms.c[buf][row] = c;
+            if (lane == 0) {
+                ms.c[buf][row] = c;
+                if (PAIR)
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(in_block(&ms.c[buf][row], rank ^ 1)),
+                                 "f"(c.x), "f"(c.y), "f"(c.z), "f"(c.w)
+                                 : "memory");
+            }
         }
     }
 }
 
-// A request's rows of this group into L2, ahead of their conversion.
+// This CTA's rows of a request into L2, ahead of their conversion.
 template <class C, int TERMS>
-__device__ void prefetch_rows(const TokenArgs &a, int r, int grp) {
+__device__ void prefetch_rows(const TokenArgs &a, int r, int grp, int rank) {
     const int rows_total = a.qlen * a.heads;
     const uint64_t keep = tc::l2_policy_last();
-    for (int row = threadIdx.x - kPrepWarp0 * 32; row < C::Rows; row += kPrepWarps * 32) {
-        const int rho = grp * C::Rows + row;
+    for (int row = threadIdx.x - kPrepWarp0 * 32; row < C::NQ; row += kPrepWarps * 32) {
+        const int rho = grp * C::Rows + rank * C::NQ + row;
         if (rho >= rows_total) break;
         const int t = rho / a.heads, h = rho - t * a.heads;
         tc::bulk_prefetch_l2(static_cast<const uint8_t *>(a.q) +
@@ -744,12 +752,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             prep_unit<NP, TERMS, PAIR>(a, sm, ms, w.r, w.len, grp, w.unit, rank);
             tc::fence_async_smem();     // generic-proxy writes -> tensor-core reads
             __syncwarp();
-            if (lane == 0) arrive_lead<PAIR>(&ms.q_ready, rank);
+            if (lane == 0) {
+                if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");      // the constants in the other CTA
+                arrive_lead<PAIR>(&ms.q_ready, rank);
+            }
             // The next request's (empty ones passed over), if this CTA gets to it.
             if (w.left > w.ntiles - w.t) {
                 int r = w.r + 1, base;
                 while (r < a.R && request_len(a.indptr, r, a.num_pages, &base) == 0) ++r;
-                if (r < a.R) prefetch_rows<C, TERMS>(a, r, grp);
+                if (r < a.R) prefetch_rows<C, TERMS>(a, r, grp, rank);
             }
         }
     }
