@@ -140,6 +140,10 @@ def _rand(n, seed):
     ([100] * 900 + [100000], 50, 5, 1),                             # one long request among many short
     ([7] * 700, 3, 1, 1),
     ([2500] * 40, 333, 10, 0),
+    ([3000] * 60 + [30000, 0, 1], 700, 16, 4),                      # a block a request, one of them in rounds
+    ([200] * 152, 50, 3, 1),
+    ([200] * 153, 50, 3, 1),
+    ([9000, 20000, 500] * 20, 3000, 64, 4),                         # two blocks a request
 ])
 def test_against_the_definition(lengths, budget, recent, sinks):
     _run(lengths, _rand(sum(lengths), 3), budget, recent, sinks, tail=5)
@@ -169,6 +173,15 @@ def test_ties_zeros_and_non_finite(n):
     for b in (1, n // 20, n // 2, n - 2):
         _run([n], w, b, 1, 1)
     _run([n], torch.full((n,), float("nan")), n // 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths", [[700] * 50, [700] * 200, [12000, 5] * 40])
+def test_ties_in_many_requests(lengths):
+    n = sum(lengths)
+    w = torch.randint(0, 4, (n,), generator=torch.Generator().manual_seed(n)).float()
+    for budget in (1, 200, 650):
+        _run(lengths, w, budget, 2, 1)
 
 
 @pytest.mark.gpu
