@@ -295,3 +295,22 @@ def test_many_wide_rows(T, D, xt, rt, pad, quant):
                                  residual_out=keep)
         assert torch.equal(again[0].view(torch.uint8), out.view(torch.uint8))
         assert torch.equal(keep.view(torch.uint8), ro.contiguous().view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,rt,quant", [
+    (60000, 256, torch.float32, "row"),
+    (45000, 1024, torch.bfloat16, None),
+    (39000, 520, None, "group"),
+    (10000, 24576, torch.bfloat16, None),
+])
+def test_rows_in_place_do_not_depend_on_the_batch(T, D, rt, quant):
+    # more rows than run at once, the next row's loads in flight while one is written over its inputs
+    x, w, r = _inputs(T, D, torch.bfloat16, rt, D)
+    parts = [slice(0, 50), slice(T // 2, T // 2 + 50), slice(T - 50, T)]
+    want = [mla.add_rms_norm(x[p], w, EPS, None if r is None else r[p], quant=quant) for p in parts]
+    out, sc, ro = mla.add_rms_norm(x, w, EPS, r, quant=quant, out=x if quant is None else None, residual_out=r)
+    for p, (o, s, q) in zip(parts, want):
+        assert torch.equal(out[p].view(torch.uint8), o.view(torch.uint8))
+        assert s is None or torch.equal(sc[p], s)
+        assert q is None or torch.equal(ro[p], q)
