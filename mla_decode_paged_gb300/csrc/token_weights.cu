@@ -768,10 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();
     __syncwarp();
     sync_all<PAIR>();
-    if (PAIR && (ms.abort_flag || load_in_block(&ms.abort_flag, rank ^ 1))) {
-        if (tid == 0 && rank == 0) land(ms);
+    if (PAIR) {
+        if ((ms.abort_flag || load_in_block(&ms.abort_flag, rank ^ 1)) && tid == 0 && rank == 0) land(ms);
+        __syncwarp();
+        sync_all<PAIR>();
     }
-    if (PAIR) sync_all<PAIR>();
     tc::fence_after();
     if (warp == kMmaWarp) tmem_free<PAIR>(ms.tmem, C::TmemCols);
 }
