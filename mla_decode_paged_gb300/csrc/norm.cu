@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(MAX) norm_kernel(const NormArgs a) {
 // ------------------------------------------------- many rows: a ring of rows
 
 constexpr int kMaxRing = 4, kMaxBlocks = 16;    // rows in a block's ring, blocks an SM
+constexpr int kRingThreads = 512, kRingVpt = 4; // of a block, at most: a row of 16,384 columns
 constexpr int kRingBytes = 110 * 1024;      // of shared memory, two blocks an SM
 
 struct RingArgs {
@@ -273,7 +274,7 @@ struct RingArgs {
 // blockDim.x threads hold a row, VPT vectors each, weights included; RES:
 // the residual's element size (0: none).
 template <typename T, int VPT, int RES>
-__global__ void __launch_bounds__(512, 2) norm_ring_kernel(const RingArgs ra) {
+__global__ void __launch_bounds__(kRingThreads, 2) norm_ring_kernel(const RingArgs ra) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float red[2][2][32];
     __shared__ __align__(8) uint64_t full[kMaxRing];
@@ -431,6 +432,7 @@ __global__ void __launch_bounds__(512, 2) norm_ring_kernel(const RingArgs ra) {
 
 template <typename T, int VPT, int RES>
 cudaError_t launch_ring(const RingArgs &ra, int sms, cudaStream_t st) {
+    static_assert(VPT <= kRingVpt, "launch's limit");
     const int smem = ra.depth * ra.row_bytes;
     cudaError_t e = smem_attr_once<norm_ring_kernel<T, VPT, RES>>(kRingBytes);
     if (e != cudaSuccess) return e;
@@ -489,8 +491,10 @@ cudaError_t launch(const NormArgs &a, int sms, cudaStream_t st) {
     // and 151.  Up to 1,024 columns a warp a row, with the next row's loads in
     // flight, is level or ahead: 8,192 x 512 4.3 us against 5.5, 65,536 x 576
     // 39 against 61, 8,192 x 1,024 14.0 against 14.7 (20,000 x 1,024 20.9
-    // against 18.8).  A row that does not fit the ring twice takes the blocks.
-    if (a.vecs > 128 && a.rows >= sms && ra.depth >= 2) {
+    // against 18.8).  A row that does not fit the ring twice takes the blocks,
+    // and so does one of more than 16,384 columns, more than a ring's block
+    // holds (without a residual up to 28,160 would fit the ring twice).
+    if (a.vecs > 128 && a.vecs <= kRingThreads * kRingVpt && a.rows >= sms && ra.depth >= 2) {
         if (a.vecs <= 512) return launch_ring_res<T, 1>(ra, sms, st);
         if (a.vecs <= 1024) return launch_ring_res<T, 2>(ra, sms, st);
         return launch_ring_res<T, 4>(ra, sms, st);

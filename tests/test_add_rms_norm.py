@@ -314,3 +314,26 @@ def test_rows_in_place_do_not_depend_on_the_batch(T, D, rt, quant):
         assert torch.equal(out[p].view(torch.uint8), o.view(torch.uint8))
         assert s is None or torch.equal(sc[p], s)
         assert q is None or torch.equal(ro[p], q)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [None, "row", "group", "static"])
+@pytest.mark.parametrize("T,D,xt", [
+    (200, 16392, torch.bfloat16),      # the first width that 512 threads of four vectors do not hold
+    (200, 20480, torch.float16),
+    (311, 24576, torch.bfloat16),
+    (200, 28160, torch.bfloat16),      # the widest of which two rows fit a ring
+    (200, 28168, torch.bfloat16),
+    (160, 32768, torch.bfloat16),
+])
+def test_wide_rows_without_a_residual_over_all_sms(T, D, xt, quant):
+    x, w, _ = _inputs(T, D, xt, None, T + D)
+    _, y = _formula(x, w)
+    out, scales, ro = mla.add_rms_norm(x, w, EPS, quant=quant, scale=0.013 if quant == "static" else None)
+    assert ro is None
+    if quant is None:
+        _check16(out, y, "out")
+    else:
+        _check8(out, scales, y, quant, 0.013)
+    few = mla.add_rms_norm(x[:3], w, EPS, quant=quant, scale=0.013 if quant == "static" else None)
+    assert torch.equal(out[:3].view(torch.uint8), few[0].view(torch.uint8))
