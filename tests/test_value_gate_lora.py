@@ -268,3 +268,41 @@ def test_rows_that_share_adapters_in_no_order(R, heads, rank):
     others = torch.arange(R, device=DEV) != 4
     assert torch.equal(got[others], want[others])
     assert got[4].isnan().any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,heads,rank,n", [
+    (100, 96, 32, 8),           # one block a head, four tiles each
+    (33, 96, 16, 33),           # the second tile holds one row
+    (385, 12, 64, 5),           # 13 tiles over 12 blocks of a head: one of them has two
+    (1000, 12, 16, 40),         # three tiles a block or two, the last of eight rows
+    (1000, 12, 128, 1000),      # and an adapter a row
+    (700, 40, 8, 3),            # eight tiles a block or seven
+])
+def test_single_rows_over_several_tiles_a_block(R, heads, rank, n):
+    s = _make(R, 1, heads, rank, n, R + rank)
+    s["lengths"][5::37] = 0
+    out = mla.value_gate_lora(**s)
+    _check(out, s)
+    assert torch.equal(mla.value_gate_lora(**s), out)
+    for r in (2, R // 2, R - 1):        # a row's own NaN stays in its row, in every tile of a block
+        s["latent"][r] = float("nan")
+    got = mla.value_gate_lora(**s)
+    others = torch.ones(R, dtype=torch.bool, device=DEV)
+    others[[2, R // 2, R - 1]] = False
+    assert torch.equal(got[others], out[others])
+    for r in (2, R // 2, R - 1):
+        assert got[r].isnan().all() if s["lengths"][r] > 0 else (got[r] == 0).all()
+    assert mla.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_a_padded_row_of_a_batch_does_not_depend_on_the_others():
+    # the same requests alone (tiles of few rows) and in a batch that takes several tiles a block
+    s = _make(600, 1, 24, 40, 9, 21)
+    out = mla.value_gate_lora(**s)
+    few = {k: (v[:7] if k in ("latent", "gate", "lengths", "adapters") else v) for k, v in s.items()}
+    want, bound = _formula(few)
+    got = mla.value_gate_lora(**{k: (v.contiguous() if isinstance(v, torch.Tensor) else v) for k, v in few.items()})
+    for o in (out[:7], got):
+        assert ((o.double() - want).abs() <= bound + 2.0**-8 * (want.abs() + bound) + 1e-40).all()
