@@ -84,7 +84,7 @@ mla_status cuda_fail(cudaError_t e, const char *where) {
 }
 
 // Page-list sizes of the calls that walk it in 32-bit token positions (a
-// tile or a block's step past the last one still fits).
+// tile or a block's round past the last one still fits).
 constexpr int64_t kMaxPages = INT32_MAX - 65535, kMaxRequests = 1 << 24;
 
 // Whether two blocks of bytes share one.

@@ -782,8 +782,9 @@ __global__ void __launch_bounds__(256) join_kernel(const TokenArgs a, const floa
                                                    float decay) {
     int base;
     const int len = request_len(a.indptr, blockIdx.x, a.num_pages, &base);
-    for (int j = blockIdx.y * 256 + threadIdx.x; j < len; j += gridDim.y * 256) {
-        const int64_t i = (int64_t)base + j;
+    // 64 bits: a step of the grid past the last token may pass 32.
+    for (int64_t j = blockIdx.y * 256 + threadIdx.x; j < len; j += gridDim.y * 256) {
+        const int64_t i = base + j;
         float sum = parts[i];
         for (int g = 1; g < a.groups; ++g) sum += parts[i + g * a.group_stride];
         out[i] = decay == 0.f ? sum : fmaf(a.weights[i], decay, sum);

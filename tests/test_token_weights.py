@@ -361,3 +361,30 @@ def test_same_bits_again_on_a_stream_and_in_a_graph():
     q.mul_(0.5)
     g.replay()
     assert torch.equal(out, mla.token_weights(q, kv, pages, indptr, 0.05, 1.0, lse, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qlen,heads,q8", [(1, 12, False), (3, 43, False), (3, 43, True)])
+def test_the_longest_page_list(qlen, heads, q8):
+    # one request of as many tokens as are accepted, over and over the same 64 rows: in one pass (12 query rows) and as
+    # groups' partial sums joined by a second kernel (129).  Every token's sum is its own, so equal rows give equal bits.
+    n = 2**31 - 65536
+    need = 4 * n * 2 + mla.token_weights_workspace(qlen, heads, n, q8) + (8 << 30)
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip("%d GB of device memory free" % (need >> 30))
+    q, kv, _, _ = _make([64], qlen, heads, heads, 21, q8)
+    head = torch.arange(64, dtype=torch.int32, device=DEV)
+    want, bound, lse = _formula(q, kv, head, [64], heads, qlen, 0.05, False)
+    pages = head.repeat(n // 64)
+    indptr = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    out = mla.token_weights(q, kv, pages, indptr, 0.05, 1.0, lse.contiguous(), heads=heads, qlen=qlen)
+    assert mla.device_status() == 0
+    del pages
+    _check(out[:64], want, bound)
+    rows = out.view(-1, 64).view(torch.int32)
+    for part in rows.split(1 << 22):
+        assert bool((part == rows[0]).all())
+    with pytest.raises(mla.MlaError, match="2\\^31 - 65536"):
+        mla.token_weights_workspace(qlen, heads, n + 1, q8)
+    del out, rows, part
+    torch.cuda.empty_cache()
