@@ -250,3 +250,32 @@ def test_repeated_streamed_and_captured():
     g.replay()
     now = mla.kv_evict(pages, indptr, w, 1000, recent=10)
     assert all(torch.equal(a, b) for a, b in zip(out, now))
+
+
+@pytest.mark.gpu
+def test_the_longest_page_list():
+    # one request of as many tokens as are accepted, all of one weight but a few: the first ones stay, and those
+    n = 2**31 - 65536
+    if torch.cuda.mem_get_info()[0] < 4 * n * 5:
+        pytest.skip("%d GB of device memory free" % (4 * n * 5 >> 30))
+    pages = torch.arange(n, dtype=torch.int32, device=DEV)
+    indptr = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    w = torch.ones(n, device=DEV)
+    heavy = [2**30 + 20000, 2**31 - 70000]
+    w[heavy] = 2.0
+    budget, recent = 2**30 + 12345, 7
+    po, io, wo = mla.kv_evict(pages, indptr, w, budget, recent=recent)
+    assert io.tolist() == [0, budget] and mla.device_status() == 0
+    first = budget - recent - len(heavy)
+    assert torch.equal(po[:first], pages[:first])
+    assert po[first:budget].tolist() == heavy + list(range(n - recent, n))
+    assert wo[first:budget].tolist() == [2.0, 2.0] + [1.0] * recent
+    assert bool((wo[:first] == 1).all()) and bool((wo[budget:] == 0).all())
+    # freed: what is left, in order
+    at = budget
+    for a, b in ((first, heavy[0]), (heavy[0] + 1, heavy[1]), (heavy[1] + 1, n - recent)):
+        assert torch.equal(po[at:at + b - a], pages[a:b])
+        at += b - a
+    assert at == n
+    del pages, w, po, wo
+    torch.cuda.empty_cache()
