@@ -479,7 +479,7 @@ int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsi
  *   recent, sinks   >= 0.
  *   pages_out, weights_out  [num_pages], indptr_out [num_requests + 1]; no
  *                   output may overlap an input or another output.
- * num_pages up to 2^31 - 65536, num_requests up to 2^24.
+ * num_pages up to 2^31 - 65536, num_requests up to 2^16.
  * A bad indptr entry sets MLA_DEV_BAD_INDPTR and its request is empty.
  */
 mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,

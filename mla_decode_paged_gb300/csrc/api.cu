@@ -86,6 +86,8 @@ mla_status cuda_fail(cudaError_t e, const char *where) {
 // Page-list sizes of the calls that walk it in 32-bit token positions (a
 // tile or a block's round past the last one still fits).
 constexpr int64_t kMaxPages = INT32_MAX - 65535, kMaxRequests = 1 << 24;
+// kv_evict's blocks each sum over all requests: 5.2 ms at this many (evict.cu).
+constexpr int kMaxEvictRequests = 1 << 16;
 
 // Whether two blocks of bytes share one.
 bool overlap(const void *p, int64_t pn, const void *q, int64_t qn) {
@@ -729,7 +731,7 @@ mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *
         !aligned(pages_out, 4) || !aligned(indptr_out, 4) || !aligned(weights_out, 4))
         return fail(MLA_ERR_INVALID, "misaligned pointer (4 bytes)");
     if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 65536");
-    if (num_requests > kMaxRequests) return fail(MLA_ERR_UNSUPPORTED, "num_requests above 2^24");
+    if (num_requests > kMaxEvictRequests) return fail(MLA_ERR_UNSUPPORTED, "num_requests above 2^16");
     const int64_t n = num_pages * 4, r = (int64_t)num_requests * 4;
     const Span in[4] = {{pages, n}, {weights, n}, {indptr, r + 4}, {budgets, r}};
     const Span to[3] = {{pages_out, n}, {weights_out, n}, {indptr_out, r + 4}};

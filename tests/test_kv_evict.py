@@ -279,3 +279,20 @@ def test_the_longest_page_list():
     assert at == n
     del pages, w, po, wo
     torch.cuda.empty_cache()
+
+
+def test_too_many_requests(lib):
+    assert _call(lib, R=65537) == mla.MLA_ERR_UNSUPPORTED
+    assert b"num_requests above 2^16" in lib.mla_last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R", [1025, 5000, 65536])
+def test_more_requests_than_a_block_has_threads(R):
+    # every block sums over all requests before its own; one long request among empty and short ones
+    lengths = [(i * 7) % 5 for i in range(R)]
+    lengths[R // 3] = 20000
+    lengths[-1] = 9
+    budgets = torch.tensor([(i * 11) % 4 for i in range(R)], dtype=torch.int32)
+    budgets[R // 3] = 777
+    _run(lengths, _rand(sum(lengths), R), budgets, 1, 1, tail=5)
