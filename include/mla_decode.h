@@ -423,9 +423,9 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
  *            + sum over rows t of r that see j, heads h, with lse[t, h] > -inf, of
  *              exp(scale * q_scale * <q[t, h, :], K_j> - lse[t, h])
  * With lse the merged LSE of the same step (mla_merge_splits) the new
- * weights of a request sum to its rows x heads.  Every entry below
- * indptr[num_requests] is written, others are left as they were.  The sum
- * has a fixed order: equal inputs give equal bits.
+ * weights of a request sum to its rows x heads.  Every request's entries
+ * (indptr[0] up to indptr[num_requests]) are written, others are left as
+ * they were.  The sum has a fixed order: equal inputs give equal bits.
  *
  *   q, q_row_stride, kv, pool_rows, pages, num_pages, indptr, num_requests,
  *   qlen, heads, scale, kv_scale, q_scale, flags: as
@@ -463,13 +463,16 @@ int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsi
  *   its last min(recent, n) tokens; its first min(sinks, n - those); and of
  *   the tokens in between those with the largest weights until n are kept
  *   (NaN counts as -inf, -0 equals +0, equal weights by the lower position).
- * Kept tokens keep their order.  With N = indptr[R] and K = indptr_out[R]:
- *   indptr_out[r]         the requests' kept tokens, as indptr counts them
+ * Kept tokens keep their order.  With N the requests' tokens in all
+ * (indptr[R] - indptr[0]: a list may start past its first entries) and
+ * K = indptr_out[R]:
+ *   indptr_out[r]         the requests' kept tokens, as indptr counts them, from 0
  *   pages_out[0 .. K)     kept rows, request by request (with indptr_out:
  *                         what mla_decode_attend takes next)
  *   pages_out[K .. N)     freed rows, request by request, in order
  *   weights_out[0 .. K)   the kept tokens' weights; [K .. N) zeros
- * Entries from N on are left as they were.  The cache itself is not touched
+ * Entries of the outputs from N on are left as they were; entries of pages
+ * that belong to no request are in neither part.  The cache itself is not touched
  * and pages are not looked up: a row is only an index here, and one that
  * several requests hold (a shared prefix) may be kept by one and freed by
  * another.

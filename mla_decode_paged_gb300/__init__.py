@@ -525,7 +525,9 @@ def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qle
     ``lse``: the step's merged LSE float32 ``[S, heads]`` (from
     :func:`merge` or :func:`decode_step`).  ``weights``: float32, one entry
     per entry of ``pages`` (None: zeros); ``out=weights`` updates in place.
-    Entries past ``indptr[-1]`` are left as they were.  ``workspace``: uint8,
+    Entries before ``indptr[0]`` and from ``indptr[-1]`` on belong to no
+    request and are left as they were (a new ``out`` holds nothing there).
+    ``workspace``: uint8,
     at least :func:`token_weights_workspace` bytes, 16-byte aligned
     (allocated if not given and needed; not shared by calls that may
     overlap).
@@ -553,8 +555,10 @@ def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=Non
     :func:`token_weights`).  Returns ``(pages_out, indptr_out,
     weights_out)``: ``pages_out`` holds the kept rows of every request in
     order (``indptr_out`` counts them; both go to :func:`attend` as they
-    are), then the freed rows; ``weights_out`` the kept tokens' weights,
-    then zeros.  A row that several requests hold (a shared prefix) may be
+    are), then the freed rows, ``indptr[-1] - indptr[0]`` rows in all (what
+    lies behind them in a longer list's outputs is not written);
+    ``weights_out`` the kept tokens' weights, then zeros, likewise.  At most
+    65,536 requests.  A row that several requests hold (a shared prefix) may be
     kept by one and freed by another.  ``budget``: an int, or int32 ``[R]``
     on the device.
     """

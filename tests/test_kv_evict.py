@@ -296,3 +296,23 @@ def test_more_requests_than_a_block_has_threads(R):
     budgets = torch.tensor([(i * 11) % 4 for i in range(R)], dtype=torch.int32)
     budgets[R // 3] = 777
     _run(lengths, _rand(sum(lengths), R), budgets, 1, 1, tail=5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R", [3, 900])
+def test_a_list_that_starts_past_its_first_entries(R):
+    # a batch's later requests, with the whole batch's page list: what belongs to none of them is in neither part
+    lengths, skip, tail = [(i * 13) % 40 + 1 for i in range(R)], 17, 6
+    total = sum(lengths)
+    g = torch.Generator().manual_seed(R)
+    pages = torch.randperm(skip + total + tail, generator=g).to(torch.int32)
+    w = _rand(skip + total + tail, R)
+    indptr = torch.tensor([skip] + (skip + torch.tensor(lengths).cumsum(0)).tolist(), dtype=torch.int32)
+    po = torch.full((skip + total + tail,), -7, dtype=torch.int32, device=DEV)
+    wo = torch.full((skip + total + tail,), -7.0, device=DEV)
+    _, io, _ = mla.kv_evict(pages.to(DEV), indptr.to(DEV), w.to(DEV), 11, recent=2, sinks=1, pages_out=po, weights_out=wo)
+    kept, freed, counts, kw = _plain(pages[skip:].tolist(), lengths, w[skip:].tolist(), [11] * R, 2, 1)
+    assert io.tolist() == [0] + torch.tensor(counts).cumsum(0).tolist()
+    assert po.tolist() == kept + freed + [-7] * (skip + tail)
+    assert wo.tolist() == kw + [0.0] * len(freed) + [-7.0] * (skip + tail)
+    assert mla.device_status() == 0

@@ -388,3 +388,19 @@ def test_the_longest_page_list(qlen, heads, q8):
         mla.token_weights_workspace(qlen, heads, n + 1, q8)
     del out, rows, part
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [12, 70])
+@pytest.mark.parametrize("qlen", [1, 3])
+def test_a_list_that_starts_past_its_first_entries(qlen, heads):
+    lengths, skip = [60, 0, 170], 37
+    q, kv, pages, indptr = _make(lengths, qlen, heads, heads, 9)
+    want, bound, lse = _formula(q, kv, pages, lengths, heads, qlen, 0.05, False)
+    more = torch.cat([torch.full((skip,), -1, dtype=torch.int32, device=DEV), pages,
+                      torch.full((9,), -1, dtype=torch.int32, device=DEV)])
+    out = torch.full((more.numel(),), -7.0, device=DEV)
+    mla.token_weights(q, kv, more, indptr + skip, 0.05, 1.0, lse.contiguous(), qlen=qlen, out=out)
+    assert (out[:skip] == -7).all() and (out[skip + 230:] == -7).all()
+    _check(out[skip:skip + 230], want, bound)
+    assert mla.device_status() == 0
