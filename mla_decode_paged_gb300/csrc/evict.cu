@@ -92,9 +92,16 @@ __device__ __forceinline__ uint32_t block_rank() {
 }
 
 // All running blocks of the cluster, their shared-memory writes before it
-// visible after it.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// visible after it.  Both halves are for whole warps: lanes that took a
+// branch before them meet first.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
     cluster_arrive();
     cluster_wait();

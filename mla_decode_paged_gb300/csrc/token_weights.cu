@@ -695,9 +695,11 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
     else tc::tmem_free(base, cols);
 }
 
-// All threads of the CTA, or of both.
+// All threads of the CTA, or of both.  (The cluster barrier is for whole
+// warps: lanes that took a branch before it meet first.)
 template <bool PAIR>
 __device__ __forceinline__ void sync_all() {
+    __syncwarp();
     if (PAIR)
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     else
@@ -766,11 +768,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Neither CTA of a pair ends while the other may still reach it.
     tc::fence_before();
-    __syncwarp();
     sync_all<PAIR>();
     if (PAIR) {
         if ((ms.abort_flag || load_in_block(&ms.abort_flag, rank ^ 1)) && tid == 0 && rank == 0) land(ms);
-        __syncwarp();
         sync_all<PAIR>();
     }
     tc::fence_after();
