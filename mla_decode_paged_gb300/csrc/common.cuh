@@ -112,6 +112,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     return true;
 }
 
+// What the lanes of a warp make of their waits (run by all of them): true in
+// every lane or in none, so that no lane leaves the warp's loop while others go
+// on to what the warp does as one.  Where it is false `abort_flag` (in shared
+// memory) tells the block's other roles to give up too.
+__device__ __forceinline__ bool warp_agrees(bool ok, int *abort_flag) {
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) *(volatile int *)abort_flag = 1;
+    return ok;
+}
+__device__ __forceinline__ bool aborted(const int *abort_flag) { return *(const volatile int *)abort_flag != 0; }
+
+// A whole warp's wait, given up once any role of the block has.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *abort_flag) {
+    return warp_agrees(!aborted(abort_flag) && mbar_wait(bar, parity), abort_flag);
+}
+
 // ------------------------------------------------------------ bulk copies
 
 // Global -> shared bulk copy of `bytes` (multiple of 16, both addresses

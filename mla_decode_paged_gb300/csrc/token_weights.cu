@@ -109,15 +109,6 @@ struct Misc {
     int start[3];               // this CTA's first request, its first tile there, tiles in all
 };
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t par, int *abort_flag) {
-    if (*(volatile int *)abort_flag) return false;
-    if (!mbar_wait(bar, par)) {
-        *(volatile int *)abort_flag = 1;
-        return false;
-    }
-    return true;
-}
-
 // A CTA's (a pair's) tiles of TOKENS in order; every role walks them on its
 // own (uniform loads).
 template <int TOKENS>
@@ -280,7 +271,7 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
         w.next(a);
         const int n = load(next);
         const int s = it % kStages;
-        if (!(ok = wait_or_abort(&ms.kv_empty[s], ((it / kStages) & 1) ^ 1, &ms.abort_flag))) break;
+        if (!(ok = warp_wait(&ms.kv_empty[s], ((it / kStages) & 1) ^ 1, &ms.abort_flag))) break;
         // A pair's tiles are both counted by CTA 0's barrier.
         if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&ms.kv_full[s], (PAIR ? 2 : 1) * part_bytes(part));
         __syncwarp();
@@ -383,11 +374,8 @@ __device__ __forceinline__ void arrive_lead(uint64_t *bar, int rank) {
             : "memory");
 }
 
-// wait_or_abort for what the other CTA has written too.
-template <bool PAIR>
-__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t par, int *abort_flag) {
-    if (!PAIR) return wait_or_abort(bar, par, abort_flag);
-    if (*(volatile int *)abort_flag) return false;
+// mbar_wait for what the other CTA has written too.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t par) {
     const long long t0 = clock64();
     while (true) {
         uint32_t ok;
@@ -401,10 +389,14 @@ __device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t par, int *abor
         if (ok) return true;
         if (clock64() - t0 > kWaitCycles) {
             flag(MLA_DEV_TIMEOUT);
-            *(volatile int *)abort_flag = 1;
             return false;
         }
     }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t par) {
+    return PAIR ? mbar_wait_cluster(bar, par) : mbar_wait(bar, par);
 }
 
 // CTA 0 issues a pair's.
@@ -421,9 +413,10 @@ __device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, 
     if (PAIR && rank > 0) return;
     for (int it = 0; w.valid(); ++it, w.next(a)) {
         const int s = it % kStages, d = it & 1;
-        if (w.first && !wait_pair<PAIR>(&ms.q_ready, w.unit & 1, &ms.abort_flag)) break;
-        if (!wait_pair<PAIR>(&ms.d_free[d], ((it >> 1) & 1) ^ 1, &ms.abort_flag)) break;
-        if (!wait_pair<PAIR>(&ms.kv_full[s], (it / kStages) & 1, &ms.abort_flag)) break;
+        const bool ready = !aborted(&ms.abort_flag) && (!w.first || wait_pair<PAIR>(&ms.q_ready, w.unit & 1)) &&
+                           wait_pair<PAIR>(&ms.d_free[d], ((it >> 1) & 1) ^ 1) &&
+                           wait_pair<PAIR>(&ms.kv_full[s], (it / kStages) & 1);
+        if (!warp_agrees(ready, &ms.abort_flag)) break;
         tc::fence_after();
         // Column blocks of 128 bytes, 32 bytes a step (an address counts 16).
         const uint32_t dt = tm + d * C::N;
@@ -634,7 +627,7 @@ __device__ __forceinline__ float token_sum(uint32_t taddr, const float4 *c, cons
             const float4 k = c[8 * g + i];
             const float x = TERMS == 2 ? fmaf(lo[b][i], 0.0625f, acc[b][i]) : acc[b][i];
             const float p = exp2_approx(fmaf(x, k.x, -k.z) + fmaf(x, k.y, -k.w));
-            if (!MASK || j < vis[8 * g + i]) sum[i & 1] += p;
+            sum[i & 1] += !MASK || j < vis[8 * g + i] ? p : 0.f;
         }
     };
     load(0, 0);
@@ -666,7 +659,7 @@ __device__ void epilogue(const TokenArgs &a, Misc<Cfg<NP, TERMS, PAIR>> &ms, int
         const bool real = j < w.len;
         float old = 0.f;
         if (a.decay != 0.f && real) old = a.weights[i] * a.decay;
-        if (!wait_or_abort(&ms.d_full[wg], (it >> 1) & 1, &ms.abort_flag)) break;
+        if (!warp_wait(&ms.d_full[wg], (it >> 1) & 1, &ms.abort_flag)) break;
         tc::fence_after();
         const bool whole = ms.all_vis[buf] >= min(j0 + kTile, w.len);
         constexpr int kHalves = PAIR ? 2 : 1;
@@ -750,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.init(a, ms);
         for (; w.valid(); w.next(a)) {
             if (!w.first) continue;
-            if (w.unit > 0 && !wait_or_abort(&ms.q_free, (w.unit - 1) & 1, &ms.abort_flag)) break;
+            if (w.unit > 0 && !warp_wait(&ms.q_free, (w.unit - 1) & 1, &ms.abort_flag)) break;
             prep_unit<NP, TERMS, PAIR>(a, sm, ms, w.r, w.len, grp, w.unit, rank);
             tc::fence_async_smem();     // generic-proxy writes -> tensor-core reads
             __syncwarp();

@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kTcThreads)
         if (32 * warp < kTcPairs)
             for (int c = 0; c < p.rank; c += 16) {
                 float d[16];
+                __syncwarp();       // lanes past the pairs store nothing
                 tc::ld16(tmem + ((uint32_t)(32 * warp) << 16) + c, d);
                 tc::wait_ld();
 #pragma unroll
@@ -695,15 +696,6 @@ __device__ __forceinline__ float ld1(uint32_t taddr) {
     return __uint_as_float(r);
 }
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t par, int *abort_flag) {
-    if (*(volatile int *)abort_flag) return false;
-    if (!mbar_wait(bar, par)) {
-        *(volatile int *)abort_flag = 1;
-        return false;
-    }
-    return true;
-}
-
 // A block's ring entries in order: tile, 16-row window, eight rows (or the
 // request's rest) of a request there, chunk of RB ranks.
 template <int NR, int RB>
@@ -774,7 +766,7 @@ __device__ void slot_filler(const LoraArgs &p, const CUtensorMap *mb, uint8_t *s
             }
         };
         if (n > 0) load();
-        if (!wait_or_abort(&sh.s_empty[s], (n & 1) ^ 1, &sh.abort_flag)) break;
+        if (!warp_wait(&sh.s_empty[s], (n & 1) ^ 1, &sh.abort_flag)) break;
         const int a = valid_adapter(p, index);
         if (lane == 0) {
             if (a >= 0) {
@@ -838,10 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after();
     const uint32_t base = smem_u32(sm), tm = sh.tmem;
-    // A whole warp's wait; its result, and with it what the loops count, is uniform.
-    const auto wait_warp = [&](uint64_t *bar, uint32_t par) {
-        return __all_sync(0xffffffffu, wait_or_abort(bar, par, &sh.abort_flag)) != 0;
-    };
+    const auto wait_warp = [&](uint64_t *bar, uint32_t par) { return warp_wait(bar, par, &sh.abort_flag); };
     if (warp == kLatentWarp) {
         // Neither W_UV nor the latent is written by the kernel before this
         // one.  Rows past S read as zeros (their outputs are not written).
@@ -974,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = request_of(p, t0 + lane);
             item += ((r - request_of(p, w0 + win)) << log_per) + ((t0 + lane - r * p.qlen) >> 3);
             const int col = T::kAddCols + (it & p.add_both) * T::kAddBuf + item * kWin + (first + lane) % kWin;
-            if (!wait_or_abort(&sh.d_full[it & 1], (it >> 1) & 1, &sh.abort_flag)) break;
+            if (!warp_wait(&sh.d_full[it & 1], (it >> 1) & 1, &sh.abort_flag)) break;
             tc::fence_after();
             float d[T::kRows];
 #pragma unroll

@@ -37,3 +37,19 @@ def test_warps_meet_before_a_cluster_barrier(path):
     assert sum(len(re.findall(r"barrier\.cluster\.arrive\S*aligned", b)) for b in found) == uses
     for body in found:
         assert re.search(r"__sync(warp|threads)\(\)", body[:body.index("barrier.cluster")]), body
+
+
+@pytest.mark.parametrize("name", ["token_weights.cu", "value_lora.cu"])
+def test_a_wait_that_runs_out_does_so_for_the_whole_warp(name):
+    # where a wait's result decides what follows, it is joined over the warp (or the block) first: a lane that left
+    # alone would be waited for by the others at their next warp-wide step
+    lines = _text(os.path.join(CSRC, name)).splitlines()
+    for i, line in enumerate(lines):
+        for m in re.finditer(r"(mbar_wait\w*|wait_pair<PAIR>)\(", line):
+            if line.lstrip().startswith(("mbar_wait", "__device__", "//", "return PAIR ?")) or re.match(
+                    r"\s*(for|if) \(.*\) mbar_wait\(", line) and "ok" not in line:
+                continue        # a definition, or a wait whose result is not used
+            statement = " ".join(lines[i:i + 5])
+            joined = "__all_sync" in line[:m.start()] or re.match(r".*?;\s+(ok = __syncthreads_and\(|if \(!warp_agrees\()",
+                                                                  statement)
+            assert joined, "%s:%d %s" % (name, i + 1, line.strip())
