@@ -399,7 +399,8 @@ __device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t par) {
     return PAIR ? mbar_wait_cluster(bar, par) : mbar_wait(bar, par);
 }
 
-// CTA 0 issues a pair's.
+// CTA 0 issues a pair's; its last commit, to `fin` in both CTAs, is waited for
+// by CTA 1 at the kernel's end.
 template <int NP, int TERMS, bool PAIR>
 __device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, PAIR>> &ms, int rank) {
     using C = Cfg<NP, TERMS, PAIR>;
@@ -763,6 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();
     sync_all<PAIR>();
     if (PAIR) {
+        // CTA 0's commits have completed there; those to this CTA's barriers land before it ends.
+        if (rank > 0 && warp == kMmaWarp) mbar_wait(&ms.fin, 0);
         if ((ms.abort_flag || load_in_block(&ms.abort_flag, rank ^ 1)) && tid == 0 && rank == 0) land(ms);
         sync_all<PAIR>();
     }

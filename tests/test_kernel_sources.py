@@ -53,3 +53,12 @@ def test_a_wait_that_runs_out_does_so_for_the_whole_warp(name):
             joined = "__all_sync" in line[:m.start()] or re.match(r".*?;\s+(ok = __syncthreads_and\(|if \(!warp_agrees\()",
                                                                   statement)
             assert joined, "%s:%d %s" % (name, i + 1, line.strip())
+
+
+def test_both_blocks_of_a_pair_wait_for_its_last_commit():
+    # commit<PAIR> arrives in both CTAs: neither may end before the last one (`fin`) has landed in it
+    text = _text(os.path.join(CSRC, "token_weights.cu"))
+    waits = re.findall(r"^.*mbar_wait\(&ms\.fin, 0\);", text, re.M)
+    assert len(waits) == 2 and any("rank > 0" in w for w in waits)
+    end = text[text.index("Neither CTA of a pair ends"):]
+    assert end.index("sync_all<PAIR>()") < end.index("mbar_wait(&ms.fin, 0)") < end.rindex("sync_all<PAIR>()", 0, end.index("tmem_free"))
