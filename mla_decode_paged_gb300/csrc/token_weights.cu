@@ -64,6 +64,7 @@ constexpr int kLatBlock = (kTile / 8) * 1024;              // one 128-byte colum
 constexpr int kRopeOff = 4 * kLatBlock;
 constexpr int kStageBytes = kRopeOff + (kTile / 8) * 512;  // 73,728
 constexpr int kOffQ = kStages * kStageBytes;
+constexpr long long kTileCycles = 1 << 16;      // more than a tile takes (some 4,700 where it takes longest)
 
 struct TokenArgs {
     const void *q;
@@ -742,9 +743,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         Walk<C::Tokens> w;
         w.init(a, ms);
-        for (; w.valid(); w.next(a)) {
+        int tiles = 0;      // of the request before this one, here
+        for (; w.valid(); w.next(a), ++tiles) {
             if (!w.first) continue;
-            if (w.unit > 0 && !warp_wait(&ms.q_free, (w.unit - 1) & 1, &ms.abort_flag)) break;
+            // The last of all the MMAs of the request before: a wait for its
+            // tiles, not for one (2,048 query rows of 2^30 tokens take seconds).
+            if (w.unit > 0 && !warp_wait(&ms.q_free, (w.unit - 1) & 1, &ms.abort_flag, kWaitCycles + tiles * kTileCycles))
+                break;
+            tiles = 0;
             prep_unit<NP, TERMS, PAIR>(a, sm, ms, w.r, w.len, grp, w.unit, rank);
             tc::fence_async_smem();     // generic-proxy writes -> tensor-core reads
             __syncwarp();

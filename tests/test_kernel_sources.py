@@ -62,3 +62,16 @@ def test_both_blocks_of_a_pair_wait_for_its_last_commit():
     assert len(waits) == 2 and any("rank > 0" in w for w in waits)
     end = text[text.index("Neither CTA of a pair ends"):]
     assert end.index("sync_all<PAIR>()") < end.index("mbar_wait(&ms.fin, 0)") < end.rindex("sync_all<PAIR>()", 0, end.index("tmem_free"))
+
+
+def test_a_wait_for_a_whole_request_goes_by_its_tiles():
+    # q_free completes with the last tile of a request, which at the sizes accepted may take longer than the limit of
+    # one step's wait: 2^30 tokens of 2,048 rows are 2^22 tiles of a pair, each about 4,700 cycles
+    common, text = (_text(os.path.join(CSRC, n)) for n in ("common.cuh", "token_weights.cu"))
+    limit = int(re.search(r"kWaitCycles = (\d+)LL", common).group(1))
+    tile = 1 << int(re.search(r"kTileCycles = 1 << (\d+);", text).group(1))
+    tiles, cycles = 2**22, 4700
+    assert tiles * cycles > limit               # one step's limit would not do
+    assert limit + tiles * tile > 2 * tiles * cycles
+    (wait,) = re.findall(r"warp_wait\(&ms\.q_free.*\)", text)
+    assert "kWaitCycles + tiles * kTileCycles" in wait
