@@ -51,6 +51,7 @@ cudaError_t add_rms_norm_launch(const void *x, int64_t x_stride, int x_type, con
                                 int64_t rows, int width, int quant, float scale, void *out, int64_t out_stride,
                                 float *out_scales, void *residual_out, int64_t residual_out_stride, int sms,
                                 cudaStream_t st);
+cudaError_t norm_status(unsigned int *flags, bool clear);
 cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                                  const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
                                  int heads, double sc, const float *lse, float decay, const float *weights, float *out,
@@ -829,8 +830,8 @@ mla_status mla_device_status(void *stream, unsigned int *flags) {
     if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
     cudaError_t (*readers[])(unsigned int *, bool) = {mla::attend_mma_status, mla::attend_tc_status, mla::merge_status,
                                                       mla::value_gate_status, mla::gather_status,
-                                                      mla::kv_append_status, mla::token_weights_status,
-                                                      mla::evict_status, mla::value_lora_status};
+                                                      mla::kv_append_status, mla::norm_status,
+                                                      mla::token_weights_status, mla::evict_status, mla::value_lora_status};
     for (auto rd : readers) {
         unsigned int f = 0;
         e = rd(&f, true);

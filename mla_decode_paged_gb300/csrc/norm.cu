@@ -537,4 +537,6 @@ cudaError_t add_rms_norm_launch(const void *x, int64_t x_stride, int x_type, con
     return x_type == MLA_TYPE_BF16 ? launch<__nv_bfloat16>(a, sms, st) : launch<__half>(a, sms, st);
 }
 
+cudaError_t norm_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }
+
 }  // namespace mla

@@ -75,3 +75,16 @@ def test_a_wait_for_a_whole_request_goes_by_its_tiles():
     assert limit + tiles * tile > 2 * tiles * cycles
     (wait,) = re.findall(r"warp_wait\(&ms\.q_free.*\)", text)
     assert "kWaitCycles + tiles * kTileCycles" in wait
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_every_status_word_is_read(path):
+    # each source has a status word of its own; what a kernel may set there, device_status has to see
+    text = re.sub(r"//.*", "", _text(path))
+    sets = re.search(r"\b(flag|mbar_wait|warp_wait|kv_row|kv_row_of_page|request_len)\(|\bTileIter<|\bUnitCursor<", text)
+    readers = re.findall(r"cudaError_t (\w+_status)\(unsigned int \*flags, bool clear\) \{ return read_status", text)
+    if not sets or os.path.basename(path) == "api.cu":
+        return
+    assert len(readers) == 1, "no reader of this source's status word"
+    table = re.search(r"\(\*readers\[\]\).*?\};", _text(os.path.join(CSRC, "api.cu")), re.S).group(0)
+    assert "mla::" + readers[0] in table
