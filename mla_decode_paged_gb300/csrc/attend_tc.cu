@@ -43,7 +43,6 @@
 //   * Registers: the softmax warpgroups take 176 (184 causal at 48 rows), the
 //     MMA and producer warpgroups 80 (72) by setmaxnreg.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <type_traits>
@@ -619,17 +618,8 @@ __device__ __noinline__ void prep_query(const PP &P, uint8_t *sm, int req, int g
 // as far down as the max-referenced p = 2^-6.  REL (the unmasked kernel): sc
 // holds s - m already.  GUARD maps s = -inf to 0 even where m is still -inf
 // (causal tiles; without the mask every column sees each tile's live tokens,
-// so m is finite by then).
-// 2^x by the hardware approximation (PTX ex2.approx.ftz.f32: relative
-// error ~2^-22, results below 2^-126 flushed to 0).  p is then rounded to
-// two e4m3 terms (~8 significant bits), so the approximation is invisible
-// next to that rounding.
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
+// so m is finite by then).  The exponential's approximation is invisible next
+// to p's rounding to the two terms (~8 significant bits).
 template <int H2, bool GUARD, bool REL>
 __device__ __forceinline__ void p_split(const float (&sc)[H2], const float (&mr)[H2], float (&l)[H2],
                                         uint32_t (&ph)[H2 / 4], uint32_t (&pl)[H2 / 4]) {
@@ -639,7 +629,7 @@ __device__ __forceinline__ void p_split(const float (&sc)[H2], const float (&mr)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float x = REL ? sc[j + e] : sc[j + e] - mr[j + e];   // REL: sc already holds s - m
-            const float pv = (!GUARD || sc[j + e] > -INFINITY) ? exp2_approx(x) : 0.f;
+            const float pv = (!GUARD || sc[j + e] > -INFINITY) ? tc::exp2_approx(x) : 0.f;
             l[j + e] += pv;
             hv[e] = __uint_as_float((__float_as_uint(pv) + 0x80000u) & 0xFFF00000u);
             lv[e] = pv - hv[e];
@@ -1034,18 +1024,6 @@ constexpr size_t smem_bytes() {
     return Cfg<NQ>::OffMisc + sizeof(Misc<NQ>) + 1024;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
 // The causal kernels' parameter layout (same fields, no padding).
 ParamsCausal causal_params(const Params &P) {
     ParamsCausal C;
@@ -1123,7 +1101,7 @@ cudaError_t attend_tc_launch(const void *q, int64_t q_row_stride, const void *kv
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (cache.dev != dev || cache.kv != kv || cache.pool_rows != pool_rows) {
-        PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+        PFN_cuTensorMapEncodeTiled_v12000 enc = tc::encode_fn();
         if (!enc) return cudaErrorNotSupported;
         cuuint64_t gdim[2] = {(cuuint64_t)MLA_D_QK, (cuuint64_t)pool_rows};
         cuuint64_t gstr[1] = {(cuuint64_t)MLA_D_QK};

@@ -1,9 +1,11 @@
 // Blackwell (sm_100-family) tensor-memory helpers: TMA gather4 into
 // swizzled shared memory, UMMA shared-memory / instruction descriptors,
-// tcgen05.mma / commit / ld / st and TMEM allocation.  Inline PTX.
+// tcgen05.mma / commit / ld / st and TMEM allocation, tiled TMA loads, the
+// exponentials by hardware approximation, and the tensor maps' encoder.  Inline PTX.
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cstdint>
 
 #include "common.cuh"
@@ -30,6 +32,22 @@ __device__ __forceinline__ void gather4_hint(void *dst, const CUtensorMap *map, 
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
         "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
         "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// Boxes of 2-D and 3-D tensor maps at (x, y) and (x, y, z).
+__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -90,6 +108,23 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One lane of the warp (all of them run it): 1 in it, 0 elsewhere.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// 8 consecutive f32 columns of this warp's 32 TMEM lanes (lane = thread).
+__device__ __forceinline__ void ld8(uint32_t taddr, float *v) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 // 16 consecutive f32 columns of this warp's 32 TMEM lanes (lane = thread).
 __device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
@@ -152,6 +187,34 @@ __device__ __forceinline__ bool bar_any(int id, int count, bool pred) {
         : "r"((uint32_t)pred), "r"(id), "r"(count)
         : "memory");
     return r != 0;
+}
+
+// 2^x by the hardware approximation (PTX ex2.approx.ftz.f32: relative
+// error ~2^-22, results below 2^-126 flushed to 0).
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + e^-x) in fp32 from the hardware exponential and reciprocal
+// approximations (relative errors near 2^-21 and 2^-23, far below the bf16
+// rounding of the product); e^-x = inf gives 0.
+__device__ __forceinline__ float sigmoid_f32(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+    return r;
+}
+
+// The driver's encoder of tensor maps; null where it has none.
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::atomic<void *> fn{nullptr};
+    void *p = fn.load(std::memory_order_acquire);
+    cudaDriverEntryPointQueryResult q;
+    if (!p && cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+        fn.store(p, std::memory_order_release);
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn.load(std::memory_order_acquire));
 }
 
 }  // namespace tc

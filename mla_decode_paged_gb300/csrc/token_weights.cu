@@ -46,7 +46,6 @@
 // two stages' copies do not cover their latency and the MMAs' 1,940 cycles.
 // A new request costs the conversion of its query, about 3,400 cycles for 16
 // rows (100 requests of 384 rows and 9 to 65 tokens: 62 us).
-#include <cudaTypedefs.h>
 #include <climits>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -349,12 +348,6 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
         tc::commit(bar);
 }
 
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
-
 // Arrive on CTA 0's `bar`, from either CTA of a pair.  RELAXED: where only
 // TMEM reads (fenced by the caller) go before it; a release at cluster scope
 // would wait for this thread's global stores, several thousand cycles under
@@ -406,7 +399,7 @@ template <int NP, int TERMS, bool PAIR>
 __device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, PAIR>> &ms, int rank) {
     using C = Cfg<NP, TERMS, PAIR>;
     const uint32_t base = smem_u32(sm), tm = ms.tmem;
-    const uint32_t one = elect_one();
+    const uint32_t one = tc::elect_one();
     const uint64_t lat0 = tc::sdesc(base, 16, 1024, tc::kSw128), rope0 = tc::sdesc(base + kRopeOff, 16, 512, tc::kSw64);
     const uint64_t q0 = tc::sdesc(base + kOffQ, 16, 1024, tc::kSw128);
     const uint64_t qr0 = tc::sdesc(base + kOffQ + C::QRope, 16, 512, tc::kSw64);
@@ -592,21 +585,6 @@ __device__ void prefetch_rows(const TokenArgs &a, int r, int grp, int rank) {
 
 // ------------------------------------------------------------------ scores
 
-__device__ __forceinline__ float exp2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ void ld8(uint32_t taddr, float (&v)[8]) {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // One token's sum over the query rows; MASK: rows count tokens below their
 // vis only.  HALVES blocks of NP columns, each its rows' hi then lo terms.
 // Eight rows' scores leave TMEM while the eight before are summed.  A loop,
@@ -620,15 +598,15 @@ __device__ __forceinline__ float token_sum(uint32_t taddr, const float4 *c, cons
     float acc[2][8], lo[2][8];
     const auto load = [&](int b, int g) {
         const uint32_t at = taddr + g * 8 + (HALVES == 2 && g >= kGroups / 2 ? NP - NQ : 0);
-        ld8(at, acc[b]);
-        if (TERMS == 2) ld8(at + NQ, lo[b]);
+        tc::ld8(at, acc[b]);
+        if (TERMS == 2) tc::ld8(at + NQ, lo[b]);
     };
     const auto add = [&](int b, int g) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float4 k = c[8 * g + i];
             const float x = TERMS == 2 ? fmaf(lo[b][i], 0.0625f, acc[b][i]) : acc[b][i];
-            const float p = exp2_approx(fmaf(x, k.x, -k.z) + fmaf(x, k.y, -k.w));
+            const float p = tc::exp2_approx(fmaf(x, k.x, -k.z) + fmaf(x, k.y, -k.w));
             sum[i & 1] += !MASK || j < vis[8 * g + i] ? p : 0.f;
         }
     };
@@ -793,23 +771,11 @@ __global__ void __launch_bounds__(256) join_kernel(const TokenArgs a, const floa
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 // The cache as [pool_rows, 576] bytes, read in rows of `cols` bytes.
 bool encode_rows(CUtensorMap *m, const void *kv, int64_t pool_rows, cuuint32_t cols, CUtensorMapSwizzle swz) {
     const cuuint64_t dim[2] = {(cuuint64_t)MLA_D_QK, (cuuint64_t)pool_rows}, stride[1] = {(cuuint64_t)MLA_D_QK};
     const cuuint32_t box[2] = {cols, 1}, es[2] = {1, 1};
-    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(kv), dim, stride, box, es,
+    return tc::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(kv), dim, stride, box, es,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -876,7 +842,7 @@ cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void
                                  const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
                                  int heads, double sc, const float *lse, float decay, const float *weights, float *out,
                                  bool causal, bool q8, void *workspace, int sms, cudaStream_t st) {
-    if (!encode_fn()) return cudaErrorNotSupported;
+    if (!tc::encode_fn()) return cudaErrorNotSupported;
     CUtensorMap ml, mr;
     if (!encode_rows(&ml, kv, pool_rows, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_rows(&mr, kv, pool_rows, 64, CU_TENSOR_MAP_SWIZZLE_64B))

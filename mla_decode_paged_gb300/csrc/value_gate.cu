@@ -33,7 +33,6 @@
 // (programmatic dependent launch): no kernel of the step writes it; the
 // latent or partials, the gate and the lengths after it.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -81,30 +80,6 @@ __device__ __forceinline__ void mma_bf16_tc(uint32_t d_tmem, uint64_t a, uint64_
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
 }
 
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// 1 / (1 + e^-x) in fp32 from the hardware exponential and reciprocal
-// approximations (relative errors near 2^-21 and 2^-23, far below the bf16
-// rounding of the product); e^-x = inf gives 0.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
-    return r;
-}
-
 // MERGE = false: ml maps the latent [S][H][512]; MERGE = true: ml is unused
 // and the rows are merged from the partials (NR = 16, one row per warp).
 template <int NR, bool MERGE>
@@ -134,14 +109,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         // W_UV is not written by the kernel before this one: fetch it first.
         mbar_arrive_expect_tx(&full_w, kColBlocks * kABlock);
-        for (int kb = 0; kb < kColBlocks; ++kb) tma_2d(sm + kAOff + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &full_w);
+        for (int kb = 0; kb < kColBlocks; ++kb) tc::tma_2d(sm + kAOff + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &full_w);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!MERGE && tid == 0) {
         // Rows past S read as zeros (their outputs are not written).
         mbar_arrive_expect_tx(&full_l, kColBlocks * T::kBBlock);
         for (int kb = 0; kb < kColBlocks; ++kb)
-            tma_3d(sm + kBOff + kb * T::kBBlock, &ml, 64 * kb, h, t0, &full_l);
+            tc::tma_3d(sm + kBOff + kb * T::kBBlock, &ml, 64 * kb, h, t0, &full_l);
     }
     if (tid < NR) active[tid] = tid < nrows && __ldg(a.lengths + (t0 + tid) / a.qlen) > 0;
     // This thread's gate words (bf16 pairs w = tid + 512 k: row w / 64, pair
@@ -240,22 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t res = 0u;
         if (active[r]) {
             const uint32_t val = tile2[w], g = gw[k];
-            res = pack_bf16x2(bf16_lo(val) * sigmoid_f32(bf16_lo(g)), bf16_hi(val) * sigmoid_f32(bf16_hi(g)));
+            res = pack_bf16x2(bf16_lo(val) * tc::sigmoid_f32(bf16_lo(g)), bf16_hi(val) * tc::sigmoid_f32(bf16_hi(g)));
         }
         *reinterpret_cast<uint32_t *>(a.out + ((long long)(t0 + r) * a.H + h) * MLA_D_V + 2 * p) = res;
     }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
 }
 
 // Tensor maps, encoded once per (device, buffer, shape) and reused while a
@@ -273,7 +236,7 @@ struct MapCache {
 cudaError_t encode_map(MapCache &c, int dev, const void *ptr, int S, int H, int rank, const cuuint64_t *dim,
                        const cuuint64_t *stride, const cuuint32_t *box) {
     if (c.hit(dev, ptr, S, H)) return cudaSuccess;
-    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tc::encode_fn();
     if (!enc) return cudaErrorNotSupported;
     c.dev = -1;
     const cuuint32_t es[3] = {1, 1, 1};

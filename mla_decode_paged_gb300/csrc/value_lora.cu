@@ -48,7 +48,6 @@
 #include <algorithm>
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -225,12 +224,6 @@ __device__ __forceinline__ void mma_bf16_tc(uint32_t d_tmem, uint64_t a, uint64_
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(one));
 }
 
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
-
 // D (+)= A[128 x 64 (kb1 - kb0)] B[N x ..]^T: column blocks kb0 .. kb1 - 1 of
 // the latent's, both 128B-swizzled.
 __device__ __forceinline__ void mma_latent(uint32_t d_tmem, uint32_t a, uint32_t a_block, uint32_t b, uint32_t b_block,
@@ -240,21 +233,6 @@ __device__ __forceinline__ void mma_latent(uint32_t d_tmem, uint32_t a, uint32_t
     for (int j = 4 * kb0; j < 4 * kb1; ++j)
         mma_bf16_tc(d_tmem, ad + (j >> 2) * (a_block >> 4) + (j & 3) * 2, bd + (j >> 2) * (b_block >> 4) + (j & 3) * 2,
                     idesc, j > 0, one);
-}
-
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
 }
 
 constexpr int kTcPairs = 48, kTcThreads = 128, kParts = 4;
@@ -294,8 +272,8 @@ __global__ void __launch_bounds__(kTcThreads)
             constexpr int kPer = kColBlocks / kParts;
             mbar_arrive_expect_tx(&full[i], kPer * (kTcXBlock + a_block));
             for (int kb = i * kPer; kb < (i + 1) * kPer; ++kb) {
-                tma_2d(sm + kb * kTcXBlock, &mx, 64 * kb, (int)row0, &full[i]);
-                tma_2d(sm + a_off + kb * a_block, &ma, 64 * kb, a * p.rank, &full[i]);
+                tc::tma_2d(sm + kb * kTcXBlock, &mx, 64 * kb, (int)row0, &full[i]);
+                tc::tma_2d(sm + a_off + kb * a_block, &ma, 64 * kb, a * p.rank, &full[i]);
             }
         }
     __syncwarp();
@@ -308,7 +286,7 @@ __global__ void __launch_bounds__(kTcThreads)
     }
     bool ok = true;
     if (warp == 0) {
-        const uint32_t one = elect_one(), idesc = idesc_bf16((p.rank + 15) / 16 * 16);
+        const uint32_t one = tc::elect_one(), idesc = idesc_bf16((p.rank + 15) / 16 * 16);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             constexpr int kPer = kColBlocks / kParts;
@@ -360,13 +338,6 @@ __global__ void __launch_bounds__(kTcThreads)
 
 constexpr int kABlock = MLA_D_V * 128;             // one column block of W_UV[h]: 16 KB
 constexpr int kXOff = kColBlocks * kABlock;        // the tile's latents
-
-// 1 / (1 + e^-x); e^-x = inf gives 0.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
-    return r;
-}
 
 // --------------------------------- project: B T by warp MMAs (one row a request)
 
@@ -519,7 +490,7 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y, rows = p.tile_rows, tiles = (p.S + rows - 1) / rows, step = gridDim.x;
     const bool issuer = warp == kFewThreads / 32;   // a whole warp; one lane copies and commits
-    const uint32_t one = elect_one();
+    const uint32_t one = tc::elect_one();
 
     // Row `tid`'s adapter and length; the first tile's on their way during the set-up.
     int index = -1, len = 0;
@@ -546,13 +517,13 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
     const auto fetch = [&](int tile, int s, uint32_t with) {
         mbar_arrive_expect_tx(&full[s], with + T::kBBytes);
         for (int kb = 0; kb < kColBlocks; ++kb)
-            tma_3d(sm + kXOff + s * T::kBBytes + kb * T::kBBlock, &ml, 64 * kb, h, tile * rows, &full[s]);
+            tc::tma_3d(sm + kXOff + s * T::kBBytes + kb * T::kBBlock, &ml, 64 * kb, h, tile * rows, &full[s]);
     };
     if (issuer && one) {
         // Nothing here but the low-rank products is written by the kernel
         // before this one: W_UV and the latent are fetched at once.
         fetch(blockIdx.x, 0, kXOff);
-        for (int kb = 0; kb < kColBlocks; ++kb) tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &full[0]);
+        for (int kb = 0; kb < kColBlocks; ++kb) tc::tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &full[0]);
         if (blockIdx.x + step < tiles) fetch(blockIdx.x + step, 1, 0);
     }
     bool ok = true;
@@ -619,7 +590,7 @@ __global__ void __launch_bounds__(kFewThreads + 32, 1)
             for (int i = 0; i < T::kRows; ++i) {
                 const int n = first + i;
                 const float val = adapted[n] ? d[i] + delta[n * kDStride + v] : d[i];
-                const float y = val * sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16));
+                const float y = val * tc::sigmoid_f32(__uint_as_float((uint32_t)gate[i] << 16));
                 // a select, so that nothing of an empty request is seen
                 x[i] = active[n] ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : 0;
             }
@@ -668,27 +639,6 @@ struct Tile {
     static_assert((512 - kAddCols) / kWin >= NR / kWin * 9, "the entries of a tile, at two rows a request or more");
     static constexpr uint32_t kSwz = RB == 32 ? tc::kSw64 : tc::kSw128, kSbo = 16 * RB;
 };
-
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok;
-}
-
-// 8 consecutive f32 TMEM columns of this warp's lanes.
-__device__ __forceinline__ void ld8(uint32_t taddr, float *v) {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
 
 __device__ __forceinline__ float ld1(uint32_t taddr) {
     uint32_t r;
@@ -771,7 +721,7 @@ __device__ void slot_filler(const LoraArgs &p, const CUtensorMap *mb, uint8_t *s
         if (lane == 0) {
             if (a >= 0) {
                 mbar_arrive_expect_tx(&sh.s_full[s], T::kBBytes);
-                tma_2d(slot, mb, k0, (a * p.H + h) * MLA_D_V, &sh.s_full[s]);
+                tc::tma_2d(slot, mb, k0, (a * p.H + h) * MLA_D_V, &sh.s_full[s]);
             } else {
                 mbar_arrive(&sh.s_full[s]);
             }
@@ -834,20 +784,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLatentWarp) {
         // Neither W_UV nor the latent is written by the kernel before this
         // one.  Rows past S read as zeros (their outputs are not written).
-        const uint32_t one = elect_one();
+        const uint32_t one = tc::elect_one();
         int fetched = 0;
         const auto fetch = [&](int tile) {
             if (one) {
                 mbar_arrive_expect_tx(&sh.x_full, T::kXBytes);
                 for (int kb = 0; kb < kColBlocks; ++kb)
-                    tma_3d(sm + kXOff + kb * T::kXBlock, &ml, 64 * kb, h, tile * NR, &sh.x_full);
+                    tc::tma_3d(sm + kXOff + kb * T::kXBlock, &ml, 64 * kb, h, tile * NR, &sh.x_full);
             }
             __syncwarp();
             ++fetched;
         };
         if (one) {
             mbar_arrive_expect_tx(&sh.w_full, kXOff);
-            for (int kb = 0; kb < kColBlocks; ++kb) tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &sh.w_full);
+            for (int kb = 0; kb < kColBlocks; ++kb) tc::tma_2d(sm + kb * kABlock, &mw, 64 * kb, MLA_D_V * h, &sh.w_full);
         }
         fetch(blockIdx.x);
         bool ok = wait_warp(&sh.w_full, 0);
@@ -876,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_wait(&sh.fin, 0);
     } else if (warp == kItemWarp) {
-        const uint32_t one = elect_one();
+        const uint32_t one = tc::elect_one();
         bool ok = true, ready = false;      // the next slot is known to be full
         int it = 0, s = 0, s_phase = 0;
         const uint64_t b_desc = tc::sdesc(base + T::kSlotOff, 16, T::kSbo, T::kSwz);
@@ -968,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float d[T::kRows];
 #pragma unroll
             for (int c = 0; c < T::kRows; c += 8)
-                ld8(tm + lanes + (it & 1) * NR + first + c, d + c);
+                tc::ld8(tm + lanes + (it & 1) * NR + first + c, d + c);
             float add[T::kRows];
 #pragma unroll
             for (int i = 0; i < T::kRows; ++i) {
@@ -989,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < T::kRows; ++i) {
                 const float val = adapted >> i & 1 ? d[i] + add[i] : d[i];
-                const float y = val * sigmoid_f32(__uint_as_float((uint32_t)in.gate[i] << 16));
+                const float y = val * tc::sigmoid_f32(__uint_as_float((uint32_t)in.gate[i] << 16));
                 // a select, so that nothing of an empty request is seen
                 x[i] = live >> i & 1 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : 0;
             }
@@ -1005,22 +955,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLatentWarp) tc::tmem_free(tm, 512);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 bool encode_bf16(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dim, const cuuint64_t *stride,
                  const cuuint32_t *box, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
     const cuuint32_t es[3] = {1, 1, 1};
-    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), dim, stride, box, es,
+    return tc::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), dim, stride, box, es,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1113,7 +1051,7 @@ cudaError_t value_lora_launch(const void *latent, const void *w_uv, const void *
                               const void *lora_a, const void *lora_b, const int32_t *adapters, const float *lora_scale,
                               int num_adapters, int rank, int R, int qlen, int H, void *out, void *workspace, int sms,
                               cudaStream_t st) {
-    if (!encode_fn()) return cudaErrorNotSupported;
+    if (!tc::encode_fn()) return cudaErrorNotSupported;
     LoraArgs p = {};
     p.latent = static_cast<const __nv_bfloat16 *>(latent);
     p.gate = static_cast<const __nv_bfloat16 *>(gate);
