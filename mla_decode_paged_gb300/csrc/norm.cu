@@ -23,8 +23,12 @@
 // one, and its weights stay in registers.
 //
 // Measured (bf16, residual added in bf16): 64 rows of 7,168 in 2.9 us; 16,384
-// rows of 7,168 with group scales in 146 us, 5.7 TB/s (one row after another
-// without the ring: 219 us); 100,000 rows of 1,024 likewise in 112 us, 6.4 TB/s.
+// rows of 7,168 with group scales in 145 us, 5.7 TB/s (one row after another
+// without the ring: 219 us); 100,000 rows of 1,024 likewise in 111 us, 6.4 TB/s.
+// Wide rows: 4,000 of 16,384 in 92 us, 5.7 TB/s (float32 residual: 128, 6.2).
+// Above that a thread of a block of up to 1,024 holds four vectors at 64
+// registers and spills 88 to 484 bytes: 4,000 of 32,768 without a residual 129
+// us (4.1 TB/s), with one 217 (4.8), in float32 357 (4.4).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -488,12 +492,15 @@ cudaError_t launch(const NormArgs &a, int sms, cudaStream_t st) {
     ra.depth = std::min(kRingBytes / ra.row_bytes, kMaxRing);
     // The ring takes rows too wide for one warp once every SM has one: 256 rows
     // of 7,168 take 4.0 us with it and 5.7 without, 500 6.2 and 9.4, 16,384 72
-    // and 151.  Up to 1,024 columns a warp a row, with the next row's loads in
-    // flight, is level or ahead: 8,192 x 512 4.3 us against 5.5, 65,536 x 576
-    // 39 against 61, 8,192 x 1,024 14.0 against 14.7 (20,000 x 1,024 20.9
-    // against 18.8).  A row that does not fit the ring twice takes the blocks,
-    // and so does one of more than 16,384 columns, more than a ring's block
-    // holds (without a residual up to 28,160 would fit the ring twice).
+    // and 151.  Up to 1,024 columns a warp takes a row, the next row's loads in
+    // flight: well ahead of the ring where there are most rows (100,000 x 1,024
+    // 70 us against 79, with a residual 119 against 148; 65,536 x 576 39 against
+    // 61, 8,192 x 512 4.3 against 5.5), up to a tenth behind it at the widest of
+    // these and fewer rows (8,192 x 1,024 8.4 against 8.2, with a residual 14.2
+    // against 12.6; 20,000 20.6 against 18.8, and 28.0 against 29.5).  A row
+    // that does not fit the ring twice takes the blocks, and so does one of more
+    // than 16,384 columns, more than a ring's block holds (without a residual up
+    // to 28,160 would fit the ring twice).
     if (a.vecs > 128 && a.vecs <= kRingThreads * kRingVpt && a.rows >= sms && ra.depth >= 2) {
         if (a.vecs <= 512) return launch_ring_res<T, 1>(ra, sms, st);
         if (a.vecs <= 1024) return launch_ring_res<T, 2>(ra, sms, st);

@@ -40,12 +40,16 @@
 // its partial sums to the workspace, joined in group order by a small kernel.
 //
 // Measured (12 heads, bf16 query): 64 requests of 1K to 8K tokens, one row
-// each, in 34.5 us, 5.0 TB/s of cache rows; 128 of 4K to 32K, four rows each,
-// in 256 us, 5.7 TB/s (loads alone top out at 5.3 to 5.7 at this
-// random order of 576-byte rows); 32 of 32K, 96 heads, in 121 us, 5.1 TB/s:
-// two stages' copies do not cover their latency and the MMAs' 1,940 cycles.
+// each, in 35 us, 5.0 TB/s of cache rows; 128 of 4K to 32K, four rows each,
+// in 257 us, 5.65 TB/s (250 on another GPU; loads alone top out at 5.3 to 5.7
+// at this random order of 576-byte rows); 32 of 32K, 96 heads, in 123 us, 5.0
+// TB/s: two stages' copies do not cover their latency and the MMAs' 1,940
+// cycles.  With an fp8 query, one column a row, 34.4, 246 and 114 us.  Four
+// rows of 96 heads (three groups) over 8 requests of 4K to 32K: 61 us, fp8 51,
+// where the bytes would take 10 and the MMAs 25 and 12.
 // A new request costs the conversion of its query, about 3,400 cycles for 16
-// rows (100 requests of 384 rows and 9 to 65 tokens: 62 us).
+// rows (100 requests of 384 rows and 9 to 65 tokens: 58 us; fp8, copied as it
+// is, 29).
 #include <climits>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

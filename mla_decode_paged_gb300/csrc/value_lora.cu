@@ -24,7 +24,7 @@
 //     order over k is free), eight warps of 64 latent columns each, joined in
 //     shared memory.  Many: tcgen05 MMAs, 48 pairs (M, the rows past them
 //     whatever follows in shared memory: unused lanes) times A (N), two
-//     blocks an SM.
+//     blocks an SM up to rank 64, one above.
 //     T goes to the workspace as two bf16 terms, hi + lo (2^-17 of the
 //     product; one term would add 2^-9, as much as the output's own rounding).
 //   project: persistent blocks, each on one head: W_UV[h] (M = 128 outputs)
@@ -974,7 +974,13 @@ bool encode_rows(CUtensorMap *m, const void *ptr, int64_t rows, int box_rows) {
 cudaError_t shrink(const LoraArgs &p, int R, int sms, cudaStream_t st) {
     const int pairs = p.qlen * p.H;
     // With more 16-pair blocks than the GPU holds at once, A's repeated reads
-    // cost more than the taller tiles' start.
+    // cost more than the taller tiles' start: at 768 of them (128 requests of
+    // eight rows, 12 heads) the whole call takes 12.3 us at rank 16 and 23.6 at
+    // rank 128 by tcgen05, 14.9 and 35.1 by warp MMAs; at 1,536 27.0 and 39.4 at
+    // rank 64, 39.3 and 52.4 at rank 72 (one block an SM).  Below that number
+    // warp MMAs are ahead for small ranks and few pairs only (192 blocks at rank
+    // 16 7.2 us against 7.6; at 384 already 10.8 against 10.0, at rank 128 21.9
+    // against 16.0): the limit is on the high side.
     if ((int64_t)R * ((pairs + 15) / 16) > 4 * (int64_t)sms && pairs > 16 && (int64_t)p.S * p.H <= INT32_MAX) {
         CUtensorMap ma, mx;
         if (!encode_rows(&ma, p.a, (int64_t)p.n * p.rank, p.rank) ||
