@@ -99,12 +99,12 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
 }
 
 // Waits for the phase of `parity` to complete.  Returns false (after
-// flagging MLA_DEV_TIMEOUT) if it has not completed within `limit`.
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, long long limit = kWaitCycles) {
+// flagging MLA_DEV_TIMEOUT) if it has not completed within kWaitCycles.
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
     long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
-        if (clock64() - t0 > limit) {
+        if (clock64() - t0 > kWaitCycles) {
             flag(MLA_DEV_TIMEOUT);
             return false;
         }
@@ -124,9 +124,23 @@ __device__ __forceinline__ bool warp_agrees(bool ok, int *abort_flag) {
 __device__ __forceinline__ bool aborted(const int *abort_flag) { return *(const volatile int *)abort_flag != 0; }
 
 // A whole warp's wait, given up once any role of the block has.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *abort_flag,
-                                          long long limit = kWaitCycles) {
-    return warp_agrees(!aborted(abort_flag) && mbar_wait(bar, parity, limit), abort_flag);
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *abort_flag) {
+    return warp_agrees(!aborted(abort_flag) && mbar_wait(bar, parity), abort_flag);
+}
+
+// The same for what many steps of the other roles lead to: `limit` cycles,
+// unless one of these gives up in between.
+__device__ __forceinline__ bool warp_wait_long(uint64_t *bar, uint32_t parity, int *abort_flag, long long limit) {
+    bool ok = mbar_try_wait(bar, parity);
+    const long long t0 = clock64();
+    while (!ok && !aborted(abort_flag)) {
+        ok = mbar_try_wait(bar, parity);
+        if (!ok && clock64() - t0 > limit) {
+            flag(MLA_DEV_TIMEOUT);
+            break;
+        }
+    }
+    return warp_agrees(ok, abort_flag);
 }
 
 // ------------------------------------------------------------ bulk copies

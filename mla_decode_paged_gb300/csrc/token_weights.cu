@@ -730,7 +730,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!w.first) continue;
             // The last of all the MMAs of the request before: a wait for its
             // tiles, not for one (2,048 query rows of 2^30 tokens take seconds).
-            if (w.unit > 0 && !warp_wait(&ms.q_free, (w.unit - 1) & 1, &ms.abort_flag, kWaitCycles + tiles * kTileCycles))
+            if (w.unit > 0 &&
+                !warp_wait_long(&ms.q_free, (w.unit - 1) & 1, &ms.abort_flag, kWaitCycles + tiles * kTileCycles))
                 break;
             tiles = 0;
             prep_unit<NP, TERMS, PAIR>(a, sm, ms, w.r, w.len, grp, w.unit, rank);

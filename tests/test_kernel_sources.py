@@ -73,15 +73,18 @@ def test_a_wait_for_a_whole_request_goes_by_its_tiles():
     tiles, cycles = 2**22, 4700
     assert tiles * cycles > limit               # one step's limit would not do
     assert limit + tiles * tile > 2 * tiles * cycles
-    (wait,) = re.findall(r"warp_wait\(&ms\.q_free.*\)", text)
+    (wait,) = re.findall(r"warp_wait\w*\(&ms\.q_free.*\)", text)
     assert "kWaitCycles + tiles * kTileCycles" in wait
+    # a role that gives up meanwhile ends it at once
+    (body,) = _bodies(common, r"bool warp_wait_long\(")
+    assert re.search(r"while \(!ok && !aborted\(abort_flag\)\)", body)
 
 
 @pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
 def test_every_status_word_is_read(path):
     # each source has a status word of its own; what a kernel may set there, device_status has to see
     text = re.sub(r"//.*", "", _text(path))
-    sets = re.search(r"\b(flag|mbar_wait|warp_wait|kv_row|kv_row_of_page|request_len)\(|\bTileIter<|\bUnitCursor<", text)
+    sets = re.search(r"\b(flag|mbar_wait|warp_wait|warp_wait_long|kv_row|kv_row_of_page|request_len)\(|\bTileIter<|\bUnitCursor<", text)
     readers = re.findall(r"cudaError_t (\w+_status)\(unsigned int \*flags, bool clear\) \{ return read_status", text)
     if not sets or os.path.basename(path) == "api.cu":
         return
