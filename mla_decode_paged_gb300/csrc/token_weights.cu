@@ -113,8 +113,8 @@ struct Misc {
     int start[3];               // this CTA's first request, its first tile there, tiles in all
 };
 
-// A CTA's (a pair's) tiles of TOKENS in order; every role walks them on its
-// own (uniform loads).
+// A CTA's (a pair's) tiles of TOKENS in order; every role, a whole warp, walks
+// them on its own (uniform loads).
 template <int TOKENS>
 struct Walk {
     int r, t, ntiles, len, base, left, unit;
@@ -142,10 +142,25 @@ struct Walk {
         t = 0;
         first = true;
         ++unit;
-        do {        // at least one more tile is to come, so a request with tokens follows
-            ++r;
-            open(a);
-        } while (ntiles == 0 && r + 1 < a.R);
+        ++r;        // at least one more tile is to come, so a request with tokens follows
+        open(a);
+        // Empty requests are passed over 32 at a time: one by one 2^24 of them
+        // took 3.5 s, more than the roles wait for each other.
+        while (ntiles == 0 && r + 1 < a.R) {
+            const int mine = r + 1 + (threadIdx.x & 31);
+            int b = 0;
+            const int n = mine < a.R ? request_len(a.indptr, mine, a.num_pages, &b) : 0;
+            const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+            if (some == 0) {
+                r = min(r + 32, a.R - 1);
+                continue;
+            }
+            const int src = __ffs(some) - 1;
+            r += 1 + src;
+            len = __shfl_sync(0xffffffffu, n, src);
+            base = __shfl_sync(0xffffffffu, b, src);
+            ntiles = (len + TOKENS - 1) / TOKENS;
+        }
     }
 };
 
@@ -741,11 +756,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");      // the constants in the other CTA
                 arrive_lead<PAIR>(&ms.q_ready, rank);
             }
-            // The next request's (empty ones passed over), if this CTA gets to it.
+            // The next request's (a few empty ones passed over), if this CTA gets to it.
             if (w.left > w.ntiles - w.t) {
                 int r = w.r + 1, base;
-                while (r < a.R && request_len(a.indptr, r, a.num_pages, &base) == 0) ++r;
-                if (r < a.R) prefetch_rows<C, TERMS>(a, r, grp, rank);
+                const int end = min(a.R, r + 32);
+                while (r < end && request_len(a.indptr, r, a.num_pages, &base) == 0) ++r;
+                if (r < end) prefetch_rows<C, TERMS>(a, r, grp, rank);
             }
         }
     }

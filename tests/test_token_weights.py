@@ -404,3 +404,24 @@ def test_a_list_that_starts_past_its_first_entries(qlen, heads):
     assert (out[:skip] == -7).all() and (out[skip + 230:] == -7).all()
     _check(out[skip:skip + 230], want, bound)
     assert mla.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,heads", [(1 << 22, 1), (20001, 80)])
+def test_many_empty_requests_between_two_tiles_of_a_block(R, heads):
+    # the tiles of the first and of the last request meet inside one CTA (or pair), whose roles each pass over all the
+    # empty requests between them; none may give up on another meanwhile
+    first, last = 128 * 151, 128 * 153
+    g = torch.Generator(device=DEV).manual_seed(R)
+    kv = torch.randn(64, 576, generator=g, device=DEV).mul_(0.5).to(torch.float8_e4m3fn).view(torch.uint8)
+    q = torch.zeros(R, heads, 576, dtype=torch.bfloat16, device=DEV)
+    q[0], q[-1] = (torch.randn(heads, 576, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    indptr = torch.full((R + 1,), first, dtype=torch.int32, device=DEV)
+    indptr[0], indptr[-1] = 0, first + last
+    pages = torch.arange(64, dtype=torch.int32, device=DEV).repeat((first + last) // 64)
+    lse = torch.zeros(R, heads, device=DEV)
+    out = mla.token_weights(q, kv, pages, indptr, 0.05, 1.0, lse)
+    assert mla.device_status() == 0
+    want, bound, _ = _formula(q[[0, -1]], kv, pages[:128], [64, 64], heads, 1, 0.05, False, lse[:2])
+    _check(out, torch.cat([want[:64].repeat(first // 64), want[64:].repeat(last // 64)]),
+           torch.cat([bound[:64].repeat(first // 64), bound[64:].repeat(last // 64)]))
