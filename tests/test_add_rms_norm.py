@@ -337,3 +337,25 @@ def test_wide_rows_without_a_residual_over_all_sms(T, D, xt, quant):
         _check8(out, scales, y, quant, 0.013)
     few = mla.add_rms_norm(x[:3], w, EPS, quant=quant, scale=0.013 if quant == "static" else None)
     assert torch.equal(out[:3].view(torch.uint8), few[0].view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,quant", [(262200, 8200, "group"), (2100000, 1024, None)])
+def test_offsets_past_31_bits(T, D, quant):
+    # more than 2^31 elements, by the ring and by a warp a row: the last rows as they are in a small call
+    assert T * D > 2**31
+    x = torch.zeros(T, D, dtype=torch.bfloat16, device=DEV)
+    parts = [slice(0, 40), slice(2**31 // D - 20, 2**31 // D + 20), slice(T - 40, T)]
+    for k, p in enumerate(parts):
+        x[p] = _inputs(40, D, torch.bfloat16, None, 50 + k)[0]
+    w = _inputs(1, D, torch.bfloat16, None, 49)[1]
+    out, sc, _ = mla.add_rms_norm(x, w, EPS, quant=quant)
+    for p in parts:
+        _, y = _formula(x[p], w)
+        if quant is None:
+            _check16(out[p], y, "rows %s" % p)
+        else:
+            _check8(out[p], sc[p], y, quant)
+    assert bool((out[100:110].float() == 0).all())
+    del x, out, sc
+    torch.cuda.empty_cache()

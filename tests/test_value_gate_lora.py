@@ -306,3 +306,27 @@ def test_a_padded_row_of_a_batch_does_not_depend_on_the_others():
     got = mla.value_gate_lora(**{k: (v.contiguous() if isinstance(v, torch.Tensor) else v) for k, v in few.items()})
     for o in (out[:7], got):
         assert ((o.double() - want).abs() <= bound + 2.0**-8 * (want.abs() + bound) + 1e-40).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,qlen,heads,rank", [(43800, 1, 96, 8), (21900, 2, 96, 8)])
+def test_offsets_past_31_bits(R, qlen, heads, rank):
+    # more than 2^31 latent elements; the first, a middle and the last requests against the formula
+    S = R * qlen
+    assert S * heads * 512 > 2**31
+    s = dict(_make(96, qlen, heads, rank, 5, 77))
+    picks = torch.cat([torch.arange(32), torch.arange(2**31 // (heads * 512 * qlen) - 16, 2**31 // (heads * 512 * qlen) + 16),
+                       torch.arange(R - 32, R)]).to(DEV)
+    rows = (picks[:, None] * qlen + torch.arange(qlen, device=DEV)).view(-1)
+    big = dict(s, latent=torch.zeros(S, heads, 512, dtype=torch.bfloat16, device=DEV),
+               gate=torch.zeros(S, heads * 128, dtype=torch.bfloat16, device=DEV),
+               lengths=torch.ones(R, dtype=torch.int32, device=DEV),
+               adapters=torch.zeros(R, dtype=torch.int32, device=DEV))
+    for k, at in (("latent", rows), ("gate", rows), ("lengths", picks), ("adapters", picks)):
+        big[k][at] = s[k]
+    out = mla.value_gate_lora(**big)
+    assert mla.device_status() == 0
+    _check(out[rows], s)
+    assert bool((out[100 * qlen:200 * qlen] == 0).all())
+    del big, out
+    torch.cuda.empty_cache()
