@@ -514,7 +514,8 @@ mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *
  *                mla_value_gate_lora_workspace() bytes; holds nothing
  *                between calls; two calls (or captured graphs) that may
  *                overlap on the GPU need one each.
- * Neither out nor the workspace overlaps another argument.
+ * Neither out nor the workspace overlaps another argument.  num_requests *
+ * qlen up to 2^29, num_adapters * heads * 128 up to 2^31 - 1.
  */
 #define MLA_MAX_LORA_RANK 128
 mla_status mla_value_gate_lora(const void *latent, const void *w_uv, const void *gate, const int32_t *lengths,
