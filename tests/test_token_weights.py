@@ -425,3 +425,23 @@ def test_many_empty_requests_between_two_tiles_of_a_block(R, heads):
     want, bound, _ = _formula(q[[0, -1]], kv, pages[:128], [64, 64], heads, 1, 0.05, False, lse[:2])
     _check(out, torch.cat([want[:64].repeat(first // 64), want[64:].repeat(last // 64)]),
            torch.cat([bound[:64].repeat(first // 64), bound[64:].repeat(last // 64)]))
+
+
+@pytest.mark.gpu
+def test_the_longest_list_named_again_and_again():
+    # 150 requests that each name nearly all of the longest list, a bad one between any two: 2.5e9 tiles claimed.
+    # Flagged, ended by what the list could hold, and nothing outside it written.
+    n = 2**31 - 65536
+    if torch.cuda.mem_get_info()[0] < 4 * n * 2 + (8 << 30):
+        pytest.skip("%d GB of device memory free" % ((4 * n * 2 >> 30) + 8))
+    R = 299
+    ind = torch.zeros(R + 1, dtype=torch.int32, device=DEV)
+    ind[1::2] = n
+    q, kv, _, _ = _make([64], 1, 1, 1, 22)
+    pages = torch.arange(64, dtype=torch.int32, device=DEV).repeat(n // 64)
+    buf = torch.full((n + 64,), -7.0, device=DEV)
+    mla.token_weights(q.expand(R, -1, -1).contiguous(), kv, pages, ind, 0.05, 1.0, torch.zeros(R, 1, device=DEV), out=buf[:n])
+    assert mla.device_status() == mla.DEV_BAD_INDPTR
+    assert bool((buf[n:] == -7).all())
+    del pages, buf
+    torch.cuda.empty_cache()
