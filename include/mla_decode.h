@@ -65,6 +65,7 @@ typedef int mla_status;
 #define MLA_DEV_TIMEOUT 4u       /* a bounded device wait ran out                */
 #define MLA_DEV_BAD_PLAN 8u      /* a work plan did not fit this launch          */
 #define MLA_DEV_BAD_ADAPTER 16u  /* an adapter index was outside [-1, num_adapters) */
+#define MLA_DEV_BAD_POSITION 32u /* a position was outside [0, num_positions)    */
 
 /*
  * mla_decode_attend -- split-KV attention of one decode step.
@@ -412,6 +413,55 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
                             int64_t residual_stride, int residual_type, const void *weight, float eps,
                             int64_t tokens, int width, int quant, float scale, void *out, int64_t out_stride,
                             float *out_scales, void *residual_out, int64_t residual_out_stride, void *stream);
+
+/*
+ * mla_norm_rope -- norm and position rotation of every head in one pass,
+ * into a tensor or into the rows of a cache: the latent rows and index keys
+ * on their way into their caches, index queries, query heads.
+ *
+ * For token t < tokens, head h < heads, in float32:
+ *   y = x[t, h, :]
+ *   y[:norm_dim] *= rsqrt(sum(y[:norm_dim]^2) / norm_dim + eps) * weight     (with a weight)
+ *   and with positions, for i < rope_dim / 2, c = cos_sin[p, i], s = cos_sin[p, rope_dim / 2 + i],
+ *   p = positions[t] and (u, v) = columns rope_start + (i, i + rope_dim / 2), or with MLA_ROPE_PAIRS
+ *   rope_start + (2i, 2i + 1):   (u, v) = (u * c - v * s, v * c + u * s)
+ * and, by `quant`, with T = t, or slots[t] where slots are given:
+ *   NONE    out[T, h] = y rounded to x's type
+ *   ROW     sc = scale_of(max |y|) as mla_add_rms_norm; out_scales[T, h] = sc
+ *   STATIC  sc = scale
+ *   and out[T, h] = e4m3(y * (1 / sc)), to nearest even, saturating at +-448.
+ * A token with a negative slot is skipped (padding); one with a slot past
+ * out_rows is skipped and sets MLA_DEV_BAD_PAGE; two tokens with the same
+ * slot: which one lands is unspecified, for each 16 columns.  A position
+ * outside [0, num_positions) rotates as position 0 and sets
+ * MLA_DEV_BAD_POSITION.  NaN and infinities as mla_add_rms_norm.
+ *
+ *   x            bf16 or f16 (x_type), token t head h at x + t*x_row_stride +
+ *                h*x_head_stride (elements; 0 where a row is shared).
+ *   weight       x's type [norm_dim], or NULL: no norm.
+ *   positions    int64 [tokens], or NULL: no rotation; cos_sin f32
+ *                [num_positions, rope_dim], 16-byte aligned.
+ *   slots        int64 [tokens], or NULL: token t to row t.
+ *   out          x's type, or e4m3 codes: rows of out_row_stride, heads of
+ *                out_head_stride elements; out_rows rows (without slots:
+ *                tokens).
+ *   out_scales   f32 [out_rows, heads] (ROW).
+ * width a multiple of 8, 8..1024; norm_dim a multiple of 8, 8..width;
+ * rope_start a multiple of 8, rope_dim of 16, rope_start + rope_dim <= width;
+ * strides multiples of 8 up to 2^30; out's rows apart, each of its heads, or
+ * its heads, each of its rows; heads 1..65536, tokens * heads and out_rows up
+ * to 2^31 - 65536.  eps and a STATIC scale as mla_add_rms_norm.  x, weight and out 16-byte aligned.  out (16 bits,
+ * without slots) may be x itself with the same strides; another overlap of
+ * an output is MLA_ERR_INVALID (columns side by side in one buffer of one
+ * row stride do not overlap).
+ */
+#define MLA_ROPE_PAIRS 1u /* a rotation's pairs are neighbours (default: half a rotation apart) */
+#define MLA_MAX_ROPE_WIDTH 1024
+mla_status mla_norm_rope(const void *x, int64_t x_row_stride, int64_t x_head_stride, int x_type, const void *weight,
+                         int norm_dim, float eps, const int64_t *positions, const float *cos_sin,
+                         int64_t num_positions, int rope_start, int rope_dim, unsigned int flags, int64_t tokens,
+                         int heads, int width, int quant, float scale, const int64_t *slots, int64_t out_rows,
+                         void *out, int64_t out_row_stride, int64_t out_head_stride, float *out_scales, void *stream);
 
 /*
  * mla_token_weights -- the attention weight that each cached token received

@@ -33,13 +33,13 @@ from . import build as _build
 D_QK, D_LATENT, D_V = 576, 512, 128
 MLA_OK, MLA_ERR_INVALID, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA = 0, -1, -2, -3
 ATTEND_CAUSAL, ATTEND_Q_FP8 = 1, 2
-DEV_BAD_PAGE, DEV_BAD_INDPTR, DEV_TIMEOUT, DEV_BAD_PLAN, DEV_BAD_ADAPTER = 1, 2, 4, 8, 16
+DEV_BAD_PAGE, DEV_BAD_INDPTR, DEV_TIMEOUT, DEV_BAD_PLAN, DEV_BAD_ADAPTER, DEV_BAD_POSITION = 1, 2, 4, 8, 16, 32
 STATIC_SCRATCH_BYTES = 32 << 20   # MLA_STATIC_SCRATCH_BYTES: the partials buffer of decode_step_static
 
 __all__ = ["Prepared", "attend", "merge", "value_gate", "merge_value_gate", "decode_step", "decode_step_static",
            "STATIC_SCRATCH_BYTES", "choose_splits", "plan_units", "debug_gather",
            "debug_wait_timeout", "debug_attend_mma",
-           "kv_append", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
+           "kv_append", "norm_rope", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
            "value_gate_lora_workspace", "token_weights_workspace", "device_status", "build", "library", "MlaError"]
 
 
@@ -96,6 +96,8 @@ def library() -> ctypes.CDLL:
     lib.mla_decode_step_static.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, i32, i32,
                                            vp, i64, vp, vp, vp, vp, vp, vp, vp]
     lib.mla_add_rms_norm.argtypes = [vp, i64, i32, vp, i64, i32, vp, f32, i64, i32, i32, f32, vp, i64, vp, vp, i64, vp]
+    lib.mla_norm_rope.argtypes = [vp, i64, i64, i32, vp, i32, f32, vp, vp, i64, i32, i32, ctypes.c_uint, i64, i32, i32,
+                                  i32, f32, vp, i64, vp, i64, i64, vp, vp]
     lib.mla_token_weights.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, f32, vp, f32, vp, vp,
                                       ctypes.c_uint, vp, i64, vp]
     lib.mla_token_weights_workspace.argtypes = [i32, i32, i64, ctypes.c_uint]
@@ -104,7 +106,7 @@ def library() -> ctypes.CDLL:
     lib.mla_value_gate_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mla_value_gate_lora_workspace.argtypes = [i32, i32, i32, i32]
     lib.mla_value_gate_lora_workspace.restype = i64
-    for name in ("mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
+    for name in ("mla_norm_rope", "mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
                  "mla_decode_attend", "mla_decode_attend_ex", "mla_decode_attend_paged", "mla_decode_attend_planned", "mla_merge_splits", "mla_value_gate", "mla_merge_value_gate", "mla_debug_gather",
                  "mla_device_status", "mla_choose_splits", "mla_kv_append", "mla_debug_wait_timeout",
                  "mla_decode_step_static", "mla_debug_attend_mma"):
@@ -514,6 +516,39 @@ def add_rms_norm(x, weight, eps, residual=None, *, quant=None, scale=None, out=N
     return r
 
 
+_ROPE_QUANT = {None: 0, "head": 1, "static": 3}
+
+
+def norm_rope(x, weight=None, eps=1e-6, *, positions=None, cos_sin=None, rope_start=0, interleaved=False, quant=None,
+              scale=None, slots=None, out=None, out_scales=None, stream=None):
+    """Norm and position rotation of every head in one pass
+    (``mla_norm_rope``): returns ``(out, out_scales)`` (None for what does
+    not apply).
+
+    ``x``: bf16 / fp16 ``[T, H, D]`` or ``[T, D]`` (one head), rows and heads
+    may be strided (D a multiple of 8 up to 1,024).  ``weight``: x's type
+    ``[n]``: the root-mean-square norm of a head's first n columns (None: no
+    norm).  ``positions``: int64 ``[T]`` and ``cos_sin``: float32
+    ``[positions, d]``, d / 2 cosines then d / 2 sines: columns
+    ``rope_start`` to ``rope_start + d`` are rotated after the norm, column i
+    with i + d / 2, or with ``interleaved`` 2i with 2i + 1 (None: no
+    rotation).  ``quant=None``: ``out`` in x's type.  Otherwise e4m3 codes
+    (float8_e4m3fn) with scales ``"head"`` ``[T, H]`` or ``"static"`` (the
+    float ``scale``; no scales returned): a code stands for code * scale.
+    ``slots``: int64 ``[T]``: token t goes to row ``slots[t]`` of ``out``
+    (and of ``out_scales``), a cache of any number of rows; negative slots
+    are skipped.  ``out=x`` works in place.
+    """
+    q = _ROPE_QUANT.get(quant)
+    if q is None:
+        raise ValueError("quant must be None, 'head' or 'static'")
+    r = (_ops_module or _ops()).norm_rope(x, weight, eps, positions, cos_sin, rope_start, interleaved, q, scale, slots,
+                                          out, out_scales, stream)
+    if type(r) is int:
+        _check(r, "mla_norm_rope")
+    return r
+
+
 def token_weights(q, kv, pages, indptr, scale, kv_scale, lse, *, heads=None, qlen=1, weights=None, decay=1.0,
                   causal=False, q_scale=1.0, out=None, workspace=None, stream=None):
     """The attention weight every cached token received in a decode step,
@@ -605,7 +640,7 @@ def debug_wait_timeout(stream=None):
 def device_status(stream=None) -> int:
     """Synchronise the stream, return and clear the device status bits
     (DEV_BAD_PAGE, DEV_BAD_INDPTR, DEV_TIMEOUT, DEV_BAD_PLAN,
-    DEV_BAD_ADAPTER)."""
+    DEV_BAD_ADAPTER, DEV_BAD_POSITION)."""
     flags = ctypes.c_uint(0)
     _check(library().mla_device_status(ctypes.c_void_p(_stream(stream)), ctypes.byref(flags)),
            "mla_device_status")

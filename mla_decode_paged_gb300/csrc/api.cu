@@ -52,6 +52,12 @@ cudaError_t add_rms_norm_launch(const void *x, int64_t x_stride, int x_type, con
                                 float *out_scales, void *residual_out, int64_t residual_out_stride, int sms,
                                 cudaStream_t st);
 cudaError_t norm_status(unsigned int *flags, bool clear);
+cudaError_t norm_rope_launch(const void *x, int64_t x_row, int64_t x_head, int x_type, const void *weight, int norm_dim,
+                             float eps, const int64_t *positions, const float *cos_sin, int64_t num_positions,
+                             int rope_start, int rope_dim, bool pairs, int64_t tokens, int heads, int width, int quant,
+                             float scale, const int64_t *slots, int64_t out_rows, void *out, int64_t out_row,
+                             int64_t out_head, float *out_scales, int sms, cudaStream_t st);
+cudaError_t norm_rope_status(unsigned int *flags, bool clear);
 cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                                  const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
                                  int heads, double sc, const float *lse, float decay, const float *weights, float *out,
@@ -122,6 +128,32 @@ bool overlap_rows(const Rows &x, const Rows &y, int64_t n) {
     const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p));
     const int64_t at = ((d % x.stride) + x.stride) % x.stride;   // where y's columns start in x's row
     return at < x.width || at + y.width > x.stride;
+}
+
+// A [rows, heads, width] tensor of strides in elements of `size` bytes.
+struct Heads {
+    const void *p;
+    int64_t row, head, rows, heads, width;
+    int size;
+
+    bool empty() const { return !p || rows == 0 || heads == 0; }
+    int64_t span() const { return ((heads - 1) * head + width) * size; }     // of a row, first byte to last
+    int64_t whole() const { return empty() ? 0 : (rows - 1) * row * size + span(); }
+    bool row_major() const { return rows == 1 || row * size >= span(); }
+    // Whether no two heads share an element: heads inside rows, or rows inside heads.
+    bool apart() const {
+        return (row_major() && (heads == 1 || head >= width)) ||
+               ((rows == 1 || row >= width) && (heads == 1 || head >= (rows - 1) * row + width));
+    }
+    bool same(const Heads &o) const { return p == o.p && row == o.row && head == o.head && size == o.size; }
+};
+
+// Whether the tensors may share a byte: by their extents, or by their columns
+// where both are rows of one stride.
+bool overlap_heads(const Heads &x, const Heads &y) {
+    if (!overlap(x.p, x.whole(), y.p, y.whole())) return false;
+    if (!x.row_major() || !y.row_major() || x.rows == 1 || y.rows == 1 || x.row * x.size != y.row * y.size) return true;
+    return overlap_rows({x.p, x.row * x.size, x.span()}, {y.p, y.row * y.size, y.span()}, std::max(x.rows, y.rows));
 }
 
 bool same_rows(const Rows &x, const Rows &y) { return x.p == y.p && x.stride == y.stride && x.width == y.width; }
@@ -662,6 +694,63 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
     return MLA_OK;
 }
 
+mla_status mla_norm_rope(const void *x, int64_t x_row_stride, int64_t x_head_stride, int x_type, const void *weight,
+                         int norm_dim, float eps, const int64_t *positions, const float *cos_sin,
+                         int64_t num_positions, int rope_start, int rope_dim, unsigned int flags, int64_t tokens,
+                         int heads, int width, int quant, float scale, const int64_t *slots, int64_t out_rows,
+                         void *out, int64_t out_row_stride, int64_t out_head_stride, float *out_scales, void *stream) {
+    if (x_type != MLA_TYPE_BF16 && x_type != MLA_TYPE_F16) return fail(MLA_ERR_INVALID, "x_type must be bf16 or f16");
+    if (flags & ~MLA_ROPE_PAIRS) return fail(MLA_ERR_INVALID, "unknown flag bits");
+    if (quant != MLA_QUANT_NONE && quant != MLA_QUANT_ROW && quant != MLA_QUANT_STATIC)
+        return fail(MLA_ERR_INVALID, "quant must be none, row or static");
+    if (tokens < 0 || out_rows < 0) return fail(MLA_ERR_INVALID, "negative tokens / out_rows");
+    if (heads < 1 || heads > 65536) return fail(MLA_ERR_INVALID, "heads outside 1..65536");
+    if (width < 8 || width > MLA_MAX_ROPE_WIDTH || width % 8 != 0)
+        return fail(MLA_ERR_INVALID, "width must be a multiple of 8 in 8..1024");
+    if (weight && (norm_dim < 8 || norm_dim > width || norm_dim % 8 != 0))
+        return fail(MLA_ERR_INVALID, "norm_dim must be a multiple of 8 in 8..width");
+    if (weight && (!(eps > 0.f) || !std::isfinite(eps))) return fail(MLA_ERR_INVALID, "eps must be finite and > 0");
+    if ((positions == nullptr) != (cos_sin == nullptr)) return fail(MLA_ERR_INVALID, "positions and cos_sin go together");
+    if (positions && (rope_start < 0 || rope_start % 8 != 0 || rope_dim < 16 || rope_dim % 16 != 0 ||
+                      rope_dim > width || rope_start > width - rope_dim))
+        return fail(MLA_ERR_INVALID, "rope_start must be a multiple of 8, rope_dim of 16, their sum at most width");
+    if (positions && (num_positions < 1 || num_positions > (int64_t)1 << 40))
+        return fail(MLA_ERR_INVALID, "num_positions outside 1..2^40");
+    if (quant == MLA_QUANT_STATIC && !(std::isfinite(scale) && scale >= 1.17549435e-38f))
+        return fail(MLA_ERR_INVALID, "scale must be finite and >= 2^-126");
+    const auto bad_stride = [](int64_t s) { return s < 0 || s % 8 != 0 || s > 1 << 30; };    // extents stay below 2^63
+    if (tokens > kMaxPages / heads) return fail(MLA_ERR_UNSUPPORTED, "tokens * heads above 2^31 - 65536");
+    const int64_t rows = slots ? out_rows : tokens;
+    if (rows > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "out_rows above 2^31 - 65536");
+    const int osize = quant == MLA_QUANT_NONE ? 2 : 1;
+    if (bad_stride(x_row_stride) || bad_stride(x_head_stride) || bad_stride(out_row_stride) || bad_stride(out_head_stride))
+        return fail(MLA_ERR_INVALID, "strides must be multiples of 8 from 0 to 2^30");
+    if (tokens == 0) return MLA_OK;
+    if (!x || (rows > 0 && !out) || (quant == MLA_QUANT_ROW && rows > 0 && !out_scales))
+        return fail(MLA_ERR_INVALID, "null pointer");
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(out, 16) || !aligned(cos_sin, 16) || !aligned(positions, 8) ||
+        !aligned(slots, 8) || !aligned(out_scales, 4))
+        return fail(MLA_ERR_INVALID, "misaligned pointer (x, weight, out, cos_sin need 16 bytes)");
+    const Heads hx = {x, x_row_stride, x_head_stride, tokens, heads, width, 2};
+    const Heads ho = {out, out_row_stride, out_head_stride, rows, heads, width, osize};
+    if (rows > 0 && !ho.apart()) return fail(MLA_ERR_INVALID, "out's heads overlap");
+    const bool in_place = !slots && ho.same(hx);
+    const int64_t nscales = quant == MLA_QUANT_ROW ? rows * heads * 4 : 0;
+    const Span in[4] = {{weight, (int64_t)norm_dim * 2}, {positions, tokens * 8},
+                        {cos_sin, num_positions * rope_dim * 4}, {slots, tokens * 8}};
+    if ((!in_place && overlap_heads(ho, hx)) || overlaps({out, ho.whole()}, in) || overlaps({out_scales, nscales}, in) ||
+        overlap(out_scales, nscales, x, hx.whole()) || overlap(out_scales, nscales, out, ho.whole()))
+        return fail(MLA_ERR_INVALID, "an output overlaps an input or another output");
+    const int sms = device_sms();
+    if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = mla::norm_rope_launch(x, x_row_stride, x_head_stride, x_type, weight, norm_dim, eps, positions,
+                                          cos_sin, num_positions, rope_start, rope_dim, (flags & MLA_ROPE_PAIRS) != 0,
+                                          tokens, heads, width, quant, scale, slots, rows, out, out_row_stride,
+                                          out_head_stride, out_scales, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm_rope launch");
+    return MLA_OK;
+}
+
 mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                              const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
                              int qlen, int heads, float scale, float kv_scale, float q_scale, const float *lse,
@@ -831,7 +920,8 @@ mla_status mla_device_status(void *stream, unsigned int *flags) {
     cudaError_t (*readers[])(unsigned int *, bool) = {mla::attend_mma_status, mla::attend_tc_status, mla::merge_status,
                                                       mla::value_gate_status, mla::gather_status,
                                                       mla::kv_append_status, mla::norm_status,
-                                                      mla::token_weights_status, mla::evict_status, mla::value_lora_status};
+                                                      mla::token_weights_status, mla::evict_status, mla::value_lora_status,
+                                                      mla::norm_rope_status};
     for (auto rd : readers) {
         unsigned int f = 0;
         e = rd(&f, true);

@@ -1,5 +1,5 @@
 // Python module of the calls whose kernels take a few microseconds
-// (add_rms_norm, token_weights, kv_evict, value_gate_lora): argument checks,
+// (add_rms_norm, token_weights, kv_evict, value_gate_lora, norm_rope): argument checks,
 // output allocation and the call into the C ABI, without the Python
 // interpreter in between.  On the Grace host a call takes 2.3 us of it with
 // its outputs given and 1.3 more for each that it allocates (2.0 through
@@ -19,6 +19,7 @@
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "../../include/mla_decode.h"
 
@@ -243,6 +244,89 @@ PyObject *add_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// Strides of a [rows, heads, width] tensor of this type with contiguous
+// heads, or of [rows, width] as one head (rows, heads of one: dense).
+struct HeadRows {
+    int64_t rows, heads, width, row, head;
+};
+HeadRows heads_of(const at::Tensor &t, const char *name, int64_t dev) {
+    const int64_t n = t.dim();
+    if ((n != 2 && n != 3) || t.layout() != at::kStrided || t.get_device() != dev ||
+        (t.size(n - 1) > 1 && t.stride(n - 1) != 1))
+        refuse(std::string(name) + " must be [T, H, D] or [T, D] with contiguous heads on the first argument's device");
+    HeadRows h = {t.size(0), n == 3 ? t.size(1) : 1, t.size(n - 1), 0, 0};
+    h.head = h.heads > 1 ? t.stride(1) : h.width;
+    h.row = h.rows > 1 ? t.stride(0) : (h.heads > 1 ? (h.heads - 1) * h.head : 0) + h.width;
+    return h;
+}
+
+// (x, weight, eps, positions, cos_sin, rope_start, pairs, quant, scale, slots, out, out_scales, stream)
+PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject * {
+        const at::Tensor &x = tensor(a[0], "x");
+        const ScalarType type = x.scalar_type();
+        if (type != at::kBFloat16 && type != at::kHalf) refuse("x must be bf16 or fp16");
+        const int64_t dev = x.get_device();
+        const HeadRows hx = heads_of(x, "x", dev);
+        const int64_t T = hx.rows;
+        if (hx.width > INT32_MAX || hx.heads > INT32_MAX) refuse("x too wide");
+        const void *weight = nullptr;
+        int64_t norm_dim = 0;
+        if (a[1] != Py_None) {
+            const at::Tensor &w = tensor(a[1], "weight");
+            norm_dim = w.numel();
+            weight = ptr(dense(w, "weight", type, {norm_dim}, dev));
+            if (norm_dim > hx.width || norm_dim == 0) refuse("weight must have 8 to D elements");
+        }
+        const float eps = real(a[2], "eps");
+        if ((a[3] != Py_None) != (a[4] != Py_None)) refuse("positions and cos_sin go together");
+        const int64_t *positions = nullptr, *slots = nullptr;
+        const float *table = nullptr;
+        int64_t table_rows = 0, rope_dim = 0;
+        if (a[3] != Py_None) {
+            positions = ptr<int64_t>(dense(tensor(a[3], "positions"), "positions", at::kLong, {T}, dev));
+            const at::Tensor &cs = tensor(a[4], "cos_sin");
+            if (cs.dim() != 2 || cs.size(1) > INT32_MAX) refuse("cos_sin must be float32 [positions, rope_dim]");
+            table_rows = cs.size(0), rope_dim = cs.size(1);
+            table = ptr<float>(dense(cs, "cos_sin", at::kFloat, {table_rows, rope_dim}, dev));
+        }
+        const int rope_start = int32(a[5], "rope_start");
+        const int pairs = PyObject_IsTrue(a[6]);
+        if (pairs < 0) return nullptr;
+        const int quant = int32(a[7], "quant");
+        if ((a[8] != Py_None) != (quant == MLA_QUANT_STATIC)) refuse("scale goes with quant='static'");
+        const float scale = a[8] == Py_None ? 0.f : real(a[8], "scale");
+        const bool scales = quant == MLA_QUANT_ROW;
+        if (!scales && a[11] != Py_None) refuse("out_scales goes with quant='head'");
+        if (a[9] != Py_None) {
+            slots = ptr<int64_t>(dense(tensor(a[9], "slots"), "slots", at::kLong, {T}, dev));
+            if (a[10] == Py_None || (scales && a[11] == Py_None)) refuse("slots need the cache as out (and out_scales)");
+        }
+        const Place at(dev, a[12]);
+        ScalarType otype = quant == MLA_QUANT_NONE ? type : kE4m3;
+        if (quant != MLA_QUANT_NONE && a[10] != Py_None && tensor(a[10], "out").scalar_type() == at::kByte) otype = at::kByte;
+        HeadRows ho = {T, hx.heads, hx.width, hx.heads * hx.width, hx.width};
+        const at::Tensor out = output(a[10], "out", at, x.sizes(), otype, [&](const at::Tensor &t) {
+            ho = heads_of(t, "out", dev);
+            if (t.scalar_type() != otype || t.dim() != x.dim() || ho.heads != hx.heads || ho.width != hx.width ||
+                (!slots && ho.rows != T))
+                refuse(std::string("out must be ") + at::toString(otype) + (slots ? " rows" : "") + " of x's shape");
+        });
+        at::Tensor out_scales;
+        if (scales) {
+            std::vector<int64_t> shape = {ho.rows};
+            if (x.dim() == 3) shape.push_back(ho.heads);
+            out_scales = dense_output(a[11], "out_scales", at, shape, at::kFloat);
+        }
+        const mla_status st = mla_norm_rope(
+            ptr(x), hx.row, hx.head, norm_type(type), weight, (int)norm_dim, eps, positions, table, table_rows, rope_start,
+            (int)rope_dim, pairs ? MLA_ROPE_PAIRS : 0u, T, (int)hx.heads, (int)hx.width, quant, scale, slots, ho.rows,
+            ptr(out), ho.row, ho.head, scales ? ptr<float>(out_scales) : nullptr, at.stream);
+        if (st != MLA_OK) return PyLong_FromLong(st);
+        return pack({out, out_scales});
+    });
+}
+
 // (q, kv, pages, indptr, scale, kv_scale, lse, heads, qlen, weights, decay, causal, q_scale, out, workspace, stream)
 PyObject *token_weights(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 16, [&]() -> PyObject * {
@@ -348,7 +432,7 @@ PyObject *value_gate_lora(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 #define MLA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MLA_METHOD(add_rms_norm), MLA_METHOD(token_weights), MLA_METHOD(kv_evict),
-                         MLA_METHOD(value_gate_lora), {nullptr, nullptr, 0, nullptr}};
+                         MLA_METHOD(value_gate_lora), MLA_METHOD(norm_rope), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "mla_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -31,17 +31,13 @@
 // us (4.1 TB/s), with one 217 (4.8), in float32 357 (4.4).
 #include <algorithm>
 
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "vec8.cuh"
 
 namespace mla {
 namespace {
-
-constexpr float kE4m3Max = 448.f;
-constexpr float kMinScale = 1.17549435e-38f;   // the smallest normal float: its reciprocal is finite
 
 struct NormArgs {
     const void *x, *residual;
@@ -52,67 +48,6 @@ struct NormArgs {
     float eps, inv_scale, inv_width;
     int vecs, groups, residual_type, quant;
 };
-
-// Maximum that keeps a NaN (a row or group that holds one gets a NaN scale).
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]);
-template <>
-__device__ __forceinline__ void unpack8<__nv_bfloat16>(const uint4 &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
-template <>
-__device__ __forceinline__ void unpack8<__half>(const uint4 &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack_f16x2(w[i]);
-        f[2 * i] = p.x;
-        f[2 * i + 1] = p.y;
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) { return pack_bf16x2(a, b); }
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) { return pack_f16x2(a, b); }
-
-template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-}
-
-// Eight e4m3 codes of f * inv, saturating (NaN stays NaN).
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float inv) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE,
-                                                    __NV_E4M3);
-        const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv),
-                                                    __NV_SATFINITE, __NV_E4M3);
-        w[i] = a | b << 16;
-    }
-    return make_uint2(w[0], w[1]);
-}
-
-// amax -> the scale of an e4m3 block: 1 for a block of zeros, never below
-// the smallest normal float; NaN stays NaN.
-__device__ __forceinline__ float block_scale(float amax) {
-    return amax == 0.f ? 1.f : max_nan(__fdiv_rn(amax, kE4m3Max), kMinScale);
-}
 
 // Sum (MAX: NaN-keeping maximum) over a row's threads; `warps` of them hold
 // the row, starting at warp `warp0` of the block.  With one warp a row no
