@@ -49,6 +49,7 @@ extern "C" {
 #define MLA_D_LATENT 512 /* latent (value) width                            */
 #define MLA_D_ROPE 64
 #define MLA_D_V 128      /* W_UV output width per head                      */
+#define MLA_D_NOPE 128   /* query columns per head that W_UK takes          */
 #define MLA_MAX_HEADS 128
 #define MLA_MAX_QLEN 16
 #define MLA_MAX_SPLITS 256
@@ -462,6 +463,35 @@ mla_status mla_norm_rope(const void *x, int64_t x_row_stride, int64_t x_head_str
                          int64_t num_positions, int rope_start, int rope_dim, unsigned int flags, int64_t tokens,
                          int heads, int width, int quant, float scale, const int64_t *slots, int64_t out_rows,
                          void *out, int64_t out_row_stride, int64_t out_head_stride, float *out_scales, void *stream);
+
+/*
+ * mla_query_absorb -- the query that mla_decode_attend takes, from the
+ * projection's heads: W_UK absorbed, the position columns rotated.
+ *
+ * For token t < tokens, head h < heads, in float32, rounded once:
+ *   y[c]       = sum_{n < 128} q[t, h, n] * w_uk[h, n, c]          (c < 512)
+ *   y[512 + i] = q[t, h, 128 + i], i < 64, rotated as mla_norm_rope rotates
+ *                (rope_start 128, rope_dim 64) with positions
+ *   out[t, h, :] = bf16(y), or with MLA_ABSORB_OUT_FP8 e4m3(y * (1 / q_scale)),
+ *                  to nearest even, saturating at +-448
+ *
+ *   q            bf16, token t head h at q + t*q_row_stride + h*q_head_stride
+ *                (elements, multiples of 8, at least 192).
+ *   w_uk         bf16 [heads, 128, 512].
+ *   positions, cos_sin, num_positions   as mla_norm_rope (cos_sin [., 64]);
+ *                NULL: no rotation.
+ *   out          token t head h at out + t*out_row_stride + h*576 (elements;
+ *                >= heads*576, a multiple of 8, of 16 for e4m3): the rows of
+ *                a padded query, of which heads 0 .. heads - 1 are written.
+ * heads 1..128, tokens up to 2^31 - 65536, strides up to 2^30; q_scale
+ * (MLA_ABSORB_OUT_FP8 only) finite and >= 2^-126.  q, w_uk, out, cos_sin
+ * 16-byte aligned.  out overlaps no input.
+ */
+#define MLA_ABSORB_PAIRS 1u   /* as MLA_ROPE_PAIRS        */
+#define MLA_ABSORB_OUT_FP8 2u /* out holds e4m3 codes     */
+mla_status mla_query_absorb(const void *q, int64_t q_row_stride, int64_t q_head_stride, const void *w_uk,
+                            const int64_t *positions, const float *cos_sin, int64_t num_positions, unsigned int flags,
+                            int64_t tokens, int heads, float q_scale, void *out, int64_t out_row_stride, void *stream);
 
 /*
  * mla_token_weights -- the attention weight that each cached token received

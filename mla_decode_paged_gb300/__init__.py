@@ -39,7 +39,7 @@ STATIC_SCRATCH_BYTES = 32 << 20   # MLA_STATIC_SCRATCH_BYTES: the partials buffe
 __all__ = ["Prepared", "attend", "merge", "value_gate", "merge_value_gate", "decode_step", "decode_step_static",
            "STATIC_SCRATCH_BYTES", "choose_splits", "plan_units", "debug_gather",
            "debug_wait_timeout", "debug_attend_mma",
-           "kv_append", "norm_rope", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
+           "kv_append", "norm_rope", "query_absorb", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
            "value_gate_lora_workspace", "token_weights_workspace", "device_status", "build", "library", "MlaError"]
 
 
@@ -98,6 +98,7 @@ def library() -> ctypes.CDLL:
     lib.mla_add_rms_norm.argtypes = [vp, i64, i32, vp, i64, i32, vp, f32, i64, i32, i32, f32, vp, i64, vp, vp, i64, vp]
     lib.mla_norm_rope.argtypes = [vp, i64, i64, i32, vp, i32, f32, vp, vp, i64, i32, i32, ctypes.c_uint, i64, i32, i32,
                                   i32, f32, vp, i64, vp, i64, i64, vp, vp]
+    lib.mla_query_absorb.argtypes = [vp, i64, i64, vp, vp, vp, i64, ctypes.c_uint, i64, i32, f32, vp, i64, vp]
     lib.mla_token_weights.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, f32, vp, f32, vp, vp,
                                       ctypes.c_uint, vp, i64, vp]
     lib.mla_token_weights_workspace.argtypes = [i32, i32, i64, ctypes.c_uint]
@@ -106,7 +107,7 @@ def library() -> ctypes.CDLL:
     lib.mla_value_gate_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mla_value_gate_lora_workspace.argtypes = [i32, i32, i32, i32]
     lib.mla_value_gate_lora_workspace.restype = i64
-    for name in ("mla_norm_rope", "mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
+    for name in ("mla_norm_rope", "mla_query_absorb", "mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
                  "mla_decode_attend", "mla_decode_attend_ex", "mla_decode_attend_paged", "mla_decode_attend_planned", "mla_merge_splits", "mla_value_gate", "mla_merge_value_gate", "mla_debug_gather",
                  "mla_device_status", "mla_choose_splits", "mla_kv_append", "mla_debug_wait_timeout",
                  "mla_decode_step_static", "mla_debug_attend_mma"):
@@ -546,6 +547,25 @@ def norm_rope(x, weight=None, eps=1e-6, *, positions=None, cos_sin=None, rope_st
                                           out, out_scales, stream)
     if type(r) is int:
         _check(r, "mla_norm_rope")
+    return r
+
+
+def query_absorb(q, w_uk, *, positions=None, cos_sin=None, interleaved=False, q_scale=None, out=None, stream=None):
+    """The query that :func:`attend` takes (``mla_query_absorb``): returns
+    ``out [S, H, 576]``, its first 512 columns the product of a head's first
+    128 with ``w_uk[h]``, its last 64 the head's last 64, rotated.
+
+    ``q``: bf16 ``[S, H, 192]``, rows and heads may be strided (H up to 128);
+    ``w_uk``: bf16 ``[H, 128, 512]``; ``positions``: int64 ``[S]`` and
+    ``cos_sin``: float32 ``[positions, 64]`` as in :func:`norm_rope`, whose
+    column pairs ``interleaved`` picks (None: no rotation).  ``q_scale``: the
+    output is e4m3 codes that stand for code * q_scale, for
+    ``attend(..., q_scale=q_scale)`` (None: bf16).  ``out``: a tensor of
+    ``[S, H or more, 576]`` whose first H heads are written (a padded query).
+    """
+    r = (_ops_module or _ops()).query_absorb(q, w_uk, positions, cos_sin, interleaved, q_scale, out, stream)
+    if type(r) is int:
+        _check(r, "mla_query_absorb")
     return r
 
 

@@ -58,6 +58,10 @@ cudaError_t norm_rope_launch(const void *x, int64_t x_row, int64_t x_head, int x
                              float scale, const int64_t *slots, int64_t out_rows, void *out, int64_t out_row,
                              int64_t out_head, float *out_scales, int sms, cudaStream_t st);
 cudaError_t norm_rope_status(unsigned int *flags, bool clear);
+cudaError_t query_absorb_launch(const void *q, int64_t q_row, int64_t q_head, const void *w_uk, const int64_t *positions,
+                                const float *cos_sin, int64_t num_positions, bool pairs, int T, int H, float q_scale,
+                                bool fp8, void *out, int64_t out_row, int sms, cudaStream_t st);
+cudaError_t query_absorb_status(unsigned int *flags, bool clear);
 cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                                  const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
                                  int heads, double sc, const float *lse, float decay, const float *weights, float *out,
@@ -751,6 +755,44 @@ mla_status mla_norm_rope(const void *x, int64_t x_row_stride, int64_t x_head_str
     return MLA_OK;
 }
 
+mla_status mla_query_absorb(const void *q, int64_t q_row_stride, int64_t q_head_stride, const void *w_uk,
+                            const int64_t *positions, const float *cos_sin, int64_t num_positions, unsigned int flags,
+                            int64_t tokens, int heads, float q_scale, void *out, int64_t out_row_stride, void *stream) {
+    if (flags & ~(MLA_ABSORB_PAIRS | MLA_ABSORB_OUT_FP8)) return fail(MLA_ERR_INVALID, "unknown flag bits");
+    const bool fp8 = (flags & MLA_ABSORB_OUT_FP8) != 0;
+    if (tokens < 0) return fail(MLA_ERR_INVALID, "negative tokens");
+    if (heads < 1 || heads > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID, "heads outside 1..128");
+    if ((positions == nullptr) != (cos_sin == nullptr)) return fail(MLA_ERR_INVALID, "positions and cos_sin go together");
+    if (positions && (num_positions < 1 || num_positions > (int64_t)1 << 40))
+        return fail(MLA_ERR_INVALID, "num_positions outside 1..2^40");
+    if (fp8 && !(std::isfinite(q_scale) && q_scale >= 1.17549435e-38f))
+        return fail(MLA_ERR_INVALID, "q_scale must be finite and >= 2^-126");
+    const int width = MLA_D_NOPE + MLA_D_ROPE, es = fp8 ? 1 : 2;
+    const auto bad_stride = [&](int64_t s) { return s < width || s % 8 != 0 || s > 1 << 30; };
+    if (bad_stride(q_row_stride) || bad_stride(q_head_stride))
+        return fail(MLA_ERR_INVALID, "q's strides must be multiples of 8 from 192 to 2^30");
+    if (out_row_stride < (int64_t)heads * MLA_D_QK || out_row_stride % (16 / es) != 0 || out_row_stride > 1 << 30)
+        return fail(MLA_ERR_INVALID, fp8 ? "out_row_stride must be >= heads*576, a multiple of 16 (e4m3) and at most 2^30"
+                                         : "out_row_stride must be >= heads*576, a multiple of 8 and at most 2^30");
+    if (tokens > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "tokens above 2^31 - 65536");
+    if (tokens == 0) return MLA_OK;
+    if (!q || !w_uk || !out) return fail(MLA_ERR_INVALID, "null pointer");
+    if (!aligned(q, 16) || !aligned(w_uk, 16) || !aligned(out, 16) || !aligned(cos_sin, 16) || !aligned(positions, 8))
+        return fail(MLA_ERR_INVALID, "misaligned pointer (q, w_uk, out, cos_sin need 16 bytes)");
+    const Heads hq = {q, q_row_stride, q_head_stride, tokens, heads, width, 2};
+    const Heads ho = {out, out_row_stride, MLA_D_QK, tokens, heads, MLA_D_QK, es};
+    const Span in[3] = {{w_uk, (int64_t)heads * MLA_D_NOPE * MLA_D_LATENT * 2}, {positions, tokens * 8},
+                        {cos_sin, num_positions * MLA_D_ROPE * 4}};
+    if (overlap_heads(ho, hq) || overlaps({out, ho.whole()}, in)) return fail(MLA_ERR_INVALID, "out overlaps an input");
+    const int sms = device_sms();
+    if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = mla::query_absorb_launch(q, q_row_stride, q_head_stride, w_uk, positions, cos_sin, num_positions,
+                                             (flags & MLA_ABSORB_PAIRS) != 0, (int)tokens, heads, q_scale, fp8, out,
+                                             out_row_stride, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "query_absorb launch");
+    return MLA_OK;
+}
+
 mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                              const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
                              int qlen, int heads, float scale, float kv_scale, float q_scale, const float *lse,
@@ -921,7 +963,7 @@ mla_status mla_device_status(void *stream, unsigned int *flags) {
                                                       mla::value_gate_status, mla::gather_status,
                                                       mla::kv_append_status, mla::norm_status,
                                                       mla::token_weights_status, mla::evict_status, mla::value_lora_status,
-                                                      mla::norm_rope_status};
+                                                      mla::norm_rope_status, mla::query_absorb_status};
     for (auto rd : readers) {
         unsigned int f = 0;
         e = rd(&f, true);

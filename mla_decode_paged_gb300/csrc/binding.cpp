@@ -1,5 +1,5 @@
 // Python module of the calls whose kernels take a few microseconds
-// (add_rms_norm, token_weights, kv_evict, value_gate_lora, norm_rope): argument checks,
+// (add_rms_norm, token_weights, kv_evict, value_gate_lora, norm_rope, query_absorb): argument checks,
 // output allocation and the call into the C ABI, without the Python
 // interpreter in between.  On the Grace host a call takes 2.3 us of it with
 // its outputs given and 1.3 more for each that it allocates (2.0 through
@@ -327,6 +327,50 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (q, w_uk, positions, cos_sin, pairs, q_scale, out, stream)
+PyObject *query_absorb(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject * {
+        constexpr int64_t kWidth = MLA_D_NOPE + MLA_D_ROPE;
+        const at::Tensor &q = tensor(a[0], "q");
+        const int64_t dev = q.get_device();
+        if (q.scalar_type() != at::kBFloat16 || q.dim() != 3 || q.size(2) != kWidth) refuse("q must be bf16 [S, H, 192]");
+        const HeadRows hq = heads_of(q, "q", dev);
+        const int64_t S = hq.rows, H = hq.heads;
+        if (H > MLA_MAX_HEADS) refuse("q must have at most 128 heads");
+        const at::Tensor &w = dense(tensor(a[1], "w_uk"), "w_uk", at::kBFloat16, {H, MLA_D_NOPE, MLA_D_LATENT}, dev);
+        if ((a[2] != Py_None) != (a[3] != Py_None)) refuse("positions and cos_sin go together");
+        const int64_t *positions = nullptr;
+        const float *table = nullptr;
+        int64_t table_rows = 0;
+        if (a[2] != Py_None) {
+            positions = ptr<int64_t>(dense(tensor(a[2], "positions"), "positions", at::kLong, {S}, dev));
+            const at::Tensor &cs = tensor(a[3], "cos_sin");
+            table_rows = cs.dim() == 2 ? cs.size(0) : -1;
+            table = ptr<float>(dense(cs, "cos_sin", at::kFloat, {table_rows, MLA_D_ROPE}, dev));
+        }
+        const int pairs = PyObject_IsTrue(a[4]);
+        if (pairs < 0) return nullptr;
+        const bool fp8 = a[5] != Py_None;
+        const float q_scale = fp8 ? real(a[5], "q_scale") : 1.f;
+        const Place at(dev, a[7]);
+        ScalarType otype = fp8 ? kE4m3 : at::kBFloat16;
+        if (fp8 && a[6] != Py_None && tensor(a[6], "out").scalar_type() == at::kByte) otype = at::kByte;
+        int64_t out_row = H * MLA_D_QK;
+        const at::Tensor out = output(a[6], "out", at, {S, H, MLA_D_QK}, otype, [&](const at::Tensor &t) {
+            const HeadRows ho = heads_of(t, "out", dev);
+            if (t.scalar_type() != otype || t.dim() != 3 || ho.rows != S || ho.heads < H || ho.width != MLA_D_QK ||
+                ho.head != MLA_D_QK)
+                refuse(std::string("out must be ") + at::toString(otype) + " [S, H or more, 576] with contiguous rows of heads");
+            if (ho.rows > 1) out_row = ho.row;
+        });
+        const mla_status st = mla_query_absorb(ptr(q), hq.row, hq.head, ptr(w), positions, table, table_rows,
+                                               (pairs ? MLA_ABSORB_PAIRS : 0u) | (fp8 ? MLA_ABSORB_OUT_FP8 : 0u), S, (int)H,
+                                               q_scale, ptr(out), out_row, at.stream);
+        if (st != MLA_OK) return PyLong_FromLong(st);
+        return wrap(out);
+    });
+}
+
 // (q, kv, pages, indptr, scale, kv_scale, lse, heads, qlen, weights, decay, causal, q_scale, out, workspace, stream)
 PyObject *token_weights(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 16, [&]() -> PyObject * {
@@ -432,7 +476,8 @@ PyObject *value_gate_lora(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 #define MLA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MLA_METHOD(add_rms_norm), MLA_METHOD(token_weights), MLA_METHOD(kv_evict),
-                         MLA_METHOD(value_gate_lora), MLA_METHOD(norm_rope), {nullptr, nullptr, 0, nullptr}};
+                         MLA_METHOD(value_gate_lora), MLA_METHOD(norm_rope),
+                         MLA_METHOD(query_absorb), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "mla_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
