@@ -50,6 +50,7 @@ extern "C" {
 #define MLA_D_ROPE 64
 #define MLA_D_V 128      /* W_UV output width per head                      */
 #define MLA_D_NOPE 128   /* query columns per head that W_UK takes          */
+#define MLA_D_INDEX 128  /* index query / key width                          */
 #define MLA_MAX_HEADS 128
 #define MLA_MAX_QLEN 16
 #define MLA_MAX_SPLITS 256
@@ -535,6 +536,37 @@ mla_status mla_token_weights(const void *q, int64_t q_row_stride, const void *kv
 /* Bytes of workspace that mla_token_weights needs (0 up to 64 query rows a
  * request, 128 of an fp8 query); a negative mla_status on bad sizes. */
 int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsigned int flags);
+
+/*
+ * mla_index_scores -- a cheap score of every cached token for every query
+ * row, from an index cache of 128 bytes a token beside the latent cache:
+ * what a sparse attention picks the tokens it attends over by.
+ *
+ * For request r, its token j (entry i = indptr[r] + j of pages), its query
+ * row tq < qlen (t = r * qlen + tq) and K_j = e4m3fn(k[pages[i]]):
+ *   out[tq * num_pages + i] = scale * sum_{h < heads} weights[t, h] * q_scales[t, h]
+ *                                                     * max(0, <e4m3fn(q[t, h, :]), K_j>)
+ * in float32 (NaN stays NaN), or -inf with MLA_ATTEND_CAUSAL where row tq does
+ * not see the token (it sees the first L_r - qlen + tq + 1).  Every request's
+ * entries are written, others are left as they were.  The sum has a fixed
+ * order: equal inputs give equal bits.
+ *
+ *   q            e4m3 codes [num_requests * qlen, heads, 128].
+ *   weights      f32 [num_requests * qlen, heads]; q_scales likewise, or NULL: 1.
+ *   k            e4m3 codes [pool_rows, 128]; its scale, if it has one, goes
+ *                into `scale`.
+ *   pages, num_pages, indptr, num_requests, qlen   as mla_decode_attend.
+ *   out          f32 [qlen, num_pages] (written); overlaps no input.
+ * heads 1..128; scale finite; num_pages up to 2^31 - 65536, num_requests up
+ * to 2^24, num_requests * qlen * heads up to 2^31 - 1.  q and k 16-byte
+ * aligned.  A page outside the pool reads as row 0 and sets MLA_DEV_BAD_PAGE;
+ * a bad indptr entry sets MLA_DEV_BAD_INDPTR and leaves its request's entries
+ * as they were.
+ */
+mla_status mla_index_scores(const void *q, const float *weights, const float *q_scales, const void *k,
+                            int64_t pool_rows, const int32_t *pages, int64_t num_pages, const int32_t *indptr,
+                            int num_requests, int qlen, int heads, float scale, float *out, unsigned int flags,
+                            void *stream);
 
 /*
  * mla_kv_evict -- cut every request's page list to a budget, by weight.

@@ -39,7 +39,7 @@ STATIC_SCRATCH_BYTES = 32 << 20   # MLA_STATIC_SCRATCH_BYTES: the partials buffe
 __all__ = ["Prepared", "attend", "merge", "value_gate", "merge_value_gate", "decode_step", "decode_step_static",
            "STATIC_SCRATCH_BYTES", "choose_splits", "plan_units", "debug_gather",
            "debug_wait_timeout", "debug_attend_mma",
-           "kv_append", "norm_rope", "query_absorb", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
+           "kv_append", "norm_rope", "query_absorb", "index_scores", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
            "value_gate_lora_workspace", "token_weights_workspace", "device_status", "build", "library", "MlaError"]
 
 
@@ -99,6 +99,7 @@ def library() -> ctypes.CDLL:
     lib.mla_norm_rope.argtypes = [vp, i64, i64, i32, vp, i32, f32, vp, vp, i64, i32, i32, ctypes.c_uint, i64, i32, i32,
                                   i32, f32, vp, i64, vp, i64, i64, vp, vp]
     lib.mla_query_absorb.argtypes = [vp, i64, i64, vp, vp, vp, i64, ctypes.c_uint, i64, i32, f32, vp, i64, vp]
+    lib.mla_index_scores.argtypes = [vp, vp, vp, vp, i64, vp, i64, vp, i32, i32, i32, f32, vp, ctypes.c_uint, vp]
     lib.mla_token_weights.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, f32, vp, f32, vp, vp,
                                       ctypes.c_uint, vp, i64, vp]
     lib.mla_token_weights_workspace.argtypes = [i32, i32, i64, ctypes.c_uint]
@@ -107,7 +108,7 @@ def library() -> ctypes.CDLL:
     lib.mla_value_gate_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mla_value_gate_lora_workspace.argtypes = [i32, i32, i32, i32]
     lib.mla_value_gate_lora_workspace.restype = i64
-    for name in ("mla_norm_rope", "mla_query_absorb", "mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
+    for name in ("mla_norm_rope", "mla_query_absorb", "mla_index_scores", "mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
                  "mla_decode_attend", "mla_decode_attend_ex", "mla_decode_attend_paged", "mla_decode_attend_planned", "mla_merge_splits", "mla_value_gate", "mla_merge_value_gate", "mla_debug_gather",
                  "mla_device_status", "mla_choose_splits", "mla_kv_append", "mla_debug_wait_timeout",
                  "mla_decode_step_static", "mla_debug_attend_mma"):
@@ -600,6 +601,29 @@ def token_weights_workspace(qlen, heads, num_pages, fp8_query=False):
     if n < 0:
         _check(int(n), "mla_token_weights_workspace")
     return n
+
+
+def index_scores(q, weights, k, pages, indptr, *, q_scales=None, scale=1.0, qlen=1, causal=False, out=None,
+                 stream=None):
+    """A cheap score of every cached token for every query row
+    (``mla_index_scores``): returns ``out`` float32 ``[qlen, len(pages)]``,
+    ``out[tq, i] = scale * sum_h weights[t, h] * q_scales[t, h] *
+    max(0, <q[t, h], k[pages[i]]>)`` for the tokens i of row t's request,
+    -inf with ``causal`` where row tq does not see the token.
+
+    ``q``: e4m3 codes (float8_e4m3fn or uint8) ``[S, H, 128]``, H up to 128,
+    S = (len(indptr) - 1) * qlen; ``weights`` and ``q_scales`` (None: ones):
+    float32 ``[S, H]`` (both from :func:`norm_rope` with ``quant="head"`` and
+    a projection); ``k``: e4m3 codes ``[pool, 128]``, the index cache
+    (:func:`norm_rope` with ``slots`` writes it; its static scale goes into
+    ``scale``); ``pages`` and ``indptr`` as in :func:`attend`.  Entries that
+    belong to no request are left as they were (a new ``out`` holds nothing
+    there).
+    """
+    r = (_ops_module or _ops()).index_scores(q, weights, k, pages, indptr, q_scales, scale, qlen, causal, out, stream)
+    if type(r) is int:
+        _check(r, "mla_index_scores")
+    return r
 
 
 def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=None, indptr_out=None, weights_out=None,

@@ -62,6 +62,10 @@ cudaError_t query_absorb_launch(const void *q, int64_t q_row, int64_t q_head, co
                                 const float *cos_sin, int64_t num_positions, bool pairs, int T, int H, float q_scale,
                                 bool fp8, void *out, int64_t out_row, int sms, cudaStream_t st);
 cudaError_t query_absorb_status(unsigned int *flags, bool clear);
+cudaError_t index_scores_launch(const void *q, const float *weights, const float *q_scales, const void *k,
+                                int64_t pool_rows, const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R,
+                                int qlen, int heads, float scale, float *out, bool causal, int sms, cudaStream_t st);
+cudaError_t index_scores_status(unsigned int *flags, bool clear);
 cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                                  const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
                                  int heads, double sc, const float *lse, float decay, const float *weights, float *out,
@@ -852,6 +856,39 @@ int64_t mla_token_weights_workspace(int qlen, int heads, int64_t num_pages, unsi
     return mla::token_weights_workspace(qlen * heads, (flags & MLA_ATTEND_Q_FP8) != 0, num_pages);
 }
 
+mla_status mla_index_scores(const void *q, const float *weights, const float *q_scales, const void *k,
+                            int64_t pool_rows, const int32_t *pages, int64_t num_pages, const int32_t *indptr,
+                            int num_requests, int qlen, int heads, float scale, float *out, unsigned int flags,
+                            void *stream) {
+    if (flags & ~MLA_ATTEND_CAUSAL) return fail(MLA_ERR_INVALID, "unknown flag bits");
+    if (num_requests < 0 || pool_rows < 0 || num_pages < 0)
+        return fail(MLA_ERR_INVALID, "negative num_requests / pool_rows / num_pages");
+    if (qlen < 1 || qlen > MLA_MAX_QLEN) return fail(MLA_ERR_INVALID, "qlen outside 1..16");
+    if (heads < 1 || heads > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID, "heads outside 1..128");
+    if (!std::isfinite(scale)) return fail(MLA_ERR_INVALID, "non-finite scale");
+    if (num_requests == 0 || num_pages == 0) return MLA_OK;
+    if (!q || !weights || !k || !pages || !indptr || !out) return fail(MLA_ERR_INVALID, "null pointer");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(weights, 4) || !aligned(q_scales, 4) || !aligned(pages, 4) ||
+        !aligned(indptr, 4) || !aligned(out, 4))
+        return fail(MLA_ERR_INVALID, "misaligned pointer (q, k need 16 bytes)");
+    if (pool_rows == 0) return fail(MLA_ERR_INVALID, "empty index pool");
+    if (pool_rows > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "pool_rows above 2^31 - 1");
+    if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 65536");
+    if (num_requests > kMaxRequests) return fail(MLA_ERR_UNSUPPORTED, "num_requests above 2^24");
+    const int64_t rows = (int64_t)num_requests * qlen * heads;
+    if (rows > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "num_requests * qlen * heads above 2^31 - 1");
+    const Span in[6] = {{q, rows * MLA_D_INDEX}, {weights, rows * 4}, {q_scales, rows * 4}, {k, pool_rows * MLA_D_INDEX},
+                        {pages, num_pages * 4}, {indptr, ((int64_t)num_requests + 1) * 4}};
+    if (overlaps({out, num_pages * qlen * 4}, in)) return fail(MLA_ERR_INVALID, "out overlaps an input");
+    const int sms = device_sms();
+    if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = mla::index_scores_launch(q, weights, q_scales, k, pool_rows, pages, num_pages, indptr, num_requests,
+                                             qlen, heads, scale, out, (flags & MLA_ATTEND_CAUSAL) != 0, sms,
+                                             static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "index_scores launch");
+    return MLA_OK;
+}
+
 mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
                         const float *weights, const int32_t *budgets, int budget, int recent, int sinks,
                         int32_t *pages_out, int32_t *indptr_out, float *weights_out, void *stream) {
@@ -963,7 +1000,8 @@ mla_status mla_device_status(void *stream, unsigned int *flags) {
                                                       mla::value_gate_status, mla::gather_status,
                                                       mla::kv_append_status, mla::norm_status,
                                                       mla::token_weights_status, mla::evict_status, mla::value_lora_status,
-                                                      mla::norm_rope_status, mla::query_absorb_status};
+                                                      mla::norm_rope_status, mla::query_absorb_status,
+                                                      mla::index_scores_status};
     for (auto rd : readers) {
         unsigned int f = 0;
         e = rd(&f, true);

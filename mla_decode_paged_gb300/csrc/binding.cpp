@@ -1,5 +1,5 @@
 // Python module of the calls whose kernels take a few microseconds
-// (add_rms_norm, token_weights, kv_evict, value_gate_lora, norm_rope, query_absorb): argument checks,
+// (add_rms_norm, token_weights, kv_evict, value_gate_lora, norm_rope, query_absorb, index_scores): argument checks,
 // output allocation and the call into the C ABI, without the Python
 // interpreter in between.  On the Grace host a call takes 2.3 us of it with
 // its outputs given and 1.3 more for each that it allocates (2.0 through
@@ -414,6 +414,38 @@ PyObject *token_weights(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (q, weights, k, pages, indptr, q_scales, scale, qlen, causal, out, stream)
+PyObject *index_scores(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject * {
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[2], "k"), &pages = tensor(a[3], "pages"),
+                         &indptr = tensor(a[4], "indptr");
+        const int64_t dev = q.get_device();
+        if ((q.scalar_type() != kE4m3 && q.scalar_type() != at::kByte) || q.dim() != 3) refuse("q must be e4m3 codes [S, H, 128]");
+        const int64_t S = q.size(0), H = q.size(1), R = indptr.numel() - 1, pages_n = pages.numel();
+        dense(q, "q", q.scalar_type(), {S, H, MLA_D_INDEX}, dev);
+        const at::Tensor &w = dense(tensor(a[1], "weights"), "weights", at::kFloat, {S, H}, dev);
+        if (k.scalar_type() != kE4m3 && k.scalar_type() != at::kByte) refuse("k must be e4m3 codes [pool, 128]");
+        const int64_t pool = k.dim() == 2 ? k.size(0) : -1;
+        dense(k, "k", k.scalar_type(), {pool, MLA_D_INDEX}, dev);
+        dense(pages, "pages", at::kInt, {pages_n}, dev);
+        const float *q_scales = nullptr;
+        if (a[5] != Py_None) q_scales = ptr<float>(dense(tensor(a[5], "q_scales"), "q_scales", at::kFloat, {S, H}, dev));
+        const float scale = real(a[6], "scale");
+        const int qlen = int32(a[7], "qlen");
+        if (R < 0 || R > INT32_MAX || S != R * qlen || H > INT32_MAX) refuse("q's rows do not match indptr / qlen");
+        dense(indptr, "indptr", at::kInt, {R + 1}, dev);
+        const int causal = PyObject_IsTrue(a[8]);
+        if (causal < 0) return nullptr;
+        const Place at(dev, a[10]);
+        const at::Tensor out = dense_output(a[9], "out", at, {qlen < 0 ? 0 : qlen, pages_n}, at::kFloat);
+        const mla_status st = mla_index_scores(ptr(q), ptr<float>(w), q_scales, ptr(k), pool, ptr<int32_t>(pages), pages_n,
+                                               ptr<int32_t>(indptr), (int)R, qlen, (int)H, scale, ptr<float>(out),
+                                               causal ? MLA_ATTEND_CAUSAL : 0u, at.stream);
+        if (st != MLA_OK) return PyLong_FromLong(st);
+        return wrap(out);
+    });
+}
+
 // (pages, indptr, weights, budget, recent, sinks, pages_out, indptr_out, weights_out, stream)
 PyObject *kv_evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 10, [&]() -> PyObject * {
@@ -477,7 +509,7 @@ PyObject *value_gate_lora(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define MLA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MLA_METHOD(add_rms_norm), MLA_METHOD(token_weights), MLA_METHOD(kv_evict),
                          MLA_METHOD(value_gate_lora), MLA_METHOD(norm_rope),
-                         MLA_METHOD(query_absorb), {nullptr, nullptr, 0, nullptr}};
+                         MLA_METHOD(query_absorb), MLA_METHOD(index_scores), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "mla_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -56,6 +56,7 @@
 
 #include "common.cuh"
 #include "tc.cuh"
+#include "tile_walk.cuh"
 
 namespace mla {
 namespace {
@@ -113,110 +114,6 @@ struct Misc {
     int start[3];               // this CTA's first request, its first tile there, tiles in all
 };
 
-// A CTA's (a pair's) tiles of TOKENS in order; every role, a whole warp, walks
-// them on its own (uniform loads).
-template <int TOKENS>
-struct Walk {
-    int r, t, ntiles, len, base, left, unit;
-    bool first;     // the tile is its unit's first in this CTA
-
-    template <class C>
-    __device__ void init(const TokenArgs &a, const Misc<C> &ms) {
-        r = ms.start[0];
-        t = ms.start[1];
-        left = ms.start[2];
-        unit = 0;
-        first = true;
-        if (left > 0) open(a);
-    }
-    __device__ void open(const TokenArgs &a) {
-        len = request_len(a.indptr, r, a.num_pages, &base);
-        ntiles = (len + TOKENS - 1) / TOKENS;
-    }
-    __device__ bool valid() const { return left > 0; }
-    __device__ bool last() const { return left == 1 || t + 1 == ntiles; }
-    __device__ void next(const TokenArgs &a) {
-        --left;
-        first = false;
-        if (++t < ntiles || left <= 0) return;
-        t = 0;
-        first = true;
-        ++unit;
-        ++r;        // at least one more tile is to come, so a request with tokens follows
-        open(a);
-        // Empty requests are passed over 32 at a time: one by one 2^24 of them
-        // took 3.5 s, more than the roles wait for each other.
-        while (ntiles == 0 && r + 1 < a.R) {
-            const int mine = r + 1 + (threadIdx.x & 31);
-            int b = 0;
-            const int n = mine < a.R ? request_len(a.indptr, mine, a.num_pages, &b) : 0;
-            const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
-            if (some == 0) {
-                r = min(r + 32, a.R - 1);
-                continue;
-            }
-            const int src = __ffs(some) - 1;
-            r += 1 + src;
-            len = __shfl_sync(0xffffffffu, n, src);
-            base = __shfl_sync(0xffffffffu, b, src);
-            ntiles = (len + TOKENS - 1) / TOKENS;
-        }
-    }
-};
-
-// This CTA's range of the batch's tiles -> ms.start.  Requests that share
-// entries (a bad indptr only) count up to what the page list could hold.
-template <class C>
-__device__ void find_start(const TokenArgs &a, Misc<C> &ms, int v) {
-    __shared__ long long part[kThreads / 32 + 1];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const auto tiles_of = [&](int r) {
-        int base;
-        return (request_len(a.indptr, r, a.num_pages, &base) + C::Tokens - 1) / C::Tokens;
-    };
-    int mine = 0;
-    long long sum = 0;
-    for (int r = tid; r < a.R; r += kThreads) {
-        const int n = tiles_of(r);
-        if (r == tid) mine = n;
-        sum += n;
-    }
-    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) part[warp] = sum;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) total += part[w];
-    total = min(total, (long long)(a.num_pages / C::Tokens + a.R));
-    const int64_t lo = total * v / a.virt, hi = total * (v + 1) / a.virt;
-    if (tid == 0) ms.start[2] = (int)(hi - lo);
-    int64_t before = 0;   // tiles of the requests before this chunk
-    for (int r0 = 0; r0 < a.R && before <= lo; r0 += kThreads) {
-        const int r = r0 + tid;
-        const int n = r0 == 0 ? mine : r < a.R ? tiles_of(r) : 0;
-        int incl = n;
-        for (int d = 1; d < 32; d <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += x;
-        }
-        __syncthreads();
-        if (lane == 31) part[warp] = incl;
-        __syncthreads();
-        int64_t at = before;
-        int64_t all = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) at += part[w];
-            all += part[w];
-        }
-        at += incl - n;
-        if (n > 0 && at <= lo && lo < at + n) {
-            ms.start[0] = r;
-            ms.start[1] = (int)(lo - at);
-        }
-        before += all;
-    }
-    __syncthreads();
-}
-
 // ------------------------------------------------------------------ producers
 
 // The place of `p` in the shared memory of the pair's block `rank`.
@@ -249,7 +146,7 @@ __device__ void producer(const TokenArgs &a, const CUtensorMap *mlat, const CUte
                          Misc<C> &ms, int rank) {
     const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kProdWarp0;
     Walk<C::Tokens> w;
-    w.init(a, ms);
+    w.init(a, ms.start);
     const uint64_t pol = tc::l2_policy(true);   // the rows stream through L2; the query and the outputs stay
     // The page indices of this lane's four tokens; how many of them the request has.
     const auto load = [&](int (&rows)[4]) {
@@ -423,7 +320,7 @@ __device__ void mma_issuer(const TokenArgs &a, uint8_t *sm, Misc<Cfg<NP, TERMS, 
     const uint64_t q0 = tc::sdesc(base + kOffQ, 16, 1024, tc::kSw128);
     const uint64_t qr0 = tc::sdesc(base + kOffQ + C::QRope, 16, 512, tc::kSw64);
     Walk<C::Tokens> w;
-    w.init(a, ms);
+    w.init(a, ms.start);
     if (PAIR && rank > 0) return;
     for (int it = 0; w.valid(); ++it, w.next(a)) {
         const int s = it % kStages, d = it & 1;
@@ -650,7 +547,7 @@ __device__ void epilogue(const TokenArgs &a, Misc<Cfg<NP, TERMS, PAIR>> &ms, int
     const uint32_t taddr = ms.tmem + wg * C::N + ((uint32_t)(32 * wq) << 16);
     float *out = a.out + (int64_t)grp * a.group_stride;
     Walk<C::Tokens> w;
-    w.init(a, ms);
+    w.init(a, ms.start);
     for (int it = 0; w.valid(); ++it, w.next(a)) {
         if ((it & 1) != wg) continue;
         const int j0 = w.t * C::Tokens + rank * kTile, j = j0 + 32 * wq + lane, buf = w.unit % kConstBufs;
@@ -730,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();
     sync_all<PAIR>();
     tc::fence_after();
-    find_start<C>(a, ms, unit / a.groups);
+    find_start<C::Tokens, kThreads>(a, ms.start, unit / a.groups);
     if (warp < kEpiWarps) {
         epilogue<NP, TERMS, PAIR>(a, ms, grp, rank);
     } else if (warp == kMmaWarp) {
@@ -739,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         producer<C, PAIR>(a, &mlat, &mrope, sm, ms, rank);
     } else {
         Walk<C::Tokens> w;
-        w.init(a, ms);
+        w.init(a, ms.start);
         int tiles = 0;      // of the request before this one, here
         for (; w.valid(); w.next(a), ++tiles) {
             if (!w.first) continue;
