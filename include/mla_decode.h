@@ -569,6 +569,47 @@ mla_status mla_index_scores(const void *q, const float *weights, const float *q_
                             void *stream);
 
 /*
+ * mla_index_select -- the tokens that each query row attends to: the blocks
+ * of best score, as a page list a row.
+ *
+ * Row b = r * qlen + tq sees the first n tokens of request r: L_r, or with
+ * MLA_ATTEND_CAUSAL max(0, L_r - qlen + tq + 1).  Of its nb = ceil(n / block)
+ * blocks of `block` tokens it keeps k = min(nb, topk): its last
+ * min(recent, k); its first min(sinks, k - those); and of the blocks in
+ * between those with the largest scores until k are kept, a block's score
+ * the largest of its tokens' scores[tq * num_pages + indptr[r] + j] (NaN
+ * counts as -inf, -0 equals +0, equal blocks by the lower position).  With
+ * K = indptr_out[num_requests * qlen]:
+ *   indptr_out[b]              tokens kept by the rows before b, from 0
+ *   pages_out[0 .. K)          the kept blocks' entries of pages, row by row, in order
+ *   pages_out[K .. capacity)   -1
+ * which mla_decode_attend takes as num_requests * qlen requests of one query
+ * row.  How many tokens a row keeps does not depend on its scores.
+ *
+ *   scores       f32 [qlen, num_pages], from mla_index_scores; entries that a
+ *                row does not see are not read.
+ *   pages        int32 [num_pages]; indptr int32 [num_requests + 1].
+ *   topk, recent, sinks   >= 0, in blocks; block a power of two, 1..256, and
+ *                recent >= 1 with blocks of more than one token (a row's last
+ *                block may be cut short).
+ *   pages_out    int32 [capacity], capacity at least
+ *                mla_index_select_capacity(); indptr_out int32
+ *                [num_requests * qlen + 1]; no output overlaps an input or
+ *                the other.
+ * num_pages, capacity up to 2^31 - 65536, num_requests * qlen up to 2^24.  A
+ * bad indptr entry sets MLA_DEV_BAD_INDPTR and its request is empty.
+ */
+mla_status mla_index_select(const float *scores, const int32_t *pages, int64_t num_pages, const int32_t *indptr,
+                            int num_requests, int qlen, int topk, int block, int recent, int sinks,
+                            unsigned int flags, int32_t *pages_out, int64_t capacity, int32_t *indptr_out,
+                            void *stream);
+
+/* Entries that mla_index_select may keep: a row at most topk * block of them
+ * and no more than num_pages, all rows of a request together at most qlen
+ * times its own; a negative mla_status on bad sizes. */
+int64_t mla_index_select_capacity(int num_requests, int qlen, int64_t num_pages, int topk, int block);
+
+/*
  * mla_kv_evict -- cut every request's page list to a budget, by weight.
  *
  * Request r of L tokens keeps n = min(L, max(budget, 0)) of them:

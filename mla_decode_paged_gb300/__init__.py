@@ -39,8 +39,9 @@ STATIC_SCRATCH_BYTES = 32 << 20   # MLA_STATIC_SCRATCH_BYTES: the partials buffe
 __all__ = ["Prepared", "attend", "merge", "value_gate", "merge_value_gate", "decode_step", "decode_step_static",
            "STATIC_SCRATCH_BYTES", "choose_splits", "plan_units", "debug_gather",
            "debug_wait_timeout", "debug_attend_mma",
-           "kv_append", "norm_rope", "query_absorb", "index_scores", "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora",
-           "value_gate_lora_workspace", "token_weights_workspace", "device_status", "build", "library", "MlaError"]
+           "kv_append", "norm_rope", "query_absorb", "index_scores", "index_select", "index_select_capacity",
+           "add_rms_norm", "token_weights", "kv_evict", "value_gate_lora", "value_gate_lora_workspace",
+           "token_weights_workspace", "device_status", "build", "library", "MlaError"]
 
 
 class MlaError(RuntimeError):
@@ -100,6 +101,9 @@ def library() -> ctypes.CDLL:
                                   i32, f32, vp, i64, vp, i64, i64, vp, vp]
     lib.mla_query_absorb.argtypes = [vp, i64, i64, vp, vp, vp, i64, ctypes.c_uint, i64, i32, f32, vp, i64, vp]
     lib.mla_index_scores.argtypes = [vp, vp, vp, vp, i64, vp, i64, vp, i32, i32, i32, f32, vp, ctypes.c_uint, vp]
+    lib.mla_index_select.argtypes = [vp, vp, i64, vp, i32, i32, i32, i32, i32, i32, ctypes.c_uint, vp, i64, vp, vp]
+    lib.mla_index_select_capacity.argtypes = [i32, i32, i64, i32, i32]
+    lib.mla_index_select_capacity.restype = i64
     lib.mla_token_weights.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, f32, vp, f32, vp, vp,
                                       ctypes.c_uint, vp, i64, vp]
     lib.mla_token_weights_workspace.argtypes = [i32, i32, i64, ctypes.c_uint]
@@ -108,7 +112,7 @@ def library() -> ctypes.CDLL:
     lib.mla_value_gate_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mla_value_gate_lora_workspace.argtypes = [i32, i32, i32, i32]
     lib.mla_value_gate_lora_workspace.restype = i64
-    for name in ("mla_norm_rope", "mla_query_absorb", "mla_index_scores", "mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
+    for name in ("mla_norm_rope", "mla_query_absorb", "mla_index_scores", "mla_index_select", "mla_add_rms_norm", "mla_token_weights", "mla_kv_evict", "mla_value_gate_lora",
                  "mla_decode_attend", "mla_decode_attend_ex", "mla_decode_attend_paged", "mla_decode_attend_planned", "mla_merge_splits", "mla_value_gate", "mla_merge_value_gate", "mla_debug_gather",
                  "mla_device_status", "mla_choose_splits", "mla_kv_append", "mla_debug_wait_timeout",
                  "mla_decode_step_static", "mla_debug_attend_mma"):
@@ -624,6 +628,38 @@ def index_scores(q, weights, k, pages, indptr, *, q_scales=None, scale=1.0, qlen
     if type(r) is int:
         _check(r, "mla_index_scores")
     return r
+
+
+def index_select(scores, pages, indptr, topk, *, block=1, recent=0, sinks=0, causal=False, pages_out=None,
+                 indptr_out=None, stream=None):
+    """The tokens that each query row attends to (``mla_index_select``):
+    returns ``(pages_out, indptr_out)``, a page list a query row.
+
+    ``scores``: float32 ``[qlen, len(pages)]`` from :func:`index_scores`;
+    ``pages`` / ``indptr``: the requests' lists.  A row's tokens (with
+    ``causal`` those it sees) in blocks of ``block`` (a power of two up to
+    256): its last ``recent`` blocks, its first ``sinks`` and, between them,
+    those of largest maximal score, ``topk`` blocks in all (equal ones by the
+    lower position); ``recent`` is at least 1 with ``block`` > 1.
+    ``indptr_out`` int32 ``[R * qlen + 1]`` and ``pages_out`` (at least
+    :func:`index_select_capacity` entries, -1 behind the last list) go to
+    :func:`attend` with ``qlen=1``: every query row a request of its own,
+    whose length, min(tokens, topk * block) for blocks of one token, does not
+    depend on the scores.
+    """
+    r = (_ops_module or _ops()).index_select(scores, pages, indptr, topk, block, recent, sinks, causal, pages_out,
+                                             indptr_out, stream)
+    if type(r) is int:
+        _check(r, "mla_index_select")
+    return r
+
+
+def index_select_capacity(requests, qlen, num_pages, topk, block=1):
+    """Entries of ``pages_out`` that :func:`index_select` needs."""
+    n = library().mla_index_select_capacity(requests, qlen, num_pages, topk, block)
+    if n < 0:
+        _check(int(n), "mla_index_select_capacity")
+    return n
 
 
 def kv_evict(pages, indptr, weights, budget, *, recent=0, sinks=0, pages_out=None, indptr_out=None, weights_out=None,

@@ -66,6 +66,10 @@ cudaError_t index_scores_launch(const void *q, const float *weights, const float
                                 int64_t pool_rows, const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R,
                                 int qlen, int heads, float scale, float *out, bool causal, int sms, cudaStream_t st);
 cudaError_t index_scores_status(unsigned int *flags, bool clear);
+cudaError_t index_select_launch(const float *scores, const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R,
+                                int qlen, int topk, int block, int recent, int sinks, bool causal, int32_t *pages_out,
+                                int64_t capacity, int32_t *indptr_out, int sms, cudaStream_t st);
+cudaError_t index_select_status(unsigned int *flags, bool clear);
 cudaError_t token_weights_launch(const void *q, int64_t q_row_stride, const void *kv, int64_t pool_rows,
                                  const int32_t *pages, int64_t num_pages, const int32_t *indptr, int R, int qlen,
                                  int heads, double sc, const float *lse, float decay, const float *weights, float *out,
@@ -889,6 +893,53 @@ mla_status mla_index_scores(const void *q, const float *weights, const float *q_
     return MLA_OK;
 }
 
+namespace {
+const char *bad_select_sizes(int num_requests, int qlen, int64_t num_pages, int topk, int block) {
+    if (num_requests < 0 || num_pages < 0) return "negative num_requests / num_pages";
+    if (qlen < 1 || qlen > MLA_MAX_QLEN) return "qlen outside 1..16";
+    if (topk < 0) return "negative topk";
+    if (block < 1 || block > 256 || (block & (block - 1)) != 0) return "block must be a power of two in 1..256";
+    return nullptr;
+}
+}  // namespace
+
+int64_t mla_index_select_capacity(int num_requests, int qlen, int64_t num_pages, int topk, int block) {
+    if (const char *why = bad_select_sizes(num_requests, qlen, num_pages, topk, block)) return fail(MLA_ERR_INVALID, why);
+    if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages above 2^31 - 65536");
+    const int64_t rows = (int64_t)num_requests * qlen;
+    if (rows > kMaxRequests) return fail(MLA_ERR_UNSUPPORTED, "num_requests * qlen above 2^24");
+    return std::min(rows * std::min((int64_t)topk * block, num_pages), qlen * num_pages);
+}
+
+mla_status mla_index_select(const float *scores, const int32_t *pages, int64_t num_pages, const int32_t *indptr,
+                            int num_requests, int qlen, int topk, int block, int recent, int sinks,
+                            unsigned int flags, int32_t *pages_out, int64_t capacity, int32_t *indptr_out,
+                            void *stream) {
+    if (flags & ~MLA_ATTEND_CAUSAL) return fail(MLA_ERR_INVALID, "unknown flag bits");
+    const int64_t need = mla_index_select_capacity(num_requests, qlen, num_pages, topk, block);
+    if (need < 0) return (mla_status)need;
+    if (recent < 0 || sinks < 0) return fail(MLA_ERR_INVALID, "negative recent / sinks");
+    if (block > 1 && recent < 1) return fail(MLA_ERR_INVALID, "recent must be at least 1 with blocks of more than one token");
+    if (capacity < need) return fail(MLA_ERR_INVALID, "pages_out too small");
+    if (capacity > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "capacity above 2^31 - 65536");
+    if (!indptr || !indptr_out || (num_pages > 0 && (!pages || !scores)) || (capacity > 0 && !pages_out))
+        return fail(MLA_ERR_INVALID, "null pointer");
+    if (!aligned(scores, 4) || !aligned(pages, 4) || !aligned(indptr, 4) || !aligned(pages_out, 4) || !aligned(indptr_out, 4))
+        return fail(MLA_ERR_INVALID, "misaligned pointer (4 bytes)");
+    const int64_t rows = (int64_t)num_requests * qlen;
+    const Span in[3] = {{scores, num_pages * qlen * 4}, {pages, num_pages * 4}, {indptr, ((int64_t)num_requests + 1) * 4}};
+    const Span to[2] = {{pages_out, capacity * 4}, {indptr_out, (rows + 1) * 4}};
+    if (overlaps(to[0], in) || overlaps(to[1], in)) return fail(MLA_ERR_INVALID, "an output overlaps an input");
+    if (overlap(to[0].p, to[0].n, to[1].p, to[1].n)) return fail(MLA_ERR_INVALID, "two outputs overlap");
+    const int sms = device_sms();
+    if (sms <= 0) return fail(MLA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = mla::index_select_launch(scores, pages, num_pages, indptr, num_requests, qlen, topk, block, recent,
+                                             sinks, (flags & MLA_ATTEND_CAUSAL) != 0, pages_out, capacity, indptr_out, sms,
+                                             static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "index_select launch");
+    return MLA_OK;
+}
+
 mla_status mla_kv_evict(const int32_t *pages, int64_t num_pages, const int32_t *indptr, int num_requests,
                         const float *weights, const int32_t *budgets, int budget, int recent, int sinks,
                         int32_t *pages_out, int32_t *indptr_out, float *weights_out, void *stream) {
@@ -1001,7 +1052,7 @@ mla_status mla_device_status(void *stream, unsigned int *flags) {
                                                       mla::kv_append_status, mla::norm_status,
                                                       mla::token_weights_status, mla::evict_status, mla::value_lora_status,
                                                       mla::norm_rope_status, mla::query_absorb_status,
-                                                      mla::index_scores_status};
+                                                      mla::index_scores_status, mla::index_select_status};
     for (auto rd : readers) {
         unsigned int f = 0;
         e = rd(&f, true);

@@ -1,5 +1,6 @@
 // Python module of the calls whose kernels take a few microseconds
-// (add_rms_norm, token_weights, kv_evict, value_gate_lora, norm_rope, query_absorb, index_scores): argument checks,
+// (add_rms_norm, token_weights, kv_evict, value_gate_lora, norm_rope,
+// query_absorb, index_scores, index_select): argument checks,
 // output allocation and the call into the C ABI, without the Python
 // interpreter in between.  On the Grace host a call takes 2.3 us of it with
 // its outputs given and 1.3 more for each that it allocates (2.0 through
@@ -446,6 +447,36 @@ PyObject *index_scores(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (scores, pages, indptr, topk, block, recent, sinks, causal, pages_out, indptr_out, stream)
+PyObject *index_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject * {
+        const at::Tensor &scores = tensor(a[0], "scores"), &pages = tensor(a[1], "pages"), &indptr = tensor(a[2], "indptr");
+        const int64_t dev = scores.get_device(), pages_n = pages.numel(), R = indptr.numel() - 1;
+        if (scores.dim() != 2 || scores.size(0) > MLA_MAX_QLEN) refuse("scores must be float32 [qlen, pages], qlen up to 16");
+        const int qlen = (int)scores.size(0);
+        if (R < 0 || R > INT32_MAX) refuse("indptr must have R + 1 entries");
+        dense(scores, "scores", at::kFloat, {qlen, pages_n}, dev);
+        dense(pages, "pages", at::kInt, {pages_n}, dev);
+        dense(indptr, "indptr", at::kInt, {R + 1}, dev);
+        const int topk = int32(a[3], "topk"), block = int32(a[4], "block"), recent = int32(a[5], "recent"),
+                  sinks = int32(a[6], "sinks");
+        const int causal = PyObject_IsTrue(a[7]);
+        if (causal < 0) return nullptr;
+        const Place at(dev, a[10]);
+        const int64_t need = mla_index_select_capacity((int)R, qlen, pages_n, topk, block);
+        if (need < 0) return PyLong_FromLongLong(need);
+        const at::Tensor po = output(a[8], "pages_out", at, {need}, at::kInt, [&](const at::Tensor &t) {
+            dense(t, "pages_out", at::kInt, {t.numel()}, dev);
+        });
+        const at::Tensor io = dense_output(a[9], "indptr_out", at, {R * qlen + 1}, at::kInt);
+        const mla_status st = mla_index_select(ptr<float>(scores), ptr<int32_t>(pages), pages_n, ptr<int32_t>(indptr), (int)R,
+                                               qlen, topk, block, recent, sinks, causal ? MLA_ATTEND_CAUSAL : 0u,
+                                               ptr<int32_t>(po), po.numel(), ptr<int32_t>(io), at.stream);
+        if (st != MLA_OK) return PyLong_FromLong(st);
+        return pack({po, io});
+    });
+}
+
 // (pages, indptr, weights, budget, recent, sinks, pages_out, indptr_out, weights_out, stream)
 PyObject *kv_evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 10, [&]() -> PyObject * {
@@ -509,7 +540,8 @@ PyObject *value_gate_lora(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define MLA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MLA_METHOD(add_rms_norm), MLA_METHOD(token_weights), MLA_METHOD(kv_evict),
                          MLA_METHOD(value_gate_lora), MLA_METHOD(norm_rope),
-                         MLA_METHOD(query_absorb), MLA_METHOD(index_scores), {nullptr, nullptr, 0, nullptr}};
+                         MLA_METHOD(query_absorb), MLA_METHOD(index_scores),
+                         MLA_METHOD(index_select), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "mla_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
