@@ -31,6 +31,13 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
+// Blocks an SM holds, by what their registers allow (40 to 128 a thread):
+// where one more of them would spill, rows in flight are worth less (16,384
+// rows of 576 columns, 5 vectors a lane: 7.4 us with three blocks, 9.8 with
+// four and 120 bytes spilled).
+constexpr int blocks_per_sm(int vpt, bool head) {
+    return vpt <= 2 ? (head ? 6 : 4) : vpt == 3 ? 4 : vpt <= 5 ? (head ? 2 : 3) : 2;
+}
 
 struct RopeArgs {
     const void *x, *weight;
@@ -38,201 +45,305 @@ struct RopeArgs {
     const float *cos_sin;
     void *out;
     float *scales;
-    int64_t x_row, x_head, out_row, out_head, num_positions, out_rows;
+    int64_t num_positions, out_rows;
+    uint32_t x_row, x_head, out_row, out_head;      // strides, at most 2^30
     uint32_t rows, heads, magic, shift;     // row / heads = row * magic >> (31 + shift), rows below 2^31
     int vecs, norm_vecs, rope0, rope_vecs, half;    // half: half the rotation's columns
+    int turns;              // pairs of a lane's places that hold halves of the rotation
     float eps, inv_norm, inv_scale;
     int quant;
 };
 
-// One row a group of G lanes, VPT vectors a lane.  PAIRS: neighbours make a
-// pair.
-template <typename T, int G, int VPT, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs a) {
+// Two neighbouring columns in float32, and both at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Eight columns as four pairs.
+struct Vec {
+    uint64_t p[4];
+};
+template <typename T>
+__device__ __forceinline__ Vec unpack(const uint4 &raw) {
+    float f[8];
+    unpack8<T>(raw, f);
+    return {{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+}
+__device__ __forceinline__ Vec load8(const float *p) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    return {{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
+}
+__device__ __forceinline__ void spread(const Vec &v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = parts(v.p[i]);
+        f[2 * i] = x.x;
+        f[2 * i + 1] = x.y;
+    }
+}
+
+// Four e4m3 codes of two pairs.
+__device__ __forceinline__ uint32_t codes(uint64_t a, uint64_t b) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(parts(a), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(parts(b), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t round2(uint64_t v) {
+    const float2 f = parts(v);
+    return pack2<T>(f.x, f.y);
+}
+
+// One row a group of G lanes, VPT vectors a lane.  NORM: with a weight.
+// PAIRS: neighbours make a pair.  HEAD: a scale a row, so its values are held
+// until all of them are known.
+template <typename T, int G, int VPT, bool NORM, bool PAIRS, bool HEAD>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD)) norm_rope_kernel(const RopeArgs a) {
+    __shared__ uint4 weight[NORM ? MLA_MAX_ROPE_WIDTH / 8 : 1];
     const int lane = threadIdx.x & 31, in = lane % G;
     constexpr int kPerWarp = 32 / G;
+    constexpr bool kAhead = !HEAD && G < 32 && VPT <= (PAIRS ? 4 : 2);      // the next row's loads beside this one's work
     const uint32_t step = gridDim.x * (kThreads / G);
-    // The warp's rows are neighbours and its lanes stay together: a group past the last row holds none.
+    // The warp's rows are neighbours and its lanes stay together: a group past
+    // the last row repeats it and stores nothing.
     const uint32_t first = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kPerWarp;
-    const auto token_of = [&](uint32_t row) { return (uint32_t)(((uint64_t)row * a.magic) >> (31 + a.shift)); };
-    const auto row_of = [&](uint32_t row, uint32_t t) {
-        return static_cast<const uint4 *>(static_cast<const void *>(
-            static_cast<const T *>(a.x) + (int64_t)t * a.x_row + (int64_t)(row - t * a.heads) * a.x_head));
-    };
-    uint4 xv[VPT];
-    int64_t pos = 0, slot = 0;
-    const auto fetch = [&](uint32_t row) {
-        if (row >= a.rows) return;
-        const uint32_t t = token_of(row);
-        const uint4 *x = row_of(row, t);
+    // This lane's vectors, and a bit each: it has one, it is normed, it is
+    // rotated.  Halves: the first 2 * a.turns places of a lane hold the two
+    // vectors of its pairs, front and back, or in lanes past the pairs others.
+    int vec[VPT];
+    uint32_t mine = 0, normed = 0, turned = 0;
+    const int half_vecs = a.rope_vecs >> 1, spare = a.turns * G - half_vecs;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k)
-            if (in + k * G < a.vecs) xv[k] = x[in + k * G];
-        if (a.positions) pos = __ldg(a.positions + t);
-        slot = a.slots ? __ldg(a.slots + t) : (int64_t)t;
-    };
-    uint4 wv[VPT];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k)
-        wv[k] = in + k * G < a.norm_vecs ? __ldg(static_cast<const uint4 *>(a.weight) + in + k * G) : make_uint4(0, 0, 0, 0);
-    fetch(first + lane / G);
-    for (uint32_t row0 = first; row0 < a.rows; row0 += step) {
-        const uint32_t row = row0 + lane / G;
-        const bool real = row < a.rows;
-        const uint32_t t = real ? token_of(row) : 0;
-        const uint4 *x = row_of(real ? row : 0, t);
-        const int64_t to = slot;
-        int64_t p = pos;
-        if (a.positions && (p < 0 || p >= a.num_positions)) {
-            if (real && in == 0 && to >= 0) flag(MLA_DEV_BAD_POSITION);
-            p = 0;
-        }
-        float y[VPT][8], ssq = 0.f, up = 1.f, rstd = 1.f;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = in + k * G;
-            if (real && v < a.vecs) {
-                unpack8<T>(xv[k], y[k]);
-                if (v < a.norm_vecs)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ssq = fmaf(y[k][i], y[k][i], ssq);
+    for (int k = 0; k < VPT; ++k) {
+        int v = in + k * G;
+        if (PAIRS) {
+            if (v >= a.rope0 && v < a.rope0 + a.rope_vecs) turned |= 1u << k;
+        } else {
+            const int u = in + (k >> 1) * G;        // of this place's pair
+            if (k < 2 * a.turns && u < half_vecs) {
+                v = a.rope0 + u + (k & 1) * half_vecs;
+                turned |= 1u << k;
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[k][i] = 0.f;
+                v = k < 2 * a.turns ? in - (G - spare) + (k & 1) * spare : 2 * spare + (k - 2 * a.turns) * G + in;
+                if (v >= a.rope0) v += a.rope_vecs;
             }
         }
-        fetch(row + step);      // of the next row, on their way meanwhile
-        if (a.norm_vecs > 0) {
+        if (v < a.vecs) mine |= 1u << k;
+        if (NORM && v < a.norm_vecs) normed |= 1u << k;
+        vec[k] = v;
+    }
+    uint4 next[VPT];
+    int64_t pos = 0, slot = 0;
+    uint32_t head;
+    const auto fetch = [&](uint32_t row) {
+        row = min(row, a.rows - 1);
+        const uint32_t t = (uint32_t)(((uint64_t)row * a.magic) >> (31 + a.shift));
+        head = row - t * a.heads;
+        if (a.positions) pos = __ldg(a.positions + t);
+        slot = a.slots ? __ldg(a.slots + t) : (int64_t)t;
+        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) +
+                                                         ((uint64_t)t * a.x_row + (uint64_t)head * a.x_head));
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) next[k] = (mine >> k & 1) ? x[vec[k]] : make_uint4(0, 0, 0, 0);
+    };
+    if (kAhead) fetch(first + lane / G);
+    if (NORM) {
+        for (int i = threadIdx.x; i < a.norm_vecs; i += kThreads) weight[i] = __ldg(static_cast<const uint4 *>(a.weight) + i);
+        __syncthreads();
+    }
+    for (uint32_t row0 = first; row0 < a.rows; row0 += step) {
+        const uint32_t row = row0 + lane / G;
+        if (!kAhead) fetch(row);
+        const uint32_t h = head;
+        // Where the row goes; a negative slot is padding.
+        const int64_t to = slot;
+        bool write = row < a.rows;
+        if (a.slots) {
+            if (write && to >= a.out_rows && in == 0) flag(MLA_DEV_BAD_PAGE);
+            write = write && to >= 0 && to < a.out_rows;
+        }
+        const float *cs = a.cos_sin;
+        if (a.positions) {
+            const bool bad = (uint64_t)pos >= (uint64_t)a.num_positions;
+            if (bad && to >= 0 && in == 0) flag(MLA_DEV_BAD_POSITION);
+            cs += bad ? 0 : pos * (2 * a.half);
+        }
+        uint4 xv[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) xv[k] = next[k];
+        if (kAhead) fetch(row + step);
+        float rstd = 1.f;
+        if (NORM) {
+            uint64_t sums[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const Vec y = unpack<T>(xv[k]);
+                if (normed >> k & 1)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sums[i & 1] = fma2(y.p[i], y.p[i], sums[i & 1]);
+            }
+            const float2 s0 = parts(sums[0]), s1 = parts(sums[1]);
+            float ssq = (s0.x + s0.y) + (s1.x + s1.y);
 #pragma unroll
             for (int d = G / 2; d >= 1; d >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, d);
             rstd = rsqrtf(fmaf(ssq, a.inv_norm, a.eps));
-            const bool over = ssq == INFINITY;
-            if (__any_sync(0xffffffffu, over)) {
-                // The squares overflow (or an element is infinite): the same
-                // row scaled by 2^-80, beside whose mean square eps is nothing.
+            if (__any_sync(0xffffffffu, ssq == INFINITY)) {
+                // The squares overflow (or an element is infinite): the sum of
+                // the row scaled by 2^-80, beside whose mean eps is nothing.
+                // (The factor may be subnormal, down to 2^-128: 2^-22 off.)
                 float small = 0.f;
 #pragma unroll
-                for (int k = 0; k < VPT; ++k)
-                    if (in + k * G < a.norm_vecs)
+                for (int k = 0; k < VPT; ++k) {
+                    if (!(normed >> k & 1)) continue;
+                    float y[8];
+                    unpack8<T>(xv[k], y);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float z = y[k][i] * 0x1p-80f;
-                            small = fmaf(z, z, small);
-                        }
+                    for (int i = 0; i < 8; ++i) small = fmaf(y[i] * 0x1p-80f, y[i] * 0x1p-80f, small);
+                }
 #pragma unroll
                 for (int d = G / 2; d >= 1; d >>= 1) small += __shfl_xor_sync(0xffffffffu, small, d);
-                if (over) {
-                    up = 0x1p-80f;
-                    rstd = rsqrtf(small * a.inv_norm);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                if (in + k * G >= a.norm_vecs) continue;
-                float w[8];
-                unpack8<T>(wv[k], w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[k][i] = y[k][i] * up * rstd * w[i];
+                if (ssq == INFINITY) rstd = rsqrtf(small * a.inv_norm) * 0x1p-80f;
             }
         }
-        if (a.positions) {
-            const float *cs = a.cos_sin + p * (2 * a.half);
+        const uint64_t rstd2 = pair(rstd, rstd);
+        // Vector k of this lane, normed; with PAIRS rotated too.
+        const auto value = [&](int k) {
+            Vec y = unpack<T>(xv[k]);
+            if (NORM && (normed >> k & 1)) {
+                const Vec f = unpack<T>(weight[vec[k]]);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int v = in + k * G, j = v - a.rope0;
-                if (!real || j < 0 || j >= a.rope_vecs) continue;
-                if (PAIRS) {
-                    const float4 c = __ldg(reinterpret_cast<const float4 *>(cs) + j);
-                    const float4 s = __ldg(reinterpret_cast<const float4 *>(cs + a.half) + j);
-                    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+                for (int i = 0; i < 4; ++i) y.p[i] = mul2(mul2(y.p[i], rstd2), f.p[i]);
+            }
+            if (PAIRS && (turned >> k & 1)) {
+                const float *at = cs + 4 * (vec[k] - a.rope0);
+                const float4 c = __ldg(reinterpret_cast<const float4 *>(at));
+                const float4 s = __ldg(reinterpret_cast<const float4 *>(at + a.half));
+                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = y[k][2 * i], w = y[k][2 * i + 1];
-                        y[k][2 * i] = u * cc[i] - w * ss[i];
-                        y[k][2 * i + 1] = w * cc[i] + u * ss[i];
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u = parts(y.p[i]);
+                    y.p[i] = pair(u.x * cc[i] - u.y * ss[i], u.y * cc[i] + u.x * ss[i]);
+                }
+            }
+            return y;
+        };
+        // The vectors of places k and k + 1, halves of the same pairs, rotated.
+        const auto rotate = [&](Vec &u, Vec &v, int k) {
+            const float *at = cs + 8 * (vec[k] - a.rope0);
+            const Vec c = load8(at), s = load8(at + a.half);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t w = fma2(v.p[i] ^ 0x8000000080000000ull, s.p[i], mul2(u.p[i], c.p[i]));
+                v.p[i] = fma2(u.p[i], s.p[i], mul2(v.p[i], c.p[i]));
+                u.p[i] = w;
+            }
+        };
+        // use(k, its value) for every place.
+        const auto each = [&](auto use) {
+#pragma unroll
+            for (int k = 0; k < VPT; k += PAIRS ? 1 : 2) {
+                Vec u = value(k);
+                if (PAIRS || k + 1 == VPT) {
+                    use(k, u);
                 } else {
-                    const int hv = a.rope_vecs >> 1;        // vectors of half a rotation
-                    const bool front = j < hv;
-                    const int other = front ? v + hv : v - hv, at = front ? j : j - hv;
-                    float o[8];
-                    unpack8<T>(x[other], o);
-                    if (other < a.norm_vecs) {
-                        float w[8];
-                        unpack8<T>(__ldg(static_cast<const uint4 *>(a.weight) + other), w);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = o[i] * up * rstd * w[i];
-                    }
-#pragma unroll
-                    for (int i4 = 0; i4 < 2; ++i4) {
-                        const float4 c = __ldg(reinterpret_cast<const float4 *>(cs) + 2 * at + i4);
-                        const float4 s = __ldg(reinterpret_cast<const float4 *>(cs + a.half) + 2 * at + i4);
-                        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float turn = o[4 * i4 + i] * ss[i];
-                            y[k][4 * i4 + i] = y[k][4 * i4 + i] * cc[i] + (front ? -turn : turn);
-                        }
-                    }
+                    Vec v = value(k + 1 < VPT ? k + 1 : k);
+                    if (turned >> k & 1) rotate(u, v, k);
+                    use(k, u);
+                    use(k + 1, v);
                 }
             }
+        };
+        const uint64_t at = (uint64_t)to * a.out_row + (uint64_t)h * a.out_head;
+        if (!HEAD && a.quant == MLA_QUANT_NONE) {
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + at);
+            each([&](int k, const Vec &v) {
+                const uint4 y = make_uint4(round2<T>(v.p[0]), round2<T>(v.p[1]), round2<T>(v.p[2]), round2<T>(v.p[3]));
+                if (write && (mine >> k & 1)) o[vec[k]] = y;
+            });
+            continue;
         }
-        // Where the row goes; a negative slot is padding.
-        bool write = real && to >= 0;
-        if (write && to >= a.out_rows) {
-            if (in == 0) flag(MLA_DEV_BAD_PAGE);
-            write = false;
-        }
-        const uint32_t h = real ? row - t * a.heads : 0;
-        float inv = a.inv_scale;
-        if (a.quant == MLA_QUANT_ROW) {
+        uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + at);
+        const auto store = [&](int k, const Vec &v, uint64_t inv) {
+            const uint2 q = make_uint2(codes(mul2(v.p[0], inv), mul2(v.p[1], inv)), codes(mul2(v.p[2], inv), mul2(v.p[3], inv)));
+            if (write && (mine >> k & 1)) o[vec[k]] = q;
+        };
+        if (HEAD) {
+            Vec held[HEAD ? VPT : 1];
             float amax = 0.f;
+            each([&](int k, const Vec &v) {
+                held[HEAD ? k : 0] = v;
+                float y[8];
+                spread(v, y);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(y[k][i]));
+                for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(y[i]));
+            });
 #pragma unroll
             for (int d = G / 2; d >= 1; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-            const float sc = block_scale(amax);
-            if (write && in == 0) a.scales[to * a.heads + h] = sc;
-            inv = __fdiv_rn(1.f, sc);
-        }
-        __syncwarp();       // in place: no lane stores before the others have read their pairs
-        if (!write) continue;
-        const int64_t at = to * a.out_row + (int64_t)h * a.out_head;
-        if (a.quant == MLA_QUANT_NONE) {
-            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + at);
+            const float sc = block_scale(amax), inv = __fdiv_rn(1.f, sc);
+            if (write && in == 0) a.scales[(uint64_t)to * a.heads + h] = sc;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                if (in + k * G < a.vecs) o[in + k * G] = pack8<T>(y[k]);
+            for (int k = 0; k < VPT; ++k) store(k, held[HEAD ? k : 0], pair(inv, inv));
         } else {
-            uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + at);
-#pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                if (in + k * G < a.vecs) o[in + k * G] = pack8_e4m3(y[k], inv);
+            each([&](int k, const Vec &v) { store(k, v, pair(a.inv_scale, a.inv_scale)); });
         }
     }
 }
 
+template <typename T, int G, int VPT, bool NORM, bool PAIRS, bool HEAD>
+cudaError_t launch_kernel(RopeArgs a, int sms, cudaStream_t st) {
+    a.turns = PAIRS ? 0 : (a.rope_vecs / 2 + G - 1) / G;
+    const uint32_t per_block = kThreads / G, blocks = (a.rows + per_block - 1) / per_block;
+    norm_rope_kernel<T, G, VPT, NORM, PAIRS, HEAD>
+        <<<std::min(blocks, (uint32_t)sms * blocks_per_sm(VPT, HEAD)), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T, int G, int VPT>
 cudaError_t launch(const RopeArgs &a, bool pairs, int sms, cudaStream_t st) {
-    const uint32_t per_block = kThreads / G, blocks = (a.rows + per_block - 1) / per_block;
-    const unsigned grid = std::min(blocks, (uint32_t)sms * 16);
-    if (pairs) norm_rope_kernel<T, G, VPT, true><<<grid, kThreads, 0, st>>>(a);
-    else norm_rope_kernel<T, G, VPT, false><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    const bool head = a.quant == MLA_QUANT_ROW;
+    if (a.weight) {
+        if (pairs) return head ? launch_kernel<T, G, VPT, true, true, true>(a, sms, st) : launch_kernel<T, G, VPT, true, true, false>(a, sms, st);
+        return head ? launch_kernel<T, G, VPT, true, false, true>(a, sms, st) : launch_kernel<T, G, VPT, true, false, false>(a, sms, st);
+    }
+    if (pairs) return head ? launch_kernel<T, G, VPT, false, true, true>(a, sms, st) : launch_kernel<T, G, VPT, false, true, false>(a, sms, st);
+    return head ? launch_kernel<T, G, VPT, false, false, true>(a, sms, st) : launch_kernel<T, G, VPT, false, false, false>(a, sms, st);
 }
 
 template <typename T>
 cudaError_t launch_width(const RopeArgs &a, bool pairs, int sms, cudaStream_t st) {
-    if (a.vecs <= 8) return launch<T, 8, 1>(a, pairs, sms, st);
-    if (a.vecs <= 16) return launch<T, 8, 2>(a, pairs, sms, st);
-    if (a.vecs <= 24) return launch<T, 8, 3>(a, pairs, sms, st);
-    if (a.vecs <= 32) return launch<T, 16, 2>(a, pairs, sms, st);
-    if (a.vecs <= 48) return launch<T, 16, 3>(a, pairs, sms, st);
-    if (a.vecs <= 64) return launch<T, 32, 2>(a, pairs, sms, st);
-    if (a.vecs <= 96) return launch<T, 32, 3>(a, pairs, sms, st);
-    return launch<T, 32, 4>(a, pairs, sms, st);
+    // The fewest lanes that hold a row in few registers and, with halves, both
+    // of a pair in one lane.  Rows of 384 columns and more that leave the SMs
+    // idle take a warp each (64 of 576 2.6 us, with 16 lanes 3.0; 1,024 3.0
+    // and 3.4; 16,384 8.6 and 7.4), very many of them 8 lanes (65,536 27 us,
+    // with 16 32; 1,024 4.1 and 3.4).
+    const auto fits = [&](int g, int vpt) { return a.vecs <= g * vpt && (pairs || 2 * ((a.rope_vecs / 2 + g - 1) / g) <= vpt); };
+    if (fits(4, 2)) return launch<T, 4, 2>(a, pairs, sms, st);
+    if (fits(8, 2)) return launch<T, 8, 2>(a, pairs, sms, st);
+    if (fits(8, 3)) return launch<T, 8, 3>(a, pairs, sms, st);
+    if (fits(8, 4)) return launch<T, 8, 4>(a, pairs, sms, st);
+    if (fits(16, 3)) return launch<T, 16, 3>(a, pairs, sms, st);
+    if (a.rows < 16 * (uint32_t)sms && fits(32, 3)) return launch<T, 32, 3>(a, pairs, sms, st);
+    if (a.rows < 16 * (uint32_t)sms && fits(32, 4)) return launch<T, 32, 4>(a, pairs, sms, st);
+    if (a.rows >= 64 * (uint32_t)sms && fits(8, 9)) return launch<T, 8, 9>(a, pairs, sms, st);
+    if (fits(16, 5)) return launch<T, 16, 5>(a, pairs, sms, st);
+    return launch<T, 16, 8>(a, pairs, sms, st);
 }
 
 }  // namespace
@@ -246,16 +357,16 @@ cudaError_t norm_rope_launch(const void *x, int64_t x_row, int64_t x_head, int x
                              int64_t out_head, float *out_scales, int sms, cudaStream_t st) {
     RopeArgs a = {};
     a.x = x;
-    a.x_row = x_row;
-    a.x_head = x_head;
+    a.x_row = (uint32_t)x_row;
+    a.x_head = (uint32_t)x_head;
     a.weight = weight;
     a.positions = positions;
     a.slots = slots;
     a.cos_sin = cos_sin;
     a.out = out;
     a.scales = out_scales;
-    a.out_row = out_row;
-    a.out_head = out_head;
+    a.out_row = (uint32_t)out_row;
+    a.out_head = (uint32_t)out_head;
     a.num_positions = num_positions;
     a.out_rows = out_rows;
     a.rows = (uint32_t)(tokens * heads);
