@@ -13,6 +13,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr uint32_t kKeyZero = 0x80000000u, kKeyLowest = ~0xff800000u;     // no key is below kKeyLowest
+
 __device__ __forceinline__ uint32_t block_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -45,15 +47,18 @@ __device__ __forceinline__ uint32_t remote(const uint32_t *p, uint32_t rank) {
 // A thread's bins.
 template <int N>
 struct Bins {
-    static_assert(N == 2 || N == 4, "one vector");
+    static_assert(N == 2 || N % 4 == 0, "whole vectors");
     uint32_t n[N];
 };
 template <int N>
 __device__ __forceinline__ Bins<N> local_bins(const uint32_t *p) {
     Bins<N> b;
-    if constexpr (N == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        b.n[0] = v.x, b.n[1] = v.y, b.n[2] = v.z, b.n[3] = v.w;
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + i);
+            b.n[i] = v.x, b.n[i + 1] = v.y, b.n[i + 2] = v.z, b.n[i + 3] = v.w;
+        }
     } else {
         const uint2 v = *reinterpret_cast<const uint2 *>(p);
         b.n[0] = v.x, b.n[1] = v.y;
@@ -62,6 +67,7 @@ __device__ __forceinline__ Bins<N> local_bins(const uint32_t *p) {
 }
 template <int N>
 __device__ __forceinline__ Bins<N> remote_bins(const uint32_t *p, uint32_t rank) {
+    static_assert(N <= 4, "one vector");
     uint32_t addr;
     Bins<N> b;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));

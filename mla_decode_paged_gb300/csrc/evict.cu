@@ -59,7 +59,6 @@ struct EvictArgs {
 __device__ __forceinline__ float key_weight(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
-constexpr uint32_t kKeyZero = 0x80000000u, kKeyLowest = ~0xff800000u;     // no key is below kKeyLowest
 
 __device__ __forceinline__ int kept_tokens(const EvictArgs &a, int r, int len) {
     const int b = a.budgets ? __ldg(a.budgets + r) : a.budget;

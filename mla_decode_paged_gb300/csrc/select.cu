@@ -44,80 +44,87 @@ namespace mla {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kRound = 8192;       // token blocks a thread block holds
-constexpr int kCand = 1024;        // keys that one warp searches
+constexpr int kLong = 8192, kShort = 4096;     // token blocks a thread block holds, of 512 and more threads, of 256
+constexpr int kCand = 1024, kFew = 512;    // keys of a bin, of a row, that one warp searches
+constexpr int kCounted = 1024;     // rows whose kept tokens every cluster counts itself
 
 struct SelectArgs {
     const float *scores;
     const int32_t *pages, *indptr;
     int64_t num_pages, capacity;
+    uint32_t over_qlen;             // 2^32 / qlen, rounded up
     int R, qlen, topk, log_block, recent, sinks;
     bool causal, scanned;           // scanned: indptr_out is there
     int32_t *pages_out, *indptr_out;
 };
 
-// A query row: its first entry, the tokens it sees, their blocks, the blocks and tokens it keeps.
+// A query row: its request and place there, its first entry, the tokens it
+// sees, their blocks, the blocks and tokens it keeps.
 struct Row {
-    int base, seen, blocks, kept, tokens;
+    int r, tq, base, seen, blocks, kept, tokens;
 };
 __device__ __forceinline__ Row row_of(const SelectArgs &a, int b) {
     Row x;
-    const int r = b / a.qlen, tq = b - r * a.qlen;
-    const int len = request_len(a.indptr, r, a.num_pages, &x.base);
-    x.seen = a.causal ? max(0, len - a.qlen + tq + 1) : len;
+    x.r = a.qlen == 1 ? b : (int)__umulhi((uint32_t)b, a.over_qlen);       // b below 2^24
+    x.tq = b - x.r * a.qlen;
+    int begin = __ldg(a.indptr + x.r), end = __ldg(a.indptr + x.r + 1);
+    if (begin < 0 || end < begin || end > a.num_pages) {        // as request_len does
+        flag(MLA_DEV_BAD_INDPTR);
+        begin = end = 0;
+    }
+    x.base = begin;
+    x.seen = a.causal ? max(0, end - begin - a.qlen + x.tq + 1) : end - begin;
     x.blocks = (x.seen + (1 << a.log_block) - 1) >> a.log_block;
     x.kept = min(x.blocks, a.topk);
-    x.tokens = x.kept == x.blocks ? x.seen : (x.kept << a.log_block) - ((x.blocks << a.log_block) - x.seen);
+    x.tokens = x.kept == x.blocks ? x.seen : ((x.kept - x.blocks) << a.log_block) + x.seen;
     return x;
 }
 
-template <int THREADS>
+// Where key i of a round lies: eight neighbours and a gap, so that threads
+// that read their neighbours fall in different banks.
+__host__ __device__ constexpr int place(int i) { return i + (i >> 3); }
+
+template <int THREADS, int ROUND, bool CLUSTER>
 struct __align__(16) Shared {
-    uint32_t key[kRound];           // a round's keys (place); then the blocks that stay, in order
+    uint32_t key[place(ROUND)];     // a round's keys; then the blocks that stay, in order
     uint32_t hist[kBins];
-    uint32_t sums[kBins];           // of this block's share of the bins, over the cluster
-    uint32_t cand[kCand], all[kCand];   // keys of the m-th largest's bin: this block's, the cluster's
-    uint32_t red[2][32], scan[32], totals[32];
+    uint32_t sums[CLUSTER ? kBins : 4];     // of this block's share of the bins, over the cluster
+    uint32_t cand[kCand], all[CLUSTER ? kCand : 4];     // keys of the m-th largest's bin: this block's, the cluster's
+    uint32_t red[2][32], scan[2][32], ends[16];
     uint32_t least, most;           // of this block's keys of that bin
     uint32_t ncand;
     uint32_t sum[2];                // this block's sure blocks and ties, for the cluster
     uint32_t pick[4];
 };
 
-// Where key i of a round lies: a thread's PER neighbours in vectors of four,
-// their order turned by the thread so that eight threads' vectors fall in
-// different banks.
-template <int PER>
-__device__ __forceinline__ int place(int i) {
-    const int t = i / PER, c = i / 4 % (PER / 4);
-    return t * PER + ((c ^ (PER == 16 ? t >> 1 & 3 : t >> 2 & 1)) << 2) + (i & 3);
-}
-
-// Blocks it takes to hold a row's tokens, as a power of two up to log_cs.
-__device__ __forceinline__ int blocks_for(int tokens, int log_cs) {
+// Thread blocks that share a row of so many tokens, as a power of two up to log_cs.
+__device__ __forceinline__ int blocks_for(int tokens, int log_cs, int slice) {
     int le = 0;
-    while (le < log_cs && (tokens >> le) > kRound) ++le;
+#pragma unroll 1
+    while (le < log_cs && (tokens >> le) > slice) ++le;
     return le;
 }
 
-// The need-th largest of the n keys at p, which agree above their lowest 21
-// bits (run by a warp): a value T that exactly `need` of them reach, and
-// true, or the key itself, how many of it belong to them, and false.
+// The need-th largest of the n keys at p (zeros do not count), which agree
+// with T above their lowest `bits` bits (run by a warp): a value T that
+// exactly `need` of them reach, and true, or the key itself, how many of it
+// belong to them, and false.
 template <int N>
-__device__ bool search(const uint32_t *p, uint32_t n, uint32_t &T, uint32_t &need) {
+__device__ __forceinline__ bool search(const uint32_t *p, uint32_t n, int bits, uint32_t &T, uint32_t &need) {
     const int lane = threadIdx.x & 31;
     uint32_t x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = lane + 32 * i < n ? p[lane + 32 * i] : 0;
-    for (int bit = 20; bit >= 0; --bit) {
+#pragma unroll 1
+    for (int bit = bits - 1; bit >= 0; --bit) {
         const uint32_t t = T | 1u << bit;
-        uint32_t c = 0;
+        uint32_t c[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < N; ++i) c += x[i] >= t;
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (c < need) continue;
+        for (int i = 0; i < N; ++i) c[i & 3] += x[i] >= t;
+        const uint32_t all = __reduce_add_sync(0xffffffffu, (c[0] + c[1]) + (c[2] + c[3]));
+        if (all < need) continue;
         T = t;
-        if (c == need) return true;
+        if (all == need) return true;
     }
     uint32_t above = 0;
 #pragma unroll
@@ -126,130 +133,202 @@ __device__ bool search(const uint32_t *p, uint32_t n, uint32_t &T, uint32_t &nee
     return false;
 }
 
-// 2^log_cs blocks (a cluster) per row.
+// Sum of x over the threads before this one and over all of the block's, by
+// way of `totals`, which is free again after the block's next barrier but one.
+// (Not inlined, as what else is run more than once: SMs of one GPC that start
+// together wait for each other's instructions.)
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) select_kernel(const SelectArgs a, int log_cs) {
-    constexpr int kWarps = THREADS / 32, kPer = kRound / THREADS, kOwn = kBins / THREADS;   // keys of a thread; bins it sums
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared<THREADS> &sh = *reinterpret_cast<Shared<THREADS> *>(smem_raw);
+__device__ __noinline__ uint2 block_sums(uint32_t x, uint32_t *totals) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t incl = x;
+#pragma unroll 1
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) totals[warp] = incl;
+    __syncthreads();
+    const uint32_t t = lane < THREADS / 32 ? totals[lane] : 0;
+    return make_uint2(incl - x + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0), __reduce_add_sync(0xffffffffu, t));
+}
+
+// Keys of the token blocks r0 .. s1 - 1 of a row, a round at most, into their
+// places: those of lo .. hi - 1, of `seen` tokens at w; 0 elsewhere, up to
+// `held` places.
+template <int THREADS, int ROUND, bool BLOCKED>
+__device__ __noinline__ void load_keys(uint32_t *key, const float *w, int r0, int s1, int lo, int hi, int seen, int held,
+                                       int lb) {
+    constexpr int kWarps = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = block_rank();
-    const int rows = a.R * a.qlen, b = blockIdx.x >> log_cs, lb = a.log_block;
+    const int f0 = max(lo - r0, 0), f1 = min(hi - r0, min(ROUND, s1 - r0));
+    __syncthreads();        // the histogram's zeros; the round before has been read
+    if (!BLOCKED) {
+        const float *from = w + r0 + tid;
+        uint32_t *to = key + place(tid);
+        const uint32_t width = max(f1 - f0, 0);
+#pragma unroll 1
+        for (int i0 = tid - f0; i0 < held - f0; i0 += 4 * THREADS, from += 4 * THREADS, to += 4 * place(THREADS)) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = (uint32_t)(i0 + THREADS * j) < width ? __ldg(from + THREADS * j) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = weight_key(v[j]);
+                if (i0 + THREADS * j < held - f0) to[place(THREADS) * j] = (uint32_t)(i0 + THREADS * j) < width ? x : 0;
+            }
+        }
+    } else {
+        // Block maxima (NaN ignored: as -inf).  Up to 32 tokens a block: a
+        // warp's 32 lanes hold several, joined by shuffles.  More: a warp
+        // holds some blocks' tokens in eight registers a lane.
+#pragma unroll 1
+        for (int i = tid; i < held; i += THREADS) key[place(i)] = 0;
+        __syncthreads();
+        const int t1 = min((r0 + f1) << lb, seen), ls = lb > 5 ? lb - 5 : 0;    // 2^ls reads a block
+#pragma unroll 1
+        for (int t0 = ((r0 + f0) << lb) + 32 * 8 * warp; t0 < t1; t0 += 32 * 8 * kWarps) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int t = t0 + 32 * k + lane;
+                v[k] = t < t1 ? __ldg(w + t) : -INFINITY;
+            }
+            if (ls >= 1)
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) v[k] = fmaxf(v[k], v[k + 1]);
+            if (ls >= 2)
+#pragma unroll
+                for (int k = 0; k < 8; k += 4) v[k] = fmaxf(v[k], v[k + 2]);
+            if (ls >= 3) v[0] = fmaxf(v[0], v[4]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int t = t0 + 32 * k;
+                if ((k & ((1 << ls) - 1)) != 0 || t >= t1) continue;
+                uint32_t x = weight_key(v[k]);
+                bool leads = lane == 0;
+                if (lb >= 5) {
+                    x = __reduce_max_sync(0xffffffffu, x);
+                } else {
+#pragma unroll 1
+                    for (int d = 1; d < 1 << lb; d <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    leads = (lane & ((1 << lb) - 1)) == 0 && t + lane < t1;
+                }
+                if (leads) key[place(((t + lane) >> lb) - r0)] = x;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// 2^log_cs blocks (a cluster) per row.
+template <int THREADS, int ROUND, bool CLUSTER, bool BLOCKED>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) select_kernel(const SelectArgs a, int log_cs) {
+    constexpr int kWarps = THREADS / 32, kOwn = kBins / THREADS;       // bins a thread sums
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Shared<THREADS, ROUND, CLUSTER> &sh = *reinterpret_cast<Shared<THREADS, ROUND, CLUSTER> *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = CLUSTER ? block_rank() : 0;
+    const int rows = a.R * a.qlen, b = CLUSTER ? blockIdx.x >> log_cs : blockIdx.x, lb = BLOCKED ? a.log_block : 0;
     const Row row = row_of(a, b);
-    const uint32_t my_tokens = !a.scanned && tid < rows ? (uint32_t)row_of(a, tid).tokens : 0;
     // The blocks past those that hold the row end (a cluster barrier waits for
     // running threads only).
-    const int le = blocks_for(row.seen, log_cs);
+    const int le = CLUSTER ? blocks_for(row.seen, log_cs, ROUND) : 0;
     const uint32_t E = 1u << le;
     if (rank >= E) return;
-    const bool one = le == 0;
+    const bool one = !CLUSTER || le == 0;
     const int recent = min(a.recent, row.kept), sinks = min(a.sinks, row.kept - recent);
     const int lo = sinks, hi = row.blocks - recent;     // the blocks that may go
     const int m = row.kept - recent - sinks;            // how many of them stay
     const bool select = m > 0 && m < hi - lo;           // the same in every block of the cluster
-    const float *w = a.scores + (int64_t)(b % a.qlen) * a.num_pages + row.base;
+    const float *w = a.scores + (int64_t)row.tq * a.num_pages + row.base;
 
     // This block's slice, in rounds.  Key 0: none that may go.
     const int slice = (((row.blocks + (int)E - 1) >> le) + 31) / 32 * 32;
     const int s0 = (int)min((int64_t)slice * rank, (int64_t)row.blocks), s1 = min(slice, row.blocks - s0) + s0;
-    const int rounds = (s1 - s0 + kRound - 1) / kRound;
-    uint32_t key[kPer];
-    const auto load = [&](int q) {
-        const int r0 = s0 + q * kRound, n = min(kRound, s1 - r0), f0 = max(lo - r0, 0), f1 = min(hi - r0, n);
-        if (rounds > 1) __syncthreads();    // the round before has been read
-        if (lb == 0) {
-            float v[kPer];
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int i = tid + THREADS * j;
-                v[j] = i >= f0 && i < f1 ? __ldg(w + r0 + i) : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int i = tid + THREADS * j;
-                sh.key[place<kPer>(i)] = i >= f0 && i < f1 ? weight_key(v[j]) : 0;
-            }
-        } else {
-            // Block maxima: warps take 32 tokens in turn, eight of these reads
-            // in flight; the lanes of a block join by shuffles.
-            for (int i = tid; i < kRound; i += THREADS) sh.key[i] = 0;
-            __syncthreads();
-            const int t1 = min((r0 + f1) << lb, row.seen);
-            for (int at = ((r0 + f0) << lb) + 32 * warp; at < t1; at += 32 * 8 * kWarps) {
-                float v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int t = at + 32 * kWarps * k + lane;
-                    v[k] = t < t1 ? __ldg(w + t) : 0.f;
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int t = at + 32 * kWarps * k + lane;
-                    if (t - lane >= t1) break;
-                    uint32_t x = t < t1 ? weight_key(v[k]) : 0;
-                    if (lb >= 5) {
-                        x = __reduce_max_sync(0xffffffffu, x);
-                        if (lane == 0) atomicMax(&sh.key[place<kPer>((t >> lb) - r0)], x);
-                    } else {
-                        for (int d = 1; d < 1 << lb; d <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        if ((t & ((1 << lb) - 1)) == 0 && t < t1) sh.key[place<kPer>((t >> lb) - r0)] = x;
-                    }
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < kPer / 4; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(sh.key + place<kPer>(tid * kPer + 4 * c));
-            key[4 * c] = v.x, key[4 * c + 1] = v.y, key[4 * c + 2] = v.z, key[4 * c + 3] = v.w;
-        }
-    };
-    for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<uint4 *>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
-    if (!one)
-        for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<uint4 *>(sh.sums)[i] = make_uint4(0, 0, 0, 0);
+    const int rounds = (s1 - s0 + ROUND - 1) / ROUND;
+    // A round's keys are `per` neighbours in each thread, as few as hold the longest round.
+    const int longest = min(s1 - s0, ROUND), per = max(1, (longest + THREADS - 1) / THREADS);
+    const int held = THREADS * per;     // places of a round's keys; those past the round hold 0
+    const auto load = [&](int q) { load_keys<THREADS, ROUND, BLOCKED>(sh.key, w, s0 + q * ROUND, s1, lo, hi, row.seen, held, lb); };
+#pragma unroll 1
+    for (int i = tid; i < kBins; i += THREADS) {
+        sh.hist[i] = 0;
+        if (CLUSTER) sh.sums[i] = 0;
+    }
     if (tid == 0) {
         sh.ncand = 0;
         sh.least = ~0u;
         sh.most = 0;
     }
     if (!one) cluster_arrive();     // waited for before the first sums are added to
-    if (select && rounds > 0) load(0);      // (its barriers order the zeros above, too)
+    if (select && rounds > 0) load(0);
 
     // The m-th largest key T of [lo, hi), and how many keys equal to T stay.
     uint32_t T = 0, ties = 0;
     bool tied = false;              // some of the equal keys go
-    if (!one) cluster_wait();
+    if (!select && !one) cluster_wait();
     if (select) {
         uint32_t need = (uint32_t)m;
         bool found = false;         // the keys that begin with T's digits so far all stay
-        for (int digit = 0; digit < 3; ++digit) {
+        const bool few = BLOCKED && one && longest <= kFew;     // one warp searches them all
+        if (few) {
+            if (warp == 0) {
+                // (to where they lie without gaps)
+#pragma unroll 1
+                for (int i = lane; i < kFew; i += 32) sh.cand[i] = i < held ? sh.key[place(i)] : 0;
+                __syncwarp();
+                found = search<kFew / 32>(sh.cand, kFew, 32, T, need);
+                if (lane == 0) sh.pick[0] = T, sh.pick[1] = need, sh.pick[3] = found;
+            }
+            __syncthreads();
+            T = sh.pick[0];
+            need = sh.pick[1];
+            found = sh.pick[3] != 0;
+        }
+#pragma unroll 1
+        for (int digit = few ? 3 : 0; digit < 3; ++digit) {
             const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
             const uint32_t mask = digit == 2 ? 1023u : 2047u;
-            const uint32_t top_bits = digit == 0 ? 0u : digit == 1 ? 0xffe00000u : 0xfffffc00u;     // found so far
+            const uint32_t top_bits = digit == 1 ? 0xffe00000u : 0xfffffc00u;     // found so far
             if (digit > 0) {
                 // Too many keys in T's bin for one warp.
-                __syncthreads();
-                for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
-                if (!one) {
-                    cluster_sync();         // all have read the sums
-                    for (int i = tid; i < kBins; i += THREADS) sh.sums[i] = 0;
-                    cluster_sync();
+                if (!one) cluster_sync();       // all have read the sums
+                else __syncthreads();
+#pragma unroll 1
+                for (int i = tid; i < kBins; i += THREADS) {
+                    sh.hist[i] = 0;
+                    if (CLUSTER) sh.sums[i] = 0;
                 }
-                __syncthreads();
+                if (!one) cluster_sync();
+                else __syncthreads();
             }
+#pragma unroll 1
             for (int q = 0; q < rounds; ++q) {
                 if (rounds > 1) load(q);
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (key[j] != 0 && ((key[j] ^ T) & top_bits) == 0) atomicAdd(&sh.hist[key[j] >> shift & mask], 1u);
+                const uint32_t *from = sh.key + place(tid);
+                if (digit == 0) {
+                    // Without a condition before them additions of 1 to the
+                    // same bin are joined by the hardware (8,192 scores, many
+                    // of them 0, in 360 cycles and not one by one); key 0
+                    // falls in a bin that no score's key does.
+#pragma unroll 4
+                    for (int i = 0; i < per; ++i) atomicAdd(&sh.hist[from[place(THREADS) * i] >> 21], 1u);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < per; ++i) {
+                        const uint32_t x = from[place(THREADS) * i];
+                        if (x != 0 && ((x ^ T) & top_bits) == 0) atomicAdd(&sh.hist[x >> shift & mask], 1u);
+                    }
+                }
             }
             __syncthreads();
             // Bins from the top: thread t holds the kOwn from kBins - 1 - kOwn * t down, summed over the cluster.
             const uint32_t top = kBins - 1 - kOwn * tid, low = top - (kOwn - 1);
             Bins<kOwn> bin = local_bins<kOwn>(sh.hist + low);
-            if (!one) {
+            if constexpr (CLUSTER) if (!one) {
                 const uint32_t share = kBins >> le, owner = low >> (11 - le);       // a block's bins; these bins' block
                 uint32_t *at = sh.sums + (low & (share - 1));
+                if (digit == 0) cluster_wait();
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j)
                     if (bin.n[j]) remote_add(at + j, owner, bin.n[j]);
@@ -259,24 +338,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) select_kernel
             uint32_t sum = 0;
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) sum += bin.n[j];
-            uint32_t incl = sum;
+            uint32_t above = block_sums<THREADS>(sum, sh.scan[0]).x;
+            if (above < need && need <= above + sum) {
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += y;
-            }
-            if (lane == 31) sh.scan[warp] = incl;
-            __syncthreads();
-            uint32_t above = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[lane] : 0);
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) {
-                const uint32_t n = bin.n[kOwn - 1 - j];
-                if (above < need && need <= above + n) {
-                    sh.pick[0] = top - j;
-                    sh.pick[1] = need - above;
-                    sh.pick[2] = n;
+                for (int j = 0; j < kOwn; ++j) {
+                    const uint32_t n = bin.n[kOwn - 1 - j];
+                    if (above < need && need <= above + n) sh.pick[0] = top - j, sh.pick[1] = need - above, sh.pick[2] = n;
+                    above += n;
                 }
-                above += n;
             }
             __syncthreads();
             T |= sh.pick[0] << shift;
@@ -287,42 +356,44 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) select_kernel
             if (digit > 0) continue;
             if (n <= kCand) {
                 // The bin's keys, in no order, and the search among them.
+#pragma unroll 1
                 for (int q = 0; q < rounds; ++q) {
                     if (rounds > 1) load(q);
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j)
-                        if ((key[j] ^ T) >> 21 == 0) sh.cand[atomicAdd(&sh.ncand, 1u)] = key[j];
+                    const uint32_t *from = sh.key + place(tid);
+#pragma unroll 4
+                    for (int i = 0; i < per; ++i) {
+                        const uint32_t x = from[place(THREADS) * i];
+                        if ((x ^ T) >> 21 == 0) sh.cand[atomicAdd(&sh.ncand, 1u)] = x;
+                    }
                 }
                 if (one) __syncthreads();
                 else cluster_sync();
                 if (warp == 0) {
                     const uint32_t *p = sh.cand;
-                    if (!one) {
-                        // Every block's, one after another.
+                    if (CLUSTER && !one) {
+                        // Every block's, one after another: where each block's end.
                         const uint32_t mine = lane < E ? remote(&sh.ncand, lane) : 0;
-                        uint32_t ends = mine;
-#pragma unroll
+                        uint32_t end = mine;
+#pragma unroll 1
                         for (int d = 1; d < 16; d <<= 1) {
-                            const uint32_t y = __shfl_up_sync(0xffffffffu, ends, d);
-                            if (lane >= d) ends += y;
+                            const uint32_t y = __shfl_up_sync(0xffffffffu, end, d);
+                            if (lane >= d) end += y;
                         }
-                        for (uint32_t i0 = 0; i0 < n; i0 += 32) {
-                            const uint32_t i = i0 + lane;
-                            uint32_t r = 0;         // the block of the i-th: those that end before it
-#pragma unroll
-                            for (int d = 0; d < 16; ++d) r += d < (int)E && __shfl_sync(0xffffffffu, ends, d) <= i;
-                            const uint32_t from = __shfl_sync(0xffffffffu, ends - mine, r & 31);
-                            if (i < n) sh.all[i] = remote(&sh.cand[i - from], r);
+                        if (lane < 16) sh.ends[lane] = end;
+                        __syncwarp();
+#pragma unroll 1
+                        for (uint32_t i = lane; i < n; i += 32) {
+                            uint32_t r = 0;         // the block of the i-th: the first that ends past it
+#pragma unroll 1
+                            for (uint32_t d = 8; d > 0; d >>= 1)
+                                if (sh.ends[r + d - 1] <= i) r += d;
+                            sh.all[i] = remote(&sh.cand[i - (r > 0 ? sh.ends[r - 1] : 0)], r);
                         }
                         __syncwarp();
                         p = sh.all;
                     }
-                    found = n <= 256 ? search<8>(p, n, T, need) : search<kCand / 32>(p, n, T, need);
-                    if (lane == 0) {
-                        sh.pick[0] = T;
-                        sh.pick[1] = need;
-                        sh.pick[3] = found;
-                    }
+                    found = n <= 256 ? search<8>(p, n, 21, T, need) : search<kCand / 32>(p, n, 21, T, need);
+                    if (lane == 0) sh.pick[0] = T, sh.pick[1] = need, sh.pick[3] = found;
                 }
                 __syncthreads();
                 T = sh.pick[0];
@@ -333,12 +404,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) select_kernel
             if (one && rounds == 1) {
                 // All equal, as scores that no head likes are?
                 uint32_t least = ~0u, most = 0;
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if ((key[j] ^ T) >> 21 == 0) {
-                        least = min(least, key[j]);
-                        most = max(most, key[j]);
+                const uint32_t *from = sh.key + place(tid);
+#pragma unroll 1
+                for (int i = 0; i < per; ++i) {
+                    const uint32_t x = from[place(THREADS) * i];
+                    if ((x ^ T) >> 21 == 0) {
+                        least = min(least, x);
+                        most = max(most, x);
                     }
+                }
                 least = __reduce_min_sync(0xffffffffu, least);
                 most = __reduce_max_sync(0xffffffffu, most);
                 if (lane == 0) {
@@ -357,75 +431,64 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) select_kernel
     }
 
     // Kept tokens of the rows before this one, and of all.
-    uint32_t before, all_tokens;
+    uint32_t before = 0, all_tokens = 0;
     if (a.scanned) {
         before = (uint32_t)__ldg(a.indptr_out + b);
         all_tokens = (uint32_t)__ldg(a.indptr_out + rows);
     } else {
-        const uint32_t x = __reduce_add_sync(0xffffffffu, tid < b ? my_tokens : 0);
-        const uint32_t y = __reduce_add_sync(0xffffffffu, my_tokens);
-        if (lane == 0) {
-            sh.red[0][warp] = x;
-            sh.red[1][warp] = y;
+#pragma unroll 1
+        for (int i = tid; i < rows; i += THREADS) {
+            const uint32_t n = (uint32_t)row_of(a, i).tokens;
+            before += i < b ? n : 0;
+            all_tokens += n;
         }
+        before = __reduce_add_sync(0xffffffffu, before);
+        all_tokens = __reduce_add_sync(0xffffffffu, all_tokens);
+        if (lane == 0) sh.red[0][warp] = before, sh.red[1][warp] = all_tokens;
     }
 
     // A block outside [lo, hi), or any when all stay, is sure; between, those
     // above T are, and those equal to T are ties (sure too when all of them
-    // stay).  Bits of this thread's keys.
+    // stay).  Bits of this thread's keys of a round; their counts (at most
+    // ROUND each in a block), summed over the threads.
     const bool all = m >= hi - lo;
     uint32_t sure = 0, tie = 0;
     const auto upto = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
-    const auto mark = [&](int q) {
-        const int i0 = s0 + q * kRound + tid * kPer, n = min(s1, s0 + (q + 1) * kRound) - i0;      // keys of the round here
-        const uint32_t valid = upto(min(n, kPer)), inside = upto(hi - i0) & ~upto(lo - i0);
+    const auto mark = [&](int q, int buffer) {
+        const int e0 = tid * per, i0 = s0 + q * ROUND + e0, n = min(s1, s0 + (q + 1) * ROUND) - i0;
+        const uint32_t valid = upto(min(n, per)), inside = upto(hi - i0) & ~upto(lo - i0);
         sure = all ? valid : valid & ~inside;
         tie = 0;
         if (select) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                if (key[j] >= T) sure |= 1u << j;
-                if (key[j] == T) tie |= 1u << j;
+            uint32_t ge = 0, eq = 0;
+#pragma unroll 2
+            for (int j = 0; j < per; ++j) {
+                const uint32_t x = sh.key[place(e0 + j)];
+                ge |= (uint32_t)(x >= T) << j;
+                eq |= (uint32_t)(x == T) << j;
             }
-            tie &= valid & inside;
-            sure &= valid;
-            if (tied) sure &= ~tie;
-            else tie = 0;
+            sure |= ge & valid;         // (a key outside is 0)
+            if (tied) {
+                tie = eq & valid & inside;
+                sure &= ~tie;
+            }
         }
-        return (uint32_t)__popc(sure) | (uint32_t)__popc(tie) << 16;     // at most kRound each in a block's round
+        return block_sums<THREADS>((uint32_t)__popc(sure) | (uint32_t)__popc(tie) << 16, sh.scan[buffer]);
     };
-    // Prefix over the block's threads of such counts, and their sum.
-    const auto scan = [&](uint32_t x, uint32_t &total) {
-        uint32_t incl = x;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-        }
-        if (lane == 31) sh.totals[warp] = incl;
-        __syncthreads();
-        const uint32_t t = lane < kWarps ? sh.totals[lane] : 0;
-        total = __reduce_add_sync(0xffffffffu, t);
-        return incl - x + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
-    };
-    uint32_t total, at = 0;
+    uint2 at = make_uint2(0, 0);
     uint32_t block_kept = 0, block_ties = 0;        // sure blocks and ties of the thread blocks before this one
-    if (rounds <= 1) {
-        at = scan(rounds > 0 ? mark(0) : 0, total);
-        if (!one && tid == 0) sh.sum[0] = total & 0xffff, sh.sum[1] = total >> 16;
-    } else {
-        uint32_t sum = 0, nties = 0;
-        for (int q = 0; q < rounds; ++q) {
-            if (select) load(q);
-            __syncthreads();
-            scan(mark(q), total);
-            sum += total & 0xffff;
-            nties += total >> 16;
-        }
-        if (!one && tid == 0) sh.sum[0] = sum, sh.sum[1] = nties;
+#pragma unroll 1
+    for (int q = 0; q < max(rounds, 1); ++q) {
+        if (rounds > 1 && select) load(q);
+        else if (q > 0) __syncthreads();
+        at = mark(q, 1);
+        block_kept += at.y & 0xffff;
+        block_ties += at.y >> 16;
     }
+    if (!one && tid == 0) sh.sum[0] = block_kept, sh.sum[1] = block_ties;
+    block_kept = block_ties = 0;
     if (!a.scanned) {
-        // (written before the barrier in scan)
+        // (written before the barrier in mark)
         before = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red[0][lane] : 0);
         all_tokens = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red[1][lane] : 0);
         if (tid == 0 && rank == 0) {
@@ -446,40 +509,43 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) select_kernel
     // Placement, in position order.  Places past the output (only requests
     // that share entries, a bad indptr, make them) are dropped.
     const int32_t *pages = a.pages + row.base;
-    const int64_t limit = a.capacity;
+    const uint32_t limit = (uint32_t)a.capacity;
+#pragma unroll 1
     for (int q = 0; q < rounds; ++q) {
         if (rounds > 1) {
             if (select) load(q);
-            __syncthreads();
-            at = scan(mark(q), total);
+            else __syncthreads();
+            at = mark(q, 1);
+            __syncthreads();        // the keys have been read
         }
         // kept blocks of the row before this round: the sure ones and the ties among the first `ties`
         const uint32_t first = block_kept + min(block_ties, ties);
-        uint32_t tie_at = block_ties + (at >> 16);
-        uint32_t put = block_kept + (at & 0xffff) + min(tie_at, ties) - first;
-        block_kept += total & 0xffff;
-        block_ties += total >> 16;
+        const uint32_t tie_at = block_ties + (at.x >> 16);
+        uint32_t put = block_kept + (at.x & 0xffff) + min(tie_at, ties) - first;
+        block_kept += at.y & 0xffff;
+        block_ties += at.y >> 16;
         const uint32_t n = (block_kept + min(block_ties, ties) - first) << lb;      // tokens
-        const int i0 = s0 + q * kRound + tid * kPer;
-        if (rounds > 1) __syncthreads();
-        int32_t *list = reinterpret_cast<int32_t *>(sh.key);       // the keys are in registers
-        uint32_t keep = sure | tie;
-        while (keep) {
-            const int j = __ffs(keep) - 1;
-            keep &= keep - 1;
-            if ((tie >> j & 1) && tie_at++ >= ties) continue;
-            list[put++] = i0 + j;
-        }
+        int32_t *list = reinterpret_cast<int32_t *>(sh.key);
+        // Of this thread's ties those among the first `ties`.
+        const uint32_t mine = __popc(tie), past = tie_at + mine > ties ? min(mine, tie_at + mine - ties) : 0;
+#pragma unroll 1
+        for (uint32_t i = 0; i < past; ++i) tie &= ~(0x80000000u >> __clz(tie));
+        const uint32_t keep = sure | tie;
+        const int i0 = s0 + q * ROUND + tid * per;
+#pragma unroll 2
+        for (int j = 0; j < per; ++j)
+            if (keep >> j & 1) list[put++] = i0 + j;
         __syncthreads();
         const uint32_t to = before + (first << lb);
+#pragma unroll 4
         for (uint32_t x = tid; x < n; x += THREADS) {
             const int i = (list[x >> lb] << lb) + (int)(x & ((1u << lb) - 1));
             if (i < row.seen && to + x < limit) a.pages_out[to + x] = __ldg(pages + i);
         }
     }
     if (rank == 0)
-        for (int64_t i = all_tokens + ((int64_t)b * THREADS + tid); i < limit; i += (int64_t)rows * THREADS)
-            a.pages_out[i] = -1;
+#pragma unroll 1
+        for (uint64_t i = all_tokens + ((uint64_t)b * THREADS + tid); i < limit; i += (uint64_t)rows * THREADS) a.pages_out[i] = -1;
     if (!one) cluster_sync();                  // no block ends while another may read its shared memory
 }
 
@@ -506,10 +572,10 @@ __global__ void __launch_bounds__(256) empty_kernel(const SelectArgs a) {
     for (int64_t i = at; i < a.capacity; i += (int64_t)gridDim.x * 256) a.pages_out[i] = -1;
 }
 
-template <int THREADS>
-cudaError_t launch(SelectArgs a, int log_cs, cudaStream_t st) {
-    constexpr int smem = sizeof(Shared<THREADS>);
-    cudaError_t e = smem_attr_once<select_kernel<THREADS>>(smem);
+template <int THREADS, int ROUND, bool CLUSTER, bool BLOCKED>
+cudaError_t launch_kernel(SelectArgs a, int log_cs, cudaStream_t st) {
+    constexpr int smem = sizeof(Shared<THREADS, ROUND, CLUSTER>);
+    cudaError_t e = smem_attr_once<select_kernel<THREADS, ROUND, CLUSTER, BLOCKED>>(smem);
     if (e != cudaSuccess) return e;
     static std::atomic<unsigned long long> wide{0};     // devices where clusters of 16 have been allowed
     if (log_cs > 3) {
@@ -518,13 +584,13 @@ cudaError_t launch(SelectArgs a, int log_cs, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
         if (!(bit & wide.load(std::memory_order_acquire))) {
-            e = cudaFuncSetAttribute(select_kernel<THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            e = cudaFuncSetAttribute(select_kernel<THREADS, ROUND, CLUSTER, BLOCKED>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
             wide.fetch_or(bit, std::memory_order_release);
         }
     }
     const int rows = a.R * a.qlen;
-    a.scanned = rows > THREADS;
+    a.scanned = rows > kCounted;
     if (a.scanned) {
         indptr_kernel<<<1, 1024, 0, st>>>(a);
         e = cudaGetLastError();
@@ -541,7 +607,13 @@ cudaError_t launch(SelectArgs a, int log_cs, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = log_cs > 0 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, select_kernel<THREADS>, a, log_cs);
+    return cudaLaunchKernelEx(&cfg, select_kernel<THREADS, ROUND, CLUSTER, BLOCKED>, a, log_cs);
+}
+
+template <int THREADS, int ROUND, bool CLUSTER>
+cudaError_t launch(const SelectArgs &a, int log_cs, cudaStream_t st) {
+    return a.log_block > 0 ? launch_kernel<THREADS, ROUND, CLUSTER, true>(a, log_cs, st)
+                           : launch_kernel<THREADS, ROUND, CLUSTER, false>(a, log_cs, st);
 }
 
 }  // namespace
@@ -562,6 +634,7 @@ cudaError_t index_select_launch(const float *scores, const int32_t *pages, int64
     while ((1 << a.log_block) < block) ++a.log_block;
     a.recent = recent;
     a.sinks = sinks;
+    a.over_qlen = qlen > 1 ? (uint32_t)((0x100000000ull + qlen - 1) / qlen) : 0;
     a.causal = causal;
     a.pages_out = pages_out;
     a.indptr_out = indptr_out;
@@ -570,12 +643,14 @@ cudaError_t index_select_launch(const float *scores, const int32_t *pages, int64
         empty_kernel<<<(unsigned)std::min<int64_t>((capacity + 255) / 256 + 1, sms), 256, 0, st>>>(a);
         return cudaGetLastError();
     }
-    // The lengths are on the device: a cluster holds a row of the mean length
-    // in one round, and a few rows take the blocks that half the SMs hold.
-    const int64_t mean = (num_pages + R - 1) / R;
+    // The lengths are on the device.  Rows of the mean length share a thread
+    // block's round or a cluster's; few rows take the blocks that half the SMs
+    // hold; more rows than SMs that fit half a round of 256 threads take these.
+    const int64_t mean = (num_pages + R - 1) / R, blocks = mean >> a.log_block;
+    if (rows > sms && blocks <= kShort / 2) return launch<256, kShort, false>(a, 0, st);
     int log_cs = 0;
-    while (log_cs < 4 && ((mean >> a.log_block >> log_cs) > kRound || (rows << (log_cs + 1)) <= sms / 2)) ++log_cs;
-    return log_cs == 0 && rows <= sms ? launch<1024>(a, log_cs, st) : launch<512>(a, log_cs, st);
+    while (log_cs < 4 && ((blocks >> log_cs) > kLong || (rows << (log_cs + 1)) <= sms / 2)) ++log_cs;
+    return log_cs == 0 && rows <= sms ? launch<1024, kLong, false>(a, log_cs, st) : launch<512, kLong, true>(a, log_cs, st);
 }
 
 cudaError_t index_select_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }

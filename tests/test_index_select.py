@@ -161,6 +161,8 @@ def _rand(qlen, total, seed=0):
     ([9, 0, 2, 40] * 300, 1, 8, 1, 1, 0),
     ([9, 0, 2, 40] * 300, 2, 3, 8, 1, 1),
     ([40000] * 3 + [50] * 100, 1, 512, 1, 0, 0),
+    ([50] * 300 + [20000, 9000, 4097, 4096] + [700] * 100, 1, 512, 1, 3, 1),
+    ([300] * 160 + [70000, 33000], 2, 600, 8, 1, 0),
 ])
 def test_lists(lengths, qlen, topk, block, recent, sinks, causal):
     _run(_rand(qlen, sum(lengths)), lengths, topk, block, recent, sinks, causal)
