@@ -35,6 +35,27 @@ inline cudaError_t smem_attr_once(int bytes) {
     return e;
 }
 
+// Launches a kernel that may start while the one before it on the stream still
+// runs (programmatic dependent launch): it calls grid_wait() before it touches
+// memory that other kernels touch.
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, int smem, cudaStream_t st,
+                                const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// Until the kernels before this one have completed and their writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 static inline cudaError_t read_status(unsigned int *flags, bool clear) {
     cudaError_t e = cudaMemcpyFromSymbol(flags, g_status, sizeof(unsigned int));
     if (e == cudaSuccess && clear) {

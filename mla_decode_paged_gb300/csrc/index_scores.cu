@@ -33,12 +33,13 @@
 namespace mla {
 namespace {
 
-constexpr int kMmaWarp = 8, kProdWarp0 = 9, kProdWarps = 4, kPrepWarp = 13;
+constexpr int kMmaWarp = 16, kProdWarp0 = 17, kProdWarps = 4, kPrepWarp = 21;
 constexpr int kThreads = (kPrepWarp + 1) * 32;
 constexpr int kTile = 128, kRow = MLA_D_INDEX, kStages = 8, kAhead = 8;
 constexpr int kStageBytes = kTile * kRow;
 constexpr int kCols = 256;                          // columns of a group, at most
-constexpr int kQBufs = 2, kConstBufs = 4;           // requests' queries; their weights, which outlive two more requests'
+constexpr int kTmemCols = 512;                      // four tiles of up to 128 columns in flight, or two
+constexpr int kQBufs = 2, kConstBufs = 8;           // requests' queries; their weights (six requests' may be in flight)
 constexpr int kOffQ = kStages * kStageBytes, kOffMisc = kOffQ + kQBufs * kCols * kRow;
 constexpr long long kTileCycles = 1 << 16;          // more than a tile takes
 
@@ -49,12 +50,13 @@ struct ScoreArgs {
     int64_t pool_rows, num_pages;
     int R, qlen, heads, causal, groups, virt;
     int rows, hp;           // query rows of a group; a row's columns
+    int bufs;               // accumulators: 4, or 2 where rows * hp exceeds 128
     float scale;
 };
 
 struct Misc {
     float4 w[kConstBufs][kCols / 4];
-    uint64_t kv_full[kStages], kv_empty[kStages], d_full[2], d_free[2], q_full[kQBufs], q_free[kQBufs], fin;
+    uint64_t kv_full[kStages], kv_empty[kStages], d_full[4], d_free[4], q_full[kQBufs], q_free[kQBufs], fin;
     uint32_t tmem;
     int abort_flag;
     int start[3];
@@ -77,11 +79,8 @@ __device__ void producer(const ScoreArgs &a, const CUtensorMap *mk, uint8_t *sm,
         const int64_t at = (int64_t)w.base + (int64_t)(w.t + tiles) * kTile + 32 * lane;
         if (lane < 5 && at < a.num_pages) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pages + at));
     };
-    int it = 0;
-    const auto skip = [&](int n) {
-        for (int k = 0; k < n && w.valid(); ++k, ++it) w.next(a);
-    };
-    skip(pw);
+    int it = pw;
+    w.skip(a, pw);
     if (w.valid())
         for (int k = kProdWarps; k < kAhead; k += kProdWarps) ahead(k);
     int rows[4];
@@ -92,7 +91,8 @@ __device__ void producer(const ScoreArgs &a, const CUtensorMap *mk, uint8_t *sm,
         ahead(kAhead);
         const int now = it, s = now % kStages;
         // The next tile's indices are on their way while this one's copies are issued.
-        skip(kProdWarps);
+        w.skip(a, kProdWarps);
+        it += kProdWarps;
         int next[4];
         const int nn = load(next);
         // Past the request the copy fills zeros (row -1).
@@ -132,15 +132,16 @@ __device__ void mma_issuer(const ScoreArgs &a, uint8_t *sm, Misc &ms) {
     const uint64_t k0 = tc::sdesc(base, 16, 1024, tc::kSw128), q0 = tc::sdesc(base + kOffQ, 16, 1024, tc::kSw128);
     Walk<kTile> w;
     w.init(a, ms.start);
+    const int log_bufs = a.bufs >> 1, cols = kTmemCols >> log_bufs;
     for (int it = 0; w.valid(); ++it, w.next(a)) {
-        const int s = it % kStages, d = it & 1, b = w.unit % kQBufs;
+        const int s = it % kStages, d = it & (a.bufs - 1), b = w.unit % kQBufs;
         if (w.first && !warp_wait(&ms.q_full[b], (w.unit / kQBufs) & 1, &ms.abort_flag)) break;
-        if (!warp_wait(&ms.d_free[d], ((it >> 1) & 1) ^ 1, &ms.abort_flag)) break;
+        if (!warp_wait(&ms.d_free[d], ((it >> log_bufs) & 1) ^ 1, &ms.abort_flag)) break;
         if (!warp_wait(&ms.kv_full[s], (it / kStages) & 1, &ms.abort_flag)) break;
         tc::fence_after();
         const uint64_t kd = k0 + s * (kStageBytes >> 4), qd = q0 + b * ((kCols * kRow) >> 4);
 #pragma unroll
-        for (int j = 0; j < kRow / 32; ++j) mma(tm + d * kCols, kd + 2 * j, qd + 2 * j, idesc, j > 0, one);
+        for (int j = 0; j < kRow / 32; ++j) mma(tm + d * cols, kd + 2 * j, qd + 2 * j, idesc, j > 0, one);
         if (one) {
             tc::commit(&ms.kv_empty[s]);
             tc::commit(&ms.d_full[d]);
@@ -157,7 +158,6 @@ __device__ void mma_issuer(const ScoreArgs &a, uint8_t *sm, Misc &ms) {
 // The requests' queries and weights.
 __device__ void prepare(const ScoreArgs &a, const CUtensorMap *mq, uint8_t *sm, Misc &ms, int grp) {
     const int lane = threadIdx.x & 31;
-    constexpr int kPer = kCols / 32;
     const int tq0 = grp * a.rows, rows = min(a.rows, a.qlen - tq0);
     Walk<kTile> w;
     w.init(a, ms.start);
@@ -171,74 +171,93 @@ __device__ void prepare(const ScoreArgs &a, const CUtensorMap *mq, uint8_t *sm, 
         tiles = 0;
         const int u = w.unit, b = u % kQBufs;
         const int64_t row0 = (int64_t)w.r * a.qlen + tq0;
-        float c[kPer];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int n = lane + 32 * k, tq = n / a.hp, h = n - tq * a.hp;
-            c[k] = 0.f;
-            if (tq < rows && h < a.heads) {
-                const int64_t at = (row0 + tq) * a.heads + h;
-                c[k] = __ldg(a.weights + at) * (a.q_scales ? __ldg(a.q_scales + at) : 1.f) * a.scale;
-            }
-        }
         // All MMAs of the request two before: a wait for tiles, not for one.
         if (!(ok = warp_wait_long(&ms.q_free[b], ((u / kQBufs) & 1) ^ 1, &ms.abort_flag,
                                   kWaitCycles + pending * kTileCycles)))
             break;
-        float *to = reinterpret_cast<float *>(ms.w[u % kConstBufs]);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) to[lane + 32 * k] = c[k];
-        __syncwarp();
         if (lane == 0) {
             mbar_arrive_expect_tx(&ms.q_full[b], rows * a.heads * kRow);
             for (int tq = 0; tq < rows; ++tq)
                 tc::tma_2d(sm + kOffQ + (b * kCols + tq * a.hp) * kRow, mq, 0, (int)((row0 + tq) * a.heads), &ms.q_full[b]);
         }
         __syncwarp();
+        // (Their readers are done, too: see kConstBufs.)
+        float *to = reinterpret_cast<float *>(ms.w[u % kConstBufs]);
+        float c[kCols / 32];
+        int tq = 0, h = lane;       // of column lane + 32 k
+#pragma unroll
+        for (int k = 0; k < kCols / 32; ++k, h += 32) {
+            if (h >= a.hp) h -= a.hp, ++tq;
+            if (h >= a.hp) h -= a.hp, ++tq;
+            c[k] = 0.f;
+            if (tq < rows && h < a.heads) {
+                const int64_t at = (row0 + tq) * a.heads + h;
+                c[k] = __ldg(a.weights + at) * (a.q_scales ? __ldg(a.q_scales + at) : 1.f) * a.scale;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kCols / 32; ++k) to[lane + 32 * k] = c[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.q_full[b]);
         issued = u + 1;
     }
     if (!ok)        // flagged: the copies in flight land before the CTA ends
         for (int u = max(issued - kQBufs, 0); u < issued; ++u) mbar_wait(&ms.q_full[u % kQBufs], (u / kQBufs) & 1);
 }
 
+// Warpgroup wg takes the tiles of accumulator wg, or with two accumulators
+// half of the query rows of accumulator wg & 1's.
 __device__ void epilogue(const ScoreArgs &a, Misc &ms, int grp) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2, wq = warp & 3;
-    const uint32_t taddr = ms.tmem + wg * kCols + ((uint32_t)(32 * wq) << 16);
-    const int tq0 = grp * a.rows, rows = min(a.rows, a.qlen - tq0), steps = a.hp / 16;
+    const int log_bufs = a.bufs >> 1, d = wg & (a.bufs - 1), cols = kTmemCols >> log_bufs, steps = a.hp / 16;
+    const int all = min(a.rows, a.qlen - grp * a.rows), half = (all + 1) / 2;
+    const int first = a.bufs == 4 || wg < 2 ? 0 : half, rows = a.bufs == 4 ? all : wg < 2 ? half : all - half;
+    const uint32_t taddr = ms.tmem + d * cols + first * a.hp + ((uint32_t)(32 * wq) << 16);
+    const int tq0 = grp * a.rows + first, chunks = rows * steps;
     Walk<kTile> w;
     w.init(a, ms.start);
-    for (int it = 0; w.valid(); ++it, w.next(a)) {
-        if ((it & 1) != wg) continue;
+    w.skip(a, d);
+    for (int it = 0; w.valid(); ++it, w.skip(a, a.bufs)) {      // every bufs-th tile
         const int j = w.t * kTile + 32 * wq + lane;
         float *out = a.out + (int64_t)tq0 * a.num_pages + w.base + j;
-        if (!warp_wait(&ms.d_full[wg], (it >> 1) & 1, &ms.abort_flag)) break;
+        if (!warp_wait(&ms.d_full[d], it & 1, &ms.abort_flag)) break;
         tc::fence_after();
-        const float4 *c = ms.w[w.unit % kConstBufs];
-        uint32_t at = taddr;
-        for (int tq = 0; tq < rows; ++tq, out += a.num_pages) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int k = 0; k < steps; ++k, at += 16, c += 4) {
-                float x[16];
-                tc::ld16(at, x);
-                tc::wait_ld();
+        const float4 *c = ms.w[w.unit % kConstBufs] + first * (a.hp / 4);
+        uint64_t sum[2] = {0, 0};
+        int step = 0, seen = a.causal ? w.len - a.qlen + tq0 + 1 : w.len;       // tokens that the row sees
+        // 16 heads' columns of this token; a row's last ones end its sum.
+        const auto add = [&](const float (&x)[16]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 ws = c[i];
-                    sum[0] = fmaf(max_nan(x[4 * i], 0.f), ws.x, sum[0]);
-                    sum[1] = fmaf(max_nan(x[4 * i + 1], 0.f), ws.y, sum[1]);
-                    sum[2] = fmaf(max_nan(x[4 * i + 2], 0.f), ws.z, sum[2]);
-                    sum[3] = fmaf(max_nan(x[4 * i + 3], 0.f), ws.w, sum[3]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float4 ws = *c++;
+                sum[0] = fma2(pair(max_nan(x[4 * i], 0.f), max_nan(x[4 * i + 1], 0.f)), pair(ws.x, ws.y), sum[0]);
+                sum[1] = fma2(pair(max_nan(x[4 * i + 2], 0.f), max_nan(x[4 * i + 3], 0.f)), pair(ws.z, ws.w), sum[1]);
             }
-            if (tq == rows - 1) {
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.d_free[wg]);
-            }
-            const bool seen = !a.causal || j < w.len - a.qlen + tq0 + tq + 1;
-            if (j < w.len) *out = seen ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : -INFINITY;
+            if (++step < steps) return;
+            const float2 s0 = parts(sum[0]), s1 = parts(sum[1]);
+            if (j < w.len) *out = j < seen ? (s0.x + s1.x) + (s0.y + s1.y) : -INFINITY;
+            out += a.num_pages;
+            sum[0] = sum[1] = 0;
+            step = 0;
+            if (a.causal) ++seen;
+        };
+        float x[2][16];
+        if (chunks > 0) tc::ld16(taddr, x[0]);
+        tc::wait_ld();
+#pragma unroll 1
+        for (int g = 0; g < chunks; g += 2) {
+            // The next columns leave TMEM while these are summed.
+            if (g + 1 < chunks) tc::ld16(taddr + 16 * (g + 1), x[1]);
+            add(x[0]);
+            tc::wait_ld();
+            if (g + 1 >= chunks) break;
+            if (g + 2 < chunks) tc::ld16(taddr + 16 * (g + 2), x[0]);
+            add(x[1]);
+            tc::wait_ld();
         }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.d_free[d]);
     }
 }
 
@@ -249,15 +268,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc &ms = *reinterpret_cast<Misc *>(sm + kOffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, grp = blockIdx.x % a.groups;
     if (tid == 0) {
+        tc::prefetch_map(&mk);
+        tc::prefetch_map(&mq);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&ms.kv_full[s], 1);
             mbar_init(&ms.kv_empty[s], 1);
         }
-        for (int d = 0; d < 2; ++d) {
+        for (int d = 0; d < 4; ++d) {
             mbar_init(&ms.d_full[d], 1);
-            mbar_init(&ms.d_free[d], 4);
-            mbar_init(&ms.q_full[d], 1);
-            mbar_init(&ms.q_free[d], 1);
+            mbar_init(&ms.d_free[d], a.bufs == 4 ? 4 : 8);      // warps that read it
+        }
+        for (int b = 0; b < kQBufs; ++b) {
+            mbar_init(&ms.q_full[b], 2);        // the copies' and the weights'
+            mbar_init(&ms.q_free[b], 1);
         }
         mbar_init(&ms.fin, 1);
         ms.abort_flag = 0;
@@ -265,17 +288,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_fence_init();
     }
     // Columns that no copy fills hold zeros: their weights are 0, but a NaN code would stay.
-    for (int i = tid; i < kQBufs * kCols * (kRow / 16); i += kThreads) {
-        const int n = i / (kRow / 16) % kCols, tq = n / a.hp;
-        if (n - tq * a.hp >= a.heads || tq >= min(a.rows, a.qlen - grp * a.rows))
-            *reinterpret_cast<uint4 *>(sm + kOffQ + 16 * i) = make_uint4(0, 0, 0, 0);
+    const int rows = min(a.rows, a.qlen - grp * a.rows);
+    if (a.hp != a.heads || rows < a.rows) {
+#pragma unroll 1
+        for (int i = tid; i < kQBufs * kCols * (kRow / 16); i += kThreads) {
+            const int n = i / (kRow / 16) % kCols, tq = n / a.hp;
+            if (n - tq * a.hp >= a.heads || tq >= rows) *reinterpret_cast<uint4 *>(sm + kOffQ + 16 * i) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_async_smem();
     }
-    tc::fence_async_smem();
-    if (warp == kMmaWarp) tc::tmem_alloc(&ms.tmem, 2 * kCols);
+    if (warp == kMmaWarp) tc::tmem_alloc(&ms.tmem, kTmemCols);
     tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
+    grid_wait();
     find_start<kTile, kThreads>(a, ms.start, blockIdx.x / a.groups);
+    tc::fence_after();
     if (warp < kMmaWarp) epilogue(a, ms, grp);
     else if (warp == kMmaWarp) mma_issuer(a, sm, ms);
     else if (warp < kPrepWarp) producer(a, &mk, sm, ms);
@@ -283,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == kMmaWarp) tc::tmem_free(ms.tmem, 2 * kCols);
+    if (warp == kMmaWarp) tc::tmem_free(ms.tmem, kTmemCols);
 }
 
 // [rows, 128] bytes, read `box` rows at a time.
@@ -322,13 +348,13 @@ cudaError_t index_scores_launch(const void *q, const float *weights, const float
     const int most = kCols / a.hp;
     a.groups = (qlen + most - 1) / most;
     a.rows = (qlen + a.groups - 1) / a.groups;
+    a.bufs = a.rows * a.hp <= kTmemCols / 4 ? 4 : 2;
     a.virt = sms / a.groups < 1 ? 1 : sms / a.groups;
     constexpr int smem = kOffMisc + sizeof(Misc) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = smem_attr_once<index_scores_kernel>(smem);
     if (e != cudaSuccess) return e;
-    index_scores_kernel<<<a.virt * a.groups, kThreads, smem, st>>>(mk, mq, a);
-    return cudaGetLastError();
+    return launch_early(index_scores_kernel, a.virt * a.groups, kThreads, smem, st, mk, mq, a);
 }
 
 cudaError_t index_scores_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }

@@ -51,6 +51,11 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x,
         : "memory");
 }
 
+// Brings a tensor map to where the copies read it from.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // L2 cache policy for data read once (evict first) or as usual.
 __device__ __forceinline__ uint64_t l2_policy(bool evict_first) {
     uint64_t p;

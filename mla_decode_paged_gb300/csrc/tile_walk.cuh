@@ -33,6 +33,18 @@ struct Walk {
     }
     __device__ bool valid() const { return left > 0; }
     __device__ bool last() const { return left == 1 || t + 1 == ntiles; }
+    // Past n tiles, or past the last.
+    template <class A>
+    __device__ __forceinline__ void skip(const A &a, int n) {
+        if (left > n && t + n < ntiles) {
+            t += n;
+            left -= n;
+            first = false;
+            return;
+        }
+#pragma unroll 1
+        for (int k = 0; k < n && left > 0; ++k) next(a);
+    }
     template <class A>
     __device__ void next(const A &a) {
         --left;
@@ -64,16 +76,47 @@ struct Walk {
 };
 
 // Share v's range of the batch's tiles -> start.  Run by all THREADS of the
-// block; start[0] and start[1] are 0 before.  Requests that share entries (a
-// bad indptr only) count up to what the page list could hold.
+// block (it passes a barrier before it reads start); start[0] and start[1] are
+// 0 before.  Requests that share entries (a bad indptr only) count up to what
+// the page list could hold.
 template <int TOKENS, int THREADS, class A>
 __device__ void find_start(const A &a, int (&start)[3], int v) {
     __shared__ long long part[THREADS / 32 + 1];
+    __shared__ uint32_t part32[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const auto tiles_of = [&](int r) {
         int base;
         return (request_len(a.indptr, r, a.num_pages, &base) + TOKENS - 1) / TOKENS;
     };
+    const int64_t most = a.num_pages / TOKENS + a.R;     // tiles
+    // Shares that differ by one at most, the larger ones first.
+    const auto range = [&](uint32_t total, uint32_t &lo, uint32_t &n) {
+        const uint32_t each = total / (uint32_t)a.virt, more = total - each * a.virt;
+        lo = each * v + min((uint32_t)v, more);
+        n = each + ((uint32_t)v < more ? 1 : 0);
+    };
+    if (a.R <= THREADS && most * a.R < INT32_MAX) {      // in one step, in 32 bits
+        const uint32_t n = tid < a.R ? tiles_of(tid) : 0;
+        uint32_t incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += x;
+        }
+        if (lane == 31) part32[warp] = incl;
+        __syncthreads();
+        const uint32_t w = lane < THREADS / 32 ? part32[lane] : 0;
+        const uint32_t at = incl - n + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+        uint32_t lo, count;
+        range(min(__reduce_add_sync(0xffffffffu, w), (uint32_t)most), lo, count);
+        if (tid == 0) start[2] = (int)count;
+        if (at <= lo && lo < at + n) {
+            start[0] = tid;
+            start[1] = (int)(lo - at);
+        }
+        __syncthreads();
+        return;
+    }
     int mine = 0;
     long long sum = 0;
     for (int r = tid; r < a.R; r += THREADS) {
@@ -86,9 +129,10 @@ __device__ void find_start(const A &a, int (&start)[3], int v) {
     __syncthreads();
     long long total = 0;
     for (int w = 0; w < THREADS / 32; ++w) total += part[w];
-    total = min(total, (long long)(a.num_pages / TOKENS + a.R));
-    const int64_t lo = total * v / a.virt, hi = total * (v + 1) / a.virt;
-    if (tid == 0) start[2] = (int)(hi - lo);
+    uint32_t first, count;
+    range((uint32_t)min(total, (long long)most), first, count);
+    const int64_t lo = first;
+    if (tid == 0) start[2] = (int)count;
     int64_t before = 0;   // tiles of the requests before this chunk
     for (int r0 = 0; r0 < a.R && before <= lo; r0 += THREADS) {
         const int r = r0 + tid;
