@@ -337,6 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc<C> &ms = *reinterpret_cast<Misc<C> *>(sm + C::OffMisc);
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
+        tc::prefetch_map(&mq);
+        tc::prefetch_map(&mw);
+        tc::prefetch_map(&mo);
         for (int s = 0; s < C::Subs; ++s) {
             mbar_init(&ms.w_full[s], 1);
             mbar_init(&ms.w_free[s], 1);
@@ -357,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    grid_wait();
     if (warp < kProdWarp) epilogue<C, FP8>(a, &mo, sm, ms);
     else if (warp == kProdWarp) producer<C>(a, &mq, &mw, sm, ms);
     else if (warp == kMmaWarp) mma_issuer<C>(a, sm, ms);
@@ -397,8 +401,7 @@ cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mw, const CUtensorM
     cudaError_t e = smem_attr_once<absorb_kernel<NC, FP8>>(smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.H * C::Chunks * a.tiles;
-    absorb_kernel<NC, FP8><<<(unsigned)(units < sms ? units : sms), kThreads, smem, st>>>(mq, mw, mo, a);
-    return cudaGetLastError();
+    return launch_early(absorb_kernel<NC, FP8>, (unsigned)(units < sms ? units : sms), kThreads, smem, st, mq, mw, mo, a);
 }
 
 }  // namespace

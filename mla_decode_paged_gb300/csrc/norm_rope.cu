@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD)) norm_rope_
 #pragma unroll
         for (int k = 0; k < VPT; ++k) next[k] = (mine >> k & 1) ? x[vec[k]] : make_uint4(0, 0, 0, 0);
     };
+    grid_wait();
     if (kAhead) fetch(first + lane / G);
     if (NORM) {
         for (int i = threadIdx.x; i < a.norm_vecs; i += kThreads) weight[i] = __ldg(static_cast<const uint4 *>(a.weight) + i);
@@ -288,9 +289,8 @@ template <typename T, int G, int VPT, bool NORM, bool PAIRS, bool HEAD>
 cudaError_t launch_kernel(RopeArgs a, int sms, cudaStream_t st) {
     a.turns = PAIRS ? 0 : (a.rope_vecs / 2 + G - 1) / G;
     const uint32_t per_block = kThreads / G, blocks = (a.rows + per_block - 1) / per_block;
-    norm_rope_kernel<T, G, VPT, NORM, PAIRS, HEAD>
-        <<<std::min(blocks, (uint32_t)sms * blocks_per_sm(VPT, HEAD)), kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(norm_rope_kernel<T, G, VPT, NORM, PAIRS, HEAD>,
+                        std::min(blocks, (uint32_t)sms * blocks_per_sm(VPT, HEAD)), kThreads, 0, st, a);
 }
 
 template <typename T, int G, int VPT>

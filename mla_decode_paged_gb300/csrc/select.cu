@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = CLUSTER ? block_rank() : 0;
     const int rows = a.R * a.qlen, b = CLUSTER ? blockIdx.x >> log_cs : blockIdx.x, lb = BLOCKED ? a.log_block : 0;
+    grid_wait();
     const Row row = row_of(a, b);
     // The blocks past those that hold the row end (a cluster barrier waits for
     // running threads only).
@@ -555,6 +556,7 @@ __global__ void __launch_bounds__(1024) indptr_kernel(const SelectArgs a) {
     __shared__ uint32_t total;
     const int rows = a.R * a.qlen, tid = threadIdx.x;
     uint32_t carry = 0;
+    grid_wait();
     if (tid == 0) a.indptr_out[0] = 0;
     for (int b0 = 0; b0 < rows; b0 += 1024) {
         const uint32_t n = b0 + tid < rows ? (uint32_t)row_of(a, b0 + tid).tokens : 0;
@@ -592,8 +594,7 @@ cudaError_t launch_kernel(SelectArgs a, int log_cs, cudaStream_t st) {
     const int rows = a.R * a.qlen;
     a.scanned = rows > kCounted;
     if (a.scanned) {
-        indptr_kernel<<<1, 1024, 0, st>>>(a);
-        e = cudaGetLastError();
+        e = launch_early(indptr_kernel, 1, 1024, 0, st, a);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -601,12 +602,14 @@ cudaError_t launch_kernel(SelectArgs a, int log_cs, cudaStream_t st) {
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1u << log_cs;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;    // it calls grid_wait()
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1u << log_cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = log_cs > 0 ? 1 : 0;
+    cfg.numAttrs = log_cs > 0 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, select_kernel<THREADS, ROUND, CLUSTER, BLOCKED>, a, log_cs);
 }
 
