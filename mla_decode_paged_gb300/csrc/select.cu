@@ -24,9 +24,10 @@
 // again for every step.  The m-th largest key: a histogram of the first 11
 // bits, summed over the cluster through distributed shared memory, names the
 // bin that holds it; one warp finds it bit by bit among that bin's keys, up
-// to 1,024 of them.  More (many equal scores, mostly) take two more
-// histograms, of 11 and 10 bits, unless all of them are equal.  The kept
-// blocks are listed in shared memory and their tokens' pages copied from
+// to 1,024 of them.  More take another histogram, of the next 11 bits, and
+// the same search, then one of the last 10, unless all of them are equal.
+// (First digits of 12 bits: a row of 32K 13.7 us and not 12.1, as twice the
+// bins have to be summed over the cluster.)  The kept blocks are listed in shared memory and their tokens' pages copied from
 // there, coalesced.
 //
 // A row's place in the output is the sum of the kept tokens of the rows
@@ -90,7 +91,7 @@ struct __align__(16) Shared {
     uint32_t hist[kBins];
     uint32_t sums[CLUSTER ? kBins : 4];     // of this block's share of the bins, over the cluster
     uint32_t cand[kCand], all[CLUSTER ? kCand : 4];     // keys of the m-th largest's bin: this block's, the cluster's
-    uint32_t red[2][32], scan[2][32], ends[16];
+    uint32_t red[2][32], scan[2][32];
     uint32_t least, most;           // of this block's keys of that bin
     uint32_t ncand;
     uint32_t sum[2];                // this block's sure blocks and ties, for the cluster
@@ -115,6 +116,18 @@ __device__ __forceinline__ bool search(const uint32_t *p, uint32_t n, int bits, 
     uint32_t x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = lane + 32 * i < n ? p[lane + 32 * i] : 0;
+    if (bits == 32) {       // the bits that all of them share
+        uint32_t ones = ~0u, any = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            ones &= x[i] != 0 ? x[i] : ~0u;
+            any |= x[i];
+        }
+        ones = __reduce_and_sync(0xffffffffu, ones);
+        any = __reduce_or_sync(0xffffffffu, any);
+        bits = 32 - __clz(ones ^ any);
+        T = bits < 32 ? any & ~((1u << bits) - 1) : 0;
+    }
 #pragma unroll 1
     for (int bit = bits - 1; bit >= 0; --bit) {
         const uint32_t t = T | 1u << bit;
@@ -180,28 +193,30 @@ __device__ __noinline__ void load_keys(uint32_t *key, const float *w, int r0, in
     } else {
         // Block maxima (NaN ignored: as -inf).  Up to 32 tokens a block: a
         // warp's 32 lanes hold several, joined by shuffles.  More: a warp
-        // holds some blocks' tokens in eight registers a lane.
+        // holds some blocks' tokens in sixteen registers a lane.
 #pragma unroll 1
         for (int i = tid; i < held; i += THREADS) key[place(i)] = 0;
         __syncthreads();
         const int t1 = min((r0 + f1) << lb, seen), ls = lb > 5 ? lb - 5 : 0;    // 2^ls reads a block
 #pragma unroll 1
-        for (int t0 = ((r0 + f0) << lb) + 32 * 8 * warp; t0 < t1; t0 += 32 * 8 * kWarps) {
-            float v[8];
+        for (int t0 = ((r0 + f0) << lb) + 32 * 16 * warp; t0 < t1; t0 += 32 * 16 * kWarps) {
+            float v[16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 16; ++k) {
                 const int t = t0 + 32 * k + lane;
                 v[k] = t < t1 ? __ldg(w + t) : -INFINITY;
             }
             if (ls >= 1)
 #pragma unroll
-                for (int k = 0; k < 8; k += 2) v[k] = fmaxf(v[k], v[k + 1]);
+                for (int k = 0; k < 16; k += 2) v[k] = fmaxf(v[k], v[k + 1]);
             if (ls >= 2)
 #pragma unroll
-                for (int k = 0; k < 8; k += 4) v[k] = fmaxf(v[k], v[k + 2]);
-            if (ls >= 3) v[0] = fmaxf(v[0], v[4]);
+                for (int k = 0; k < 16; k += 4) v[k] = fmaxf(v[k], v[k + 2]);
+            if (ls >= 3)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 16; k += 8) v[k] = fmaxf(v[k], v[k + 4]);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
                 const int t = t0 + 32 * k;
                 if ((k & ((1 << ls) - 1)) != 0 || t >= t1) continue;
                 uint32_t x = weight_key(v[k]);
@@ -231,6 +246,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
     const int rows = a.R * a.qlen, b = CLUSTER ? blockIdx.x >> log_cs : blockIdx.x, lb = BLOCKED ? a.log_block : 0;
     grid_wait();
     const Row row = row_of(a, b);
+    const uint32_t my_tokens = !a.scanned && tid < rows ? (uint32_t)row_of(a, tid).tokens : 0;      // its loads beside the row's
     // The blocks past those that hold the row end (a cluster barrier waits for
     // running threads only).
     const int le = CLUSTER ? blocks_for(row.seen, log_cs, ROUND) : 0;
@@ -290,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
         for (int digit = few ? 3 : 0; digit < 3; ++digit) {
             const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
             const uint32_t mask = digit == 2 ? 1023u : 2047u;
-            const uint32_t top_bits = digit == 1 ? 0xffe00000u : 0xfffffc00u;     // found so far
+            const uint32_t top_bits = digit == 0 ? 0u : digit == 1 ? 0xffe00000u : 0xfffffc00u;     // found so far
             if (digit > 0) {
                 // Too many keys in T's bin for one warp.
                 if (!one) cluster_sync();       // all have read the sums
@@ -327,8 +343,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
             const uint32_t top = kBins - 1 - kOwn * tid, low = top - (kOwn - 1);
             Bins<kOwn> bin = local_bins<kOwn>(sh.hist + low);
             if constexpr (CLUSTER) if (!one) {
-                const uint32_t share = kBins >> le, owner = low >> (11 - le);       // a block's bins; these bins' block
-                uint32_t *at = sh.sums + (low & (share - 1));
+                // Bins in use lie together: each block sums every 2^le-th thread's.
+                const uint32_t owner = tid & (E - 1);
+                uint32_t *at = sh.sums + (tid >> le) * kOwn;
                 if (digit == 0) cluster_wait();
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j)
@@ -354,7 +371,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
             const uint32_t n = sh.pick[2];
             found = need == n;
             if (found || digit == 2) break;
-            if (digit > 0) continue;
             if (n <= kCand) {
                 // The bin's keys, in no order, and the search among them.
 #pragma unroll 1
@@ -364,36 +380,26 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
 #pragma unroll 4
                     for (int i = 0; i < per; ++i) {
                         const uint32_t x = from[place(THREADS) * i];
-                        if ((x ^ T) >> 21 == 0) sh.cand[atomicAdd(&sh.ncand, 1u)] = x;
+                        if ((x ^ T) >> shift == 0) sh.cand[atomicAdd(&sh.ncand, 1u)] = x;
                     }
                 }
                 if (one) __syncthreads();
                 else cluster_sync();
-                if (warp == 0) {
-                    const uint32_t *p = sh.cand;
-                    if (CLUSTER && !one) {
-                        // Every block's, one after another: where each block's end.
-                        const uint32_t mine = lane < E ? remote(&sh.ncand, lane) : 0;
-                        uint32_t end = mine;
+                if (CLUSTER && !one) {
+                    // Every block's, one after another: a warp copies a block's.
+                    const uint32_t mine = lane < E ? remote(&sh.ncand, lane) : 0;
 #pragma unroll 1
-                        for (int d = 1; d < 16; d <<= 1) {
-                            const uint32_t y = __shfl_up_sync(0xffffffffu, end, d);
-                            if (lane >= d) end += y;
-                        }
-                        if (lane < 16) sh.ends[lane] = end;
-                        __syncwarp();
-#pragma unroll 1
-                        for (uint32_t i = lane; i < n; i += 32) {
-                            uint32_t r = 0;         // the block of the i-th: the first that ends past it
-#pragma unroll 1
-                            for (uint32_t d = 8; d > 0; d >>= 1)
-                                if (sh.ends[r + d - 1] <= i) r += d;
-                            sh.all[i] = remote(&sh.cand[i - (r > 0 ? sh.ends[r - 1] : 0)], r);
-                        }
-                        __syncwarp();
-                        p = sh.all;
+                    for (uint32_t r = warp; r < E; r += kWarps) {
+                        const uint32_t first = __reduce_add_sync(0xffffffffu, lane < r ? mine : 0);
+                        const uint32_t count = __shfl_sync(0xffffffffu, mine, r);
+#pragma unroll 2
+                        for (uint32_t i = lane; i < count; i += 32) sh.all[first + i] = remote(&sh.cand[i], r);
                     }
-                    found = n <= 256 ? search<8>(p, n, 21, T, need) : search<kCand / 32>(p, n, 21, T, need);
+                    __syncthreads();
+                }
+                if (warp == 0) {
+                    const uint32_t *p = CLUSTER && !one ? sh.all : sh.cand;
+                    found = n <= 256 ? search<8>(p, n, shift, T, need) : search<kCand / 32>(p, n, shift, T, need);
                     if (lane == 0) sh.pick[0] = T, sh.pick[1] = need, sh.pick[3] = found;
                 }
                 __syncthreads();
@@ -402,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
                 found = sh.pick[3] != 0;
                 break;
             }
-            if (one && rounds == 1) {
+            if (digit == 0 && one && rounds == 1) {
                 // All equal, as scores that no head likes are?
                 uint32_t least = ~0u, most = 0;
                 const uint32_t *from = sh.key + place(tid);
@@ -437,8 +443,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
         before = (uint32_t)__ldg(a.indptr_out + b);
         all_tokens = (uint32_t)__ldg(a.indptr_out + rows);
     } else {
+        before = tid < b ? my_tokens : 0;
+        all_tokens = my_tokens;
 #pragma unroll 1
-        for (int i = tid; i < rows; i += THREADS) {
+        for (int i = tid + THREADS; i < rows; i += THREADS) {
             const uint32_t n = (uint32_t)row_of(a, i).tokens;
             before += i < b ? n : 0;
             all_tokens += n;
@@ -462,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) 
         tie = 0;
         if (select) {
             uint32_t ge = 0, eq = 0;
-#pragma unroll 2
+#pragma unroll 4
             for (int j = 0; j < per; ++j) {
                 const uint32_t x = sh.key[place(e0 + j)];
                 ge |= (uint32_t)(x >= T) << j;
