@@ -8,7 +8,9 @@
 //
 // Bound by DRAM: a row reads 384 bytes and writes 1,152 (bf16) or 576
 // (e4m3), 85 or 137 FLOP a byte; a head's W_UK is 128 KB more, which counts
-// up to some hundred tokens.
+// up to some hundred tokens.  4,096 tokens x 96 heads to e4m3 78 us (4.8 TB/s),
+// to bf16 111 (5.4); 512 x 12 8.4; 64 x 12 3.5, which is the chain of loads,
+// MMAs and stores of one unit.
 //
 // Design: one persistent CTA per SM walks a contiguous range of units (head,
 // chunk of NC columns, tile of 128 tokens; tokens fastest, so W_UK's chunk

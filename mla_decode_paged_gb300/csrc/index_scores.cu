@@ -9,7 +9,10 @@
 //
 // Bound by DRAM up to about 128 heads x rows a request (128 bytes a token,
 // and 4 a row of output), by the epilogue's two operations a token, head and
-// row above.
+// row above.  Rows of 128 bytes from random places come at 5.6 TB/s at most
+// (plain 16-byte loads of as many in flight as the SMs hold).  32 requests of
+// 32K tokens, 64 heads: 30.6 us (4.7 TB/s); 128 x 4 rows of 4K to 32K, 32
+// heads: 76 (4.8; without the sums 65); 64 requests of 1K to 8K, 64 heads: 13.
 //
 // Design: one persistent CTA per SM walks a contiguous range of the batch's
 // 128-token tiles.  Tokens are the MMA's M dimension, heads of some query
@@ -17,10 +20,11 @@
 // thread sums its heads, and no sum crosses threads (equal inputs give equal
 // bits).  A cache row is 128 bytes, one swizzled row of the operand, so a
 // gather4 fetches four tokens whole.
-//   warps 0..7    two warpgroups take the tiles in turn: the sums, the output
-//   warp 8        MMA issuer (D double-buffered in TMEM)
-//   warps 9..12   producers, a tile in four each: a gather4 a lane
-//   warp 13       a request's query by TMA and its weights, two requests deep
+//   warps 0..15   four warpgroups take the tiles in turn: the sums, the output
+//                 (two: 106 us for the 128 x 4 rows)
+//   warp 16       MMA issuer; four accumulators in TMEM up to 128 columns, two above
+//   warps 17..20  producers, a tile in four each: a gather4 a lane
+//   warp 21       a request's query by TMA and its weights, two requests deep
 // Rows whose heads exceed 256 columns are cut into groups on neighbouring
 // CTAs, which read the same tiles at about the same time.
 #include <cuda_runtime.h>

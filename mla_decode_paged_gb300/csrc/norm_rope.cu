@@ -11,15 +11,18 @@
 //   scale = amax / 448 over the row, or given.
 //
 // Bound by DRAM (4 bytes an element, 3 with an e4m3 output, each moved once)
-// for many rows, by launch and the chain position -> table -> store for few.
+// for many rows, by launch and the chain position -> table -> store for few:
+// 4,096 tokens x 96 heads of 192 columns 46.8 us (6.45 TB/s), 16,384 rows of
+// 576 columns normed, rotated, quantized and scattered 10.4 (3.2 TB/s), 64 x
+// 64 heads of 128 to codes with a scale a row 1.9.
 //
 // A group of G lanes holds a row in registers between its loads and its
-// stores: lane i has the 8-column vectors i, i + G, ... (16-byte loads).  The
-// sum of squares and the maximum are joined by shuffles inside the group, so
-// rows pass no barrier.  The other column of a pair is half a rotation away,
-// in another lane: its vector is loaded a second time (it is in L1 by then)
-// rather than shuffled, which would need a lane and a register picked by the
-// span's place.  Pairs of neighbours are inside a vector.
+// stores: 8-column vectors (16-byte loads), dealt to the lanes so that the
+// two halves of a rotated pair lie in one lane (with partners loaded a second
+// time the 96 heads took 68 us).  The sum of squares and the maximum are
+// joined by shuffles inside the group, so rows pass no barrier; the arithmetic
+// takes two columns an instruction, without which the 96 heads are bound by
+// issue.  Weights are in shared memory.
 #include <algorithm>
 
 #include <cuda_runtime.h>
