@@ -8,8 +8,8 @@
 //
 // Bound by DRAM: a row reads 384 bytes and writes 1,152 (bf16) or 576
 // (e4m3), 85 or 137 FLOP a byte; a head's W_UK is 128 KB more, which counts
-// up to some hundred tokens.  4,096 tokens x 96 heads to e4m3 78 us (4.8 TB/s),
-// to bf16 111 (5.4); 512 x 12 8.4; 64 x 12 3.5, which is the chain of loads,
+// up to some hundred tokens.  4,096 tokens x 96 heads to e4m3 75 us (5.2 TB/s),
+// to bf16 113 (5.5); 2,048 x 12 8.4; 64 x 12 3.5, which is the chain of loads,
 // MMAs and stores of one unit.
 //
 // Design: one persistent CTA per SM walks a contiguous range of units (head,
@@ -17,13 +17,13 @@
 // stays in shared memory until the head changes).  The queries are the MMA's
 // M = 128 rows, K-major as they lie in memory; W_UK's columns are its N, and
 // W_UK[h] [128][512], columns contiguous, is the MN-major operand as it lies:
-// nothing is transposed.  SUB columns at a time go to one of two accumulators
-// in TMEM, each with a warpgroup of its own that rounds and stores it while
-// the MMAs fill the other: a warp's 32 rows of 128 bytes pass through shared
+// nothing is transposed.  128 columns at a time go to one of four accumulators
+// in TMEM, whose two warpgroups round and store them in turn while the MMAs
+// fill the others (two accumulators of 256: e4m3 78 us, bf16 112): a warp's 32 rows of 128 bytes pass through shared
 // memory, so that eight lanes write a row (by TMA stores of 128 rows x 128
 // bytes, 1,270 cycles each: 122 us for 4,096 x 96 heads in bf16, 107 in e4m3).
-//   warps 0..7    two epilogue warpgroups, one an accumulator
-//   warp 8        TMA loads: W_UK a SUB at a time, the tiles' queries
+//   warps 0..7    two epilogue warpgroups
+//   warp 8        TMA loads: W_UK 128 columns at a time, the tiles' queries
 //   warp 9        MMA issuer
 //   warps 10..13  the rotated columns, registers only
 #include <cuda_runtime.h>
@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kProdWarp = 8, kMmaWarp = 9, kRopeWarp0 = 10, kRopeWarps = 4;
 constexpr int kThreads = (kRopeWarp0 + kRopeWarps) * 32;
+constexpr int kBufs = 4;       // accumulators
 constexpr int kTile = 128, kNope = 128, kBlock = kTile * 128;     // 128 rows of 128 bytes
 constexpr int kHeadCols = kNope + MLA_D_ROPE;
 
@@ -53,13 +54,13 @@ struct AbsorbArgs {
 
 template <int NC, bool FP8>
 struct Cfg {
-    static constexpr int Sub = NC < 256 ? NC : 256, Subs = NC / Sub, Chunks = MLA_D_LATENT / NC;
+    static constexpr int Sub = NC < 128 ? NC : 128, Subs = NC / Sub, Chunks = MLA_D_LATENT / NC;
     static constexpr int Stages = NC == 512 ? 2 : 3;        // query tiles
     static constexpr int Cols = FP8 ? 128 : 64;             // of a row's 128 bytes
     static_assert(Sub % Cols == 0, "whole stores");
     static constexpr int OffQ = NC / 64 * kBlock, OffOut = OffQ + Stages * 2 * kBlock;
     static constexpr int OffMisc = OffOut + 2 * kBlock;
-    static constexpr uint32_t TmemCols = 2 * Sub;
+    static constexpr uint32_t TmemCols = kBufs * Sub;
     // kind::f16: bf16 operands, B MN-major, f32 sums, M = 128, N = Sub.
     static constexpr uint32_t Idesc =
         (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(Sub >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -67,7 +68,7 @@ struct Cfg {
 
 template <class C>
 struct Misc {
-    uint64_t w_full[C::Subs], w_free[C::Subs], q_full[C::Stages], q_free[C::Stages], d_full[2], d_free[2], fin;
+    uint64_t w_full[C::Subs], w_free[C::Subs], q_full[C::Stages], q_free[C::Stages], d_full[kBufs], d_free[kBufs], fin;
     uint32_t tmem;
     int abort_flag;
 };
@@ -161,9 +162,9 @@ __device__ void mma_issuer(const AbsorbArgs &a, uint8_t *sm, Misc<C> &ms) {
         if (!(ok = warp_wait(&ms.q_full[s], (it / C::Stages) & 1, &ms.abort_flag))) break;
         const uint64_t qd = tc::sdesc(base + C::OffQ + 2 * s * kBlock, 16, 1024, tc::kSw128);
         for (int sub = 0; sub < C::Subs; ++sub, ++g) {
-            const int d = g & 1;
+            const int d = g % kBufs;
             if (w.fresh && !(ok = warp_wait(&ms.w_full[sub], (loads - 1) & 1, &ms.abort_flag))) break;
-            if (!(ok = warp_wait(&ms.d_free[d], ((g >> 1) & 1) ^ 1, &ms.abort_flag))) break;
+            if (!(ok = warp_wait(&ms.d_free[d], ((g / kBufs) & 1) ^ 1, &ms.abort_flag))) break;
             tc::fence_after();
             // 16 of n a step: 32 bytes of a query's row, 16 rows of 128 bytes of each of W_UK's 64-column blocks.
             const uint64_t wd = tc::sdesc(base + sub * (C::Sub / 64) * kBlock, kBlock, 1024, tc::kSw128);
@@ -188,7 +189,7 @@ __device__ void mma_issuer(const AbsorbArgs &a, uint8_t *sm, Misc<C> &ms) {
 template <class C, bool FP8>
 __device__ void epilogue(const AbsorbArgs &a, uint8_t *sm, Misc<C> &ms) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2, row0 = 32 * (warp & 3);
-    const uint32_t taddr = ms.tmem + wg * C::Sub + ((uint32_t)row0 << 16);
+    const uint32_t taddr = ms.tmem + ((uint32_t)row0 << 16);
     uint8_t *buf = sm + C::OffOut + warp * (32 * 128);      // of this warp's 32 rows of 128 bytes
     constexpr int kSize = FP8 ? 1 : 2;
     int g = 0;
@@ -196,7 +197,8 @@ __device__ void epilogue(const AbsorbArgs &a, uint8_t *sm, Misc<C> &ms) {
     for (Walk<C> w(a); ok && w.valid(); w.next()) {
         for (int sub = 0; sub < C::Subs; ++sub, ++g) {
             if ((g & 1) != wg) continue;
-            if (!(ok = warp_wait(&ms.d_full[wg], (g >> 1) & 1, &ms.abort_flag))) break;
+            const int d = g % kBufs;
+            if (!(ok = warp_wait(&ms.d_full[d], (g / kBufs) & 1, &ms.abort_flag))) break;
             tc::fence_after();
             // Eight lanes write a row's 128 bytes, four rows at once.
             const int t0 = w.tile * kTile + row0 + (lane >> 3), rows = a.T - t0;
@@ -211,7 +213,7 @@ __device__ void epilogue(const AbsorbArgs &a, uint8_t *sm, Misc<C> &ms) {
                     float v[C::Cols / 2];
 #pragma unroll
                     for (int i = 0; i < C::Cols / 32; ++i)
-                        tc::ld16(taddr + b * C::Cols + half * (C::Cols / 2) + 16 * i,
+                        tc::ld16(taddr + d * C::Sub + b * C::Cols + half * (C::Cols / 2) + 16 * i,
                                  *reinterpret_cast<float(*)[16]>(v + 16 * i));
                     tc::wait_ld();
 #pragma unroll
@@ -231,7 +233,7 @@ __device__ void epilogue(const AbsorbArgs &a, uint8_t *sm, Misc<C> &ms) {
                 if (b == C::Sub / C::Cols - 1) {
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.d_free[wg]);
+                    if (lane == 0) mbar_arrive(&ms.d_free[d]);
                 }
                 // Through shared memory (chunks turned by the row: no conflicts) into whole rows.
                 __syncwarp();
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms.q_full[s], 1);
             mbar_init(&ms.q_free[s], 1);
         }
-        for (int d = 0; d < 2; ++d) {
+        for (int d = 0; d < kBufs; ++d) {
             mbar_init(&ms.d_full[d], 1);
             mbar_init(&ms.d_free[d], 4);
         }
