@@ -13,11 +13,12 @@
 // Bound by DRAM (4 bytes an element, 3 with an e4m3 output, each moved once)
 // for many rows, by launch and the chain position -> table -> store for few:
 // 4,096 tokens x 96 heads of 192 columns 46.8 us (6.45 TB/s), 16,384 rows of
-// 576 columns normed, rotated, quantized and scattered 10.4 (3.2 TB/s), 64 x
+// 576 columns normed, rotated, quantized and scattered 9.4 (3.5 TB/s), 64 x
 // 64 heads of 128 to codes with a scale a row 1.9.
 //
 // A group of G lanes holds a row in registers between its loads and its
-// stores: 8-column vectors (16-byte loads), dealt to the lanes so that the
+// stores: 8-column vectors (16-byte loads, for wide rows by way of shared
+// memory, the next row's on their way meanwhile), dealt to the lanes so that the
 // two halves of a rotated pair lie in one lane (with partners loaded a second
 // time the 96 heads took 68 us).  The sum of squares and the maximum are
 // joined by shuffles inside the group, so rows pass no barrier; the arithmetic
@@ -36,11 +37,18 @@ namespace {
 constexpr int kThreads = 256;
 // Blocks an SM holds, by what their registers allow (40 to 128 a thread):
 // where one more of them would spill, rows in flight are worth less (16,384
-// rows of 576 columns, 5 vectors a lane: 7.4 us with three blocks, 9.8 with
+// rows of 576 columns, 5 vectors a lane: 9.1 us with three blocks, 11.0 with
 // four and 120 bytes spilled).
 constexpr int blocks_per_sm(int vpt, bool head) {
     return vpt <= 2 ? (head ? 6 : 4) : vpt == 3 ? 4 : vpt <= 5 ? (head ? 2 : 3) : 2;
 }
+
+// Rows (one a group) a warp has on their way or in work through shared memory;
+// 0: through registers.  Where a row takes most of the registers the next
+// one's loads would otherwise wait for its stores (65,536 rows of 576 columns
+// 23.6 us and not 26.8, 16,384 of 1,024 13.5 and 14.6; three rows 27; with 5
+// vectors a lane no gain, and 4,096 rows 3.3 us and not 3.1).
+constexpr int deep(int vpt) { return vpt >= 8 ? 2 : 0; }
 
 struct RopeArgs {
     const void *x, *weight;
@@ -100,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD)) norm_rope_
     __shared__ uint4 weight[NORM ? MLA_MAX_ROPE_WIDTH / 8 : 1];
     const int lane = threadIdx.x & 31, in = lane % G;
     constexpr int kPerWarp = 32 / G;
-    constexpr bool kAhead = !HEAD && G < 32 && VPT <= (PAIRS ? 4 : 2);      // the next row's loads beside this one's work
+    constexpr bool kAhead = !HEAD && deep(VPT) == 0 && G < 32 && VPT <= (PAIRS ? 4 : 2);      // the next row's loads beside this one's work
     const uint32_t step = gridDim.x * (kThreads / G);
     // The warp's rows are neighbours and its lanes stay together: a group past
     // the last row repeats it and stores nothing.
@@ -130,7 +138,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD)) norm_rope_
         if (NORM && v < a.norm_vecs) normed |= 1u << k;
         vec[k] = v;
     }
-    uint4 next[VPT];
+    constexpr int kDeep = deep(VPT);
+    extern __shared__ uint4 ring[];
+    uint4 *at_ring = ring + (threadIdx.x >> 5) * (kDeep * VPT * 32) + lane;
+    uint4 next[kDeep ? 1 : VPT];
     int64_t pos = 0, slot = 0;
     uint32_t head;
     const auto fetch = [&](uint32_t row) {
@@ -139,20 +150,40 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD)) norm_rope_
         head = row - t * a.heads;
         if (a.positions) pos = __ldg(a.positions + t);
         slot = a.slots ? __ldg(a.slots + t) : (int64_t)t;
+        if (kDeep) return;
         const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) +
                                                          ((uint64_t)t * a.x_row + (uint64_t)head * a.x_head));
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) next[k] = (mine >> k & 1) ? x[vec[k]] : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < VPT; ++k) next[kDeep ? 0 : k] = (mine >> k & 1) ? x[vec[k]] : make_uint4(0, 0, 0, 0);
+    };
+    // Into the ring: every lane its own vectors, which it alone reads.
+    const auto copy = [&](uint32_t row0, int stage) {
+        if (row0 < a.rows) {
+            const uint32_t row = min(row0 + lane / G, a.rows - 1);
+            const uint32_t t = (uint32_t)(((uint64_t)row * a.magic) >> (31 + a.shift));
+            const uint4 *x = reinterpret_cast<const uint4 *>(
+                static_cast<const T *>(a.x) + ((uint64_t)t * a.x_row + (uint64_t)(row - t * a.heads) * a.x_head));
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                if (mine >> k & 1) cp_async16(at_ring + (stage * VPT + k) * 32, x + vec[k]);
+        }
+        cp_async_commit();
     };
     grid_wait();
     if (kAhead) fetch(first + lane / G);
+    if (kDeep) {
+        fetch(first + lane / G);
+#pragma unroll
+        for (int i = 0; i + 1 < kDeep; ++i) copy(first + i * step, i);
+    }
+    int stage = 0;
     if (NORM) {
         for (int i = threadIdx.x; i < a.norm_vecs; i += kThreads) weight[i] = __ldg(static_cast<const uint4 *>(a.weight) + i);
         __syncthreads();
     }
     for (uint32_t row0 = first; row0 < a.rows; row0 += step) {
         const uint32_t row = row0 + lane / G;
-        if (!kAhead) fetch(row);
+        if (!kAhead && !kDeep) fetch(row);
         const uint32_t h = head;
         // Where the row goes; a negative slot is padding.
         const int64_t to = slot;
@@ -169,8 +200,17 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD)) norm_rope_
         }
         uint4 xv[VPT];
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) xv[k] = next[k];
+        for (int k = 0; k < VPT; ++k) xv[k] = next[kDeep ? 0 : k];
         if (kAhead) fetch(row + step);
+        if (kDeep) {
+            // The place of the row before, whose values have been used, takes the row kDeep - 1 ahead.
+            copy(row0 + (kDeep - 1) * step, stage == 0 ? kDeep - 1 : stage - 1);
+            fetch(row + step);
+            cp_async_wait<kDeep ? kDeep - 1 : 0>();
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) xv[k] = (mine >> k & 1) ? at_ring[(stage * VPT + k) * 32] : make_uint4(0, 0, 0, 0);
+            stage = stage == kDeep - 1 ? 0 : stage + 1;
+        }
         float rstd = 1.f;
         if (NORM) {
             uint64_t sums[2] = {0, 0};
@@ -292,8 +332,13 @@ template <typename T, int G, int VPT, bool NORM, bool PAIRS, bool HEAD>
 cudaError_t launch_kernel(RopeArgs a, int sms, cudaStream_t st) {
     a.turns = PAIRS ? 0 : (a.rope_vecs / 2 + G - 1) / G;
     const uint32_t per_block = kThreads / G, blocks = (a.rows + per_block - 1) / per_block;
+    constexpr int smem = deep(VPT) * VPT * kThreads * 16;
+    if (smem > 0) {
+        cudaError_t e = smem_attr_once<norm_rope_kernel<T, G, VPT, NORM, PAIRS, HEAD>>(smem);
+        if (e != cudaSuccess) return e;
+    }
     return launch_early(norm_rope_kernel<T, G, VPT, NORM, PAIRS, HEAD>,
-                        std::min(blocks, (uint32_t)sms * blocks_per_sm(VPT, HEAD)), kThreads, 0, st, a);
+                        std::min(blocks, (uint32_t)sms * blocks_per_sm(VPT, HEAD)), kThreads, smem, st, a);
 }
 
 template <typename T, int G, int VPT>
@@ -312,8 +357,8 @@ cudaError_t launch_width(const RopeArgs &a, bool pairs, int sms, cudaStream_t st
     // The fewest lanes that hold a row in few registers and, with halves, both
     // of a pair in one lane.  Rows of 384 columns and more that leave the SMs
     // idle take a warp each (64 of 576 2.6 us, with 16 lanes 3.0; 1,024 3.0
-    // and 3.4; 16,384 8.6 and 7.4), very many of them 8 lanes (65,536 27 us,
-    // with 16 32; 1,024 4.1 and 3.4).
+    // and 3.4; 16,384 8.6 and 7.4), very many of them 8 lanes (65,536 24 us,
+    // with 16 33; 1,024 4.1 and 3.4).
     const auto fits = [&](int g, int vpt) { return a.vecs <= g * vpt && (pairs || 2 * ((a.rope_vecs / 2 + g - 1) / g) <= vpt); };
     if (fits(4, 2)) return launch<T, 4, 2>(a, pairs, sms, st);
     if (fits(8, 2)) return launch<T, 8, 2>(a, pairs, sms, st);
