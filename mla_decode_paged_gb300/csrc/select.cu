@@ -166,6 +166,17 @@ __device__ __noinline__ uint2 block_sums(uint32_t x, uint32_t *totals) {
     return make_uint2(incl - x + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0), __reduce_add_sync(0xffffffffu, t));
 }
 
+// Lanes that differ in bit S: the maxima of the 16 >> S values that both hold, half of them in each.
+template <int S>
+__device__ __forceinline__ void halve(float (&v)[16]) {
+    const bool up = threadIdx.x >> S & 1;
+#pragma unroll
+    for (int i = 0; i < 8 >> S; ++i) {
+        const float keep = up ? v[i + (8 >> S)] : v[i], give = up ? v[i] : v[i + (8 >> S)];
+        v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 1 << S));
+    }
+}
+
 // Keys of the token blocks r0 .. s1 - 1 of a row, a round at most, into their
 // places: those of lo .. hi - 1, of `seen` tokens at w; 0 elsewhere, up to
 // `held` places.
@@ -192,13 +203,20 @@ __device__ __noinline__ void load_keys(uint32_t *key, const float *w, int r0, in
             }
         }
     } else {
-        // Block maxima (NaN ignored: as -inf).  Up to 32 tokens a block: a
-        // warp's 32 lanes hold several, joined by shuffles.  More: a warp
-        // holds some blocks' tokens in sixteen registers a lane.
+        // Block maxima (NaN ignored: as -inf).  A warp holds 16 chunks of 32
+        // tokens, one a register.  Each of up to four steps joins lanes that
+        // differ in one bit and leaves either with half of the chunks, so that
+        // 16 maxima cost 15 exchanges; further bits of larger blocks are joined
+        // one by one (a join of every chunk on its own: 512 rows by blocks of
+        // 16 51 us).
 #pragma unroll 1
         for (int i = tid; i < held; i += THREADS) key[place(i)] = 0;
         __syncthreads();
-        const int t1 = min((r0 + f1) << lb, seen), ls = lb > 5 ? lb - 5 : 0;    // 2^ls reads a block
+        const int t1 = min((r0 + f1) << lb, seen);
+        const int to_last = lb < 5 ? 32 : 1 << (9 - lb);       // the last of the bits joined one by one
+        // Chunks chunk .. chunk + kept - 1 end up in this lane (kept 0: in another too, which writes).
+        const int each = max(16 >> lb, 1), chunk = __brev(lane) >> 28 & ~(each - 1), off = lb < 5 ? lane >> lb << lb : 0;
+        const int kept = lb >= 5 && (lane & 32 - to_last) != 0 ? 0 : each;
 #pragma unroll 1
         for (int t0 = ((r0 + f0) << lb) + 32 * 16 * warp; t0 < t1; t0 += 32 * 16 * kWarps) {
             float v[16];
@@ -207,29 +225,16 @@ __device__ __noinline__ void load_keys(uint32_t *key, const float *w, int r0, in
                 const int t = t0 + 32 * k + lane;
                 v[k] = t < t1 ? __ldg(w + t) : -INFINITY;
             }
-            if (ls >= 1)
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) v[k] = fmaxf(v[k], v[k + 1]);
-            if (ls >= 2)
-#pragma unroll
-                for (int k = 0; k < 16; k += 4) v[k] = fmaxf(v[k], v[k + 2]);
-            if (ls >= 3)
-#pragma unroll
-                for (int k = 0; k < 16; k += 8) v[k] = fmaxf(v[k], v[k + 4]);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int t = t0 + 32 * k;
-                if ((k & ((1 << ls) - 1)) != 0 || t >= t1) continue;
-                uint32_t x = weight_key(v[k]);
-                bool leads = lane == 0;
-                if (lb >= 5) {
-                    x = __reduce_max_sync(0xffffffffu, x);
-                } else {
+            halve<0>(v);
+            if (lb >= 2) halve<1>(v);
+            if (lb >= 3) halve<2>(v);
+            if (lb >= 4) halve<3>(v);
 #pragma unroll 1
-                    for (int d = 1; d < 1 << lb; d <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    leads = (lane & ((1 << lb) - 1)) == 0 && t + lane < t1;
-                }
-                if (leads) key[place(((t + lane) >> lb) - r0)] = x;
+            for (int d = 16; d >= to_last; d >>= 1) v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], d));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int t = t0 + 32 * (chunk + k) + off;
+                if (k < kept && t < t1) key[place((t >> lb) - r0)] = weight_key(v[k]);
             }
         }
     }
