@@ -13,7 +13,7 @@
 //
 // Bound by the 4 bytes a score that are read for many long rows, by the chain
 // of dependent steps for one: 64 requests of 1K to 8K tokens 8.6 us, one of
-// 128K 14, 512 rows of 4K to 32K by blocks of 64 26 (1.9 TB/s).
+// 128K 14, 512 rows of 4K to 32K by blocks of 64 19 (2.5 TB/s).
 //
 // Design: a cluster of thread blocks per row, as many of them as it takes to
 // hold it (the others end at once), each with a contiguous slice of its token
@@ -192,12 +192,12 @@ __device__ __noinline__ void load_keys(uint32_t *key, const float *w, int r0, in
         uint32_t *to = key + place(tid);
         const uint32_t width = max(f1 - f0, 0);
 #pragma unroll 1
-        for (int i0 = tid - f0; i0 < held - f0; i0 += 4 * THREADS, from += 4 * THREADS, to += 4 * place(THREADS)) {
-            float v[4];
+        for (int i0 = tid - f0; i0 < held - f0; i0 += 8 * THREADS, from += 8 * THREADS, to += 8 * place(THREADS)) {
+            float v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = (uint32_t)(i0 + THREADS * j) < width ? __ldg(from + THREADS * j) : 0.f;
+            for (int j = 0; j < 8; ++j) v[j] = (uint32_t)(i0 + THREADS * j) < width ? __ldg(from + THREADS * j) : 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const uint32_t x = weight_key(v[j]);
                 if (i0 + THREADS * j < held - f0) to[place(THREADS) * j] = (uint32_t)(i0 + THREADS * j) < width ? x : 0;
             }
@@ -243,7 +243,7 @@ __device__ __noinline__ void load_keys(uint32_t *key, const float *w, int r0, in
 
 // 2^log_cs blocks (a cluster) per row.
 template <int THREADS, int ROUND, bool CLUSTER, bool BLOCKED>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 5 : 1024 / THREADS) select_kernel(const SelectArgs a, int log_cs) {
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BLOCKED ? 4 : 5) : 1024 / THREADS) select_kernel(const SelectArgs a, int log_cs) {
     constexpr int kWarps = THREADS / 32, kOwn = kBins / THREADS;       // bins a thread sums
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Shared<THREADS, ROUND, CLUSTER> &sh = *reinterpret_cast<Shared<THREADS, ROUND, CLUSTER> *>(smem_raw);

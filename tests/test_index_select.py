@@ -169,6 +169,16 @@ def test_lists(lengths, qlen, topk, block, recent, sinks, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("requests", [1, 90])
+@pytest.mark.parametrize("block", [1, 2, 4, 8, 16, 32, 64, 128, 256])
+def test_every_block_size_below_zero(block, requests):
+    # scores below 0 throughout: what no token filled must not count
+    lengths = [(17 * block + 3 + 577 * i) % 5000 + 1 for i in range(requests)]
+    scores = -torch.rand(2, sum(lengths), generator=torch.Generator().manual_seed(block)) - 0.5
+    _run(scores, lengths, 7, block, 1, 1, True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("block", [1, 4, 64])
 def test_ties_nan_and_infinities(block):
     n = 6000
