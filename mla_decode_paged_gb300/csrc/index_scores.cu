@@ -12,7 +12,7 @@
 // row above.  Rows of 128 bytes from random places come at 5.6 TB/s at most
 // (plain 16-byte loads of as many in flight as the SMs hold).  32 requests of
 // 32K tokens, 64 heads: 30.6 us (4.7 TB/s); 128 x 4 rows of 4K to 32K, 32
-// heads: 76 (4.8; without the sums 65); 64 requests of 1K to 8K, 64 heads: 13.
+// heads: 74 (5.0; without the sums 65); 64 requests of 1K to 8K, 64 heads: 13.
 //
 // Design: one persistent CTA per SM walks a contiguous range of the batch's
 // 128-token tiles.  Tokens are the MMA's M dimension, heads of some query
@@ -23,7 +23,8 @@
 //   warps 0..15   four warpgroups take the tiles in turn: the sums, the output
 //                 (two: 106 us for the 128 x 4 rows)
 //   warp 16       MMA issuer; four accumulators in TMEM up to 128 columns, two above
-//   warps 17..20  producers, a tile in four each: a gather4 a lane
+//   warps 17..20  producers, a tile in four each: a gather4 a lane (the lanes'
+//                 copies are issued one by one: two warps 106 us, six 76)
 //   warp 21       a request's query by TMA and its weights, two requests deep
 // Rows whose heads exceed 256 columns are cut into groups on neighbouring
 // CTAs, which read the same tiles at about the same time.
@@ -227,21 +228,23 @@ __device__ void epilogue(const ScoreArgs &a, Misc &ms, int grp) {
         if (!warp_wait(&ms.d_full[d], it & 1, &ms.abort_flag)) break;
         tc::fence_after();
         const float4 *c = ms.w[w.unit % kConstBufs] + first * (a.hp / 4);
-        uint64_t sum[2] = {0, 0};
+        float sum[4] = {0, 0, 0, 0};
         int step = 0, seen = a.causal ? w.len - a.qlen + tq0 + 1 : w.len;       // tokens that the row sees
-        // 16 heads' columns of this token; a row's last ones end its sum.
+        // 16 heads' columns of this token; a row's last ones end its sum.  (Two
+        // columns an instruction: 76 us for 128 x 4 rows and not 74.)
         const auto add = [&](const float (&x)[16]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 ws = *c++;
-                sum[0] = fma2(pair(max_nan(x[4 * i], 0.f), max_nan(x[4 * i + 1], 0.f)), pair(ws.x, ws.y), sum[0]);
-                sum[1] = fma2(pair(max_nan(x[4 * i + 2], 0.f), max_nan(x[4 * i + 3], 0.f)), pair(ws.z, ws.w), sum[1]);
+                sum[0] = fmaf(max_nan(x[4 * i], 0.f), ws.x, sum[0]);
+                sum[1] = fmaf(max_nan(x[4 * i + 1], 0.f), ws.y, sum[1]);
+                sum[2] = fmaf(max_nan(x[4 * i + 2], 0.f), ws.z, sum[2]);
+                sum[3] = fmaf(max_nan(x[4 * i + 3], 0.f), ws.w, sum[3]);
             }
             if (++step < steps) return;
-            const float2 s0 = parts(sum[0]), s1 = parts(sum[1]);
-            if (j < w.len) *out = j < seen ? (s0.x + s1.x) + (s0.y + s1.y) : -INFINITY;
+            if (j < w.len) *out = j < seen ? (sum[0] + sum[2]) + (sum[1] + sum[3]) : -INFINITY;
             out += a.num_pages;
-            sum[0] = sum[1] = 0;
+            sum[0] = sum[1] = sum[2] = sum[3] = 0;
             step = 0;
             if (a.causal) ++seen;
         };
