@@ -434,7 +434,7 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
  *   and out[T, h] = e4m3(y * (1 / sc)), to nearest even, saturating at +-448.
  * A token with a negative slot is skipped (padding); one with a slot past
  * out_rows is skipped and sets MLA_DEV_BAD_PAGE; two tokens with the same
- * slot: which one lands is unspecified, for each 16 columns.  A position
+ * slot: which one lands is unspecified, for each 8 columns.  A position
  * outside [0, num_positions) rotates as position 0 and sets
  * MLA_DEV_BAD_POSITION.  NaN and infinities as mla_add_rms_norm.
  *

@@ -7,11 +7,13 @@ The three calls of one decode step of a Multi-head Latent Attention layer:
     latent, lse_merged = merge(o, lse)
     out = value_gate(latent, w_uv, gate, lengths, qlen)
 
-and the operators around them: ``kv_append``, ``add_rms_norm``,
-``token_weights`` / ``kv_evict`` and ``value_gate_lora``.
+and the operators around them: ``kv_append``, ``add_rms_norm``, ``norm_rope``
+and ``query_absorb`` in front of attend, ``index_scores`` / ``index_select``
+for attention to chosen tokens only, ``token_weights`` / ``kv_evict`` and
+``value_gate_lora``.
 
-This module only marshals arguments (for the last four calls through a
-compiled module, ``csrc/binding.cpp``): it checks dtypes / shapes, allocates
+This module only marshals arguments (for the operators but ``kv_append``
+through a compiled module, ``csrc/binding.cpp``): it checks dtypes / shapes, allocates
 outputs with torch (device memory), passes raw pointers and the current CUDA
 stream to the native library, and turns error codes into exceptions.  Every
 step of the computation runs in the library's CUDA kernels; there is no

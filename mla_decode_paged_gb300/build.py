@@ -7,7 +7,7 @@ so the library carries no dependency on a particular libcudart build).
 them with the host compiler against the installed torch (its version is in
 the module's file name) and linked to the library.  The library needs
 neither: where the module cannot be built (no Python headers, say) the library
-is there all the same, and the four calls that go through the module raise.
+is there all the same, and the calls that go through the module raise.
 """
 
 from __future__ import annotations
