@@ -12,7 +12,7 @@
 // blocks of more than one token that stays).
 //
 // Bound by the 4 bytes a score that are read for many long rows, by the chain
-// of dependent steps for one: 64 requests of 1K to 8K tokens 8.6 us, one of
+// of dependent steps for one: 64 requests of 1K to 8K tokens 8.4 us, one of
 // 128K 14, 512 rows of 4K to 32K by blocks of 64 19 (2.5 TB/s).
 //
 // Design: a cluster of thread blocks per row, as many of them as it takes to
@@ -383,11 +383,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BLOCKED ? 4 : 5) : 
                 for (int q = 0; q < rounds; ++q) {
                     if (rounds > 1) load(q);
                     const uint32_t *from = sh.key + place(tid);
+                    uint32_t in = 0;
 #pragma unroll 4
-                    for (int i = 0; i < per; ++i) {
-                        const uint32_t x = from[place(THREADS) * i];
-                        if ((x ^ T) >> shift == 0) sh.cand[atomicAdd(&sh.ncand, 1u)] = x;
+                    for (int i = 0; i < per; ++i) in |= (uint32_t)((from[place(THREADS) * i] ^ T) >> shift == 0) << i;
+                    const uint32_t mine = __popc(in);
+                    uint32_t end = mine, at = 0;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const uint32_t y = __shfl_up_sync(0xffffffffu, end, d);
+                        if (lane >= d) end += y;
                     }
+                    if (lane == 31 && end > 0) at = atomicAdd(&sh.ncand, end);
+                    at = __shfl_sync(0xffffffffu, at, 31) + end - mine;
+#pragma unroll 1
+                    for (uint32_t i = 0; i < mine; ++i, in &= in - 1) sh.cand[at + i] = from[place(THREADS) * (__ffs(in) - 1)];
                 }
                 if (one) __syncthreads();
                 else cluster_sync();
@@ -519,6 +528,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BLOCKED ? 4 : 5) : 
         }
         block_kept = __reduce_add_sync(0xffffffffu, block_kept);
         block_ties = __reduce_add_sync(0xffffffffu, block_ties);
+        cluster_arrive();       // the last of the others' shared memory has been read
     }
 
     // Placement, in position order.  Places past the output (only requests
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BLOCKED ? 4 : 5) : 
     if (rank == 0)
 #pragma unroll 1
         for (uint64_t i = all_tokens + ((uint64_t)b * THREADS + tid); i < limit; i += (uint64_t)rows * THREADS) a.pages_out[i] = -1;
-    if (!one) cluster_sync();                  // no block ends while another may read its shared memory
+    if (!one) cluster_wait();                  // no block ends while another may read its shared memory
 }
 
 // indptr_out of all rows, by one block.

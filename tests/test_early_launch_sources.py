@@ -75,4 +75,6 @@ def test_the_scores_wait_for_a_request_goes_by_its_tiles():
 
 def test_no_block_of_a_cluster_ends_while_its_memory_is_read():
     body = _function(_text("select.cu"), r"\bselect_kernel\(")
-    assert body.rstrip().endswith("if (!one) cluster_sync();")
+    assert body.rstrip().endswith("if (!one) cluster_wait();")
+    assert body.rindex("remote(") < body.rindex("cluster_arrive();") < body.rindex("cluster_wait();")
+    assert body.count("cluster_arrive();") == 2 and body.count("cluster_wait();") == 3       # the first's on either path
