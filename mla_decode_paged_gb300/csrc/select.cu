@@ -17,8 +17,8 @@
 //
 // Design: a cluster of thread blocks per row, as many of them as it takes to
 // hold it (the others end at once), each with a contiguous slice of its token
-// blocks: 8,192 keys (order-preserving 32-bit images of the scores), formed in
-// shared memory from coalesced reads, then 8 or 16 neighbours in a thread's
+// blocks: 8,192 or 16,384 keys (order-preserving 32-bit images of the scores), formed in
+// shared memory from coalesced reads, then up to 32 neighbours in a thread's
 // registers, so that one prefix sum over the threads places what stays (with
 // 32 lanes of a warp side by side every key needed its ballots: three times
 // the instructions).  A longer slice is taken in rounds of that size, read
@@ -46,7 +46,7 @@ namespace mla {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kLong = 8192, kShort = 4096;     // token blocks a thread block holds, of 512 and more threads, of 256
+constexpr int kLong = 8192, kShort = 4096;     // token blocks a thread block holds, of 512 and more threads (or twice these), of 256
 constexpr int kCand = 1024, kFew = 512;    // keys of a bin, of a row, that one warp searches
 constexpr int kCounted = 1024;     // rows whose kept tokens every cluster counts itself
 
@@ -501,18 +501,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BLOCKED ? 4 : 5) : 
     };
     uint2 at = make_uint2(0, 0);
     uint32_t block_kept = 0, block_ties = 0;        // sure blocks and ties of the thread blocks before this one
+    if (one && rounds > 1) {
+        __syncthreads();        // nothing needs the sums; every round's are formed below
+    } else {
 #pragma unroll 1
-    for (int q = 0; q < max(rounds, 1); ++q) {
-        if (rounds > 1 && select) load(q);
-        else if (q > 0) __syncthreads();
-        at = mark(q, 1);
-        block_kept += at.y & 0xffff;
-        block_ties += at.y >> 16;
+        for (int q = 0; q < max(rounds, 1); ++q) {
+            if (rounds > 1 && select) load(q);
+            else if (q > 0) __syncthreads();
+            at = mark(q, 1);
+            block_kept += at.y & 0xffff;
+            block_ties += at.y >> 16;
+        }
     }
     if (!one && tid == 0) sh.sum[0] = block_kept, sh.sum[1] = block_ties;
     block_kept = block_ties = 0;
     if (!a.scanned) {
-        // (written before the barrier in mark)
+        // (written before the barrier above)
         before = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red[0][lane] : 0);
         all_tokens = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red[1][lane] : 0);
         if (tid == 0 && rank == 0) {
@@ -670,14 +674,25 @@ cudaError_t index_select_launch(const float *scores, const int32_t *pages, int64
         empty_kernel<<<(unsigned)std::min<int64_t>((capacity + 255) / 256 + 1, sms), 256, 0, st>>>(a);
         return cudaGetLastError();
     }
-    // The lengths are on the device.  Rows of the mean length share a thread
-    // block's round or a cluster's; few rows take the blocks that half the SMs
-    // hold; more rows than SMs that fit half a round of 256 threads take these.
+    // The lengths are on the device: the rule goes by their mean.  More rows
+    // than SMs that fit half a round of 256 threads take these.  Longer ones
+    // take blocks of 16,384, in clusters that hold the mean (512 rows of 8K to
+    // 16K 33 us, in clusters with rounds of 8,192 57; 300 of 40K to 128K 160
+    // and 330; but 256 of 128 to 128K 120 and 89, where the longest go by
+    // rounds).  Up to as many rows as SMs share a thread block's round, of
+    // 16,384 too (100 rows of 16K 12 us, in clusters 16), or a cluster's, and
+    // few rows take the blocks that half the SMs hold.
     const int64_t mean = (num_pages + R - 1) / R, blocks = mean >> a.log_block;
-    if (rows > sms && blocks <= kShort / 2) return launch<256, kShort, false>(a, 0, st);
     int log_cs = 0;
+    if (rows > sms) {
+        if (blocks <= kShort / 2) return launch<256, kShort, false>(a, 0, st);
+        if (blocks <= kLong) return launch<512, kLong, true>(a, 0, st);
+        while (log_cs < 4 && (blocks >> log_cs) > 2 * kLong) ++log_cs;
+        return launch<512, 2 * kLong, true>(a, log_cs, st);
+    }
+    if (blocks > kLong && blocks <= 2 * kLong) return launch<1024, 2 * kLong, false>(a, 0, st);
     while (log_cs < 4 && ((blocks >> log_cs) > kLong || (rows << (log_cs + 1)) <= sms / 2)) ++log_cs;
-    return log_cs == 0 && rows <= sms ? launch<1024, kLong, false>(a, log_cs, st) : launch<512, kLong, true>(a, log_cs, st);
+    return log_cs == 0 ? launch<1024, kLong, false>(a, 0, st) : launch<512, kLong, true>(a, log_cs, st);
 }
 
 cudaError_t index_select_status(unsigned int *flags, bool clear) { return read_status(flags, clear); }

@@ -169,6 +169,20 @@ def test_lists(lengths, qlen, topk, block, recent, sinks, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lengths,topk,block,recent,sinks", [
+    ([12000] * 170 + [16384, 16385, 40000, 1, 0], 700, 1, 2, 1),        # more rows than SMs, of a block's round and longer
+    ([20000] * 170 + [100000, 33000, 5], 700, 1, 0, 0),                 # in clusters, and longer than these hold
+    ([70000] * 160 + [131072, 3, 0, 300], 2048, 2, 1, 1),
+    ([12000] * 10 + [50000, 16384, 16385, 0, 7], 700, 1, 2, 1),         # fewer
+    ([30000] * 10 + [90000, 32768, 32770, 0, 7], 700, 2, 1, 0),
+])
+@pytest.mark.parametrize("ties", [False, True])
+def test_many_long_rows(lengths, topk, block, recent, sinks, ties):
+    scores = _rand(1, sum(lengths))
+    _run((4 * scores).round() if ties else scores, lengths, topk, block, recent, sinks)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("requests", [1, 90])
 @pytest.mark.parametrize("block", [1, 2, 4, 8, 16, 32, 64, 128, 256])
 def test_every_block_size_below_zero(block, requests):
