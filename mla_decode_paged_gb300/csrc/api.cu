@@ -722,7 +722,8 @@ mla_status mla_norm_rope(const void *x, int64_t x_row_stride, int64_t x_head_str
     if (weight && (norm_dim < 8 || norm_dim > width || norm_dim % 8 != 0))
         return fail(MLA_ERR_INVALID, "norm_dim must be a multiple of 8 in 8..width");
     if (weight && (!(eps > 0.f) || !std::isfinite(eps))) return fail(MLA_ERR_INVALID, "eps must be finite and > 0");
-    if ((positions == nullptr) != (cos_sin == nullptr)) return fail(MLA_ERR_INVALID, "positions and cos_sin go together");
+    if (tokens > 0 && (positions == nullptr) != (cos_sin == nullptr))
+        return fail(MLA_ERR_INVALID, "positions and cos_sin go together");
     if (positions && (rope_start < 0 || rope_start % 8 != 0 || rope_dim < 16 || rope_dim % 16 != 0 ||
                       rope_dim > width || rope_start > width - rope_dim))
         return fail(MLA_ERR_INVALID, "rope_start must be a multiple of 8, rope_dim of 16, their sum at most width");
@@ -770,7 +771,8 @@ mla_status mla_query_absorb(const void *q, int64_t q_row_stride, int64_t q_head_
     const bool fp8 = (flags & MLA_ABSORB_OUT_FP8) != 0;
     if (tokens < 0) return fail(MLA_ERR_INVALID, "negative tokens");
     if (heads < 1 || heads > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID, "heads outside 1..128");
-    if ((positions == nullptr) != (cos_sin == nullptr)) return fail(MLA_ERR_INVALID, "positions and cos_sin go together");
+    if (tokens > 0 && (positions == nullptr) != (cos_sin == nullptr))
+        return fail(MLA_ERR_INVALID, "positions and cos_sin go together");
     if (positions && (num_positions < 1 || num_positions > (int64_t)1 << 40))
         return fail(MLA_ERR_INVALID, "num_positions outside 1..2^40");
     if (fp8 && !(std::isfinite(q_scale) && q_scale >= 1.17549435e-38f))

@@ -310,8 +310,9 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor out = output(a[10], "out", at, x.sizes(), otype, [&](const at::Tensor &t) {
             ho = heads_of(t, "out", dev);
             if (t.scalar_type() != otype || t.dim() != x.dim() || ho.heads != hx.heads || ho.width != hx.width ||
-                (!slots && ho.rows != T))
-                refuse(std::string("out must be ") + at::toString(otype) + (slots ? " rows" : "") + " of x's shape");
+                (a[9] == Py_None && ho.rows != T))
+                refuse(std::string("out must be ") + at::toString(otype) + (a[9] == Py_None ? "" : " rows") +
+                       " of x's shape");
         });
         at::Tensor out_scales;
         if (scales) {

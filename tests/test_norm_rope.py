@@ -106,6 +106,12 @@ def test_empty(lib):
     assert _call(lib, T=0, x=None, out=None, sc=None) == mla.MLA_OK
 
 
+def test_no_tokens(lib):
+    # an empty tensor's pointer is null
+    assert _call(lib, T=0, x=None, pos=None, out=None, sc=None) == mla.MLA_OK
+    assert _call(lib, T=0, x=None, pos=None, slots=None, out=None, sc=None, quant=0) == mla.MLA_OK
+
+
 def test_binding_refusals():
     mla.build()
     x, w = torch.zeros(4, 2, 64, dtype=BF), torch.ones(64, dtype=BF)
@@ -323,6 +329,13 @@ def test_no_cache_rows():
     mla.norm_rope(x, slots=torch.full((3,), -1, device=DEV), out=torch.empty(0, 1, 64, dtype=BF, device=DEV))
     assert mla.device_status() == 0
     assert mla.norm_rope(x[:0])[0].shape == (0, 1, 64)
+    none, table = torch.zeros(0, dtype=torch.int64, device=DEV), torch.zeros(8, 32, device=DEV)
+    for quant in (None, "head"):
+        out, scales = mla.norm_rope(x[:0], positions=none, cos_sin=table, quant=quant)
+        assert out.shape == (0, 1, 64) and (quant is None or scales.shape == (0, 1))
+    out = torch.ones(5, 1, 64, dtype=BF, device=DEV)
+    mla.norm_rope(x[:0], positions=none, cos_sin=table, slots=none, out=out)
+    assert (out == 1).all()
 
 
 @pytest.mark.gpu

@@ -64,6 +64,7 @@ def test_refusals(lib, kw, msg):
 def test_sizes(lib):
     assert _call(lib, T=1 << 31) == mla.MLA_ERR_UNSUPPORTED
     assert _call(lib, T=0, q=None, w=None, out=None) == mla.MLA_OK
+    assert _call(lib, T=0, q=None, pos=None, out=None) == mla.MLA_OK      # an empty tensor's pointer is null
 
 
 def test_binding_refusals():
@@ -185,6 +186,15 @@ def test_infinite_and_nan_rows_stay_alone():
     for t, h in ((5, 1), (9, 2), (11, 0)):
         got[t, h] = want[t, h]
     assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    q, w = torch.zeros(0, 2, 192, dtype=BF, device=DEV), torch.zeros(2, 128, 512, dtype=BF, device=DEV)
+    pos, cs = torch.zeros(0, dtype=torch.int64, device=DEV), torch.zeros(8, 64, device=DEV)
+    for kw in ({}, dict(positions=pos, cos_sin=cs), dict(positions=pos, cos_sin=cs, q_scale=0.5)):
+        assert mla.query_absorb(q, w, **kw).shape == (0, 2, 576)
+    assert mla.device_status() == 0
 
 
 @pytest.mark.gpu
