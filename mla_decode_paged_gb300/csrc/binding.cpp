@@ -20,6 +20,8 @@
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <tuple>
+#include <utility>
 #include <vector>
 
 #include "../../include/mla_decode.h"
@@ -115,6 +117,21 @@ struct Place {
         if (!own) return at::Tensor(at::detail::empty_cuda(shape, options));
         c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(stream, device.index()));
         return at::Tensor(at::detail::empty_cuda(shape, options));
+    }
+    // Two tensors in one allocation (0.4 us less than two), the second 256-byte aligned in it.
+    std::pair<at::Tensor, at::Tensor> empty(at::IntArrayRef shape, ScalarType type, at::IntArrayRef shape2,
+                                            ScalarType type2) const {
+        const int64_t bytes = (c10::multiply_integers(shape) * (int64_t)c10::elementSize(type) + 255) / 256 * 256;
+        const int64_t bytes2 = c10::multiply_integers(shape2) * (int64_t)c10::elementSize(type2);
+        const at::Tensor whole = empty({bytes + bytes2}, at::kByte);
+        const auto part = [&](at::IntArrayRef s, ScalarType t, int64_t offset) {
+            at::Tensor x = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                                    c10::scalarTypeToTypeMeta(t));
+            x.unsafeGetTensorImpl()->set_sizes_contiguous(s);
+            x.unsafeGetTensorImpl()->set_storage_offset(offset / (int64_t)c10::elementSize(t));
+            return x;
+        };
+        return {part(shape, type, 0), part(shape2, type2, bytes)};
     }
 };
 
@@ -307,18 +324,25 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         ScalarType otype = quant == MLA_QUANT_NONE ? type : kE4m3;
         if (quant != MLA_QUANT_NONE && a[10] != Py_None && tensor(a[10], "out").scalar_type() == at::kByte) otype = at::kByte;
         HeadRows ho = {T, hx.heads, hx.width, hx.heads * hx.width, hx.width};
-        const at::Tensor out = output(a[10], "out", at, x.sizes(), otype, [&](const at::Tensor &t) {
-            ho = heads_of(t, "out", dev);
-            if (t.scalar_type() != otype || t.dim() != x.dim() || ho.heads != hx.heads || ho.width != hx.width ||
-                (a[9] == Py_None && ho.rows != T))
-                refuse(std::string("out must be ") + at::toString(otype) + (a[9] == Py_None ? "" : " rows") +
-                       " of x's shape");
-        });
-        at::Tensor out_scales;
-        if (scales) {
-            std::vector<int64_t> shape = {ho.rows};
-            if (x.dim() == 3) shape.push_back(ho.heads);
-            out_scales = dense_output(a[11], "out_scales", at, shape, at::kFloat);
+        at::Tensor out, out_scales;
+        std::vector<int64_t> scales_shape;
+        if (scales && a[10] == Py_None && a[11] == Py_None) {
+            scales_shape = x.sizes().vec();
+            scales_shape.pop_back();
+            std::tie(out, out_scales) = at.empty(x.sizes(), otype, scales_shape, at::kFloat);
+        } else {
+            out = output(a[10], "out", at, x.sizes(), otype, [&](const at::Tensor &t) {
+                ho = heads_of(t, "out", dev);
+                if (t.scalar_type() != otype || t.dim() != x.dim() || ho.heads != hx.heads || ho.width != hx.width ||
+                    (a[9] == Py_None && ho.rows != T))
+                    refuse(std::string("out must be ") + at::toString(otype) + (a[9] == Py_None ? "" : " rows") +
+                           " of x's shape");
+            });
+            if (scales) {
+                scales_shape = {ho.rows};
+                if (x.dim() == 3) scales_shape.push_back(ho.heads);
+                out_scales = dense_output(a[11], "out_scales", at, scales_shape, at::kFloat);
+            }
         }
         const mla_status st = mla_norm_rope(
             ptr(x), hx.row, hx.head, norm_type(type), weight, (int)norm_dim, eps, positions, table, table_rows, rope_start,
@@ -466,10 +490,15 @@ PyObject *index_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Place at(dev, a[10]);
         const int64_t need = mla_index_select_capacity((int)R, qlen, pages_n, topk, block);
         if (need < 0) return PyLong_FromLongLong(need);
-        const at::Tensor po = output(a[8], "pages_out", at, {need}, at::kInt, [&](const at::Tensor &t) {
-            dense(t, "pages_out", at::kInt, {t.numel()}, dev);
-        });
-        const at::Tensor io = dense_output(a[9], "indptr_out", at, {R * qlen + 1}, at::kInt);
+        at::Tensor po, io;
+        if (a[8] == Py_None && a[9] == Py_None) {
+            std::tie(po, io) = at.empty({need}, at::kInt, {R * qlen + 1}, at::kInt);
+        } else {
+            po = output(a[8], "pages_out", at, {need}, at::kInt, [&](const at::Tensor &t) {
+                dense(t, "pages_out", at::kInt, {t.numel()}, dev);
+            });
+            io = dense_output(a[9], "indptr_out", at, {R * qlen + 1}, at::kInt);
+        }
         const mla_status st = mla_index_select(ptr<float>(scores), ptr<int32_t>(pages), pages_n, ptr<int32_t>(indptr), (int)R,
                                                qlen, topk, block, recent, sinks, causal ? MLA_ATTEND_CAUSAL : 0u,
                                                ptr<int32_t>(po), po.numel(), ptr<int32_t>(io), at.stream);
