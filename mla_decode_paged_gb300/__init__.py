@@ -545,7 +545,8 @@ def norm_rope(x, weight=None, eps=1e-6, *, positions=None, cos_sin=None, rope_st
     float ``scale``; no scales returned): a code stands for code * scale.
     ``slots``: int64 ``[T]``: token t goes to row ``slots[t]`` of ``out``
     (and of ``out_scales``), a cache of any number of rows; negative slots
-    are skipped.  ``out=x`` works in place.
+    are skipped.  ``out=x`` works in place.  Codes and scales that are both new
+    share an allocation.
     """
     q = _ROPE_QUANT.get(quant)
     if q is None:

@@ -173,6 +173,7 @@ def test_lists(lengths, qlen, topk, block, recent, sinks, causal):
     ([12000] * 170 + [16384, 16385, 40000, 1, 0], 700, 1, 2, 1),        # more rows than SMs, of a block's round and longer
     ([20000] * 170 + [100000, 33000, 5], 700, 1, 0, 0),                 # in clusters, and longer than these hold
     ([70000] * 160 + [131072, 3, 0, 300], 2048, 2, 1, 1),
+    ([140000] * 154 + [9], 2048, 1, 0, 0),                              # in the largest clusters
     ([12000] * 10 + [50000, 16384, 16385, 0, 7], 700, 1, 2, 1),         # fewer
     ([30000] * 10 + [90000, 32768, 32770, 0, 7], 700, 2, 1, 0),
 ])
