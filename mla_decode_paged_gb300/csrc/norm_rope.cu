@@ -14,7 +14,7 @@
 // for many rows, by launch and the chain position -> table -> store for few:
 // 4,096 tokens x 96 heads of 192 columns 46.8 us (6.45 TB/s), 16,384 rows of
 // 576 columns normed, rotated, quantized and scattered 9.4 (3.5 TB/s), 64 x
-// 64 heads of 128 to codes with a scale a row 1.9.
+// 64 heads of 128 to codes with a scale a row 1.8.
 //
 // A group of G lanes holds a row in registers between its loads and its
 // stores: 8-column vectors (16-byte loads, for wide rows by way of shared
@@ -39,8 +39,8 @@ constexpr int kThreads = 256;
 // where one more of them would spill, rows in flight are worth less (16,384
 // rows of 576 columns, 5 vectors a lane: 9.1 us with three blocks, 11.0 with
 // four and 120 bytes spilled).
-constexpr int blocks_per_sm(int vpt, bool head) {
-    return vpt <= 2 ? (head ? 6 : 4) : vpt == 3 ? 4 : vpt <= 5 ? (head ? 2 : 3) : 2;
+constexpr int blocks_per_sm(int vpt, bool head, bool pairs) {
+    return vpt <= 2 ? (head && pairs ? 6 : 4) : vpt == 3 ? 4 : vpt <= 5 ? (head ? 2 : 3) : 2;
 }
 
 // Rows (one a group) a warp has on their way or in work through shared memory;
@@ -104,11 +104,14 @@ __device__ __forceinline__ uint32_t round2(uint64_t v) {
 // PAIRS: neighbours make a pair.  HEAD: a scale a row, so its values are held
 // until all of them are known.
 template <typename T, int G, int VPT, bool NORM, bool PAIRS, bool HEAD>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD)) norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) norm_rope_kernel(const RopeArgs a) {
     __shared__ uint4 weight[NORM ? MLA_MAX_ROPE_WIDTH / 8 : 1];
     const int lane = threadIdx.x & 31, in = lane % G;
     constexpr int kPerWarp = 32 / G;
-    constexpr bool kAhead = !HEAD && deep(VPT) == 0 && G < 32 && VPT <= (PAIRS ? 4 : 2);      // the next row's loads beside this one's work
+    // The next row's loads beside this one's work.  (With a scale a row only
+    // where halves make the work long: 16,384 x 64 heads of 128 82 us and not
+    // 87, in pairs 78 and not 76, with six blocks an SM in its place.)
+    constexpr bool kAhead = deep(VPT) == 0 && G < 32 && VPT <= (PAIRS ? 4 : 2) && !(HEAD && PAIRS);
     const uint32_t step = gridDim.x * (kThreads / G);
     // The warp's rows are neighbours and its lanes stay together: a group past
     // the last row repeats it and stores nothing.
@@ -338,7 +341,7 @@ cudaError_t launch_kernel(RopeArgs a, int sms, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     return launch_early(norm_rope_kernel<T, G, VPT, NORM, PAIRS, HEAD>,
-                        std::min(blocks, (uint32_t)sms * blocks_per_sm(VPT, HEAD)), kThreads, smem, st, a);
+                        std::min(blocks, (uint32_t)sms * blocks_per_sm(VPT, HEAD, PAIRS)), kThreads, smem, st, a);
 }
 
 template <typename T, int G, int VPT>
