@@ -12,7 +12,7 @@
 // blocks of more than one token that stays).
 //
 // Bound by the 4 bytes a score that are read for many long rows, by the chain
-// of dependent steps for one: 64 requests of 1K to 8K tokens 8.4 us, one of
+// of dependent steps for one: 64 requests of 1K to 8K tokens 8.6 us, one of
 // 128K 14, 512 rows of 4K to 32K by blocks of 64 19 (2.5 TB/s).
 //
 // Design: a cluster of thread blocks per row, as many of them as it takes to
