@@ -441,7 +441,8 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
  *   x            bf16 or f16 (x_type), token t head h at x + t*x_row_stride +
  *                h*x_head_stride (elements; 0 where a row is shared).
  *   weight       x's type [norm_dim], or NULL: no norm.
- *   positions    int64 [tokens], or NULL: no rotation; cos_sin f32
+ *   positions    int64 [tokens], or NULL: no rotation (num_positions,
+ *                rope_start and rope_dim are then not looked at); cos_sin f32
  *                [num_positions, rope_dim], 16-byte aligned.
  *   slots        int64 [tokens], or NULL: token t to row t.
  *   out          x's type, or e4m3 codes: rows of out_row_stride, heads of

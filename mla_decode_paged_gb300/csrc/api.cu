@@ -729,6 +729,7 @@ mla_status mla_norm_rope(const void *x, int64_t x_row_stride, int64_t x_head_str
         return fail(MLA_ERR_INVALID, "rope_start must be a multiple of 8, rope_dim of 16, their sum at most width");
     if (positions && (num_positions < 1 || num_positions > (int64_t)1 << 40))
         return fail(MLA_ERR_INVALID, "num_positions outside 1..2^40");
+    if (!positions) num_positions = rope_start = rope_dim = 0;      // no rotation, whatever they say
     if (quant == MLA_QUANT_STATIC && !(std::isfinite(scale) && scale >= 1.17549435e-38f))
         return fail(MLA_ERR_INVALID, "scale must be finite and >= 2^-126");
     const auto bad_stride = [](int64_t s) { return s < 0 || s % 8 != 0 || s > 1 << 30; };    // extents stay below 2^63

@@ -396,3 +396,26 @@ def test_past_32_bits():
     _check(held[-1:], None, y, top, None, None)
     assert held[5:-1].eq(1).all() and not held[:5].any()
     assert mla.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [0, 1, 3])
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("np_,start,rope", [(100, 64, 64), (0, 0, 128), (-1, 3, 4096), (1 << 62, -8, -16), (1, 1 << 30, 1 << 30)])
+def test_without_positions_nothing_is_rotated(lib, np_, start, rope, flags, quant):
+    # through the C ABI, where sizes of a rotation may be left in a call that has no positions
+    T, H, width = 37, 3, 128
+    x, w, _, _ = _inputs(T, H, width, width, 0, BF)
+    out = torch.empty(T, H, width, dtype=BF if quant == 0 else E4M3, device=DEV)
+    sc = torch.empty(T, H, device=DEV)
+    scale = 0.05 if quant == 3 else 0.0
+    st = lib.mla_norm_rope(x.data_ptr(), H * width, width, 0, w.data_ptr(), width, 1e-6, None, None, np_, start, rope, flags, T,
+                           H, width, quant, scale, None, T, out.data_ptr(), H * width, width, sc.data_ptr(), None)
+    assert st == mla.MLA_OK
+    torch.cuda.synchronize()
+    want, scales = mla.norm_rope(x, w, 1e-6, quant={0: None, 1: "head", 3: "static"}[quant], scale=scale or None)
+    assert torch.equal(out.view(torch.uint8), want.view(torch.uint8))
+    assert quant != 1 or torch.equal(sc, scales)
+    y, top = _plain(x, w, 1e-6, None, None, 0, False)
+    _check(out, scales, y, top, {0: None, 1: "head", 3: "static"}[quant], scale)
+    assert mla.device_status() == 0
