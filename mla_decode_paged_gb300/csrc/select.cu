@@ -78,7 +78,8 @@ __device__ __forceinline__ Row row_of(const SelectArgs &a, int b) {
     x.seen = a.causal ? max(0, end - begin - a.qlen + x.tq + 1) : end - begin;
     x.blocks = (x.seen + (1 << a.log_block) - 1) >> a.log_block;
     x.kept = min(x.blocks, a.topk);
-    x.tokens = x.kept == x.blocks ? x.seen : ((x.kept - x.blocks) << a.log_block) + x.seen;
+    // Where some stay, the last one does: all whole but that.
+    x.tokens = x.kept == 0 ? 0 : x.seen - ((x.blocks - x.kept) << a.log_block);
     return x;
 }
 

@@ -307,3 +307,29 @@ def test_many_rows():
     R, qlen = 1 << 13, 16
     lengths = torch.randint(0, 12, (R,), generator=torch.Generator().manual_seed(2)).tolist()
     _run(_rand(qlen, sum(lengths)), lengths, 4, 1, 1, 0, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("block", [1, 2, 4, 64, 256])
+@pytest.mark.parametrize("lengths,qlen", [
+    ([5], 1),
+    ([10, 0, 63, 64, 65, 3], 3),
+    ([3, 700, 1, 66] * 64, 4),          # 1,024 rows: each cluster counts the rows before its own
+    ([3, 700, 1, 66, 9] * 205, 1),      # 1,025: a kernel of its own does
+    ([20001], 1),                       # a cluster
+    ([9001, 20001, 1] * 60, 1),
+])
+def test_no_block_stays(lengths, qlen, block, causal):
+    # every list is empty, whatever the last block's length; a caller's larger output is -1 throughout
+    po = torch.full((777,), 7, dtype=torch.int32, device=DEV)
+    po, io = _run(_rand(qlen, sum(lengths)), lengths, 0, block, 1, 2, causal, pages_out=po)
+    assert not io.any() and po.eq(-1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block", [1, 8])
+@pytest.mark.parametrize("lengths,qlen", [([9, 0, 2, 40] * 256, 1), ([9, 0, 2, 40, 5] * 205, 1), ([33, 4, 0, 8] * 64, 4)])
+def test_rows_around_those_that_every_cluster_counts(lengths, qlen, block):
+    # 1,024 rows and 1,025
+    _run(_rand(qlen, sum(lengths)), lengths, 3, block, 1, 1, True, pages_out=torch.full((30000,), 7, dtype=torch.int32, device=DEV))
