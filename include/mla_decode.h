@@ -431,7 +431,9 @@ mla_status mla_add_rms_norm(const void *x, int64_t x_stride, int x_type, const v
  *   NONE    out[T, h] = y rounded to x's type
  *   ROW     sc = scale_of(max |y|) as mla_add_rms_norm; out_scales[T, h] = sc
  *   STATIC  sc = scale
- *   and out[T, h] = e4m3(y * (1 / sc)), to nearest even, saturating at +-448.
+ *   and out[T, h] = e4m3(y * (1 / sc)), to nearest even, saturating at +-448; but
+ *   with STATIC and columns that are neither normed nor rotated e4m3(y / sc), the
+ *   quotient in float32: such columns get the codes that mla_kv_append gives them.
  * A token with a negative slot is skipped (padding); one with a slot past
  * out_rows is skipped and sets MLA_DEV_BAD_PAGE; two tokens with the same
  * slot: which one lands is unspecified, for each 8 columns.  A position

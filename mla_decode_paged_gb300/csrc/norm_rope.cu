@@ -23,7 +23,11 @@
 // time the 96 heads took 68 us).  The sum of squares and the maximum are
 // joined by shuffles inside the group, so rows pass no barrier; the arithmetic
 // takes two columns an instruction, without which the 96 heads are bound by
-// issue.  Weights are in shared memory.
+// issue.  Weights are in shared memory.  Codes are those of products with the
+// scale's reciprocal, one rounding beside those of y itself; but where columns
+// of x come through as they are and the scale is given, those of the quotient,
+// as kv_append writes them to the same rows (two multiply-adds and a clamp more
+// an element: 16,384 x 64 rotated heads of 128 83 us and not 71).
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -50,6 +54,10 @@ constexpr int blocks_per_sm(int vpt, bool head, bool pairs) {
 // vectors a lane no gain, and 4,096 rows 3.3 us and not 3.1).
 constexpr int deep(int vpt) { return vpt >= 8 ? 2 : 0; }
 
+// Whether these lanes may form quotients (16,384 rows of 576 columns, none its
+// own, 8.2 us; where 9 vectors a lane had the code too, 9.3).
+constexpr bool exact(int vpt) { return vpt <= 5; }
+
 struct RopeArgs {
     const void *x, *weight;
     const int64_t *positions, *slots;
@@ -61,8 +69,9 @@ struct RopeArgs {
     uint32_t rows, heads, magic, shift;     // row / heads = row * magic >> (31 + shift), rows below 2^31
     int vecs, norm_vecs, rope0, rope_vecs, half;    // half: half the rotation's columns
     int turns;              // pairs of a lane's places that hold halves of the rotation
-    float eps, inv_norm, inv_scale;
+    float eps, inv_norm, scale, inv_scale;
     int quant;
+    bool exact;             // a given scale divides, as some columns are x's own
 };
 
 // Eight columns as four pairs.
@@ -305,9 +314,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) nor
             continue;
         }
         uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + at);
-        const auto store = [&](int k, const Vec &v, uint64_t inv) {
-            const uint2 q = make_uint2(codes(mul2(v.p[0], inv), mul2(v.p[1], inv)), codes(mul2(v.p[2], inv), mul2(v.p[3], inv)));
+        const auto store = [&](int k, uint64_t q0, uint64_t q1, uint64_t q2, uint64_t q3) {
+            const uint2 q = make_uint2(codes(q0, q1), codes(q2, q3));
             if (write && (mine >> k & 1)) o[vec[k]] = q;
+        };
+        const auto store_product = [&](int k, const Vec &v, float inv) {
+            const uint64_t f = pair(inv, inv);
+            store(k, mul2(v.p[0], f), mul2(v.p[1], f), mul2(v.p[2], f), mul2(v.p[3], f));
         };
         if (HEAD) {
             Vec held[HEAD ? VPT : 1];
@@ -324,9 +337,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) nor
             const float sc = block_scale(amax), inv = __fdiv_rn(1.f, sc);
             if (write && in == 0) a.scales[(uint64_t)to * a.heads + h] = sc;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) store(k, held[HEAD ? k : 0], pair(inv, inv));
+            for (int k = 0; k < VPT; ++k) store_product(k, held[HEAD ? k : 0], inv);
+        } else if (exact(VPT) && a.exact) {
+            const Divisor d = divisor_of(a.scale);
+            each([&](int k, const Vec &v) { store(k, quotient2(v.p[0], d), quotient2(v.p[1], d), quotient2(v.p[2], d), quotient2(v.p[3], d)); });
         } else {
-            each([&](int k, const Vec &v) { store(k, v, pair(a.inv_scale, a.inv_scale)); });
+            each([&](int k, const Vec &v) { store_product(k, v, a.inv_scale); });
         }
     }
 }
@@ -370,8 +386,9 @@ cudaError_t launch_width(const RopeArgs &a, bool pairs, int sms, cudaStream_t st
     if (fits(16, 3)) return launch<T, 16, 3>(a, pairs, sms, st);
     if (a.rows < 16 * (uint32_t)sms && fits(32, 3)) return launch<T, 32, 3>(a, pairs, sms, st);
     if (a.rows < 16 * (uint32_t)sms && fits(32, 4)) return launch<T, 32, 4>(a, pairs, sms, st);
-    if (a.rows >= 64 * (uint32_t)sms && fits(8, 9)) return launch<T, 8, 9>(a, pairs, sms, st);
+    if (a.rows >= 64 * (uint32_t)sms && fits(8, 9) && !a.exact) return launch<T, 8, 9>(a, pairs, sms, st);
     if (fits(16, 5)) return launch<T, 16, 5>(a, pairs, sms, st);
+    if (a.exact) return launch<T, 32, 4>(a, pairs, sms, st);
     return launch<T, 16, 8>(a, pairs, sms, st);
 }
 
@@ -409,7 +426,10 @@ cudaError_t norm_rope_launch(const void *x, int64_t x_row, int64_t x_head, int x
     a.half = rope_dim / 2;
     a.eps = eps;
     a.inv_norm = weight ? 1.f / (float)norm_dim : 0.f;
-    a.inv_scale = quant == MLA_QUANT_STATIC ? 1.f / scale : 1.f;
+    a.scale = quant == MLA_QUANT_STATIC ? scale : 1.f;
+    a.inv_scale = 1.f / a.scale;
+    const int norm_end = 8 * a.norm_vecs, rope_end = rope_start + rope_dim;
+    a.exact = quant == MLA_QUANT_STATIC && !(norm_end >= width || (rope_end >= width && norm_end >= rope_start));
     a.quant = quant;
     return x_type == MLA_TYPE_BF16 ? launch_width<__nv_bfloat16>(a, pairs, sms, st)
                                    : launch_width<__half>(a, pairs, sms, st);

@@ -95,4 +95,34 @@ __device__ __forceinline__ float block_scale(float amax) {
     return amax == 0.f ? 1.f : max_nan(__fdiv_rn(amax, kE4m3Max), kMinScale);
 }
 
+// A quotient y / s without a division an element: q = y * r with r = 1 / s,
+// then q + (y - q * s) * r.  Where y's significand is not below s's, q is
+// within one unit of y / s and the result is y / s rounded (Markstein's
+// theorem).  Else q is within 1.5 and the result, before its own rounding,
+// within 5 * 2^-24 of a unit: no pair y, s lies so near to a border between two
+// e4m3 codes that this moves it over one (all pairs that might are tested).
+// The remainder is exact or one of its bits short; rounded down, a zero
+// remainder keeps the sign of a zero y.  `up` brings y and s nearer to 1 by a
+// power of two where a remainder could underflow, and q is held to 2^15, as
+// that of an infinite one would be no number.
+struct Divisor {
+    float up, inv, s;       // s negated
+};
+__device__ __forceinline__ Divisor divisor_of(float s) {
+    const float up = s < 0x1p-64f ? 0x1p64f : s > 0x1p64f ? 0x1p-64f : 1.f;
+    return {up, __fdiv_rn(1.f, s * up), -s * up};
+}
+// Two quotients whose e4m3 codes are those of y / s.
+__device__ __forceinline__ uint64_t quotient2(uint64_t y, const Divisor &d) {
+    const uint64_t inv = pair(d.inv, d.inv), s = pair(d.s, d.s);
+    y = mul2(y, pair(d.up, d.up));
+    float2 f = parts(mul2(y, inv));
+    asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(f.x) : "f"(0x1p15f));
+    asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(f.y) : "f"(0x1p15f));
+    const uint64_t q = pair(f.x, f.y);
+    uint64_t rest;
+    asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(rest) : "l"(q), "l"(s), "l"(y));
+    return fma2(rest, inv, q);
+}
+
 }  // namespace mla

@@ -419,3 +419,105 @@ def test_without_positions_nothing_is_rotated(lib, np_, start, rope, flags, quan
     y, top = _plain(x, w, 1e-6, None, None, 0, False)
     _check(out, scales, y, top, {0: None, 1: "head", 3: "static"}[quant], scale)
     assert mla.device_status() == 0
+
+
+def _patterns(type_, width):
+    """Every value of a 16-bit type, in rows of `width` (the last ones once more)."""
+    bits = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16)
+    return bits[torch.arange(-(-(1 << 16) // width) * width) % (1 << 16)].view(type_).view(-1, width)
+
+
+def _codes(y, sc):
+    """e4m3 codes of the float32 quotient y / sc (IEEE division, to nearest), saturating; every NaN one code."""
+    q = (y / sc).clamp(-448, 448)
+    return torch.where(q.isnan(), torch.tensor(0x7f, dtype=torch.uint8), q.to(E4M3).view(torch.uint8))
+
+
+def _same_codes(got, want):
+    got = got.cpu().view(torch.uint8)
+    got = torch.where(got == 0xff, torch.tensor(0x7f, dtype=torch.uint8), got)
+    assert torch.equal(got, want)
+
+
+SCALES = [0.03, 0.05, 1 / 3, 1.0, 0.7853982, 447.0, 3.0e-5, 1.1e18, 3.0e38, 2.0 ** -64, 1.9e19, 5.0e-20, 2.0 ** -126, 1.3e-38,
+          math.pi * 2.0 ** -100]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("type_", [BF, FP])
+@pytest.mark.parametrize("width", [8, 40, 128, 192, 576, 1024])
+def test_codes_with_a_given_scale_are_those_of_the_quotient(width, type_):
+    # no norm and no rotation: y is x, so a code is known to the bit, ties among them
+    x = _patterns(type_, width)
+    for scale in SCALES:
+        sc = torch.tensor(scale, dtype=torch.float32)
+        want = _codes(x.float(), sc)
+        _same_codes(mla.norm_rope(x.to(DEV), quant="static", scale=scale)[0], want)
+    want = _codes(x.float(), torch.tensor(0.03))
+    heads = x[:x.shape[0] // 2 * 2].view(-1, 2, width)
+    _same_codes(mla.norm_rope(heads.to(DEV), quant="static", scale=0.03)[0], want[:heads.shape[0] * 2].view_as(heads))
+    many = x.repeat(-(-12000 // x.shape[0]), 1)
+    _same_codes(mla.norm_rope(many.to(DEV), quant="static", scale=0.03)[0], want.repeat(many.shape[0] // x.shape[0], 1))
+    if width > 40:                  # beside a norm and a rotation: columns 16 to 24 and the last ones are x's
+        g, pos = torch.ones(16, dtype=type_, device=DEV), torch.zeros(x.shape[0], dtype=torch.int64, device=DEV)
+        for pairs in (False, True):
+            got = mla.norm_rope(x.to(DEV), g, positions=pos, cos_sin=_table(1, 16).to(DEV), rope_start=24, interleaved=pairs,
+                                quant="static", scale=0.03)[0]
+            mine = torch.tensor([*range(16, 24), *range(40, width)])
+            _same_codes(got.cpu().view(torch.uint8)[:, mine], want[:, mine])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k_scale", [0.03, 0.05, 1 / 3, 1.0, 447.0, 2.0 ** -120, 3.0e38])
+def test_the_two_writers_of_a_cache_agree(k_scale):
+    # kv_append and norm_rope into the same latent rows: every bf16 value
+    x = _patterns(BF, 576).to(DEV)
+    slots = torch.randperm(x.shape[0] + 3, generator=torch.Generator().manual_seed(1))[:x.shape[0]].to(DEV)
+    a, b = (torch.zeros(x.shape[0] + 3, 576, dtype=torch.uint8, device=DEV) for _ in range(2))
+    mla.kv_append(a, x[:, :512].contiguous(), x[:, 512:].contiguous(), slots, k_scale)
+    mla.norm_rope(x, quant="static", scale=k_scale, slots=slots, out=b)
+    nan = x.isnan().cpu()
+    a, b = a[slots].cpu(), b[slots].cpu()
+    assert torch.equal(a[~nan], b[~nan])
+    assert (b[nan] & 0x7f).eq(0x7f).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pairs", [False, True])
+def test_quotients_beside_a_tie(pairs):
+    # Any float32 comes through the rotation: 1 * c - 0 * s.  With r = RN(1 / b) the quotient is q0 = RN(a r) corrected
+    # once by its remainder.  For a >= b (significands) q0 is within one unit and the result is RN(a / b) (Markstein);
+    # for a < b it is within 1.5, and the corrected one off, before its rounding, by the remainder (1.5 x 2^-24 b) times
+    # r's error (2^-25) and the remainder's own (2^-47) times r: with b times that R = 2^49 |a - b m| is 6 + 4 at most.
+    # A code can differ from the division's only where a / b is so near to half a unit beside a border t = k / 64 of two
+    # codes: A 2^26 = B (k 2^20 +- 1 or 2) + R.  All such A and B, with room in R:
+    found = []
+    for k in range(16, 64):
+        for by in (-2, -1, 1, 2):
+            m = (k << 20) + by
+            for r in range(-24, 25):
+                step = 1 << 26
+                d = math.gcd(m, step)
+                if r == 0 or r % d:
+                    continue
+                b = (-r // d * pow(m // d, -1, step // d)) % (step // d)
+                while b < 1 << 24:
+                    a = (b * m + r) >> 26
+                    if b >= 1 << 23 and 0 < a < 1 << 24:
+                        found.append((a, b))
+                    b += step // d
+    assert len(found) > 500
+    for a, b in found:
+        width = 24                          # eight columns are not rotated, so codes are the quotient's
+        y = torch.tensor([[float(a) * 2.0 ** -e for e in range(18, 26)]], dtype=torch.float32)      # quotients t * 2^(23 - e)
+        scale = float(b) * 2.0 ** -23
+        cs = torch.cat([y, torch.zeros_like(y)], 1).to(DEV)
+        x = torch.zeros(1, 1, width, dtype=BF)
+        if pairs:
+            x[..., 0:16:2] = 1
+        else:
+            x[..., :8] = 1
+        pos = torch.zeros(1, dtype=torch.int64, device=DEV)
+        out = mla.norm_rope(x.to(DEV), positions=pos, cos_sin=cs, interleaved=pairs, quant="static", scale=scale)[0].cpu()[0, 0]
+        got = out.view(torch.uint8)[0:16:2] if pairs else out.view(torch.uint8)[:8]
+        assert torch.equal(got, _codes(y[0], torch.tensor(scale, dtype=torch.float32))), (a, b)
