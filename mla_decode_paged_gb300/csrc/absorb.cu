@@ -279,14 +279,14 @@ __device__ void rotate(const AbsorbArgs &a) {
 #pragma unroll
             for (int k = 0; k < kHeads; ++k) {
                 const uint4 *from = reinterpret_cast<const uint4 *>(x + min(h + k, heads - 1) * a.q_head);
-                u[k] = __ldg(from + v0);
-                v[k] = __ldg(from + v1);
+                u[k] = from[v0];
+                v[k] = from[v1];
             }
         };
         fetch(0);
         float c[8], s[8];
         if (a.positions) {
-            int64_t p = __ldg(a.positions + t);
+            int64_t p = a.positions[t];
             if ((uint64_t)p >= (uint64_t)a.num_positions) {
                 if (i4 == 0 && h0 == 0 && real) flag(MLA_DEV_BAD_POSITION);
                 p = 0;
@@ -294,8 +294,8 @@ __device__ void rotate(const AbsorbArgs &a) {
             const float4 *cs = reinterpret_cast<const float4 *>(a.cos_sin + p * MLA_D_ROPE) + 2 * i4;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                *reinterpret_cast<float4 *>(&c[4 * j]) = __ldg(cs + j);
-                *reinterpret_cast<float4 *>(&s[4 * j]) = __ldg(cs + kHalf / 4 + j);
+                *reinterpret_cast<float4 *>(&c[4 * j]) = cs[j];
+                *reinterpret_cast<float4 *>(&s[4 * j]) = cs[kHalf / 4 + j];
             }
         } else {
 #pragma unroll

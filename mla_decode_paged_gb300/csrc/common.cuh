@@ -54,6 +54,8 @@ inline cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned th
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 // Until the kernels before this one have completed and their writes are visible.
+// (To plain loads: a read-only one, __ldg, may be moved before it, as its data
+// is taken not to change while the kernel runs.)
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 static inline cudaError_t read_status(unsigned int *flags, bool clear) {
@@ -286,7 +288,7 @@ __device__ __forceinline__ void split_range(int len, int n, int k, int *start, i
 // the same way.
 __device__ __forceinline__ int request_len(const int32_t *indptr, int r, int64_t num_pages, int *base,
                                            int log2p = 0, const int32_t *last_page_len = nullptr) {
-    int a = __ldg(indptr + r), b = __ldg(indptr + r + 1);
+    const int a = indptr[r], b = indptr[r + 1];
     if (a < 0 || b < a || (int64_t)b > num_pages) {
         flag(MLA_DEV_BAD_INDPTR);
         *base = 0;

@@ -76,7 +76,7 @@ __device__ void producer(const ScoreArgs &a, const CUtensorMap *mk, uint8_t *sm,
         const int tok0 = w.t * kTile + 4 * lane;
         const int n = w.valid() ? min(max(w.len - tok0, 0), 4) : 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rows[i] = i < n ? __ldg(a.pages + (int64_t)w.base + tok0 + i) : -1;
+        for (int i = 0; i < 4; ++i) rows[i] = i < n ? a.pages[(int64_t)w.base + tok0 + i] : -1;
         return n;
     };
     // The page list is brought to L2 kAhead tiles before its indices are read.
@@ -197,7 +197,7 @@ __device__ void prepare(const ScoreArgs &a, const CUtensorMap *mq, uint8_t *sm, 
             c[k] = 0.f;
             if (tq < rows && h < a.heads) {
                 const int64_t at = (row0 + tq) * a.heads + h;
-                c[k] = __ldg(a.weights + at) * (a.q_scales ? __ldg(a.q_scales + at) : 1.f) * a.scale;
+                c[k] = a.weights[at] * (a.q_scales ? a.q_scales[at] : 1.f) * a.scale;
             }
         }
 #pragma unroll

@@ -85,7 +85,7 @@ __device__ __forceinline__ Vec unpack(const uint4 &raw) {
     return {{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
 }
 __device__ __forceinline__ Vec load8(const float *p) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
     return {{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
 }
 __device__ __forceinline__ void spread(const Vec &v, float (&f)[8]) {
@@ -160,13 +160,17 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) nor
         row = min(row, a.rows - 1);
         const uint32_t t = (uint32_t)(((uint64_t)row * a.magic) >> (31 + a.shift));
         head = row - t * a.heads;
-        if (a.positions) pos = __ldg(a.positions + t);
-        slot = a.slots ? __ldg(a.slots + t) : (int64_t)t;
-        if (kDeep) return;
+        if (kDeep) {
+            if (a.positions) pos = a.positions[t];
+            slot = a.slots ? a.slots[t] : (int64_t)t;
+            return;
+        }
         const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) +
                                                          ((uint64_t)t * a.x_row + (uint64_t)head * a.x_head));
 #pragma unroll
         for (int k = 0; k < VPT; ++k) next[kDeep ? 0 : k] = (mine >> k & 1) ? x[vec[k]] : make_uint4(0, 0, 0, 0);
+        if (a.positions) pos = a.positions[t];
+        slot = a.slots ? a.slots[t] : (int64_t)t;
     };
     // Into the ring: every lane its own vectors, which it alone reads.
     const auto copy = [&](uint32_t row0, int stage) {
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) nor
     }
     int stage = 0;
     if (NORM) {
-        for (int i = threadIdx.x; i < a.norm_vecs; i += kThreads) weight[i] = __ldg(static_cast<const uint4 *>(a.weight) + i);
+        for (int i = threadIdx.x; i < a.norm_vecs; i += kThreads) weight[i] = static_cast<const uint4 *>(a.weight)[i];
         __syncthreads();
     }
     for (uint32_t row0 = first; row0 < a.rows; row0 += step) {
@@ -267,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) nor
             }
             if (PAIRS && (turned >> k & 1)) {
                 const float *at = cs + 4 * (vec[k] - a.rope0);
-                const float4 c = __ldg(reinterpret_cast<const float4 *>(at));
-                const float4 s = __ldg(reinterpret_cast<const float4 *>(at + a.half));
+                const float4 c = *reinterpret_cast<const float4 *>(at);
+                const float4 s = *reinterpret_cast<const float4 *>(at + a.half);
                 const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -292,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) nor
         // use(k, its value) for every place.
         const auto each = [&](auto use) {
 #pragma unroll
-            for (int k = 0; k < VPT; k += PAIRS ? 1 : 2) {
+            for (int i = 0; i < VPT; i += PAIRS ? 1 : 2) {
+                const int k = PAIRS ? VPT - 1 - i : i;
                 Vec u = value(k);
                 if (PAIRS || k + 1 == VPT) {
                     use(k, u);

@@ -69,7 +69,7 @@ __device__ __forceinline__ Row row_of(const SelectArgs &a, int b) {
     Row x;
     x.r = a.qlen == 1 ? b : (int)__umulhi((uint32_t)b, a.over_qlen);       // b below 2^24
     x.tq = b - x.r * a.qlen;
-    int begin = __ldg(a.indptr + x.r), end = __ldg(a.indptr + x.r + 1);
+    int begin = a.indptr[x.r], end = a.indptr[x.r + 1];
     if (begin < 0 || end < begin || end > a.num_pages) {        // as request_len does
         flag(MLA_DEV_BAD_INDPTR);
         begin = end = 0;
@@ -196,7 +196,7 @@ __device__ __noinline__ void load_keys(uint32_t *key, const float *w, int r0, in
         for (int i0 = tid - f0; i0 < held - f0; i0 += 8 * THREADS, from += 8 * THREADS, to += 8 * place(THREADS)) {
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = (uint32_t)(i0 + THREADS * j) < width ? __ldg(from + THREADS * j) : 0.f;
+            for (int j = 0; j < 8; ++j) v[j] = (uint32_t)(i0 + THREADS * j) < width ? from[THREADS * j] : 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t x = weight_key(v[j]);
@@ -224,7 +224,7 @@ __device__ __noinline__ void load_keys(uint32_t *key, const float *w, int r0, in
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const int t = t0 + 32 * k + lane;
-                v[k] = t < t1 ? __ldg(w + t) : -INFINITY;
+                v[k] = t < t1 ? w[t] : -INFINITY;
             }
             halve<0>(v);
             if (lb >= 2) halve<1>(v);
@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BLOCKED ? 4 : 5) : 
     // Kept tokens of the rows before this one, and of all.
     uint32_t before = 0, all_tokens = 0;
     if (a.scanned) {
-        before = (uint32_t)__ldg(a.indptr_out + b);
-        all_tokens = (uint32_t)__ldg(a.indptr_out + rows);
+        before = (uint32_t)a.indptr_out[b];
+        all_tokens = (uint32_t)a.indptr_out[rows];
     } else {
         before = tid < b ? my_tokens : 0;
         all_tokens = my_tokens;
@@ -567,10 +567,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BLOCKED ? 4 : 5) : 
             if (keep >> j & 1) list[put++] = i0 + j;
         __syncthreads();
         const uint32_t to = before + (first << lb);
-#pragma unroll 4
-        for (uint32_t x = tid; x < n; x += THREADS) {
-            const int i = (list[x >> lb] << lb) + (int)(x & ((1u << lb) - 1));
-            if (i < row.seen && to + x < limit) a.pages_out[to + x] = __ldg(pages + i);
+#pragma unroll 1
+        for (uint32_t x0 = tid; x0 < n; x0 += 4 * THREADS) {     // four loads, then their stores
+            int32_t page[4];
+            uint32_t some = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = x0 + j * THREADS;
+                if (x >= n) break;
+                const int i = (list[x >> lb] << lb) + (int)(x & ((1u << lb) - 1));
+                if (i >= row.seen || to + x >= limit) continue;
+                some |= 1u << j;
+                page[j] = pages[i];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (some >> j & 1) a.pages_out[to + x0 + j * THREADS] = page[j];
         }
     }
     if (rank == 0)

@@ -78,3 +78,26 @@ def test_no_block_of_a_cluster_ends_while_its_memory_is_read():
     assert body.rstrip().endswith("if (!one) cluster_wait();")
     assert body.rindex("remote(") < body.rindex("cluster_arrive();") < body.rindex("cluster_wait();")
     assert body.count("cluster_arrive();") == 2 and body.count("cluster_wait();") == 3       # the first's on either path
+
+
+@pytest.mark.parametrize("name", ["absorb.cu", "index_scores.cu", "norm_rope.cu", "select.cu", "cluster.cuh", "tile_walk.cuh",
+                                  "vec8.cuh", "tc.cuh"])
+def test_a_kernel_that_starts_early_reads_by_plain_loads(name):
+    # a read-only load says that its data does not change while the kernel runs, and may be moved before grid_wait()
+    assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", _text(name))
+
+
+def test_the_requests_lengths_are_read_by_plain_loads():
+    body = _function(_text("common.cuh"), r"int request_len\(")
+    assert "indptr[r]" in body and "__ldg(indptr" not in body
+
+
+@pytest.mark.parametrize("name", ["absorb.cu", "index_scores.cu", "norm_rope.cu", "select.cu"])
+def test_no_argument_is_dereferenced_before_the_wait(name):
+    text = _text(name)
+    early = set(re.findall(r"launch_early\((\w+)", text)) | set(re.findall(r"cudaLaunchKernelEx\(&cfg, (\w+)", text))
+    for kernel in early:
+        body = _function(text, r"\b%s\(" % kernel)
+        before = body[body.index("{"):body.index("grid_wait();")]
+        before = re.sub(r"const auto (fetch|copy) = .*?\n    \};", "", before, flags=re.S)       # called after it
+        assert not re.search(r"\ba\.\w+ ?\[|\*a\.|\ba\.(x|weight|positions|slots|cos_sin|q|weights|q_scales|pages|indptr|scores)\b", before)
