@@ -29,11 +29,11 @@ __device__ __forceinline__ void merge_fma8(float (&acc)[8], float w, uint4 v) {
 // heads); `row` indexes the nrow axis.  On return (every lane): r0 / r1 the
 // lane's two 16-byte vectors of the bf16 latent, and lse_row the merged LSE
 // (-inf for a row whose splits are all empty, whose latent is then 0).
-__device__ __forceinline__ void merge_row(const __nv_bfloat16 *__restrict__ o, const float *__restrict__ lse,
+__device__ __forceinline__ void merge_row(const __nv_bfloat16 *o, const float *lse,
                                           int num_splits, long long nrow, long long row, int lane, uint4 &r0,
                                           uint4 &r1, float &lse_row) {
     float mx = -INFINITY;
-    for (int k = lane; k < num_splits; k += 32) mx = fmaxf(mx, __ldg(lse + (long long)k * nrow + row));
+    for (int k = lane; k < num_splits; k += 32) mx = fmaxf(mx, lse[(long long)k * nrow + row]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
 
@@ -47,7 +47,7 @@ __device__ __forceinline__ void merge_row(const __nv_bfloat16 *__restrict__ o, c
             float w = 0.f;
             bool valid = false;
             if (k < num_splits) {
-                const float l = __ldg(lse + (long long)k * nrow + row);
+                const float l = lse[(long long)k * nrow + row];
                 valid = l > -INFINITY;
                 w = valid ? expf(l - mx) : 0.f;
             }
@@ -70,8 +70,8 @@ __device__ __forceinline__ void merge_row(const __nv_bfloat16 *__restrict__ o, c
                     if (src[j] >= 0) {
                         const uint4 *p = reinterpret_cast<const uint4 *>(
                             o + ((long long)(kb + src[j]) * nrow + row) * MLA_D_LATENT);
-                        v0[j] = __ldg(p + lane);
-                        v1[j] = __ldg(p + 32 + lane);
+                        v0[j] = p[lane];
+                        v1[j] = p[32 + lane];
                     }
                 }
 #pragma unroll

@@ -118,16 +118,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < kColBlocks; ++kb)
             tc::tma_3d(sm + kBOff + kb * T::kBBlock, &ml, 64 * kb, h, t0, &full_l);
     }
-    if (tid < NR) active[tid] = tid < nrows && __ldg(a.lengths + (t0 + tid) / a.qlen) > 0;
+    if (tid < NR) active[tid] = tid < nrows && a.lengths[(t0 + tid) / a.qlen] > 0;
     // This thread's gate words (bf16 pairs w = tid + 512 k: row w / 64, pair
     // w % 64), loaded while the copies, the merge and the MMAs are in flight.
     uint32_t gw[T::kPairs];
 #pragma unroll
     for (int k = 0; k < T::kPairs; ++k) {
         const int w = tid + kThreads * k, r = w / (MLA_D_V / 2), p = w - r * (MLA_D_V / 2);
-        gw[k] = r < nrows ? __ldg(reinterpret_cast<const uint32_t *>(
-                                a.gate + ((long long)(t0 + r) * a.H + h) * MLA_D_V + 2 * p))
-                          : 0u;
+        gw[k] = r < nrows ? *reinterpret_cast<const uint32_t *>(a.gate + ((long long)(t0 + r) * a.H + h) * MLA_D_V + 2 * p) : 0u;
     }
     if constexpr (MERGE) {
         // Row r = warp.  Lane l holds latent columns 8l .. 8l+7 (column block

@@ -101,3 +101,9 @@ def test_no_argument_is_dereferenced_before_the_wait(name):
         before = body[body.index("{"):body.index("grid_wait();")]
         before = re.sub(r"const auto (fetch|copy) = .*?\n    \};", "", before, flags=re.S)       # called after it
         assert not re.search(r"\ba\.\w+ ?\[|\*a\.|\ba\.(x|weight|positions|slots|cos_sin|q|weights|q_scales|pages|indptr|scores)\b", before)
+
+
+@pytest.mark.parametrize("name", ["value_gate.cu", "merge_row.cuh"])
+def test_the_value_kernel_reads_by_plain_loads(name):
+    # launched while attend or merge still run; its gate and lengths may be written by whatever kernel comes before
+    assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", _text(name))
