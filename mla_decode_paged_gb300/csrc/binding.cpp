@@ -263,7 +263,8 @@ PyObject *add_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // Strides of a [rows, heads, width] tensor of this type with contiguous
-// heads, or of [rows, width] as one head (rows, heads of one: dense).
+// heads, or of [rows, width] as one head (rows, heads of one: dense; a lone
+// row has no stride to exceed the limit, however far apart its heads lie).
 struct HeadRows {
     int64_t rows, heads, width, row, head;
 };
@@ -274,7 +275,7 @@ HeadRows heads_of(const at::Tensor &t, const char *name, int64_t dev) {
         refuse(std::string(name) + " must be [T, H, D] or [T, D] with contiguous heads on the first argument's device");
     HeadRows h = {t.size(0), n == 3 ? t.size(1) : 1, t.size(n - 1), 0, 0};
     h.head = h.heads > 1 ? t.stride(1) : h.width;
-    h.row = h.rows > 1 ? t.stride(0) : (h.heads > 1 ? (h.heads - 1) * h.head : 0) + h.width;
+    h.row = h.rows > 1 ? t.stride(0) : h.width;
     return h;
 }
 

@@ -521,3 +521,22 @@ def test_quotients_beside_a_tie(pairs):
         out = mla.norm_rope(x.to(DEV), positions=pos, cos_sin=cs, interleaved=pairs, quant="static", scale=scale)[0].cpu()[0, 0]
         got = out.view(torch.uint8)[0:16:2] if pairs else out.view(torch.uint8)[:8]
         assert torch.equal(got, _codes(y[0], torch.tensor(scale, dtype=torch.float32))), (a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [None, "head"])
+def test_one_row_whose_heads_lie_far_apart(quant):
+    # one token of heads kept [H, T, D]: each stride within the limit, the last head past 2^30 elements
+    H, T, width = 96, 1 << 16, 192
+    base = torch.empty(H, T, width, dtype=BF, device=DEV)
+    x, w, pos, cs = _inputs(1, H, width, width, 64, BF)
+    base[:, 77] = x[0]
+    far = base[:, 77:78].transpose(0, 1)
+    assert far.stride(1) <= 1 << 30 < (H - 1) * far.stride(1)
+    got = mla.norm_rope(far, w, positions=pos, cos_sin=cs, rope_start=128, quant=quant)
+    want = mla.norm_rope(x, w, positions=pos, cos_sin=cs, rope_start=128, quant=quant)
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8))
+    assert quant is None or torch.equal(got[1], want[1])
+    if quant is None:
+        mla.norm_rope(far, w, positions=pos, cos_sin=cs, rope_start=128, out=far)
+        assert torch.equal(base[:, 77], want[0][0])

@@ -236,3 +236,15 @@ def test_past_32_bits():
     out = mla.query_absorb(big, w, positions=positions, cos_sin=cs)
     _check(out[-4:], *_plain(big[-4:], w, positions[-4:], cs, False))
     assert torch.equal(out[:-3], out[:1].expand(T - 3, H, 576))
+
+
+@pytest.mark.gpu
+def test_one_row_whose_heads_lie_far_apart():
+    # one token of heads kept [H, T, D]: each stride within the limit, the last head past 2^30 elements
+    H, T = 96, 1 << 16
+    base = torch.empty(H, T, 192, dtype=BF, device=DEV)
+    q, w, pos, cs = _inputs(1, H)
+    base[:, 77] = q[0]
+    far = base[:, 77:78].transpose(0, 1)
+    assert far.stride(1) <= 1 << 30 < (H - 1) * far.stride(1)
+    assert torch.equal(mla.query_absorb(far, w, positions=pos, cos_sin=cs), mla.query_absorb(q, w, positions=pos, cos_sin=cs))
