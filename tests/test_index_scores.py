@@ -263,3 +263,22 @@ def test_past_32_bits():
         want[some >= n - 16 + tq + 1] = -math.inf
         _check(out[tq, -n:][some], want, mag)
     assert mla.device_status() == 0
+
+
+def _spread(requests, most, seed):
+    """Lengths spread over the logarithm of 1 to `most`, some requests empty."""
+    u = torch.rand(requests, generator=torch.Generator().manual_seed(seed))
+    n = torch.exp(u * math.log(most)).long()
+    n[::31] = 0
+    return n.tolist()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [12, 64])
+def test_eight_causal_rows_of_a_ragged_batch(heads):
+    # 512 columns a request with 64 heads: two groups of rows
+    lengths = _spread(256, 6000, heads)
+    q, w, qs, k, pages, indptr = _inputs(lengths, 8, heads)
+    got = mla.index_scores(q, w, k, pages, indptr, q_scales=qs, scale=0.3, qlen=8, causal=True)
+    _check(got, *_plain(q, w, qs, k, pages, lengths, 8, 0.3, True))
+    assert mla.device_status() == 0

@@ -333,3 +333,15 @@ def test_no_block_stays(lengths, qlen, block, causal):
 def test_rows_around_those_that_every_cluster_counts(lengths, qlen, block):
     # 1,024 rows and 1,025
     _run(_rand(qlen, sum(lengths)), lengths, 3, block, 1, 1, True, pages_out=torch.full((30000,), 7, dtype=torch.int32, device=DEV))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block,topk", [(1, 700), (64, 12)])
+@pytest.mark.parametrize("requests,most", [(256, 20000), (24, 40000), (160, 40000)])
+def test_eight_causal_rows_of_a_ragged_batch(requests, most, block, topk):
+    # lengths over their logarithm: requests far beyond what the mean gives a block or a cluster, others empty
+    u = torch.rand(requests, generator=torch.Generator().manual_seed(requests))
+    lengths = torch.exp(u * math.log(most)).long()
+    lengths[::31] = 0
+    lengths[5] = most
+    _run(_rand(8, int(lengths.sum())), lengths.tolist(), topk, block, 2, 1, True)
