@@ -546,7 +546,9 @@ def norm_rope(x, weight=None, eps=1e-6, *, positions=None, cos_sin=None, rope_st
     ``slots``: int64 ``[T]``: token t goes to row ``slots[t]`` of ``out``
     (and of ``out_scales``), a cache of any number of rows; negative slots
     are skipped.  ``out=x`` works in place.  Codes and scales that are both new
-    share an allocation.
+    share an allocation, which either of them keeps.  A static scale divides
+    columns that are neither normed nor rotated as :func:`kv_append` does, to
+    the same codes.
     """
     q = _ROPE_QUANT.get(quant)
     if q is None:
@@ -648,7 +650,8 @@ def index_select(scores, pages, indptr, topk, *, block=1, recent=0, sinks=0, cau
     :func:`index_select_capacity` entries, -1 behind the last list) go to
     :func:`attend` with ``qlen=1``: every query row a request of its own,
     whose length, min(tokens, topk * block) for blocks of one token, does not
-    depend on the scores.
+    depend on the scores.  Two new outputs share an allocation, which either
+    of them keeps (the indptr alone the whole page list's).
     """
     r = (_ops_module or _ops()).index_select(scores, pages, indptr, topk, block, recent, sinks, causal, pages_out,
                                              indptr_out, stream)

@@ -126,8 +126,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for stale in (ops, ops_obj):        # not a module of other sources beside this library
             if os.path.exists(stale):
                 os.remove(stale)
-        warnings.warn("the library is built, its Python module is not (add_rms_norm, token_weights, kv_evict and "
-                      "value_gate_lora need it): %s" % e, RuntimeWarning, stacklevel=2)
+        warnings.warn("the library is built, its Python module is not (the operators but "
+                      "kv_append need it): %s" % e, RuntimeWarning, stacklevel=2)
     return LIB
 
 

@@ -12,7 +12,9 @@
 // row above.  Rows of 128 bytes from random places come at 5.6 TB/s at most
 // (plain 16-byte loads of as many in flight as the SMs hold).  32 requests of
 // 32K tokens, 64 heads: 30.6 us (4.7 TB/s); 128 x 4 rows of 4K to 32K, 32
-// heads: 74 (5.0; without the sums 65); 64 requests of 1K to 8K, 64 heads: 13.
+// heads: 75 (4.9; without the sums 65); 64 requests of 1K to 8K, 64 heads: 13;
+// 256 x 8 rows of 128 to 128K 161 with 12 heads (5.1), 292 with 32, 538 with 64
+// (1.2 PFLOP/s: the sums, and the tiles walked twice above 256 columns).
 //
 // Design: one persistent CTA per SM walks a contiguous range of the batch's
 // 128-token tiles.  Tokens are the MMA's M dimension, heads of some query

@@ -12,9 +12,10 @@
 //
 // Bound by DRAM (4 bytes an element, 3 with an e4m3 output, each moved once)
 // for many rows, by launch and the chain position -> table -> store for few:
-// 4,096 tokens x 96 heads of 192 columns 46.8 us (6.45 TB/s), 16,384 rows of
-// 576 columns normed, rotated, quantized and scattered 9.4 (3.5 TB/s), 64 x
-// 64 heads of 128 to codes with a scale a row 1.8.
+// 4,096 tokens x 96 heads of 192 columns 45.6 us (6.6 TB/s), 16,384 rows of
+// 576 columns normed, rotated, quantized and scattered 8.3 to 9.4 (3.9 TB/s
+// with three caches in turn, 3.5 with four, which L2 does not hold), 64 x 64
+// heads of 128 to codes with a scale a row 1.8.
 //
 // A group of G lanes holds a row in registers between its loads and its
 // stores: 8-column vectors (16-byte loads, for wide rows by way of shared
@@ -41,8 +42,8 @@ namespace {
 constexpr int kThreads = 256;
 // Blocks an SM holds, by what their registers allow (40 to 128 a thread):
 // where one more of them would spill, rows in flight are worth less (16,384
-// rows of 576 columns, 5 vectors a lane: 9.1 us with three blocks, 11.0 with
-// four and 120 bytes spilled).
+// rows of 576 columns, 5 vectors a lane: 9.4 us with three blocks, 11.2 with
+// four, which spill).
 constexpr int blocks_per_sm(int vpt, bool head, bool pairs) {
     return vpt <= 2 ? (head && pairs ? 6 : 4) : vpt == 3 ? 4 : vpt <= 5 ? (head ? 2 : 3) : 2;
 }
@@ -50,8 +51,8 @@ constexpr int blocks_per_sm(int vpt, bool head, bool pairs) {
 // Rows (one a group) a warp has on their way or in work through shared memory;
 // 0: through registers.  Where a row takes most of the registers the next
 // one's loads would otherwise wait for its stores (65,536 rows of 576 columns
-// 23.6 us and not 26.8, 16,384 of 1,024 13.5 and 14.6; three rows 27; with 5
-// vectors a lane no gain, and 4,096 rows 3.3 us and not 3.1).
+// 25.5 us and not 27.8, 16,384 of 1,024 12.1 and 13.4; three rows 26.6 and 12.7;
+// with 5 vectors a lane no gain, and 4,096 rows 3.3 us and not 3.1).
 constexpr int deep(int vpt) { return vpt >= 8 ? 2 : 0; }
 
 // Whether these lanes may form quotients (16,384 rows of 576 columns, none its
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) nor
                                                          ((uint64_t)t * a.x_row + (uint64_t)head * a.x_head));
 #pragma unroll
         for (int k = 0; k < VPT; ++k) next[kDeep ? 0 : k] = (mine >> k & 1) ? x[vec[k]] : make_uint4(0, 0, 0, 0);
+        // (After x: 16,384 x 64 heads of 128 81 us, before it 83.)
         if (a.positions) pos = a.positions[t];
         slot = a.slots ? a.slots[t] : (int64_t)t;
     };
@@ -293,7 +295,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(VPT, HEAD, PAIRS)) nor
                 u.p[i] = w;
             }
         };
-        // use(k, its value) for every place.
+        // use(k, its value) for every place; pairs of neighbours from the last
+        // one, so that a rotation at the heads' end has its cosines loaded before
+        // the row's stores (4,096 x 96 heads 45.6 us, from the first 47.5).
         const auto each = [&](auto use) {
 #pragma unroll
             for (int i = 0; i < VPT; i += PAIRS ? 1 : 2) {
@@ -380,9 +384,11 @@ template <typename T>
 cudaError_t launch_width(const RopeArgs &a, bool pairs, int sms, cudaStream_t st) {
     // The fewest lanes that hold a row in few registers and, with halves, both
     // of a pair in one lane.  Rows of 384 columns and more that leave the SMs
-    // idle take a warp each (64 of 576 2.6 us, with 16 lanes 3.0; 1,024 3.0
-    // and 3.4; 16,384 8.6 and 7.4), very many of them 8 lanes (65,536 24 us,
-    // with 16 33; 1,024 4.1 and 3.4).
+    // idle take a warp each, very many of them 8 lanes (us, of 576 columns to
+    // codes in a cache's rows, by a warp, 16 lanes and 8: 64 rows 2.3, 2.7, 3.4;
+    // 1,024 2.4, 2.8, 3.4; 4,096 3.4, 3.3, 3.6; 8,192 5.3, 5.0, 4.5; 10,000
+    // 5.9, 5.6, 6.2; 12,288 7.2, 6.4, 6.6; 16,384 10.2, 9.4, 8.3; 65,536 48, 34,
+    // 25: whole turns of the grid make the steps).
     const auto fits = [&](int g, int vpt) { return a.vecs <= g * vpt && (pairs || 2 * ((a.rope_vecs / 2 + g - 1) / g) <= vpt); };
     if (fits(4, 2)) return launch<T, 4, 2>(a, pairs, sms, st);
     if (fits(8, 2)) return launch<T, 8, 2>(a, pairs, sms, st);

@@ -32,8 +32,8 @@
 // there, coalesced.
 //
 // A row's place in the output is the sum of the kept tokens of the rows
-// before it: each cluster sums over all of them where they are no more than
-// a block's threads, a small kernel writes the indptr first where they are.
+// before it: each cluster sums over all of them up to 1,024 rows, a small
+// kernel writes the indptr first for more.
 #include <algorithm>
 #include <atomic>
 
@@ -690,8 +690,8 @@ cudaError_t index_select_launch(const float *scores, const int32_t *pages, int64
     // The lengths are on the device: the rule goes by their mean.  More rows
     // than SMs that fit half a round of 256 threads take these.  Longer ones
     // take blocks of 16,384, in clusters that hold the mean (512 rows of 8K to
-    // 16K 33 us, in clusters with rounds of 8,192 57; 300 of 40K to 128K 160
-    // and 330; but 256 of 128 to 128K 120 and 89, where the longest go by
+    // 16K 34 us, in clusters with rounds of 8,192 57; 300 of 40K to 128K 160
+    // and 330; but 256 of 128 to 128K 119 and 89, where the longest go by
     // rounds).  Up to as many rows as SMs share a thread block's round, of
     // 16,384 too (100 rows of 16K 12 us, in clusters 16), or a cluster's, and
     // few rows take the blocks that half the SMs hold.
